@@ -557,3 +557,8 @@ def fp8b_stream_probe(kind: int, x: torch.Tensor, q: torch.Tensor, scales: torch
     rc = lib().fp8b_stream_probe(int(kind), _p(x), M, K, _p(q), _p(scales), _stream(x))
     _check("fp8b_stream_probe", rc)
     return q
+
+
+from .attention import (  # noqa: E402
+    KVCache, attention_step, attn_lib, fp8_kv_cache_read, fp8_kv_cache_write, fp8_paged_attention, fp8_qk_norm_rope,
+    fp8_qkv_cache_write)
