@@ -147,52 +147,75 @@ __device__ __forceinline__ float swap_max(float v) {
   return fmaxf(v, __shfl_xor(v, 32));
 }
 
-// What a wave loads for a tile of 32 keys: per half u of 16 keys, K pieces
-// (16 bytes of each 64 positions), V words of keys 4g .. 4g+3, scales.
+// Where a region's rows of a half tile (16 keys, all in one page) lie.
+struct Bases {
+  const uint8_t *k, *v;
+  const float *ks, *vs;
+};
+struct Half {
+  int page, place;  // place: of the first key, a multiple of 16
+};
+
+// What a wave holds of a tile of 32 keys, per half u of 16: K pieces (16
+// bytes of each 64 positions) of key r, V words of keys 4g .. 4g+3, and
+// those keys' scales.
 template <int DP>
-struct Raw {
-  u32x4 k[2][DP / 64];
-  uint32_t v[2][4][DP / 64];
-  v4f ks[2], vs[2];
+struct KeyRegs {
+  u32x4 c[2][DP / 64];
+  v4f s[2];
+};
+template <int DP>
+struct ValueRegs {
+  uint32_t c[2][4][DP / 64];
+  v4f s[2];
 };
 
 template <int DP, bool FULL>
-__device__ __forceinline__ void load_tile(const AttnArgs& a, int h, const int (&page)[2], const int (&place)[2],
-                                          Raw<DP>& raw) {
+__device__ __forceinline__ void load_keys(const AttnArgs& a, const Bases& at, const Half (&hf)[2], KeyRegs<DP>& k) {
   const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
-  constexpr int W = DP / 64;
+  const int D = FULL ? DP : a.D;
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
-    const int64_t row = ((int64_t)h << a.page_shift) + place[u];
-    const float* ksp = a.k_scales + page[u] * a.k_scale_page_stride + row;
-    const float* vsp = a.v_scales + page[u] * a.v_scale_page_stride + row;
-    const uint8_t* kp = a.k_codes + page[u] * a.k_page_stride + row * a.D;
-    const uint8_t* vp = a.v_codes + page[u] * a.v_page_stride + row * a.D;
+    const uint8_t* p = at.k + (hf[u].page * a.k_page_stride + hf[u].place * D);
 #pragma unroll
-    for (int c = 0; c < W; ++c) {
-      // pieces past D are read from the row's start and zeroed by widen_k
-      const int off = FULL || 64 * c + 16 * g < a.D ? 64 * c + 16 * g : 0;
-      raw.k[u][c] = *reinterpret_cast<const u32x4*>(kp + (uint32_t)(r * a.D + off));
+    for (int c = 0; c < DP / 64; ++c) {
+      // pieces past D are read from the row's start and zeroed before use
+      const int off = FULL || 64 * c + 16 * g < D ? 64 * c + 16 * g : 0;
+      k.c[u][c] = *reinterpret_cast<const u32x4*>(p + (uint32_t)(r * D + off));
     }
-    raw.ks[u] = *reinterpret_cast<const v4f*>(ksp + 4 * g);
-    raw.vs[u] = *reinterpret_cast<const v4f*>(vsp + 4 * g);
-    const int d0 = FULL || 4 * W * r < a.D ? 4 * W * r : 0;
+    const float* q = at.ks + (hf[u].page * a.k_scale_page_stride + hf[u].place);
+    k.s[u] = *reinterpret_cast<const v4f*>(q + 4 * g);
+  }
+}
+
+template <int DP, bool FULL>
+__device__ __forceinline__ void load_values(const AttnArgs& a, const Bases& at, const Half (&hf)[2],
+                                            ValueRegs<DP>& v) {
+  const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
+  const int D = FULL ? DP : a.D;
+  constexpr int W = DP / 64;
+  const int d0 = FULL || 4 * W * r < D ? 4 * W * r : 0;  // lanes past D: their positions are not put out
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const uint8_t* p = at.v + (hf[u].page * a.v_page_stride + hf[u].place * D);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t* p = reinterpret_cast<const uint32_t*>(vp + (uint32_t)((4 * g + i) * a.D + d0));
+      const uint32_t* x = reinterpret_cast<const uint32_t*>(p + (uint32_t)((4 * g + i) * D + d0));
       if (W == 4) {
-        const u32x4 x = *reinterpret_cast<const u32x4*>(p);
+        const u32x4 y = *reinterpret_cast<const u32x4*>(x);
 #pragma unroll
-        for (int w = 0; w < W; ++w) raw.v[u][i][w] = x[w];
+        for (int w = 0; w < W; ++w) v.c[u][i][w] = y[w];
       } else if (W == 2) {
-        const u32x2 x = *reinterpret_cast<const u32x2*>(p);
+        const u32x2 y = *reinterpret_cast<const u32x2*>(x);
 #pragma unroll
-        for (int w = 0; w < W; ++w) raw.v[u][i][w] = x[w];
+        for (int w = 0; w < W; ++w) v.c[u][i][w] = y[w];
       } else {
 #pragma unroll
-        for (int w = 0; w < W; ++w) raw.v[u][i][w] = p[w];
+        for (int w = 0; w < W; ++w) v.c[u][i][w] = x[w];
       }
     }
+    const float* q = at.vs + (hf[u].page * a.v_scale_page_stride + hf[u].place);
+    v.s[u] = *reinterpret_cast<const v4f*>(q + 4 * g);
   }
 }
 
@@ -205,45 +228,35 @@ struct State {
   v4f o[DP / 16];
 };
 
-template <int DP, bool FULL, int FMT, int TERMS, bool MASKED>
-__device__ __forceinline__ void use_tile(const AttnArgs& a, const bf16x8 (&qf)[DP / 32], Raw<DP>& raw, int first,
-                                         int lo, int n, State<DP>& st) {
-  const int lane = threadIdx.x & 63, g = lane >> 4;
-  constexpr int W = DP / 64;
+// s = K Q^T with scales, log2 domain.
+template <int DP, bool FULL, int FMT>
+__device__ __forceinline__ void scores(const AttnArgs& a, const bf16x8 (&qf)[DP / 32], const KeyRegs<DP>& k,
+                                       float (&s)[8]) {
+  const int g = (threadIdx.x & 63) >> 4;
   typedef uint32_t frag __attribute__((ext_vector_type(4)));
-  float s[8];
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int c = 0; c < W; ++c) {
-      u32x4 k = raw.k[u][c];
-      if (!FULL && 64 * c + 16 * g >= a.D) k = u32x4{0, 0, 0, 0};
+    for (int c = 0; c < DP / 64; ++c) {
+      u32x4 w = k.c[u][c];
+      if (!FULL && 64 * c + 16 * g >= a.D) w = u32x4{0, 0, 0, 0};
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        const frag kf = {widen2<FMT, false>(k[2 * x]), widen2<FMT, true>(k[2 * x]),
-                         widen2<FMT, false>(k[2 * x + 1]), widen2<FMT, true>(k[2 * x + 1])};
+        const frag kf = {widen2<FMT, false>(w[2 * x]), widen2<FMT, true>(w[2 * x]), widen2<FMT, false>(w[2 * x + 1]),
+                         widen2<FMT, true>(w[2 * x + 1])};
         acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, kf), qf[2 * c + x], acc, 0, 0, 0);
       }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s[4 * u + i] = acc[i] * (raw.ks[u][i] * a.scale_log2e);
+    for (int i = 0; i < 4; ++i) s[4 * u + i] = acc[i] * (k.s[u][i] * a.scale_log2e);
   }
-  if (MASKED) {
-#pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int j = first + 16 * u + 4 * g + i;
-        if (j < lo || j >= n) {
-          // nothing of a token that is not seen may reach a product
-          s[4 * u + i] = -__builtin_inff();
-          raw.vs[u][i] = 0.0f;
-#pragma unroll
-          for (int w = 0; w < W; ++w) raw.v[u][i][w] = 0u;
-        }
-      }
-  }
+}
+
+// The weights of a tile's scores, the running maximum and sum brought up to
+// date.
+template <int DP>
+__device__ __forceinline__ void weights(float (&s)[8], State<DP>& st) {
   float mx = s[0];
 #pragma unroll
   for (int i = 1; i < 8; ++i) mx = fmaxf(mx, s[i]);
@@ -259,14 +272,18 @@ __device__ __forceinline__ void use_tile(const AttnArgs& a, const bf16x8 (&qf)[D
 #pragma unroll
       for (int i = 0; i < 4; ++i) st.o[j][i] *= alpha;
   }
-  const float m = MASKED && st.m == -__builtin_inff() ? 0.0f : st.m;
-  float p[8];
+  const float m = st.m == -__builtin_inff() ? 0.0f : st.m;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    p[i] = __builtin_amdgcn_exp2f(s[i] - m);
-    st.l += p[i];
-    p[i] *= raw.vs[i >> 2][i & 3];
+    s[i] = __builtin_amdgcn_exp2f(s[i] - m);
+    st.l += s[i];
   }
+}
+
+// O += P V, p the weights times the V scales.
+template <int DP, int FMT, int TERMS>
+__device__ __forceinline__ void accumulate(float (&p)[8], const ValueRegs<DP>& v, State<DP>& st) {
+  typedef uint32_t frag __attribute__((ext_vector_type(4)));
   // p = sum of TERMS bf16 terms, each the rounded rest of those before
   bf16x8 pf[TERMS];
 #pragma unroll
@@ -277,14 +294,14 @@ __device__ __forceinline__ void use_tile(const AttnArgs& a, const bf16x8 (&qf)[D
       p[i] -= (float)pf[t][i];
     }
 #pragma unroll
-  for (int w = 0; w < W; ++w) {
+  for (int w = 0; w < DP / 64; ++w) {
     // keys (0, 1) and (2, 3) of each half paired byte by byte
     uint32_t pr[2][2][2];
 #pragma unroll
     for (int u = 0; u < 2; ++u)
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
-        const uint32_t k0 = raw.v[u][2 * y][w], k1 = raw.v[u][2 * y + 1][w];
+        const uint32_t k0 = v.c[u][2 * y][w], k1 = v.c[u][2 * y + 1][w];
         pr[u][y][0] = __builtin_amdgcn_perm(k1, k0, 0x05010400u);
         pr[u][y][1] = __builtin_amdgcn_perm(k1, k0, 0x07030602u);
       }
@@ -305,53 +322,73 @@ __device__ __forceinline__ void use_tile(const AttnArgs& a, const bf16x8 (&qf)[D
 }
 
 // A wave's tiles t, t + kWaves, ... below `end` (relative to the span's
-// first) of one region, two tiles of loads in flight.  The page of each half
-// tile is looked up 32 tiles ahead, one per lane.
+// first) of one region.  The next tile's keys are loaded as soon as this
+// one's are used, its values likewise: a tile is always in flight and needs
+// no second set of registers.  The page of each half tile is looked up 32
+// tiles ahead, one per lane.
 template <int DP, bool FULL, int FMT, int TERMS>
 __device__ __forceinline__ void run_tiles(const AttnArgs& a, const Span& sp, int b, int h,
                                           const bf16x8 (&qf)[DP / 32], int t, int end, State<DP>& st) {
-  const int lane = threadIdx.x & 63;
+  const int lane = threadIdx.x & 63, g = lane >> 4;
   const int32_t* row = a.table + b * a.ld_table;
+  const int64_t head_row = (int64_t)h << a.page_shift;
+  const Bases at = {a.k_codes + head_row * a.D, a.v_codes + head_row * a.D, a.k_scales + head_row,
+                    a.v_scales + head_row};
   const int last = (sp.n - 1) >> 4;  // the last 16 tokens that hold one
-  int ids = 0, ahead = 0;            // ids: pages of the tiles from `ahead` on
-  const int first_t = t;
-  ahead = first_t - 32 * kWaves;     // nothing looked up yet
+  int ids = 0, ahead = t - 32 * kWaves;  // ids: pages of the 32 tiles from `ahead` on
 
-  auto fetch = [&](int tt, Raw<DP>& raw) {
+  Half hf[2];
+  auto locate = [&](int tt) {
     if (tt - ahead >= 32 * kWaves) {
       ahead = tt;
       const int grp = min(2 * (sp.tile0 + tt + (lane >> 1) * kWaves) + (lane & 1), last);
       ids = row[(grp << 4) >> a.page_shift];
       ids = ids < 0 ? 0 : (ids >= a.pages ? a.pages - 1 : ids);
     }
-    int page[2], place[2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const int at = 2 * ((tt - ahead) / kWaves) + u;
-      page[u] = __builtin_amdgcn_readlane(ids, at);
-      const int grp = min(2 * (sp.tile0 + tt) + u, last);
-      place[u] = (grp << 4) & ((1 << a.page_shift) - 1);
+      hf[u].page = __builtin_amdgcn_readlane(ids, 2 * ((tt - ahead) / kWaves) + u);
+      hf[u].place = (min(2 * (sp.tile0 + tt) + u, last) << 4) & ((1 << a.page_shift) - 1);
     }
-    load_tile<DP, FULL>(a, h, page, place, raw);
-  };
-  auto use = [&](int tt, Raw<DP>& raw) {
-    const int first = (sp.tile0 + tt) * kTile;
-    if (first >= sp.lo && first + kTile <= sp.n) use_tile<DP, FULL, FMT, TERMS, false>(a, qf, raw, first, sp.lo, sp.n, st);
-    else use_tile<DP, FULL, FMT, TERMS, true>(a, qf, raw, first, sp.lo, sp.n, st);
   };
 
-  Raw<DP> x, y;
   if (t >= end) return;
-  fetch(t, x);
+  KeyRegs<DP> k;
+  ValueRegs<DP> v;
+  locate(t);
+  load_keys<DP, FULL>(a, at, hf, k);
+  load_values<DP, FULL>(a, at, hf, v);
   for (;;) {
-    const int t1 = t + kWaves;
-    if (t1 < end) fetch(t1, y);
-    use(t, x);
-    if (t1 >= end) break;
-    t = t1 + kWaves;
-    if (t < end) fetch(t, x);
-    use(t1, y);
-    if (t >= end) break;
+    const int next = t + kWaves;
+    float s[8];
+    scores<DP, FULL, FMT>(a, qf, k, s);
+    if (next < end) {
+      locate(next);
+      load_keys<DP, FULL>(a, at, hf, k);
+    }
+    const int first = (sp.tile0 + t) * kTile;
+    if (first < sp.lo || first + kTile > sp.n) {
+      // nothing of a token that is not seen may reach a product
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int j = first + 16 * u + 4 * g + i;
+          if (j < sp.lo || j >= sp.n) {
+            s[4 * u + i] = -__builtin_inff();
+            v.s[u][i] = 0.0f;
+#pragma unroll
+            for (int w = 0; w < DP / 64; ++w) v.c[u][i][w] = 0u;
+          }
+        }
+    }
+    weights<DP>(s, st);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s[i] *= v.s[i >> 2][i & 3];
+    accumulate<DP, FMT, TERMS>(s, v, st);
+    if (next >= end) return;
+    load_values<DP, FULL>(a, at, hf, v);
+    t = next;
   }
 }
 
