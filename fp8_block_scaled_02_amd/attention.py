@@ -24,8 +24,8 @@ _attn_lib = None
 
 class _CacheStruct(ctypes.Structure):    # fp8b_kv_cache of include/fp8attn.h
     _fields_ = ([(n, ctypes.c_void_p) for n in ("k_codes", "v_codes", "k_scales", "v_scales")] +
-                [(n, ctypes.c_int64) for n in ("k_page_stride", "v_page_stride", "k_scale_page_stride",
-                                               "v_scale_page_stride", "pages", "page_size", "heads", "head_dim")] +
+                [(n, ctypes.c_int64) for n in ("page_stride", "scale_page_stride", "pages", "page_size", "heads",
+                                               "head_dim")] +
                 [("fmt", ctypes.c_int32), ("reserved", ctypes.c_int32)])
 
 
@@ -110,8 +110,8 @@ class KVCache:
 
     KVCache(pages, page_size, heads, head_dim) allocates one (its contents
     are arbitrary until written; what is not read through a length has no
-    effect); from_tensors() takes tensors the caller keeps, whose first
-    dimension may have any stride that fits (one layer of a larger
+    effect); from_tensors() takes tensors the caller keeps, whose pages may
+    lie any distance apart, the same for K and V (one layer of a larger
     allocation, K and V side by side)."""
 
     def __init__(self, pages, page_size, heads, head_dim, fmt="e5m2", device="cuda"):
@@ -142,12 +142,13 @@ class KVCache:
             _need(t[0].is_contiguous(), f"{name}: a page must be contiguous")
             _need(P == 1 or t.stride(0) >= t[0].numel(), f"{name}: pages overlap")
             strides.append(t.stride(0) if P > 1 else t[0].numel())
+        _need(strides[0] == strides[1] and strides[2] == strides[3], "K and V pages must lie equally far apart")
         _on(k_codes.device, v_codes=v_codes, k_scales=k_scales, v_scales=v_scales)
         self.k_codes, self.v_codes, self.k_scales, self.v_scales = k_codes, v_codes, k_scales, v_scales
         self.pages, self.heads, self.page_size, self.head_dim, self.fmt = P, H, S, D, fmt
         self.device = k_codes.device
         self._struct = _CacheStruct(k_codes.data_ptr(), v_codes.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
-                                    *strides, P, S, H, D, _CACHE_FMT[fmt], 0)
+                                    strides[0], strides[2], P, S, H, D, _CACHE_FMT[fmt], 0)
         self._ref = ctypes.addressof(self._struct)
 
 

@@ -12,6 +12,7 @@ inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintp
 inline hipStream_t as_stream(void* s) { return static_cast<hipStream_t>(s); }
 constexpr int64_t kMaxDim = (int64_t)1 << 30;
 constexpr int64_t kMaxStride = (int64_t)1 << 40;  // keeps every 64-bit offset in range
+constexpr int64_t kMaxPage = ((int64_t)1 << 32) - 1;  // page strides: 32-bit factors of the kernels' offsets
 constexpr int64_t kMaxTokens = ((int64_t)1 << 24) - 1;  // a launch holds below 2^32 threads of 256 a workgroup
 constexpr int64_t kMaxHeads = 65536;
 
@@ -25,15 +26,9 @@ int cache_sizes(const fp8b_kv_cache* c) {
     return FP8B_EINVAL;
   if (c->page_size < 16 || c->page_size > 4096 || (c->page_size & (c->page_size - 1)) != 0) return FP8B_EINVAL;
   const int64_t rows = c->heads * c->page_size;
-  if (c->k_page_stride < rows * c->head_dim || c->v_page_stride < rows * c->head_dim ||
-      c->k_scale_page_stride < rows || c->v_scale_page_stride < rows)
-    return FP8B_EINVAL;
-  if (c->k_page_stride > kMaxStride / 512 || c->v_page_stride > kMaxStride / 512 ||
-      c->k_scale_page_stride > kMaxStride / 512 || c->v_scale_page_stride > kMaxStride / 512)
-    return FP8B_EINVAL;
-  if (c->k_page_stride % 16 != 0 || c->v_page_stride % 16 != 0 || c->k_scale_page_stride % 4 != 0 ||
-      c->v_scale_page_stride % 4 != 0)
-    return FP8B_EALIGN;
+  if (c->page_stride < rows * c->head_dim || c->scale_page_stride < rows) return FP8B_EINVAL;
+  if (c->page_stride > kMaxPage || c->scale_page_stride > kMaxPage) return FP8B_EINVAL;
+  if (c->page_stride % 16 != 0 || c->scale_page_stride % 4 != 0) return FP8B_EALIGN;
   return FP8B_OK;
 }
 

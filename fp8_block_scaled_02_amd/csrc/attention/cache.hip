@@ -24,7 +24,7 @@ struct QkvArgs {
   const int64_t* slots;
   uint8_t *k_codes, *v_codes;
   float *k_scales, *v_scales;
-  int64_t k_page_stride, v_page_stride, k_scale_page_stride, v_scale_page_stride, total_slots;
+  int64_t page_stride, scale_page_stride, total_slots;
   int page_shift, cache_heads;
   int slot_shift;  // log2 of the row slots of a workgroup that one token takes
 };
@@ -195,8 +195,8 @@ __global__ __launch_bounds__(256) void qkv_kernel(const QkvArgs a) {
       codes[0] = FMT == 1 ? pack4_e5m2(v[0], v[1], v[2], v[3]) : pack4_e4m3(v[0], v[1], v[2], v[3]);
       codes[1] = FMT == 1 ? pack4_e5m2(v[4], v[5], v[6], v[7]) : pack4_e4m3(v[4], v[5], v[6], v[7]);
       const int64_t in_page = ((int64_t)h << a.page_shift) + place;
-      uint8_t* cp = (kind == 1 ? a.k_codes + page * a.k_page_stride : a.v_codes + page * a.v_page_stride);
-      float* sp = (kind == 1 ? a.k_scales + page * a.k_scale_page_stride : a.v_scales + page * a.v_scale_page_stride);
+      uint8_t* cp = (kind == 1 ? a.k_codes : a.v_codes) + page * a.page_stride;
+      float* sp = (kind == 1 ? a.k_scales : a.v_scales) + page * a.scale_page_stride;
       if (on) *reinterpret_cast<u32x2*>(cp + in_page * a.D + e0) = codes;
       if (lane == 0) sp[in_page] = d;
     }
@@ -234,10 +234,8 @@ int launch_qkv(const Rows& q, const Rows& k, const Rows& v, int64_t T, int D, co
     a.v_codes = cache->v_codes;
     a.k_scales = cache->k_scales;
     a.v_scales = cache->v_scales;
-    a.k_page_stride = cache->k_page_stride;
-    a.v_page_stride = cache->v_page_stride;
-    a.k_scale_page_stride = cache->k_scale_page_stride;
-    a.v_scale_page_stride = cache->v_scale_page_stride;
+    a.page_stride = cache->page_stride;
+    a.scale_page_stride = cache->scale_page_stride;
     a.total_slots = cache->pages * cache->page_size;
     a.page_shift = __builtin_ctzll((unsigned long long)cache->page_size);
   }
@@ -280,7 +278,7 @@ int launch_qkv(const Rows& q, const Rows& k, const Rows& v, int64_t T, int D, co
 struct ReadArgs {
   const uint8_t *k_codes, *v_codes;
   const float *k_scales, *v_scales;
-  int64_t k_page_stride, v_page_stride, k_scale_page_stride, v_scale_page_stride, pages;
+  int64_t page_stride, scale_page_stride, pages;
   int page_shift, heads, D;
   const int32_t* table;
   int64_t ld_table, cols;
@@ -328,8 +326,6 @@ __global__ __launch_bounds__(256) void cache_read_kernel(const ReadArgs a) {
   const uint8_t* codes = is_v ? a.v_codes : a.k_codes;
   const float* scales = is_v ? a.v_scales : a.k_scales;
   uint16_t* out = is_v ? a.v_out : a.k_out;
-  const int64_t cps = is_v ? a.v_page_stride : a.k_page_stride;
-  const int64_t sps = is_v ? a.v_scale_page_stride : a.k_scale_page_stride;
   const int per_head = a.D / 16;
   const int pieces = a.heads * per_head;
   const int share = 1 << a.slot_shift;
@@ -344,8 +340,8 @@ __global__ __launch_bounds__(256) void cache_read_kernel(const ReadArgs a) {
       const int c = p - h * per_head;
       const int64_t in_page = ((int64_t)h << a.page_shift) + place;
       const u32x4 raw =
-          __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(codes + page * cps + in_page * a.D + 16 * c));
-      const float d = scales[page * sps + in_page];
+          __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(codes + page * a.page_stride + in_page * a.D + 16 * c));
+      const float d = scales[page * a.scale_page_stride + in_page];
       u32x4 o[2];
       typedef float f2 __attribute__((ext_vector_type(2)));
 #pragma unroll
@@ -377,10 +373,8 @@ int launch_cache_read(const fp8b_kv_cache& c, const int32_t* table, int64_t ld_t
   a.v_codes = c.v_codes;
   a.k_scales = c.k_scales;
   a.v_scales = c.v_scales;
-  a.k_page_stride = c.k_page_stride;
-  a.v_page_stride = c.v_page_stride;
-  a.k_scale_page_stride = c.k_scale_page_stride;
-  a.v_scale_page_stride = c.v_scale_page_stride;
+  a.page_stride = c.page_stride;
+  a.scale_page_stride = c.scale_page_stride;
   a.pages = c.pages;
   a.page_shift = __builtin_ctzll((unsigned long long)c.page_size);
   a.heads = (int)c.heads;

@@ -26,6 +26,8 @@
 // The weights (times the V scale) are split into 2 bf16 terms for bf16
 // output and 3 for fp32 output: one term alone would be as coarse as the
 // output's own rounding; the further MFMAs are hidden behind the loads.
+#include <type_traits>
+
 #include "../common.hpp"
 #include "attn_launch.hpp"
 
@@ -34,8 +36,10 @@ namespace fp8attn {
 using namespace fp8blk;
 
 constexpr int kTile = 32;       // keys a wave takes at a time
-constexpr int kWaves = 4;       // waves of a workgroup
-constexpr int kMaxWgs = 1024;   // workgroups of a split launch: 4 for each of the 256 CUs
+constexpr int kSplitShift = 2;  // log2 of the waves of a workgroup of a split launch
+constexpr int kMaxWaves = 8;    // and of any
+constexpr int kDirectTiles = 128;
+constexpr int kMaxWgs = 512;    // workgroups of a split launch: 2 for each of the 256 CUs
 constexpr int kMinTiles = 8;    // tiles (all waves together) a workgroup of a split launch takes at least
 
 struct AttnArgs {
@@ -43,19 +47,20 @@ struct AttnArgs {
   int64_t q_b, q_h;
   const uint8_t *k_codes, *v_codes;
   const float *k_scales, *v_scales;
-  int64_t k_page_stride, v_page_stride, k_scale_page_stride, v_scale_page_stride;
+  uint32_t page_stride, scale_page_stride;
   int pages, page_shift, heads, D;
   int G, qtiles;  // query heads per KV head, and how many 16-row tiles they take
   const int32_t* table;
   int64_t ld_table;
   const int32_t* lens;
-  int B, Hq, max_len, window;
+  int cols, B, Hq, max_len, window;
   float scale_log2e;
   void* out;
   int out_f32;
   float* lse;
   float* ws;
   int split;
+  int waves_shift;  // log2 of the waves of a workgroup
 };
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
@@ -66,9 +71,8 @@ __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirs
 struct Span {
   int lo, n, tile0, tiles;
 };
-__device__ __forceinline__ Span span_of(const AttnArgs& a, int b) {
+__device__ __forceinline__ Span span_of(const AttnArgs& a, int len) {
   Span s;
-  const int len = a.lens[b];
   s.n = len < 0 ? 0 : (len < a.max_len ? len : a.max_len);
   s.lo = a.window > 0 && s.n > a.window ? s.n - a.window : 0;
   s.tile0 = s.lo / kTile;
@@ -77,59 +81,63 @@ __device__ __forceinline__ Span span_of(const AttnArgs& a, int b) {
   return s;
 }
 
-__device__ __forceinline__ int wave_sum(int v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
+// Inclusive sum over the wave's lanes: shifts by 1, 2, 4, 8 inside the rows of
+// 16, then each row's last value to the rows behind it.
+__device__ __forceinline__ int scan_add(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);
   return v;
 }
 
 // The work of a launch is the line of all tiles: sequences in order, each
 // one's regions (KV head, query tile) in order, each region's tiles in order.
-// Total tiles, or (find) the sequence that holds tile t and where it begins.
-__device__ __forceinline__ int total_tiles(const AttnArgs& a) {
+// Every workgroup takes a piece of the line, `per` tiles of it, so the work is
+// even whatever the lengths, and the host need not know them.
+struct Line {
+  int total, per;
+  int seq, begin;  // the sequence asked for and where it begins on the line
+  Span span;       // and its tokens
+};
+
+// BY_TILE: the sequence that holds the first tile of piece x (seq = B if the
+// piece lies past the end); otherwise sequence x.
+template <bool BY_TILE>
+__device__ __forceinline__ Line line_of(const AttnArgs& a, int wgs, int x) {
   const int lane = threadIdx.x & 63, R = a.heads * a.qtiles;
-  int sum = 0;
-  for (int b0 = 0; b0 < a.B; b0 += 64) {
-    const int b = b0 + lane;
-    sum += b < a.B ? span_of(a, b).tiles * R : 0;
+  Line ln;
+  ln.seq = a.B;
+  ln.begin = 0;
+  if (a.B > 64) {
+    int sum = 0;
+    for (int b = lane; b < a.B; b += 64) sum += span_of(a, a.lens[b]).tiles;
+    ln.total = __builtin_amdgcn_readlane(scan_add(sum * R), 63);
   }
-  return uniform(wave_sum(sum));
-}
-__device__ __forceinline__ void find_tile(const AttnArgs& a, int t, int& seq, int& begin) {
-  const int lane = threadIdx.x & 63, R = a.heads * a.qtiles;
-  int base = 0;
+  int base = 0, at = 0;
   for (int b0 = 0; b0 < a.B; b0 += 64) {
-    const int b = b0 + lane;
-    const int v = b < a.B ? span_of(a, b).tiles * R : 0;
-    int incl = v;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int u = __shfl_up(incl, o);
-      incl += lane >= o ? u : 0;
-    }
+    const int len = b0 + lane < a.B ? a.lens[b0 + lane] : 0;
+    const int v = b0 + lane < a.B ? span_of(a, len).tiles * R : 0;
+    const int incl = scan_add(v);
     const int all = __builtin_amdgcn_readlane(incl, 63);
-    if (t < base + all) {
-      const unsigned long long past = __ballot(base + incl <= t);  // sequences that end at or before t
-      const int k = __popcll(past);
-      seq = uniform(b0 + k);
-      begin = base + __builtin_amdgcn_readlane(incl - v, uniform(k));
-      return;
+    if (b0 == 0) {
+      if (a.B <= 64) ln.total = all;
+      const int per = (ln.total + wgs - 1) / wgs;
+      ln.per = per > kMinTiles ? per : kMinTiles;
+      at = BY_TILE ? x * ln.per : 0;
+    }
+    const int k = BY_TILE ? (int)__popcll(__ballot(base + incl <= at)) : x - b0;
+    if (BY_TILE ? at < base + all : k < 64) {
+      ln.seq = uniform(b0 + k);
+      ln.begin = base + __builtin_amdgcn_readlane(incl - v, uniform(k));
+      ln.span = span_of(a, __builtin_amdgcn_readlane(len, uniform(k)));
+      break;
     }
     base += all;
   }
-  seq = a.B;
-  begin = base;
-}
-// Where sequence b begins on the line.
-__device__ __forceinline__ int begin_of(const AttnArgs& a, int b) {
-  const int lane = threadIdx.x & 63, R = a.heads * a.qtiles;
-  int sum = 0;
-  for (int b0 = 0; b0 < b; b0 += 64) sum += b0 + lane < b ? span_of(a, b0 + lane).tiles * R : 0;
-  return uniform(wave_sum(sum));
-}
-__device__ __forceinline__ int tiles_per_wg(int total, int wgs) {
-  const int per = (total + wgs - 1) / wgs;
-  return per > kMinTiles ? per : kMinTiles;
+  return ln;
 }
 
 // Floats of a partial result: G rows of D, then G maxima, then G sums.
@@ -142,18 +150,29 @@ __device__ __forceinline__ uint32_t widen2(uint32_t w) {
   return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)w, 1.0f, HI));
 }
 
-__device__ __forceinline__ float swap_max(float v) {
-  v = fmaxf(v, __shfl_xor(v, 16));
-  return fmaxf(v, __shfl_xor(v, 32));
+__device__ __forceinline__ uint64_t lane_value(uint64_t v, int lane) {
+  return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), lane) << 32 |
+         (uint32_t)__builtin_amdgcn_readlane((int)v, lane);
 }
 
-// Where a region's rows of a half tile (16 keys, all in one page) lie.
+// Over the four lanes that share lane % 16: each swap leaves one row of the
+// pair in the first result and the other in the second.
+__device__ __forceinline__ float swap_max(float v) {
+  typedef unsigned int u2 __attribute__((ext_vector_type(2)));
+  const u2 x = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
+  const u2 y = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(y[0]), __uint_as_float(y[1]));
+}
+
+// A head's rows in page 0, and how far from there a half tile's (16 keys, all
+// in one page) lie.
 struct Bases {
   const uint8_t *k, *v;
   const float *ks, *vs;
 };
 struct Half {
-  int page, place;  // place: of the first key, a multiple of 16
+  uint64_t codes, scales;  // bytes and floats from those
 };
 
 // What a wave holds of a tile of 32 keys, per half u of 16: K pieces (16
@@ -176,14 +195,14 @@ __device__ __forceinline__ void load_keys(const AttnArgs& a, const Bases& at, co
   const int D = FULL ? DP : a.D;
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
-    const uint8_t* p = at.k + (hf[u].page * a.k_page_stride + hf[u].place * D);
+    const uint8_t* p = at.k + hf[u].codes;
 #pragma unroll
     for (int c = 0; c < DP / 64; ++c) {
       // pieces past D are read from the row's start and zeroed before use
       const int off = FULL || 64 * c + 16 * g < D ? 64 * c + 16 * g : 0;
       k.c[u][c] = *reinterpret_cast<const u32x4*>(p + (uint32_t)(r * D + off));
     }
-    const float* q = at.ks + (hf[u].page * a.k_scale_page_stride + hf[u].place);
+    const float* q = at.ks + hf[u].scales;
     k.s[u] = *reinterpret_cast<const v4f*>(q + 4 * g);
   }
 }
@@ -197,10 +216,10 @@ __device__ __forceinline__ void load_values(const AttnArgs& a, const Bases& at, 
   const int d0 = FULL || 4 * W * r < D ? 4 * W * r : 0;  // lanes past D: their positions are not put out
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
-    const uint8_t* p = at.v + (hf[u].page * a.v_page_stride + hf[u].place * D);
+    const uint8_t* p = at.v + hf[u].codes;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t* x = reinterpret_cast<const uint32_t*>(p + (uint32_t)((4 * g + i) * D + d0));
+      const uint8_t* x = p + (uint32_t)((4 * g + i) * D + d0);
       if (W == 4) {
         const u32x4 y = *reinterpret_cast<const u32x4*>(x);
 #pragma unroll
@@ -210,11 +229,10 @@ __device__ __forceinline__ void load_values(const AttnArgs& a, const Bases& at, 
 #pragma unroll
         for (int w = 0; w < W; ++w) v.c[u][i][w] = y[w];
       } else {
-#pragma unroll
-        for (int w = 0; w < W; ++w) v.c[u][i][w] = x[w];
+        v.c[u][i][0] = *reinterpret_cast<const uint32_t*>(x);
       }
     }
-    const float* q = at.vs + (hf[u].page * a.v_scale_page_stride + hf[u].place);
+    const float* q = at.vs + hf[u].scales;
     v.s[u] = *reinterpret_cast<const v4f*>(q + 4 * g);
   }
 }
@@ -285,13 +303,15 @@ template <int DP, int FMT, int TERMS>
 __device__ __forceinline__ void accumulate(float (&p)[8], const ValueRegs<DP>& v, State<DP>& st) {
   typedef uint32_t frag __attribute__((ext_vector_type(4)));
   // p = sum of TERMS bf16 terms, each the rounded rest of those before
-  bf16x8 pf[TERMS];
+  frag pf[TERMS];
 #pragma unroll
   for (int t = 0; t < TERMS; ++t)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      pf[t][i] = (__bf16)p[i];
-      p[i] -= (float)pf[t][i];
+    for (int i = 0; i < 4; ++i) {
+      const bf16x2 b = {(__bf16)p[2 * i], (__bf16)p[2 * i + 1]};
+      pf[t][i] = __builtin_bit_cast(uint32_t, b);
+      p[2 * i] -= __uint_as_float(pf[t][i] << 16);
+      p[2 * i + 1] -= __uint_as_float(pf[t][i] & 0xffff0000u);
     }
 #pragma unroll
   for (int w = 0; w < DP / 64; ++w) {
@@ -316,57 +336,64 @@ __device__ __forceinline__ void accumulate(float (&p)[8], const ValueRegs<DP>& v
       const int j = 4 * w + b;
 #pragma unroll
       for (int t = 0; t < TERMS; ++t)
-        st.o[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, vf), pf[t], st.o[j], 0, 0, 0);
+        st.o[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, vf),
+                                                         __builtin_bit_cast(bf16x8, pf[t]), st.o[j], 0, 0, 0);
     }
   }
 }
 
-// A wave's tiles t, t + kWaves, ... below `end` (relative to the span's
-// first) of one region.  The next tile's keys are loaded as soon as this
-// one's are used, its values likewise: a tile is always in flight and needs
-// no second set of registers.  The page of each half tile is looked up 32
-// tiles ahead, one per lane.
+// A wave's tiles t, t + waves, ... below `end` (relative to the span's first)
+// of one region.  The next tile's keys are loaded as soon as this one's are
+// used, its values likewise, so a tile is always in flight (two of them, for
+// 60 more registers, measured no faster).
+// The page of each half tile is looked up 32 tiles ahead, one per lane.  Past
+// the last token a half may lie anywhere in the cache (ids are clamped): what
+// is read there is masked.
 template <int DP, bool FULL, int FMT, int TERMS>
 __device__ __forceinline__ void run_tiles(const AttnArgs& a, const Span& sp, int b, int h,
                                           const bf16x8 (&qf)[DP / 32], int t, int end, State<DP>& st) {
   const int lane = threadIdx.x & 63, g = lane >> 4;
+  const int ws = a.waves_shift;
   const int32_t* row = a.table + b * a.ld_table;
   const int64_t head_row = (int64_t)h << a.page_shift;
   const Bases at = {a.k_codes + head_row * a.D, a.v_codes + head_row * a.D, a.k_scales + head_row,
                     a.v_scales + head_row};
-  const int last = (sp.n - 1) >> 4;  // the last 16 tokens that hold one
-  int ids = 0, ahead = t - 32 * kWaves;  // ids: pages of the 32 tiles from `ahead` on
+  const int tile0 = a.window > 0 ? sp.tile0 : 0;
+  int ahead = t - (32 << ws);  // the lanes hold where the halves of the 32 tiles from here on lie
+  uint64_t codes = 0, scales = 0;
 
   Half hf[2];
   auto locate = [&](int tt) {
-    if (tt - ahead >= 32 * kWaves) {
+    if (tt - ahead >= (32 << ws)) {
       ahead = tt;
-      const int grp = min(2 * (sp.tile0 + tt + (lane >> 1) * kWaves) + (lane & 1), last);
-      ids = row[(grp << 4) >> a.page_shift];
-      ids = ids < 0 ? 0 : (ids >= a.pages ? a.pages - 1 : ids);
+      const uint32_t key = 32 * (uint32_t)(tile0 + tt + ((lane >> 1) << ws)) + 16 * (lane & 1);
+      int id = row[min((int)(key >> a.page_shift), a.cols - 1)];
+      id = id < 0 ? 0 : (id >= a.pages ? a.pages - 1 : id);
+      const uint32_t place = key & ((1u << a.page_shift) - 1);
+      codes = (uint64_t)(uint32_t)id * a.page_stride + place * (uint32_t)a.D;
+      scales = (uint64_t)(uint32_t)id * a.scale_page_stride + place;
     }
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      hf[u].page = __builtin_amdgcn_readlane(ids, 2 * ((tt - ahead) / kWaves) + u);
-      hf[u].place = (min(2 * (sp.tile0 + tt) + u, last) << 4) & ((1 << a.page_shift) - 1);
+      const int at = 2 * ((tt - ahead) >> ws) + u;
+      hf[u].codes = lane_value(codes, at);
+      hf[u].scales = lane_value(scales, at);
     }
   };
 
-  if (t >= end) return;
   KeyRegs<DP> k;
   ValueRegs<DP> v;
-  locate(t);
-  load_keys<DP, FULL>(a, at, hf, k);
-  load_values<DP, FULL>(a, at, hf, v);
-  for (;;) {
-    const int next = t + kWaves;
+  // MORE: the next tile's loads go out as this one's registers come free.  A
+  // branch around them would make every wait inside the turn wait for all.
+  auto turn = [&](auto more) {
+    constexpr bool MORE = decltype(more)::value;
     float s[8];
     scores<DP, FULL, FMT>(a, qf, k, s);
-    if (next < end) {
-      locate(next);
+    if (MORE) {
+      locate(t + (1 << ws));
       load_keys<DP, FULL>(a, at, hf, k);
     }
-    const int first = (sp.tile0 + t) * kTile;
+    const int first = (tile0 + t) * kTile;
     if (first < sp.lo || first + kTile > sp.n) {
       // nothing of a token that is not seen may reach a product
 #pragma unroll
@@ -374,65 +401,67 @@ __device__ __forceinline__ void run_tiles(const AttnArgs& a, const Span& sp, int
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int j = first + 16 * u + 4 * g + i;
-          if (j < sp.lo || j >= sp.n) {
-            s[4 * u + i] = -__builtin_inff();
-            v.s[u][i] = 0.0f;
+          const bool seen = j >= sp.lo && j < sp.n;
+          s[4 * u + i] = seen ? s[4 * u + i] : -__builtin_inff();
+          v.s[u][i] = seen ? v.s[u][i] : 0.0f;
 #pragma unroll
-            for (int w = 0; w < DP / 64; ++w) v.c[u][i][w] = 0u;
-          }
+          for (int w = 0; w < DP / 64; ++w) v.c[u][i][w] = seen ? v.c[u][i][w] : 0u;
         }
     }
     weights<DP>(s, st);
 #pragma unroll
     for (int i = 0; i < 8; ++i) s[i] *= v.s[i >> 2][i & 3];
     accumulate<DP, FMT, TERMS>(s, v, st);
-    if (next >= end) return;
-    load_values<DP, FULL>(a, at, hf, v);
-    t = next;
-  }
+    if (MORE) load_values<DP, FULL>(a, at, hf, v);
+  };
+
+  if (t >= end) return;
+  locate(t);
+  load_keys<DP, FULL>(a, at, hf, k);
+  load_values<DP, FULL>(a, at, hf, v);
+  for (; t + (1 << ws) < end; t += 1 << ws) turn(std::true_type{});
+  turn(std::false_type{});
 }
 
 // One workgroup takes a piece of the line (split) or one region (not split).
-// In a piece, each region's tiles are dealt to the four waves, whose results
+// In a piece, each region's tiles are dealt to the waves, whose results
 // are joined in LDS; a region that lies whole in the piece is put out, others
 // go to the workspace: slot 2w for the region the piece begins in, slot 2w+1
 // for the one it ends in.
 template <int DP, bool FULL, int FMT, int TERMS>
-__global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_kernel(const AttnArgs a) {
+__global__ __launch_bounds__(64 * kMaxWaves) void attend_kernel(const AttnArgs a) {
   extern __shared__ float lds[];
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   const int g = lane >> 4, c = lane & 15;
   const int R = a.heads * a.qtiles;
   const int rows_max = a.G < 16 ? a.G : 16;
   constexpr int LD = DP + 4;
-  float* lds_m = lds + (int64_t)kWaves * rows_max * LD;  // [wave][16]
-  float* lds_l = lds_m + kWaves * 16;
+  const int waves = 1 << a.waves_shift;
+  float* lds_m = lds + waves * rows_max * LD;  // [wave][16]
+  float* lds_l = lds_m + waves * 16;
 
   int b, region, tile, left;  // left: tiles of this piece still to do
-  int piece0 = 0;             // where the piece begins on the line
-  int seq_begin = 0;
+  Span sp;
   if (a.split) {
-    const int total = total_tiles(a);
-    const int per = tiles_per_wg(total, gridDim.x);
-    piece0 = (int)min((int64_t)blockIdx.x * per, (int64_t)total);
-    left = min(per, total - piece0);
-    if (left <= 0) return;
-    find_tile(a, piece0, b, seq_begin);
+    const Line ln = line_of<true>(a, gridDim.x, blockIdx.x);
+    b = ln.seq;
+    if (b == a.B) return;
+    const int at = blockIdx.x * ln.per - ln.begin;
+    left = min(ln.per, ln.total - (int)blockIdx.x * ln.per);
+    sp = ln.span;
+    region = at / sp.tiles;
+    tile = at - region * sp.tiles;
   } else {
     b = blockIdx.x / R;
-    region = blockIdx.x % R;
+    region = blockIdx.x - b * R;
     tile = 0;
     left = 0x7fffffff;
-  }
-  Span sp = span_of(a, b);
-  if (a.split) {
-    region = (piece0 - seq_begin) / sp.tiles;
-    tile = (piece0 - seq_begin) % sp.tiles;
+    sp = span_of(a, a.lens[b]);
   }
 
   for (;;) {
     const int count = min(sp.tiles - tile, left);
-    const int h = uniform(region / a.qtiles), qt = uniform(region % a.qtiles);
+    const int h = a.qtiles == 1 ? region : region / a.qtiles, qt = region - h * a.qtiles;
     const int rows = min(16, a.G - 16 * qt);
     const int head0 = h * a.G + 16 * qt;
     State<DP> st;
@@ -455,7 +484,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_kernel(const At
     st.l += __shfl_xor(st.l, 16);
     st.l += __shfl_xor(st.l, 32);
     if (c < rows) {
-      float* o = lds + ((int64_t)wave * rows_max + c) * LD;
+      float* o = lds + (wave * rows_max + c) * LD;
 #pragma unroll
       for (int j = 0; j < DP / 16; j += 4)
 #pragma unroll
@@ -472,19 +501,17 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_kernel(const At
     float* part = nullptr;
     if (!whole) part = a.ws + (2 * (int64_t)blockIdx.x + (tile == 0 ? 1 : 0)) * partial_floats(rows_max, a.D);
     const int q4 = a.D / 4;
-    for (int x = tid; x < rows * q4; x += 256) {
+    for (int x = tid; x < rows * q4; x += 64 << a.waves_shift) {
       const int rr = x / q4, d = 4 * (x - rr * q4);
       float m = lds_m[rr];
-#pragma unroll
-      for (int w = 1; w < kWaves; ++w) m = fmaxf(m, lds_m[w * 16 + rr]);
+      for (int w = 1; w < waves; ++w) m = fmaxf(m, lds_m[w * 16 + rr]);
       const float ms = m == -__builtin_inff() ? 0.0f : m;
       float l = 0.0f;
       v4f o = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w) {
+      for (int w = 0; w < waves; ++w) {
         const float f = __builtin_amdgcn_exp2f(lds_m[w * 16 + rr] - ms);
         l = __builtin_fmaf(f, lds_l[w * 16 + rr], l);
-        const v4f ow = *reinterpret_cast<const v4f*>(lds + ((int64_t)w * rows_max + rr) * LD + d);
+        const v4f ow = *reinterpret_cast<const v4f*>(lds + (w * rows_max + rr) * LD + d);
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[i] = __builtin_fmaf(f, ow[i], o[i]);
       }
@@ -516,35 +543,36 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_kernel(const At
     if (++region == R) {
       region = 0;
       ++b;
-      sp = span_of(a, b);
+      sp = span_of(a, a.lens[b]);
     }
   }
 }
 
-// Joins the partial results of each region that several pieces share: one
-// workgroup per query head of a region (blockIdx.y the row).  Its threads are
-// D/4 columns by as many groups of pieces as fit.
-__global__ __launch_bounds__(256) void join_kernel(const AttnArgs a, int wgs) {
-  __shared__ float lds[256 * 4 + 256];
+// Joins the partial results of the regions that several pieces share.  A
+// workgroup takes `rows_wg` rows (query heads; blockIdx.y: which) of a region,
+// D/4 threads a row and as many groups of pieces as threads are left.
+__global__ __launch_bounds__(256) void join_kernel(const AttnArgs a, int wgs, int rows_wg) {
+  __shared__ float lds[256 * 4];
+  __shared__ float lds_ml[2][64];
   const int tid = threadIdx.x;
   const int R = a.heads * a.qtiles;
-  const int b = blockIdx.x / R, region = blockIdx.x % R;
-  const int h = region / a.qtiles, qt = region % a.qtiles;
-  const int rr = blockIdx.y;
-  if (rr >= min(16, a.G - 16 * qt)) return;
-  const int rows_max = a.G < 16 ? a.G : 16;
-  const int per = tiles_per_wg(total_tiles(a), wgs);
-  const Span sp = span_of(a, b);
-  const int t0 = begin_of(a, b) + region * sp.tiles, t1 = t0 + sp.tiles;
-  const int w0 = t0 / per, w1 = (t1 - 1) / per;
+  const int b = blockIdx.x / R, region = blockIdx.x - b * R;
+  const int h = a.qtiles == 1 ? region : region / a.qtiles, qt = region - h * a.qtiles;
+  const int rows = min(16, a.G - 16 * qt), rows_max = a.G < 16 ? a.G : 16;
+  const Line ln = line_of<false>(a, wgs, b);
+  const int t0 = ln.begin + region * ln.span.tiles, t1 = t0 + ln.span.tiles;
+  const int w0 = t0 / ln.per, w1 = (t1 - 1) / ln.per;
   if (w0 == w1) return;  // put out by the piece that held it whole
 
   const int64_t pf = partial_floats(rows_max, a.D);
-  const int q4 = a.D / 4, groups = 256 / q4;
-  const int grp = tid / q4, d = 4 * (tid - grp * q4);
+  const int q4 = a.D / 4, groups = 256 / (q4 * rows_wg);
+  const int d = 4 * (tid % q4), rr_wg = tid / q4 % rows_wg, grp = tid / q4 / rows_wg;
+  const int rr = blockIdx.y * rows_wg + rr_wg;
+  const bool on = grp < groups && rr < rows;
   float m = -__builtin_inff(), l = 0.0f;
   v4f o = {0.0f, 0.0f, 0.0f, 0.0f};
-  if (grp < groups) {
+  if (on) {
+#pragma unroll 4
     for (int w = w0 + grp; w <= w1; w += groups) {
       // the first of them ends its piece in the region, the others begin theirs
       const float* p = a.ws + (2 * (int64_t)w + (w == w0 ? 1 : 0)) * pf;
@@ -557,26 +585,31 @@ __global__ __launch_bounds__(256) void join_kernel(const AttnArgs a, int wgs) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[i] = o[i] * f0 + po[i] * f1;
     }
-    *reinterpret_cast<v4f*>(lds + 4 * tid) = o;
-    if (d == 0) {
-      lds[1024 + grp] = m;
-      lds[1024 + 128 + grp] = l;
+  }
+  if (groups > 1) {
+    if (on) {
+      *reinterpret_cast<v4f*>(lds + 4 * tid) = o;
+      if (d == 0) {
+        lds_ml[0][grp * rows_wg + rr_wg] = m;
+        lds_ml[1][grp * rows_wg + rr_wg] = l;
+      }
+    }
+    __syncthreads();
+    if (!on || grp != 0) return;
+    m = -__builtin_inff();
+    for (int k = 0; k < groups; ++k) m = fmaxf(m, lds_ml[0][k * rows_wg + rr_wg]);
+    const float ms = m == -__builtin_inff() ? 0.0f : m;
+    l = 0.0f;
+    o = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int k = 0; k < groups; ++k) {
+      const float f = __builtin_amdgcn_exp2f(lds_ml[0][k * rows_wg + rr_wg] - ms);
+      l += f * lds_ml[1][k * rows_wg + rr_wg];
+      const v4f ok = *reinterpret_cast<const v4f*>(lds + 4 * (k * rows_wg * q4 + tid));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] += f * ok[i];
     }
   }
-  __syncthreads();
-  if (grp != 0) return;
-  float mt = -__builtin_inff();
-  for (int k = 0; k < groups; ++k) mt = fmaxf(mt, lds[1024 + k]);
-  const float ms = mt == -__builtin_inff() ? 0.0f : mt;
-  l = 0.0f;
-  o = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-  for (int k = 0; k < groups; ++k) {
-    const float f = __builtin_amdgcn_exp2f(lds[1024 + k] - ms);
-    l += f * lds[1024 + 128 + k];
-    const v4f ok = *reinterpret_cast<const v4f*>(lds + 4 * (k * q4 + tid));
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] += f * ok[i];
-  }
+  if (!on) return;
   const int64_t at = (int64_t)b * a.Hq + h * a.G + 16 * qt + rr;
   const float inv = l > 0.0f ? 1.0f / l : 0.0f;
 #pragma unroll
@@ -588,7 +621,7 @@ __global__ __launch_bounds__(256) void join_kernel(const AttnArgs a, int wgs) {
     *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + at * a.D + d) =
         u32x2{__builtin_bit_cast(uint32_t, b0), __builtin_bit_cast(uint32_t, b1)};
   }
-  if (a.lse && d == 0) a.lse[at] = l > 0.0f ? (mt + __log2f(l)) * 0.69314718056f : -__builtin_inff();
+  if (a.lse && d == 0) a.lse[at] = l > 0.0f ? (m + __log2f(l)) * 0.69314718056f : -__builtin_inff();
 }
 
 // ---- host -------------------------------------------------------------------
@@ -596,6 +629,7 @@ __global__ __launch_bounds__(256) void join_kernel(const AttnArgs a, int wgs) {
 struct Shape {
   int G, qtiles, rows;
   int64_t regions, max_len, wgs;  // wgs: workgroups of a split launch; 0: one workgroup per region
+  int waves_shift;
 };
 
 static Shape shape_of(const fp8b_kv_cache& c, int64_t B, int64_t Hq, int64_t cols, int64_t max_context,
@@ -610,12 +644,18 @@ static Shape shape_of(const fp8b_kv_cache& c, int64_t B, int64_t Hq, int64_t col
   // the most tiles a region can have: a window reaches into one more
   const int64_t seen = window > 0 && window < s.max_len ? window + kTile - 1 : s.max_len;
   const int64_t tiles = (seen + kTile - 1) / kTile;
-  if (tiles <= kMinTiles) {
+  if (tiles <= kDirectTiles) {
     s.wgs = 0;
+    s.waves_shift = 3;
+    while (s.waves_shift > 0 && ((1 << s.waves_shift) > tiles ||
+                                 ((4 << s.waves_shift) > tiles && (s.regions << s.waves_shift) > 12 * 256)))
+      --s.waves_shift;
   } else {
+    s.waves_shift = kSplitShift;
     const int64_t want = (s.regions * tiles + kMinTiles - 1) / kMinTiles;
     s.wgs = want < kMaxWgs ? want : kMaxWgs;
   }
+  // TUNE
   return s;
 }
 
@@ -628,8 +668,9 @@ int64_t attention_workspace(const fp8b_kv_cache& c, int64_t B, int64_t Hq, int64
 template <int DP, bool FULL, int FMT, int TERMS>
 static int launch_one(const AttnArgs& a, unsigned grid, hipStream_t s) {
   const int rows = a.G < 16 ? a.G : 16;
-  const size_t lds = (size_t)(kWaves * rows * (DP + 4) + 2 * kWaves * 16) * sizeof(float);
-  hipLaunchKernelGGL((attend_kernel<DP, FULL, FMT, TERMS>), dim3(grid), dim3(256), lds, s, a);
+  const int waves = 1 << a.waves_shift;
+  const size_t lds = (size_t)(waves * rows * (DP + 4) + 2 * waves * 16) * sizeof(float);
+  hipLaunchKernelGGL((attend_kernel<DP, FULL, FMT, TERMS>), dim3(grid), dim3(64 * waves), lds, s, a);
   return check_launch();
 }
 template <int DP, bool FULL>
@@ -649,10 +690,8 @@ int launch_attention(const fp8b_kv_cache& c, const Attention& p, hipStream_t s) 
   a.v_codes = c.v_codes;
   a.k_scales = c.k_scales;
   a.v_scales = c.v_scales;
-  a.k_page_stride = c.k_page_stride;
-  a.v_page_stride = c.v_page_stride;
-  a.k_scale_page_stride = c.k_scale_page_stride;
-  a.v_scale_page_stride = c.v_scale_page_stride;
+  a.page_stride = (uint32_t)c.page_stride;
+  a.scale_page_stride = (uint32_t)c.scale_page_stride;
   a.pages = (int)c.pages;
   a.page_shift = __builtin_ctzll((unsigned long long)c.page_size);
   a.heads = (int)c.heads;
@@ -672,17 +711,23 @@ int launch_attention(const fp8b_kv_cache& c, const Attention& p, hipStream_t s) 
   a.lse = p.lse;
   a.ws = p.workspace;
   a.split = sh.wgs > 0;
+  a.waves_shift = sh.waves_shift;
+  a.cols = (int)p.cols;
   const unsigned grid = (unsigned)(sh.wgs > 0 ? sh.wgs : sh.regions);
   int rc;
   if (a.D == 64) rc = launch_dp<64, true>(a, c.fmt, grid, s);
   else if (a.D < 64) rc = launch_dp<64, false>(a, c.fmt, grid, s);
   else if (a.D == 128) rc = launch_dp<128, true>(a, c.fmt, grid, s);
   else if (a.D < 128) rc = launch_dp<128, false>(a, c.fmt, grid, s);
-  else if (a.D == 192) rc = launch_dp<192, true>(a, c.fmt, grid, s);
   else if (a.D == 256) rc = launch_dp<256, true>(a, c.fmt, grid, s);
   else rc = launch_dp<256, false>(a, c.fmt, grid, s);
   if (rc != FP8B_OK || !a.split) return rc;
-  hipLaunchKernelGGL(join_kernel, dim3((unsigned)sh.regions, (unsigned)sh.rows), dim3(256), 0, s, a, (int)grid);
+  // Few pieces to a region: its rows side by side in a workgroup.  Many: one
+  // row, the threads shared out over the pieces.
+  const int fit = 256 / (a.D / 4);
+  const int rows_wg = sh.wgs <= 4 * sh.regions ? (sh.rows < fit ? sh.rows : fit) : 1;
+  const dim3 jgrid((unsigned)sh.regions, (unsigned)((sh.rows + rows_wg - 1) / rows_wg));
+  hipLaunchKernelGGL(join_kernel, jgrid, dim3(256), 0, s, a, (int)grid, rows_wg);
   return check_launch();
 }
 

@@ -50,10 +50,9 @@ int fp8b_attn_abi_version(void);
  * page strides let layers, or K and V, share one allocation.
  *
  *   k_codes, v_codes    16-byte aligned; k_scales, v_scales: 16-byte aligned.
- *   k_page_stride, v_page_stride            bytes, >= heads * page_size *
- *                       head_dim, multiples of 16.
- *   k_scale_page_stride, v_scale_page_stride  floats, >= heads * page_size,
- *                       multiples of 4.
+ *   page_stride         bytes, >= heads * page_size * head_dim, a multiple
+ *                       of 16; the same for K and V.
+ *   scale_page_stride   floats, >= heads * page_size, a multiple of 4.
  *   pages      1 .. 2^31 - 1.
  *   page_size  tokens: 16, 32, 64, ... 4096 (a power of two).
  *   heads      1 .. 1024;  head_dim 16 .. 256, a multiple of 16.
@@ -62,8 +61,7 @@ int fp8b_attn_abi_version(void);
 typedef struct {
   uint8_t *k_codes, *v_codes;
   float *k_scales, *v_scales;
-  int64_t k_page_stride, v_page_stride;
-  int64_t k_scale_page_stride, v_scale_page_stride;
+  int64_t page_stride, scale_page_stride;
   int64_t pages, page_size, heads, head_dim;
   int32_t fmt, reserved;
 } fp8b_kv_cache;

@@ -57,20 +57,19 @@ def test_structs_match_the_header(M, tmp_path):
 
 
 def _cache(M, **over):
-    c = dict(k_codes=GOOD, v_codes=GOOD, k_scales=GOOD, v_scales=GOOD, k_page_stride=8 * 16 * 128,
-             v_page_stride=8 * 16 * 128, k_scale_page_stride=128, v_scale_page_stride=128, pages=10, page_size=16,
-             heads=8, head_dim=128, fmt=1, reserved=0)
+    c = dict(k_codes=GOOD, v_codes=GOOD, k_scales=GOOD, v_scales=GOOD, page_stride=8 * 16 * 128,
+             scale_page_stride=128, pages=10, page_size=16, heads=8, head_dim=128, fmt=1, reserved=0)
     c.update(over)
     return M._CacheStruct(**c)
 
 
 BAD_CACHES = [
     (dict(fmt=2), EUNSUPPORTED), (dict(pages=0), EINVAL), (dict(pages=1 << 31), EINVAL), (dict(page_size=8), EINVAL),
-    (dict(page_size=48), EINVAL), (dict(page_size=8192, k_page_stride=1 << 30, v_page_stride=1 << 30), EINVAL),
+    (dict(page_size=48), EINVAL), (dict(page_size=8192, page_stride=1 << 30, scale_page_stride=1 << 20), EINVAL),
     (dict(heads=0), EINVAL), (dict(heads=1025), EINVAL), (dict(head_dim=24), EINVAL), (dict(head_dim=272), EINVAL),
-    (dict(head_dim=0), EINVAL), (dict(k_page_stride=8 * 16 * 128 - 16), EINVAL),
-    (dict(v_page_stride=8 * 16 * 128 + 8), EALIGN), (dict(k_scale_page_stride=127), EINVAL),
-    (dict(v_scale_page_stride=130), EALIGN),
+    (dict(head_dim=0), EINVAL), (dict(page_stride=8 * 16 * 128 - 16), EINVAL),
+    (dict(page_stride=8 * 16 * 128 + 8), EALIGN), (dict(scale_page_stride=124), EINVAL),
+    (dict(scale_page_stride=130), EALIGN), (dict(page_stride=1 << 40), EINVAL),
 ]
 BAD_POINTERS = [(dict(k_codes=None), EINVAL), (dict(v_scales=None), EINVAL), (dict(v_codes=ODD), EALIGN),
                 (dict(k_scales=GOOD + 4), EALIGN)]
@@ -134,7 +133,7 @@ def test_qkv_write_refusals(M, L):
     for over, rc in BAD_CACHES + BAD_POINTERS:
         bad = _cache(M, **over)
         assert f(*_with(args, cache=_byref(bad))) == rc, over
-    small = _cache(M, head_dim=48, k_page_stride=8 * 16 * 48, v_page_stride=8 * 16 * 48)
+    small = _cache(M, head_dim=48)
     assert f(*_with(args, cache=_byref(small))) == EINVAL       # rotates 64 of 48
 
 

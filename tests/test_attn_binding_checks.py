@@ -42,6 +42,7 @@ def test_cache_layouts():
     _raises("v_scales must be", make, k, v, ks, vs.double())
     _raises("page must be contiguous", make, k, torch.zeros(4, 2, 64, 16, dtype=u8).transpose(2, 3), ks, vs)
     _raises("pages overlap", make, k[:1].expand(4, -1, -1, -1), v, ks, vs)
+    _raises("equally far apart", make, torch.zeros(4, 3, 2, 16, 64, dtype=u8)[:, 0], v, ks, vs)
     _raises("one page", make, k[:0], v[:0], ks[:0], vs[:0])
     _raises("on a GPU", F.KVCache, 4, 16, 2, 64, device="cpu")
 
