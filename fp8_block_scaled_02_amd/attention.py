@@ -65,41 +65,56 @@ def attn_lib():
     return _attn_lib
 
 
-def _call(device, fn, *args):
-    """One C call on the current stream of `device`, which is made current
+def _call(fn, dev, *args):
+    """One C call on the current stream of GPU `dev`, which is made current
     for it: a default stream is NULL, which means the current device's."""
-    f = getattr(attn_lib(), fn)
-    if device.index == torch.cuda.current_device():
-        rc = f(*args, torch.cuda.current_stream(device).cuda_stream)
+    f = getattr(_attn_lib or attn_lib(), fn)
+    if dev == torch._C._cuda_getDevice():
+        rc = f(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
-        with torch.cuda.device(device):
-            rc = f(*args, torch.cuda.current_stream(device).cuda_stream)
+        with torch.cuda.device(dev):
+            rc = f(*args, torch._C._cuda_getCurrentRawStream(dev))
     if rc != 0:
         raise Fp8Error(fn, rc)
 
 
-def _on(device, **ts):
-    """Every tensor is on the GPU `device`: the kernels dereference data_ptr()
+# The checks below build their messages only when they fail: a decode step on
+# a few sequences is bound by the host.
+
+
+def _on(dev, *ts):
+    """Every tensor is on GPU number `dev`: the kernels dereference data_ptr()
     as its memory."""
-    _need(device.type == "cuda", f"every tensor must be on a GPU (found one on {device})")
-    for name, t in ts.items():
-        if t is not None:
-            _need(t.device == device, f"{name} must be on {device} (it is on {t.device})")
+    if dev < 0:
+        raise ValueError("every tensor must be on a GPU (found one on the host)")
+    for t in ts:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"every tensor must be on cuda:{dev} (found one on {t.device})")
 
 
 def _rows(t, name):
     """(address, token stride, head stride) of bf16 [tokens, heads, D]; the
     stride of a dimension of one entry means nothing and is put in order."""
-    _need(t.dtype == torch.bfloat16 and t.dim() == 3 and (t.stride(2) == 1 or t.shape[2] == 1),
-          f"{name} must be 3-D bf16 [tokens, heads, head_dim], head rows contiguous")
+    if t.dtype != torch.bfloat16 or t.dim() != 3 or (t.stride(2) != 1 and t.shape[2] != 1):
+        raise ValueError(f"{name} must be 3-D bf16 [tokens, heads, head_dim], head rows contiguous")
     T, H, D = t.shape
-    h = t.stride(1) if H > 1 else D
-    return t.data_ptr(), (t.stride(0) if T > 1 else h * H), h
+    st, sh, _ = t.stride()
+    if H <= 1:
+        sh = D
+    return t.data_ptr(), (st if T > 1 else sh * H), sh
 
 
 def _index(t, dtype, shape, name):
-    _need(t.dtype == dtype and t.is_contiguous(), f"{name} must be contiguous {dtype}")
-    _shape(t, shape, name)
+    if t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {dtype}")
+    if t.shape != shape:
+        _shape(t, shape, name)
+
+
+def _out(t, shape, name):
+    if t.shape != shape:
+        _shape(t, shape, name)
+    return t
 
 
 class KVCache:
@@ -143,40 +158,38 @@ class KVCache:
             _need(P == 1 or t.stride(0) >= t[0].numel(), f"{name}: pages overlap")
             strides.append(t.stride(0) if P > 1 else t[0].numel())
         _need(strides[0] == strides[1] and strides[2] == strides[3], "K and V pages must lie equally far apart")
-        _on(k_codes.device, v_codes=v_codes, k_scales=k_scales, v_scales=v_scales)
+        _on(k_codes.get_device(), v_codes, k_scales, v_scales)
         self.k_codes, self.v_codes, self.k_scales, self.v_scales = k_codes, v_codes, k_scales, v_scales
         self.pages, self.heads, self.page_size, self.head_dim, self.fmt = P, H, S, D, fmt
         self.device = k_codes.device
+        self._dev = k_codes.get_device()
         self._struct = _CacheStruct(k_codes.data_ptr(), v_codes.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
                                     strides[0], strides[2], P, S, H, D, _CACHE_FMT[fmt], 0)
         self._ref = ctypes.addressof(self._struct)
 
 
 def _rope(D, T, cos_sin, positions, q_weight, k_weight, eps, interleaved):
-    r = _RopeStruct()
-    r.eps, r.interleaved = eps, int(interleaved)
-    _need((cos_sin is None) == (positions is None), "cos_sin and positions go together")
+    if (cos_sin is None) != (positions is None):
+        raise ValueError("cos_sin and positions go together")
+    cs = pos = qw = kw = None
+    n = rot = 0
     if cos_sin is not None:
-        _need(cos_sin.dtype == torch.float32 and cos_sin.dim() == 2 and cos_sin.is_contiguous(),
-              "cos_sin must be contiguous float32 [max_pos, rot_dim]")
-        rot = cos_sin.shape[1]
-        _need(16 <= rot <= D and rot % 16 == 0, f"rot_dim must be a multiple of 16 from 16 to {D}")
-        _need(cos_sin.shape[0] >= 1, "cos_sin must hold at least one position")
+        if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
+            raise ValueError("cos_sin must be contiguous float32 [max_pos, rot_dim]")
+        n, rot = cos_sin.shape
+        if not 16 <= rot <= D or rot % 16:
+            raise ValueError(f"rot_dim must be a multiple of 16 from 16 to {D}")
+        if n < 1:
+            raise ValueError("cos_sin must hold at least one position")
         _index(positions, torch.int64, (T,), "positions")
-        r.cos_sin, r.positions = cos_sin.data_ptr(), positions.data_ptr()
-        r.max_pos, r.rot_dim = cos_sin.shape[0], rot
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            _index(w, torch.bfloat16, (D,), name)
-            setattr(r, name, w.data_ptr())
-    return r
-
-
-def _like_rows(out, shape, x, name):
-    if out is None:
-        return torch.empty(shape, dtype=torch.bfloat16, device=x.device)
-    _shape(out, shape, name)
-    return out
+        cs, pos = cos_sin.data_ptr(), positions.data_ptr()
+    if q_weight is not None:
+        _index(q_weight, torch.bfloat16, (D,), "q_weight")
+        qw = q_weight.data_ptr()
+    if k_weight is not None:
+        _index(k_weight, torch.bfloat16, (D,), "k_weight")
+        kw = k_weight.data_ptr()
+    return _RopeStruct(qw, kw, cs, pos, n, rot, eps, bool(interleaved))
 
 
 def fp8_qk_norm_rope(q, k, cos_sin=None, positions=None, q_weight=None, k_weight=None, eps=1e-6, interleaved=False,
@@ -189,33 +202,36 @@ def fp8_qk_norm_rope(q, k, cos_sin=None, positions=None, q_weight=None, k_weight
     be its input."""
     qa, ka = _rows(q, "q"), _rows(k, "k")
     T, Hq, D = q.shape
-    _need(k.shape[0] == T and k.shape[2] == D, f"k must be [{T}, Hk, {D}]")
+    Tk, Hk, Dk = k.shape
+    if Tk != T or Dk != D:
+        raise ValueError(f"k must be [{T}, Hk, {D}]")
     r = _rope(D, T, cos_sin, positions, q_weight, k_weight, eps, interleaved)
-    q_out = _like_rows(q_out, q.shape, q, "q_out")
-    k_out = _like_rows(k_out, k.shape, k, "k_out")
+    q_out = torch.empty_like(q, memory_format=torch.contiguous_format) if q_out is None else _out(q_out, q.shape, "q_out")
+    k_out = torch.empty_like(k, memory_format=torch.contiguous_format) if k_out is None else _out(k_out, k.shape, "k_out")
     qo, ko = _rows(q_out, "q_out"), _rows(k_out, "k_out")
-    _on(q.device, k=k, cos_sin=cos_sin, positions=positions, q_weight=q_weight, k_weight=k_weight, q_out=q_out,
-        k_out=k_out)
-    _call(q.device, "fp8_qk_norm_rope", *qa, *ka, T, Hq, k.shape[1], D, ctypes.addressof(r), *qo, *ko)
+    dev = q.get_device()
+    _on(dev, k, cos_sin, positions, q_weight, k_weight, q_out, k_out)
+    _call("fp8_qk_norm_rope", dev, *qa, *ka, T, Hq, Hk, D, ctypes.addressof(r), *qo, *ko)
     return q_out, k_out
 
 
 def _kv_rows(k, v, cache):
     ka, va = _rows(k, "k"), _rows(v, "v")
-    _shape(k, (k.shape[0], cache.heads, cache.head_dim), "k")
-    _shape(v, k.shape, "v")
-    return ka, va
+    T = k.shape[0]
+    _out(k, (T, cache.heads, cache.head_dim), "k")
+    _out(v, k.shape, "v")
+    return T, ka, va
 
 
 def fp8_kv_cache_write(k, v, slots, cache: KVCache):
     """Quantise k, v bf16 [T, heads, D] (any token and head strides that are
     multiples of 8) into the cache at slots int64 [T]; a slot outside the
     cache, such as -1, writes nothing.  Slots should differ: one named twice
-    holds either token's row.  Returns the cache."""
-    ka, va = _kv_rows(k, v, cache)
-    _index(slots, torch.int64, (k.shape[0],), "slots")
-    _on(cache.device, k=k, v=v, slots=slots)
-    _call(cache.device, "fp8_kv_cache_write", *ka, *va, slots.data_ptr(), k.shape[0], cache._ref)
+    holds either token's row, or a mixture.  Returns the cache."""
+    T, ka, va = _kv_rows(k, v, cache)
+    _index(slots, torch.int64, (T,), "slots")
+    _on(cache._dev, k, v, slots)
+    _call("fp8_kv_cache_write", cache._dev, *ka, *va, slots.data_ptr(), T, cache._ref)
     return cache
 
 
@@ -225,25 +241,26 @@ def fp8_qkv_cache_write(q, k, v, cos_sin, positions, slots, cache: KVCache, q_we
     returns the queries, normed and rotated; the keys, normed and rotated,
     and the values go to the cache."""
     qa = _rows(q, "q")
-    ka, va = _kv_rows(k, v, cache)
-    T, Hq, D = q.shape
-    _need(k.shape[0] == T and D == cache.head_dim, f"q must be [{k.shape[0]}, Hq, {cache.head_dim}]")
+    T, ka, va = _kv_rows(k, v, cache)
+    Tq, Hq, D = q.shape
+    if Tq != T or D != cache.head_dim:
+        raise ValueError(f"q must be [{T}, Hq, {cache.head_dim}]")
     r = _rope(D, T, cos_sin, positions, q_weight, k_weight, eps, interleaved)
     _index(slots, torch.int64, (T,), "slots")
-    q_out = _like_rows(q_out, q.shape, q, "q_out")
+    q_out = torch.empty_like(q, memory_format=torch.contiguous_format) if q_out is None else _out(q_out, q.shape, "q_out")
     qo = _rows(q_out, "q_out")
-    _on(cache.device, q=q, k=k, v=v, cos_sin=cos_sin, positions=positions, slots=slots, q_weight=q_weight,
-        k_weight=k_weight, q_out=q_out)
-    _call(cache.device, "fp8_qkv_cache_write", *qa, *ka, *va, slots.data_ptr(), T, Hq, ctypes.addressof(r),
-          cache._ref, *qo)
+    _on(cache._dev, q, k, v, cos_sin, positions, slots, q_weight, k_weight, q_out)
+    _call("fp8_qkv_cache_write", cache._dev, *qa, *ka, *va, slots.data_ptr(), T, Hq, ctypes.addressof(r), cache._ref,
+          *qo)
     return q_out
 
 
-def _table(block_table, cache):
-    _need(block_table.dtype == torch.int32 and block_table.dim() == 2 and
-          (block_table.stride(1) == 1 or block_table.shape[1] == 1), "block_table must be 2-D int32, rows contiguous")
+def _table(block_table):
+    if (block_table.dtype != torch.int32 or block_table.dim() != 2 or
+            (block_table.stride(1) != 1 and block_table.shape[1] != 1)):
+        raise ValueError("block_table must be 2-D int32, rows contiguous")
     B, cols = block_table.shape
-    return block_table.data_ptr(), (block_table.stride(0) if B > 1 else cols), cols
+    return B, block_table.data_ptr(), (block_table.stride(0) if B > 1 else cols), cols
 
 
 def fp8_kv_cache_read(cache: KVCache, block_table, offsets, rows: int, k_out=None, v_out=None):
@@ -251,19 +268,20 @@ def fp8_kv_cache_read(cache: KVCache, block_table, offsets, rows: int, k_out=Non
     offsets[b + 1] of k_out, v_out [rows, heads, head_dim].  block_table
     int32 [B, cols]: each sequence's pages in order; offsets int32 [B + 1];
     rows from offsets[B] on are left as they were."""
-    table = _table(block_table, cache)
-    B = block_table.shape[0]
+    B, *table = _table(block_table)
     _index(offsets, torch.int32, (B + 1,), "offsets")
     shape = (rows, cache.heads, cache.head_dim)
     outs = []
     for t, name in ((k_out, "k_out"), (v_out, "v_out")):
-        t = _like_rows(t, shape, cache.k_codes, name)
-        _need(t.dtype == torch.bfloat16 and t.is_contiguous(), f"{name} must be contiguous bf16")
+        if t is None:
+            t = torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
+        _index(t, torch.bfloat16, shape, name)
         outs.append(t)
-    _on(cache.device, block_table=block_table, offsets=offsets, k_out=outs[0], v_out=outs[1])
-    _call(cache.device, "fp8_kv_cache_read", cache._ref, *table, offsets.data_ptr(), B, rows, outs[0].data_ptr(),
-          outs[1].data_ptr())
-    return outs[0], outs[1]
+    k_out, v_out = outs
+    _on(cache._dev, block_table, offsets, k_out, v_out)
+    _call("fp8_kv_cache_read", cache._dev, cache._ref, *table, offsets.data_ptr(), B, rows, k_out.data_ptr(),
+          v_out.data_ptr())
+    return k_out, v_out
 
 
 def fp8_paged_attention(q, cache: KVCache, block_table, context_lens, scale=None, window: int = 0,
@@ -278,29 +296,38 @@ def fp8_paged_attention(q, cache: KVCache, block_table, context_lens, scale=None
     fp32); lse, if given (float32 [B, Hq]), receives the log of the sum of
     exponentials, -inf for an empty row."""
     qa = _rows(q, "q")
-    B, Hq, D = q.shape
-    _need(D == cache.head_dim, f"q must be [B, Hq, {cache.head_dim}]")
-    _need(Hq >= 1 and Hq % cache.heads == 0, f"query heads must be a multiple of the cache's {cache.heads}")
-    table = _table(block_table, cache)
-    _need(block_table.shape[0] == B, f"block_table must have {B} rows")
+    shape = q.shape
+    B, Hq, D = shape
+    if D != cache.head_dim:
+        raise ValueError(f"q must be [B, Hq, {cache.head_dim}]")
+    if Hq < 1 or Hq % cache.heads:
+        raise ValueError(f"query heads must be a multiple of the cache's {cache.heads}")
+    Bt, table, ld, cols = _table(block_table)
+    if Bt != B:
+        raise ValueError(f"block_table must have {B} rows")
     _index(context_lens, torch.int32, (B,), "context_lens")
-    _need(out_dtype in (torch.bfloat16, torch.float32), "out_dtype must be bfloat16 or float32")
+    if out_dtype == torch.bfloat16:
+        od = OUT_BF16
+    elif out_dtype == torch.float32:
+        od = OUT_F32
+    else:
+        raise ValueError("out_dtype must be bfloat16 or float32")
     if out is None:
-        out = torch.empty(B, Hq, D, dtype=out_dtype, device=q.device)
-    _need(out.dtype == out_dtype and out.is_contiguous(), f"out must be contiguous {out_dtype}")
-    _shape(out, (B, Hq, D), "out")
+        out = torch.empty(shape, dtype=out_dtype, device=q.device)
+    else:
+        _index(out, out_dtype, shape, "out")
     if lse is not None:
         _index(lse, torch.float32, (B, Hq), "lse")
     if max_context is None:
-        max_context = min(table[2] * cache.page_size, MAX_CONTEXT)
-    _on(cache.device, q=q, block_table=block_table, context_lens=context_lens, out=out, lse=lse)
-    nbytes = attn_lib().fp8_paged_attention_workspace(cache._ref, B, Hq, table[2], max_context, window)
+        max_context = min(cols * cache.page_size, MAX_CONTEXT)
+    dev = cache._dev
+    _on(dev, q, block_table, context_lens, out, lse)
+    nbytes = (_attn_lib or attn_lib()).fp8_paged_attention_workspace(cache._ref, B, Hq, cols, max_context, window)
     if nbytes < 0:
         raise Fp8Error("fp8_paged_attention", nbytes)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device) if nbytes else None
-    _call(cache.device, "fp8_paged_attention", *qa, cache._ref, *table, context_lens.data_ptr(), B, Hq, max_context,
-          window, D ** -0.5 if scale is None else scale, out.data_ptr(),
-          OUT_BF16 if out_dtype == torch.bfloat16 else OUT_F32, None if lse is None else lse.data_ptr(),
+    _call("fp8_paged_attention", dev, *qa, cache._ref, table, ld, cols, context_lens.data_ptr(), B, Hq, max_context,
+          window, D ** -0.5 if scale is None else scale, out.data_ptr(), od, None if lse is None else lse.data_ptr(),
           None if ws is None else ws.data_ptr())
     return out
 

@@ -27,6 +27,7 @@ struct QkvArgs {
   int64_t page_stride, scale_page_stride, total_slots;
   int page_shift, cache_heads;
   int slot_shift;  // log2 of the row slots of a workgroup that one token takes
+  int items, token_items;  // rows of a slot; token_items > 1: they are of that many tokens
 };
 
 // Sum and maximum over the LPR (8, 16 or 32) adjacent lanes of a row: quad
@@ -74,10 +75,10 @@ __device__ __forceinline__ u32x4 pack8(const float (&f)[8]) {
 
 // One row (token, head) per LPR lanes, 8 values per lane, LPR * 8 >= D; the
 // lanes past D hold zeros.  A workgroup's 256 / LPR row slots are split into
-// groups of 2^slot_shift that share a token, so its cos and sin are loaded
-// once per lane and used for every head the slot takes in turn (gridDim.y
-// workgroups share the heads of a token when tokens are few).  Rows are
-// numbered queries, keys, values.
+// groups of 2^slot_shift that share a token; rows are numbered queries, keys,
+// values.  A slot takes `items` rows, the next one loaded while this one is
+// worked on: other heads of its token, whose cos and sin it keeps, or
+// (nothing to rotate, heads no more than slots) the same head of later tokens.
 //
 // FMT: 0 no cache (keys to k_out), 1 E5M2, 2 E4M3.  ROPE: 0 none, 1 halves,
 // 2 interleaved.  HBM-bound: 2 bytes in and 2 (or 1 and a scale) out per
@@ -88,12 +89,28 @@ __global__ __launch_bounds__(256) void qkv_kernel(const QkvArgs a) {
   const int lane = threadIdx.x & (LPR - 1);
   const int slot = threadIdx.x / LPR;
   const int per_token = 1 << a.slot_shift;
-  const int64_t t = (int64_t)blockIdx.x * (kSlots >> a.slot_shift) + (slot >> a.slot_shift);
-  if (t >= a.T) return;
+  const int tokens = kSlots >> a.slot_shift;  // of a workgroup at a time
+  const int rows = a.q.heads + a.k.heads + a.v.heads;
+  int64_t t = (int64_t)blockIdx.x * tokens * a.token_items + (slot >> a.slot_shift);
+  int r = (int)blockIdx.y * per_token + (slot & (per_token - 1));
+  const int row_step = (int)gridDim.y * per_token;
+  if (t >= a.T || r >= rows) return;
   const int e0 = 8 * lane;
   const bool on = e0 < a.D;
-  const int rows = a.q.heads + a.k.heads + a.v.heads;
   const int half = a.rot >> 1;
+
+  auto load = [&](int64_t tt, int rr) {
+    const bool is_q = rr < a.q.heads, is_k = !is_q && rr < a.q.heads + a.k.heads;
+    const Rows& src = is_q ? a.q : (is_k ? a.k : a.v);
+    const int h = rr - (is_q ? 0 : (is_k ? a.q.heads : a.q.heads + a.k.heads));
+    u32x4 x = {0, 0, 0, 0};
+    if (on)
+      x = __builtin_nontemporal_load(
+          reinterpret_cast<const u32x4*>(src.p + tt * src.t + (int64_t)h * src.h + e0));
+    return x;
+  };
+  u32x4 next = load(t, r);
+  int64_t next_slot = FMT != 0 ? a.slots[t] : 0;
 
   float cs[8], sn[8];
   int partner = lane;
@@ -123,22 +140,20 @@ __global__ __launch_bounds__(256) void qkv_kernel(const QkvArgs a) {
       }
     }
   }
-  int64_t page = 0;
-  int place = 0;
-  bool stored = false;
-  if (FMT != 0) {
-    const int64_t sl = a.slots[t];
-    stored = sl >= 0 && sl < a.total_slots;
-    page = sl >> a.page_shift;
-    place = (int)(sl & ((1 << a.page_shift) - 1));
-  }
 
-  for (int r = (int)blockIdx.y * per_token + (slot & (per_token - 1)); r < rows; r += (int)gridDim.y * per_token) {
-    const int kind = r < a.q.heads ? 0 : (r < a.q.heads + a.k.heads ? 1 : 2);
-    const Rows& src = kind == 0 ? a.q : (kind == 1 ? a.k : a.v);
-    const int h = kind == 0 ? r : (kind == 1 ? r - a.q.heads : r - a.q.heads - a.k.heads);
-    u32x4 raw = {0, 0, 0, 0};
-    if (on) raw = *reinterpret_cast<const u32x4*>(src.p + t * src.t + (int64_t)h * src.h + e0);
+  for (int left = a.items; left > 0; --left) {
+    u32x4 raw = next;
+    const int64_t sl = next_slot, tt = t;
+    const int rr = r;
+    if (a.token_items > 1) t += tokens;
+    else r += row_step;
+    const bool last = left == 1 || t >= a.T || r >= rows;
+    if (!last) {
+      next = load(t, r);
+      if (FMT != 0 && a.token_items > 1) next_slot = a.slots[t];
+    }
+    const int kind = rr < a.q.heads ? 0 : (rr < a.q.heads + a.k.heads ? 1 : 2);
+    const int h = kind == 0 ? rr : (kind == 1 ? rr - a.q.heads : rr - a.q.heads - a.k.heads);
     float f[8];
     if (FMT == 0 || kind < 2) {
       unpack8(raw, f);
@@ -176,9 +191,9 @@ __global__ __launch_bounds__(256) void qkv_kernel(const QkvArgs a) {
     }
     if (FMT == 0 || kind == 0) {
       const Rows& dst = kind == 0 ? a.q_out : a.k_out;
-      uint16_t* dp = const_cast<uint16_t*>(dst.p) + t * dst.t + (int64_t)h * dst.h + e0;
+      uint16_t* dp = const_cast<uint16_t*>(dst.p) + tt * dst.t + (int64_t)h * dst.h + e0;
       if (on) *reinterpret_cast<u32x4*>(dp) = raw;
-    } else if (stored) {
+    } else if (sl >= 0 && sl < a.total_slots) {
       constexpr float kMax = FMT == 1 ? 57344.0f : 448.0f;
       unpack8(raw, f);
       float amax = 0.0f;
@@ -194,14 +209,19 @@ __global__ __launch_bounds__(256) void qkv_kernel(const QkvArgs a) {
       u32x2 codes;
       codes[0] = FMT == 1 ? pack4_e5m2(v[0], v[1], v[2], v[3]) : pack4_e4m3(v[0], v[1], v[2], v[3]);
       codes[1] = FMT == 1 ? pack4_e5m2(v[4], v[5], v[6], v[7]) : pack4_e4m3(v[4], v[5], v[6], v[7]);
-      const int64_t in_page = ((int64_t)h << a.page_shift) + place;
+      const int64_t page = sl >> a.page_shift;
+      const int64_t in_page = ((int64_t)h << a.page_shift) + (sl & ((1 << a.page_shift) - 1));
       uint8_t* cp = (kind == 1 ? a.k_codes : a.v_codes) + page * a.page_stride;
       float* sp = (kind == 1 ? a.k_scales : a.v_scales) + page * a.scale_page_stride;
       if (on) *reinterpret_cast<u32x2*>(cp + in_page * a.D + e0) = codes;
       if (lane == 0) sp[in_page] = d;
     }
+    if (last) return;
   }
 }
+
+constexpr int kManyWgs = 1024;
+constexpr int kTokenItems = 4;
 
 int launch_qkv(const Rows& q, const Rows& k, const Rows& v, int64_t T, int D, const fp8b_rope* rope, const Rows& q_out,
                const Rows& k_out, const int64_t* slots, const fp8b_kv_cache* cache, hipStream_t s) {
@@ -245,11 +265,18 @@ int launch_qkv(const Rows& q, const Rows& k, const Rows& v, int64_t T, int D, co
   int shift = 0;
   while ((1 << shift) < rows && (1 << shift) < wg_slots) ++shift;
   a.slot_shift = shift;
-  const int64_t gx = (T + (wg_slots >> shift) - 1) / (wg_slots >> shift);
-  // Few tokens: one row per slot, all heads at once.  Many: a slot walks
-  // through the heads of its token and keeps the token's cos and sin.
+  const int tokens = wg_slots >> shift;
   const int turns = (rows + (1 << shift) - 1) >> shift;
-  const int64_t gy = gx >= 1024 ? 1 : turns;
+  int64_t gx = (T + tokens - 1) / tokens, gy = 1;
+  a.items = turns;
+  a.token_items = 1;
+  if (gx < kManyWgs) {  // few tokens: every row a slot of its own
+    gy = turns;
+    a.items = 1;
+  } else if (turns == 1 && kind == 0) {
+    a.items = a.token_items = kTokenItems;
+    gx = (T + (int64_t)tokens * kTokenItems - 1) / (tokens * kTokenItems);
+  }
   const dim3 grid((unsigned)gx, (unsigned)gy);
 #define FP8A_QKV(L, R, F) hipLaunchKernelGGL((qkv_kernel<L, R, F>), grid, dim3(256), 0, s, a)
 #define FP8A_QKV_F(L, R)            \

@@ -153,14 +153,14 @@ def test_cache_read_refusals(M, L):
 
 def test_attention_refusals(M, L):
     good = _cache(M)
-    args = dict(q=GOOD, q_b=4096, q_h=128, cache=_byref(good), table=GOOD, ld=100, cols=100, lens=GOOD, B=3, Hq=32,
-                most=1600, window=0, scale=0.1, out=GOOD, dtype=1, lse=None, ws=GOOD, s=None)
+    args = dict(q=GOOD, q_b=4096, q_h=128, cache=_byref(good), table=GOOD, ld=1000, cols=1000, lens=GOOD, B=3, Hq=32,
+                most=16000, window=0, scale=0.1, out=GOOD, dtype=1, lse=None, ws=GOOD, s=None)
     f = L.fp8_paged_attention
     sizes = [(dict(B=-1), EINVAL), (dict(Hq=0), EINVAL), (dict(Hq=30), EINVAL), (dict(Hq=65544), EINVAL),
              (dict(cols=0), EINVAL), (dict(most=-1), EINVAL), (dict(most=(1 << 30) + 1), EINVAL),
              (dict(window=-1), EINVAL), (dict(cache=None), EINVAL), (dict(B=1 << 22), EINVAL),
              (dict(B=1 << 16, cols=1 << 20, ld=1 << 20, most=1 << 24), EINVAL)]
-    for over, rc in sizes + [(dict(B=0), OK), (dict(dtype=2), EUNSUPPORTED), (dict(ld=99), EINVAL),
+    for over, rc in sizes + [(dict(B=0), OK), (dict(dtype=2), EUNSUPPORTED), (dict(ld=999), EINVAL),
                              (dict(scale=float("nan")), EINVAL), (dict(scale=float("inf")), EINVAL),
                              (dict(q=None), EINVAL), (dict(q=ODD), EALIGN), (dict(q_b=4), EALIGN),
                              (dict(table=None), EINVAL), (dict(lens=None), EINVAL), (dict(lens=ODD), EALIGN),

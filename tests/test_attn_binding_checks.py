@@ -23,7 +23,7 @@ class _HostCache(F.KVCache):
 
     def __init__(self):
         self.pages, self.heads, self.page_size, self.head_dim, self.fmt = 4, 2, 16, 64, "e5m2"
-        self.device, self._ref = torch.device("cpu"), 0
+        self.device, self._dev, self._ref = torch.device("cpu"), -1, 0
         self.k_codes = torch.zeros(4, 2, 16, 64, dtype=u8)
 
 

@@ -245,11 +245,12 @@ def _values(c):
     return [t[x.long()] * s.double()[..., None] for x, s in ((c.k_codes, c.k_scales), (c.v_codes, c.v_scales))]
 
 
-def _book(lens, S, g, spare=3):
-    """Pages in random order; table entries past a sequence's pages are no pages at all."""
+def _book(lens, S, g, spare=3, room=5000):
+    """Pages in random order; table entries past a sequence's pages are no pages at all.  Room for contexts
+    that are split, whatever these lengths."""
     need = [-(-n // S) for n in lens]
     order = torch.randperm(sum(need) + spare, generator=g, device=DEV).cpu()
-    table = torch.full((len(lens), max(need + [1])), -(1 << 30), dtype=torch.int32)
+    table = torch.full((len(lens), max(need + [-(-room // S)])), -(1 << 30), dtype=torch.int32)
     at = 0
     for b, n in enumerate(need):
         table[b, :n] = order[at:at + n].int()
@@ -360,6 +361,7 @@ def test_attention_pages_and_windows(F, S, window):
     c = _filled(F, pages, 2, S, 64, "e4m3", g)
     q = (2 * torch.randn(len(lens), 4, 64, generator=g, device=DEV)).bfloat16()
     _check_attention(F, c, lens, q, table, window, torch.float32)
+    _check_attention(F, c, lens, q, table, window, max_context=310)
 
 
 def test_attention_long_context_is_split_and_joined(F):
@@ -370,6 +372,7 @@ def test_attention_long_context_is_split_and_joined(F):
     q = (2 * torch.randn(4, 16, 128, generator=g, device=DEV)).bfloat16()
     _check_attention(F, c, lens, q, table, out_dtype=torch.float32)
     _check_attention(F, c, lens, q, table, window=9999)
+    _check_attention(F, c, lens, q, table, max_context=4096)
 
 
 def test_attention_many_sequences(F):
@@ -386,7 +389,6 @@ def test_attention_many_sequences(F):
 def test_attention_all_empty(F):
     g = W.gen(4, DEV)
     _, table = _book([0, 0, 0], 16, g)
-    table = table.expand(3, 1).repeat(1, 200)
     c = _filled(F, 3, 2, 16, 64, "e5m2", g)
     q = torch.randn(3, 4, 64, generator=g, device=DEV).bfloat16()
     _check_attention(F, c, [0, 0, 0], q, table)
@@ -402,7 +404,7 @@ def test_attention_sharp_and_flat_scores(F):
     n = 900
     pages, table = _book([n], 16, g)
     c = _filled(F, pages, 1, 16, 64, "e5m2", g)
-    order = table[0].long()
+    order = table[0, :-(-n // 16)].long()
     ramp = torch.linspace(0.01, 4.0, order.numel() * 16, device=DEV).view(-1, 16)
     c.k_scales[order, 0] *= ramp
     q = (20 * torch.randn(1, 4, 64, generator=g, device=DEV)).bfloat16()
@@ -454,6 +456,7 @@ def test_attention_pages_that_are_none(F):
     got = F.fp8_paged_attention(q, c, bad, lt)
     assert torch.equal(got[[0, 2]], want[[0, 2]])
     # lengths beyond the table are cut to it
+    table = table[:, :32]
     cut = torch.tensor([40, 40, 2 ** 31 - 1], dtype=torch.int32, device=DEV)
     room = torch.tensor([40, 40, table.shape[1] * 16], dtype=torch.int32, device=DEV)
     assert torch.equal(F.fp8_paged_attention(q, c, table, cut), F.fp8_paged_attention(q, c, table, room))
