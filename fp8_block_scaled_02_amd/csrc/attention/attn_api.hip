@@ -42,7 +42,7 @@ int cache_pointers(const fp8b_kv_cache* c) {
 // bf16 rows [T][heads][D] with free strides.
 int rows_check(const void* p, int64_t t, int64_t h) {
   if (!p) return FP8B_EINVAL;
-  if (t < 0 || h < 0 || t > kMaxStride || h > kMaxStride) return FP8B_EINVAL;
+  if (t < 0 || h < 0 || t > kMaxStride || h >= kMaxDim) return FP8B_EINVAL;
   if (!aligned(p, 16) || t % 8 != 0 || h % 8 != 0) return FP8B_EALIGN;
   return FP8B_OK;
 }

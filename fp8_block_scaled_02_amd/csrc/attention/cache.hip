@@ -19,15 +19,17 @@ struct QkvArgs {
   const int64_t* positions;
   int64_t max_pos;
   int rot;
-  float eps;
+  float eps, inv_D;
   Rows q_out, k_out;
   const int64_t* slots;
   uint8_t *k_codes, *v_codes;
   float *k_scales, *v_scales;
-  int64_t page_stride, scale_page_stride, total_slots;
-  int page_shift, cache_heads;
+  uint32_t page_stride, scale_page_stride;
+  int64_t total_slots;
+  int page_shift;
   int slot_shift;  // log2 of the row slots of a workgroup that one token takes
   int items, token_items;  // rows of a slot; token_items > 1: they are of that many tokens
+  bool stream;             // non-temporal stores
 };
 
 // Sum and maximum over the LPR (8, 16 or 32) adjacent lanes of a row: quad
@@ -55,6 +57,24 @@ __device__ __forceinline__ float row_max_nonneg(float v) {
   return __uint_as_float(u);
 }
 
+// The value LPR / 2 lanes away (a whole head's rotation partner): half-row
+// mirror and quad reversal (4), row rotation (8), row swap (16).
+template <int LPR>
+__device__ __forceinline__ float other_half(float v) {
+  int x = __float_as_int(v);
+  if (LPR == 8) {
+    x = __builtin_amdgcn_update_dpp(0, x, 0x141, 0xF, 0xF, false);
+    x = __builtin_amdgcn_update_dpp(0, x, 0x1B, 0xF, 0xF, false);
+  } else if (LPR == 16) {
+    x = __builtin_amdgcn_update_dpp(0, x, 0x128, 0xF, 0xF, false);
+  } else {
+    typedef unsigned int u2 __attribute__((ext_vector_type(2)));
+    const u2 y = __builtin_amdgcn_permlane16_swap((uint32_t)x, (uint32_t)x, false, false);
+    x = (int)((threadIdx.x & 16) ? y[0] : y[1]);
+  }
+  return __int_as_float(x);
+}
+
 __device__ __forceinline__ void unpack8(const u32x4& w, float (&f)[8]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -73,6 +93,59 @@ __device__ __forceinline__ u32x4 pack8(const float (&f)[8]) {
   return o;
 }
 
+// Global memory by its address (a plain pointer made of an integer would be
+// accessed as if it might be LDS).
+template <typename T>
+using global_ptr = __attribute__((address_space(1))) T*;
+
+__device__ __forceinline__ int64_t address(const void* p) { return (int64_t)reinterpret_cast<uintptr_t>(p); }
+
+// q, k or v by the row's number.
+template <typename T>
+__device__ __forceinline__ T of_kind(int row, int k0, int v0, T q, T k, T v) {
+  return row < k0 ? q : (row < v0 ? k : v);
+}
+
+// Head h's 8 values of this lane; p: head 0's, step: bytes from head to head.
+template <bool STREAM>
+__device__ __forceinline__ u32x4 load_row(int64_t p, uint32_t step, int h, bool on) {
+  const auto x = (global_ptr<const u32x4>)(p + (int64_t)((uint64_t)(uint32_t)h * step));
+  u32x4 w = {0, 0, 0, 0};
+  if (on) w = STREAM ? __builtin_nontemporal_load(x) : *x;
+  return w;
+}
+
+// Rows of a large call are read by a later kernel, from memory: non-temporal.
+template <typename T>
+__device__ __forceinline__ void store(global_ptr<T> p, T v, bool stream) {
+  if (stream) __builtin_nontemporal_store(v, p);
+  else *p = v;
+}
+
+// Codes and scale of a row of bf16 values (the quantiser of fp8_kv_quant and
+// fp8_act_quant).  FMT 1: E5M2, 2: E4M3.
+template <int LPR, int FMT>
+__device__ __forceinline__ u32x2 quantise_row(const u32x4& raw, float& d) {
+  constexpr float kMax = FMT == 1 ? 57344.0f : 448.0f;
+  float f[8], v[8];
+  unpack8(raw, f);
+  float amax = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(f[i]));
+  amax = row_max_nonneg<LPR>(amax);
+  d = block_scale(amax, kMax, 1.0f / kMax);
+  const BlockDivisor bd = make_divisor(amax, d);
+  divide_block(f, v, bd);
+  // With a normal d the quotients end at kMax (1 + 2^-23), which rounds to
+  // kMax: only a subnormal d, rounded coarsely, needs the clamp.
+  if (!bd.fast) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = fminf(fmaxf(v[i], -kMax), kMax);
+  }
+  if (FMT == 1) return u32x2{pack4_e5m2(v[0], v[1], v[2], v[3]), pack4_e5m2(v[4], v[5], v[6], v[7])};
+  return u32x2{pack4_e4m3(v[0], v[1], v[2], v[3]), pack4_e4m3(v[4], v[5], v[6], v[7])};
+}
+
 // One row (token, head) per LPR lanes, 8 values per lane, LPR * 8 >= D; the
 // lanes past D hold zeros.  A workgroup's 256 / LPR row slots are split into
 // groups of 2^slot_shift that share a token; rows are numbered queries, keys,
@@ -81,16 +154,18 @@ __device__ __forceinline__ u32x4 pack8(const float (&f)[8]) {
 // (nothing to rotate, heads no more than slots) the same head of later tokens.
 //
 // FMT: 0 no cache (keys to k_out), 1 E5M2, 2 E4M3.  ROPE: 0 none, 1 halves,
-// 2 interleaved.  HBM-bound: 2 bytes in and 2 (or 1 and a scale) out per
-// value; the arithmetic is ~10 operations per value.
+// 2 interleaved.  HBM-bound (2 bytes in and 2, or 1 and a scale, out per
+// value), but only just: 8 values are one 16-byte load and some 150
+// instructions, so addresses are kept to 32-bit products.
 template <int LPR, int ROPE, int FMT>
 __global__ __launch_bounds__(256) void qkv_kernel(const QkvArgs a) {
   constexpr int kSlots = 256 / LPR;
+  constexpr bool kStream = ROPE == 0 && FMT != 0;  // a pure cache write: non-temporal loads (2-5% faster)
   const int lane = threadIdx.x & (LPR - 1);
   const int slot = threadIdx.x / LPR;
   const int per_token = 1 << a.slot_shift;
   const int tokens = kSlots >> a.slot_shift;  // of a workgroup at a time
-  const int rows = a.q.heads + a.k.heads + a.v.heads;
+  const int k0 = a.q.heads, v0 = a.q.heads + a.k.heads, rows = v0 + a.v.heads;
   int64_t t = (int64_t)blockIdx.x * tokens * a.token_items + (slot >> a.slot_shift);
   int r = (int)blockIdx.y * per_token + (slot & (per_token - 1));
   const int row_step = (int)gridDim.y * per_token;
@@ -99,17 +174,15 @@ __global__ __launch_bounds__(256) void qkv_kernel(const QkvArgs a) {
   const bool on = e0 < a.D;
   const int half = a.rot >> 1;
 
-  auto load = [&](int64_t tt, int rr) {
-    const bool is_q = rr < a.q.heads, is_k = !is_q && rr < a.q.heads + a.k.heads;
-    const Rows& src = is_q ? a.q : (is_k ? a.k : a.v);
-    const int h = rr - (is_q ? 0 : (is_k ? a.q.heads : a.q.heads + a.k.heads));
-    u32x4 x = {0, 0, 0, 0};
-    if (on)
-      x = __builtin_nontemporal_load(
-          reinterpret_cast<const u32x4*>(src.p + tt * src.t + (int64_t)h * src.h + e0));
-    return x;
-  };
-  u32x4 next = load(t, r);
+  // Rows of this token, by kind.  Chosen by value: a choice of variables or of
+  // the arguments' structs would be memory accesses.
+  const int64_t qp = address(a.q.p) + 2 * (t * a.q.t + e0);
+  int64_t kp = address(a.k.p) + 2 * (t * a.k.t + e0), vp = address(a.v.p) + 2 * (t * a.v.t + e0);
+  const uint32_t qs = 2 * (uint32_t)a.q.h, ks = 2 * (uint32_t)a.k.h, vs = 2 * (uint32_t)a.v.h;
+  const int64_t qo = address(a.q_out.p) + 2 * (t * a.q_out.t + e0);
+  const int64_t ko = address(a.k_out.p) + 2 * (t * a.k_out.t + e0);
+  u32x4 next = load_row<kStream>(of_kind(r, k0, v0, qp, kp, vp), of_kind(r, k0, v0, qs, ks, vs),
+                                 r - of_kind(r, k0, v0, 0, k0, v0), on);
   int64_t next_slot = FMT != 0 ? a.slots[t] : 0;
 
   float cs[8], sn[8];
@@ -141,29 +214,37 @@ __global__ __launch_bounds__(256) void qkv_kernel(const QkvArgs a) {
     }
   }
 
-  for (int left = a.items; left > 0; --left) {
+  for (int left = a.items;; --left) {
     u32x4 raw = next;
-    const int64_t sl = next_slot, tt = t;
+    const int64_t sl = next_slot;
     const int rr = r;
-    if (a.token_items > 1) t += tokens;
-    else r += row_step;
+    if (a.token_items > 1) {
+      t += tokens;
+      kp += 2 * tokens * a.k.t;  // (no queries and no k_out in a launch that walks along tokens)
+      vp += 2 * tokens * a.v.t;
+    } else {
+      r += row_step;
+    }
     const bool last = left == 1 || t >= a.T || r >= rows;
     if (!last) {
-      next = load(t, r);
+      next = load_row<kStream>(of_kind(r, k0, v0, qp, kp, vp), of_kind(r, k0, v0, qs, ks, vs),
+                               r - of_kind(r, k0, v0, 0, k0, v0), on);
       if (FMT != 0 && a.token_items > 1) next_slot = a.slots[t];
     }
-    const int kind = rr < a.q.heads ? 0 : (rr < a.q.heads + a.k.heads ? 1 : 2);
-    const int h = kind == 0 ? rr : (kind == 1 ? rr - a.q.heads : rr - a.q.heads - a.k.heads);
-    float f[8];
-    if (FMT == 0 || kind < 2) {
+    const int h = rr - of_kind(rr, k0, v0, 0, k0, v0);
+    const uint16_t* w = rr < k0 ? a.q_weight : a.k_weight;
+    if ((FMT == 0 || rr < v0) && (ROPE != 0 || w != nullptr)) {
+      float f[8];
       unpack8(raw, f);
-      const uint16_t* w = kind == 0 ? a.q_weight : a.k_weight;
       if (w) {
         float ss = 0.0f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) ss = __builtin_fmaf(f[i], f[i], ss);
         ss = row_sum<LPR>(ss);
-        const float rn = 1.0f / sqrtf(ss / (float)a.D + a.eps);
+        // 1 / sqrt(mean + eps): the estimate (1 ulp) and one Newton step
+        const float x = __builtin_fmaf(ss, a.inv_D, a.eps);
+        const float y = __builtin_amdgcn_rsqf(x);
+        const float rn = __builtin_fmaf(0.5f * y, __builtin_fmaf(-x * y, y, 1.0f), y);
         u32x4 wr = {0, 0, 0, 0};
         if (on) wr = *reinterpret_cast<const u32x4*>(w + e0);
         float wf[8];
@@ -173,48 +254,40 @@ __global__ __launch_bounds__(256) void qkv_kernel(const QkvArgs a) {
       }
       if (ROPE == 1) {
         float o[8];
+        if (a.rot == 8 * LPR) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = __shfl(f[i], partner, LPR);
+          for (int i = 0; i < 8; ++i) o[i] = other_half<LPR>(f[i]);
+        } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = e0 < a.rot ? __builtin_fmaf(f[i], cs[i], o[i] * sn[i]) : f[i];
+          for (int i = 0; i < 8; ++i) o[i] = __shfl(f[i], partner, LPR);
+        }
+        // positions past rot: cos 1, sin 0
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = __builtin_fmaf(f[i], cs[i], o[i] * sn[i]);
       } else if (ROPE == 2) {
-        if (e0 < a.rot) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float x = f[2 * i], y = f[2 * i + 1];
-            f[2 * i] = __builtin_fmaf(x, cs[i], -(y * sn[i]));
-            f[2 * i + 1] = __builtin_fmaf(y, cs[i], x * sn[i]);
-          }
+        for (int i = 0; i < 4; ++i) {
+          const float x = f[2 * i], y = f[2 * i + 1];
+          f[2 * i] = __builtin_fmaf(x, cs[i], -(y * sn[i]));
+          f[2 * i + 1] = __builtin_fmaf(y, cs[i], x * sn[i]);
         }
       }
       raw = pack8(f);  // one rounding to bf16
     }
-    if (FMT == 0 || kind == 0) {
-      const Rows& dst = kind == 0 ? a.q_out : a.k_out;
-      uint16_t* dp = const_cast<uint16_t*>(dst.p) + tt * dst.t + (int64_t)h * dst.h + e0;
-      if (on) *reinterpret_cast<u32x4*>(dp) = raw;
+    if (FMT == 0 || rr < k0) {
+      const uint32_t step = 2 * (uint32_t)(rr < k0 ? a.q_out.h : a.k_out.h);
+      if (on) store((global_ptr<u32x4>)((rr < k0 ? qo : ko) + (int64_t)((uint64_t)(uint32_t)h * step)), raw, a.stream);
     } else if (sl >= 0 && sl < a.total_slots) {
-      constexpr float kMax = FMT == 1 ? 57344.0f : 448.0f;
-      unpack8(raw, f);
-      float amax = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(f[i]));
-      amax = row_max_nonneg<LPR>(amax);
-      const float d = block_scale(amax, kMax, 1.0f / kMax);
-      const BlockDivisor bd = make_divisor(amax, d);
-      float v[8];
-      divide_block(f, v, bd);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = fminf(fmaxf(v[i], -kMax), kMax);
-      u32x2 codes;
-      codes[0] = FMT == 1 ? pack4_e5m2(v[0], v[1], v[2], v[3]) : pack4_e4m3(v[0], v[1], v[2], v[3]);
-      codes[1] = FMT == 1 ? pack4_e5m2(v[4], v[5], v[6], v[7]) : pack4_e4m3(v[4], v[5], v[6], v[7]);
-      const int64_t page = sl >> a.page_shift;
-      const int64_t in_page = ((int64_t)h << a.page_shift) + (sl & ((1 << a.page_shift) - 1));
-      uint8_t* cp = (kind == 1 ? a.k_codes : a.v_codes) + page * a.page_stride;
-      float* sp = (kind == 1 ? a.k_scales : a.v_scales) + page * a.scale_page_stride;
-      if (on) *reinterpret_cast<u32x2*>(cp + in_page * a.D + e0) = codes;
-      if (lane == 0) sp[in_page] = d;
+      float d;
+      const u32x2 codes = quantise_row<LPR, FMT>(raw, d);
+      const uint32_t page = (uint32_t)(sl >> a.page_shift);
+      const uint32_t in_page = ((uint32_t)h << a.page_shift) + ((uint32_t)sl & ((1u << a.page_shift) - 1));
+      const int64_t cp = (rr < v0 ? address(a.k_codes) : address(a.v_codes)) +
+                         (int64_t)((uint64_t)page * a.page_stride + in_page * (uint32_t)a.D);
+      const int64_t sp = (rr < v0 ? address(a.k_scales) : address(a.v_scales)) +
+                         4 * (int64_t)((uint64_t)page * a.scale_page_stride + in_page);
+      if (on) store((global_ptr<u32x2>)(cp + e0), codes, a.stream);
+      if (lane == 0) *(global_ptr<float>)sp = d;
     }
     if (last) return;
   }
@@ -231,6 +304,7 @@ int launch_qkv(const Rows& q, const Rows& k, const Rows& v, int64_t T, int D, co
   a.v = v;
   a.T = T;
   a.D = D;
+  a.inv_D = 1.0f / (float)D;
   int kind = 0;
   if (rope) {
     a.q_weight = static_cast<const uint16_t*>(rope->q_weight);
@@ -254,8 +328,8 @@ int launch_qkv(const Rows& q, const Rows& k, const Rows& v, int64_t T, int D, co
     a.v_codes = cache->v_codes;
     a.k_scales = cache->k_scales;
     a.v_scales = cache->v_scales;
-    a.page_stride = cache->page_stride;
-    a.scale_page_stride = cache->scale_page_stride;
+    a.page_stride = (uint32_t)cache->page_stride;
+    a.scale_page_stride = (uint32_t)cache->scale_page_stride;
     a.total_slots = cache->pages * cache->page_size;
     a.page_shift = __builtin_ctzll((unsigned long long)cache->page_size);
   }
@@ -270,10 +344,11 @@ int launch_qkv(const Rows& q, const Rows& k, const Rows& v, int64_t T, int D, co
   int64_t gx = (T + tokens - 1) / tokens, gy = 1;
   a.items = turns;
   a.token_items = 1;
+  a.stream = gx >= kManyWgs;
   if (gx < kManyWgs) {  // few tokens: every row a slot of its own
     gy = turns;
     a.items = 1;
-  } else if (turns == 1 && kind == 0) {
+  } else if (turns == 1 && kind == 0 && q.heads == 0) {
     a.items = a.token_items = kTokenItems;
     gx = (T + (int64_t)tokens * kTokenItems - 1) / (tokens * kTokenItems);
   }
@@ -316,23 +391,26 @@ struct ReadArgs {
   int slot_shift;  // log2 of the threads that share a row
 };
 
-constexpr int kReadRows = 16;  // rows per workgroup
+constexpr int kReadTurns = 2;       // rows a thread group takes, all loaded before any is put out
+constexpr int kMaxReadRows = 512;   // of a workgroup: kReadTurns * 256
 
-// 16 rows per workgroup, K and V in blockIdx.y.  The first 16 threads look up
-// each row's sequence (binary search over offsets) and page and leave them in
-// LDS; then 2^slot_shift threads share a row, 16 codes each per turn (one
-// 16-byte load, two 16-byte stores).  HBM-bound: 1 byte in, 2 out.
+// 2^slot_shift threads share a row, 16 codes each (one 16-byte load, two
+// 16-byte stores), so a workgroup takes kReadTurns * 256 / 2^slot_shift rows; K and V in
+// blockIdx.y.  Its threads first look up each row's sequence (binary search
+// over offsets) and page and leave them in LDS.  HBM-bound: 1 byte in, 2 out.
+// Rows and pieces that do not exist are read at valid addresses and not put
+// out, so that no branch comes between the loads.
 template <int FMT>
 __global__ __launch_bounds__(256) void cache_read_kernel(const ReadArgs a) {
-  __shared__ int64_t where_page[kReadRows];
-  __shared__ int where_place[kReadRows];
+  __shared__ int row_page[kMaxReadRows];  // -1: no such row
+  __shared__ int row_place[kMaxReadRows];
   const int tid = threadIdx.x;
-  const int64_t row0 = (int64_t)blockIdx.x * kReadRows;
+  const int share = 1 << a.slot_shift, groups = 256 >> a.slot_shift, rows = kReadTurns * groups;
+  const int64_t row0 = (int64_t)blockIdx.x * rows;
   const bool is_v = blockIdx.y != 0;
-  if (tid < kReadRows) {
-    const int64_t row = row0 + tid;
-    int64_t page = -1;
-    int place = 0;
+  for (int x = tid; x < rows; x += 256) {
+    const int64_t row = row0 + x;
+    int page = -1, place = 0;
     if (row < a.R && row < a.offsets[a.B]) {
       int64_t lo = 0, hi = a.B;  // offsets[lo] <= row < offsets[hi]
       while (hi - lo > 1) {
@@ -343,52 +421,60 @@ __global__ __launch_bounds__(256) void cache_read_kernel(const ReadArgs a) {
       const int64_t tok = max(row - (int64_t)a.offsets[lo], (int64_t)0);
       const int64_t col = min(tok >> a.page_shift, a.cols - 1);
       page = a.table[lo * a.ld_table + col];
-      page = page < 0 ? 0 : (page >= a.pages ? a.pages - 1 : page);
+      page = page < 0 ? 0 : (page >= a.pages ? (int)a.pages - 1 : page);
       place = (int)(tok & ((1 << a.page_shift) - 1));
     }
-    where_page[tid] = page;
-    where_place[tid] = place;
+    row_page[x] = page;
+    row_place[x] = place;
   }
   __syncthreads();
   const uint8_t* codes = is_v ? a.v_codes : a.k_codes;
   const float* scales = is_v ? a.v_scales : a.k_scales;
-  uint16_t* out = is_v ? a.v_out : a.k_out;
+  uint16_t* out = (is_v ? a.v_out : a.k_out) + row0 * a.heads * a.D;
   const int per_head = a.D / 16;
   const int pieces = a.heads * per_head;
-  const int share = 1 << a.slot_shift;
-  const int groups = 256 >> a.slot_shift;
-  for (int rr = tid >> a.slot_shift; rr < kReadRows; rr += groups) {
-    const int64_t page = where_page[rr];
-    if (page < 0) continue;
-    const int place = where_place[rr];
-    uint16_t* dst = out + (row0 + rr) * (int64_t)a.heads * a.D;
-    for (int p = tid & (share - 1); p < pieces; p += share) {
-      const int h = a.inv ? (int)__umulhi((uint32_t)p, a.inv) : p;
-      const int c = p - h * per_head;
-      const int64_t in_page = ((int64_t)h << a.page_shift) + place;
-      const u32x4 raw =
-          __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(codes + page * a.page_stride + in_page * a.D + 16 * c));
-      const float d = scales[page * a.scale_page_stride + in_page];
+  const int grp = tid >> a.slot_shift;
+  for (int p0 = tid & (share - 1); p0 < ((pieces + share - 1) & ~(share - 1)); p0 += share) {
+    const int p = min(p0, pieces - 1);
+    const int h = a.inv ? (int)__umulhi((uint32_t)p, a.inv) : p;
+    const int c = p - h * per_head;
+    u32x4 raw[kReadTurns];
+    float d[kReadTurns];
+    bool ok[kReadTurns];
+#pragma unroll
+    for (int u = 0; u < kReadTurns; ++u) {
+      const int x = grp + u * groups;
+      ok[u] = row_page[x] >= 0 && p0 < pieces;
+      const int64_t page = max(row_page[x], 0);
+      const int in_page = (h << a.page_shift) + row_place[x];
+      raw[u] = __builtin_nontemporal_load(
+          reinterpret_cast<const u32x4*>(codes + (page * a.page_stride + (int64_t)in_page * a.D + 16 * c)));
+      d[u] = scales[page * a.scale_page_stride + in_page];
+    }
+#pragma unroll
+    for (int u = 0; u < kReadTurns; ++u) {
       u32x4 o[2];
       typedef float f2 __attribute__((ext_vector_type(2)));
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         f2 lo, hi;
         if (FMT == 1) {
-          lo = __builtin_amdgcn_cvt_scalef32_pk_f32_bf8((int)raw[i], 1.0f, false);
-          hi = __builtin_amdgcn_cvt_scalef32_pk_f32_bf8((int)raw[i], 1.0f, true);
+          lo = __builtin_amdgcn_cvt_scalef32_pk_f32_bf8((int)raw[u][i], 1.0f, false);
+          hi = __builtin_amdgcn_cvt_scalef32_pk_f32_bf8((int)raw[u][i], 1.0f, true);
         } else {
-          lo = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8((int)raw[i], 1.0f, false);
-          hi = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8((int)raw[i], 1.0f, true);
+          lo = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8((int)raw[u][i], 1.0f, false);
+          hi = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8((int)raw[u][i], 1.0f, true);
         }
-        const bf16x2 b0 = {(__bf16)(lo[0] * d), (__bf16)(lo[1] * d)};
-        const bf16x2 b1 = {(__bf16)(hi[0] * d), (__bf16)(hi[1] * d)};
+        const bf16x2 b0 = {(__bf16)(lo[0] * d[u]), (__bf16)(lo[1] * d[u])};
+        const bf16x2 b1 = {(__bf16)(hi[0] * d[u]), (__bf16)(hi[1] * d[u])};
         o[i >> 1][2 * (i & 1)] = __builtin_bit_cast(uint32_t, b0);
         o[i >> 1][2 * (i & 1) + 1] = __builtin_bit_cast(uint32_t, b1);
       }
-      u32x4* d4 = reinterpret_cast<u32x4*>(dst + 16 * p);
-      __builtin_nontemporal_store(o[0], d4);
-      __builtin_nontemporal_store(o[1], d4 + 1);
+      if (ok[u]) {
+        u32x4* q = reinterpret_cast<u32x4*>(out + (int64_t)(grp + u * groups) * a.heads * a.D + 16 * p);
+        __builtin_nontemporal_store(o[0], q);
+        __builtin_nontemporal_store(o[1], q + 1);
+      }
     }
   }
 }
@@ -422,7 +508,8 @@ int launch_cache_read(const fp8b_kv_cache& c, const int32_t* table, int64_t ld_t
   int shift = 0;
   while ((1 << shift) < pieces && shift < 8) ++shift;
   a.slot_shift = shift;
-  const dim3 grid((unsigned)((R + kReadRows - 1) / kReadRows), 2);
+  const int64_t rows = kReadTurns * (256 >> shift);
+  const dim3 grid((unsigned)((R + rows - 1) / rows), 2);
   if (c.fmt == FP8B_FMT_E5M2) hipLaunchKernelGGL(cache_read_kernel<1>, grid, dim3(256), 0, s, a);
   else hipLaunchKernelGGL(cache_read_kernel<2>, grid, dim3(256), 0, s, a);
   return check_launch();
