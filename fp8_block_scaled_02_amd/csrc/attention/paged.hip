@@ -49,7 +49,9 @@ struct AttnArgs {
   const float *k_scales, *v_scales;
   uint32_t page_stride, scale_page_stride;
   int pages, page_shift, heads, D;
-  int G, qtiles;  // query heads per KV head, and how many 16-row tiles they take
+  // query heads per KV head; how many of them a region takes (16 or 32, the
+  // last one of a KV head fewer), how many regions they make, most rows of one
+  int G, qrows, qtiles, rows_max;
   const int32_t* table;
   int64_t ld_table;
   const int32_t* lens;
@@ -246,15 +248,17 @@ struct State {
   v4f o[DP / 16];
 };
 
-// s = K Q^T with scales, log2 domain.
-template <int DP, bool FULL, int FMT>
-__device__ __forceinline__ void scores(const AttnArgs& a, const bf16x8 (&qf)[DP / 32], const KeyRegs<DP>& k,
-                                       float (&s)[8]) {
+// s = K Q^T with scales, log2 domain, for QT tiles of 16 query heads.
+template <int DP, bool FULL, int FMT, int QT>
+__device__ __forceinline__ void scores(const AttnArgs& a, const bf16x8 (&qf)[QT][DP / 32], const KeyRegs<DP>& k,
+                                       float (&s)[QT][8]) {
   const int g = (threadIdx.x & 63) >> 4;
   typedef uint32_t frag __attribute__((ext_vector_type(4)));
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
-    v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    v4f acc[QT];
+#pragma unroll
+    for (int q = 0; q < QT; ++q) acc[q] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int c = 0; c < DP / 64; ++c) {
       u32x4 w = k.c[u][c];
@@ -263,11 +267,18 @@ __device__ __forceinline__ void scores(const AttnArgs& a, const bf16x8 (&qf)[DP 
       for (int x = 0; x < 2; ++x) {
         const frag kf = {widen2<FMT, false>(w[2 * x]), widen2<FMT, true>(w[2 * x]), widen2<FMT, false>(w[2 * x + 1]),
                          widen2<FMT, true>(w[2 * x + 1])};
-        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, kf), qf[2 * c + x], acc, 0, 0, 0);
+#pragma unroll
+        for (int q = 0; q < QT; ++q)
+          acc[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, kf), qf[q][2 * c + x], acc[q],
+                                                           0, 0, 0);
       }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s[4 * u + i] = acc[i] * (k.s[u][i] * a.scale_log2e);
+    for (int i = 0; i < 4; ++i) {
+      const float ks = k.s[u][i] * a.scale_log2e;
+#pragma unroll
+      for (int q = 0; q < QT; ++q) s[q][4 * u + i] = acc[q][i] * ks;
+    }
   }
 }
 
@@ -299,20 +310,22 @@ __device__ __forceinline__ void weights(float (&s)[8], State<DP>& st) {
 }
 
 // O += P V, p the weights times the V scales.
-template <int DP, int FMT, int TERMS>
-__device__ __forceinline__ void accumulate(float (&p)[8], const ValueRegs<DP>& v, State<DP>& st) {
+template <int DP, int FMT, int TERMS, int QT>
+__device__ __forceinline__ void accumulate(float (&p)[QT][8], const ValueRegs<DP>& v, State<DP> (&st)[QT]) {
   typedef uint32_t frag __attribute__((ext_vector_type(4)));
   // p = sum of TERMS bf16 terms, each the rounded rest of those before
-  frag pf[TERMS];
+  frag pf[QT][TERMS];
 #pragma unroll
-  for (int t = 0; t < TERMS; ++t)
+  for (int q = 0; q < QT; ++q)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const bf16x2 b = {(__bf16)p[2 * i], (__bf16)p[2 * i + 1]};
-      pf[t][i] = __builtin_bit_cast(uint32_t, b);
-      p[2 * i] -= __uint_as_float(pf[t][i] << 16);
-      p[2 * i + 1] -= __uint_as_float(pf[t][i] & 0xffff0000u);
-    }
+    for (int t = 0; t < TERMS; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const bf16x2 b = {(__bf16)p[q][2 * i], (__bf16)p[q][2 * i + 1]};
+        pf[q][t][i] = __builtin_bit_cast(uint32_t, b);
+        p[q][2 * i] -= __uint_as_float(pf[q][t][i] << 16);
+        p[q][2 * i + 1] -= __uint_as_float(pf[q][t][i] & 0xffff0000u);
+      }
 #pragma unroll
   for (int w = 0; w < DP / 64; ++w) {
     // keys (0, 1) and (2, 3) of each half paired byte by byte
@@ -335,9 +348,11 @@ __device__ __forceinline__ void accumulate(float (&p)[8], const ValueRegs<DP>& v
           vf[2 * u + y] = (b & 1) ? widen2<FMT, true>(pr[u][y][b >> 1]) : widen2<FMT, false>(pr[u][y][b >> 1]);
       const int j = 4 * w + b;
 #pragma unroll
-      for (int t = 0; t < TERMS; ++t)
-        st.o[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, vf),
-                                                         __builtin_bit_cast(bf16x8, pf[t]), st.o[j], 0, 0, 0);
+      for (int q = 0; q < QT; ++q)
+#pragma unroll
+        for (int t = 0; t < TERMS; ++t)
+          st[q].o[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+              __builtin_bit_cast(bf16x8, vf), __builtin_bit_cast(bf16x8, pf[q][t]), st[q].o[j], 0, 0, 0);
     }
   }
 }
@@ -349,9 +364,9 @@ __device__ __forceinline__ void accumulate(float (&p)[8], const ValueRegs<DP>& v
 // The page of each half tile is looked up 32 tiles ahead, one per lane.  Past
 // the last token a half may lie anywhere in the cache (ids are clamped): what
 // is read there is masked.
-template <int DP, bool FULL, int FMT, int TERMS>
+template <int DP, bool FULL, int FMT, int TERMS, int QT>
 __device__ __forceinline__ void run_tiles(const AttnArgs& a, const Span& sp, int b, int h,
-                                          const bf16x8 (&qf)[DP / 32], int t, int end, State<DP>& st) {
+                                          const bf16x8 (&qf)[QT][DP / 32], int t, int end, State<DP> (&st)[QT]) {
   const int lane = threadIdx.x & 63, g = lane >> 4;
   const int ws = a.waves_shift;
   const int32_t* row = a.table + b * a.ld_table;
@@ -387,8 +402,8 @@ __device__ __forceinline__ void run_tiles(const AttnArgs& a, const Span& sp, int
   // branch around them would make every wait inside the turn wait for all.
   auto turn = [&](auto more) {
     constexpr bool MORE = decltype(more)::value;
-    float s[8];
-    scores<DP, FULL, FMT>(a, qf, k, s);
+    float s[QT][8];
+    scores<DP, FULL, FMT, QT>(a, qf, k, s);
     if (MORE) {
       locate(t + (1 << ws));
       load_keys<DP, FULL>(a, at, hf, k);
@@ -402,16 +417,20 @@ __device__ __forceinline__ void run_tiles(const AttnArgs& a, const Span& sp, int
         for (int i = 0; i < 4; ++i) {
           const int j = first + 16 * u + 4 * g + i;
           const bool seen = j >= sp.lo && j < sp.n;
-          s[4 * u + i] = seen ? s[4 * u + i] : -__builtin_inff();
+#pragma unroll
+          for (int q = 0; q < QT; ++q) s[q][4 * u + i] = seen ? s[q][4 * u + i] : -__builtin_inff();
           v.s[u][i] = seen ? v.s[u][i] : 0.0f;
 #pragma unroll
           for (int w = 0; w < DP / 64; ++w) v.c[u][i][w] = seen ? v.c[u][i][w] : 0u;
         }
     }
-    weights<DP>(s, st);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s[i] *= v.s[i >> 2][i & 3];
-    accumulate<DP, FMT, TERMS>(s, v, st);
+    for (int q = 0; q < QT; ++q) {
+      weights<DP>(s[q], st[q]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[q][i] *= v.s[i >> 2][i & 3];
+    }
+    accumulate<DP, FMT, TERMS, QT>(s, v, st);
     if (MORE) load_values<DP, FULL>(a, at, hf, v);
   };
 
@@ -428,17 +447,17 @@ __device__ __forceinline__ void run_tiles(const AttnArgs& a, const Span& sp, int
 // are joined in LDS; a region that lies whole in the piece is put out, others
 // go to the workspace: slot 2w for the region the piece begins in, slot 2w+1
 // for the one it ends in.
-template <int DP, bool FULL, int FMT, int TERMS>
+template <int DP, bool FULL, int FMT, int TERMS, int QT>
 __global__ __launch_bounds__(64 * kMaxWaves) void attend_kernel(const AttnArgs a) {
   extern __shared__ float lds[];
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   const int g = lane >> 4, c = lane & 15;
   const int R = a.heads * a.qtiles;
-  const int rows_max = a.G < 16 ? a.G : 16;
+  const int rows_max = a.rows_max;
   constexpr int LD = DP + 4;
   const int waves = 1 << a.waves_shift;
-  float* lds_m = lds + waves * rows_max * LD;  // [wave][16]
-  float* lds_l = lds_m + waves * 16;
+  float* lds_m = lds + waves * rows_max * LD;  // [wave][row]
+  float* lds_l = lds_m + waves * rows_max;
 
   int b, region, tile, left;  // left: tiles of this piece still to do
   Span sp;
@@ -462,39 +481,50 @@ __global__ __launch_bounds__(64 * kMaxWaves) void attend_kernel(const AttnArgs a
   for (;;) {
     const int count = min(sp.tiles - tile, left);
     const int h = a.qtiles == 1 ? region : region / a.qtiles, qt = region - h * a.qtiles;
-    const int rows = min(16, a.G - 16 * qt);
-    const int head0 = h * a.G + 16 * qt;
-    State<DP> st;
-    st.m = -__builtin_inff();
-    st.l = 0.0f;
+    const int rows = min(16 * QT, a.G - 16 * QT * qt);
+    const int head0 = h * a.G + 16 * QT * qt;
+    State<DP> st[QT];
 #pragma unroll
-    for (int j = 0; j < DP / 16; ++j) st.o[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int q = 0; q < QT; ++q) {
+      st[q].m = -__builtin_inff();
+      st[q].l = 0.0f;
+#pragma unroll
+      for (int j = 0; j < DP / 16; ++j) st[q].o[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    }
     if (sp.n > 0) {
-      bf16x8 qf[DP / 32];
-      const uint16_t* qp = a.q + b * a.q_b + (int64_t)(head0 + c) * a.q_h;
+      bf16x8 qf[QT][DP / 32];
 #pragma unroll
-      for (int j = 0; j < DP / 32; ++j) {
-        const int d = 64 * (j >> 1) + 16 * g + 8 * (j & 1);
-        u32x4 w = {0, 0, 0, 0};
-        if (c < rows && (FULL || d < a.D)) w = *reinterpret_cast<const u32x4*>(qp + d);
-        qf[j] = __builtin_bit_cast(bf16x8, w);
+      for (int q = 0; q < QT; ++q) {
+        const uint16_t* qp = a.q + b * a.q_b + (int64_t)(head0 + 16 * q + c) * a.q_h;
+#pragma unroll
+        for (int j = 0; j < DP / 32; ++j) {
+          const int d = 64 * (j >> 1) + 16 * g + 8 * (j & 1);
+          u32x4 w = {0, 0, 0, 0};
+          if (16 * q + c < rows && (FULL || d < a.D)) w = *reinterpret_cast<const u32x4*>(qp + d);
+          qf[q][j] = __builtin_bit_cast(bf16x8, w);
+        }
       }
-      run_tiles<DP, FULL, FMT, TERMS>(a, sp, b, h, qf, tile + wave, tile + count, st);
+      run_tiles<DP, FULL, FMT, TERMS, QT>(a, sp, b, h, qf, tile + wave, tile + count, st);
     }
-    st.l += __shfl_xor(st.l, 16);
-    st.l += __shfl_xor(st.l, 32);
-    if (c < rows) {
-      float* o = lds + (wave * rows_max + c) * LD;
 #pragma unroll
-      for (int j = 0; j < DP / 16; j += 4)
+    for (int q = 0; q < QT; ++q) {
+      float l = st[q].l;
+      l += __shfl_xor(l, 16);
+      l += __shfl_xor(l, 32);
+      if (16 * q + c < rows) {
+        const int at = wave * rows_max + 16 * q + c;
+        float* o = lds + at * LD;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          *reinterpret_cast<v4f*>(o + (DP / 16) * (4 * g + i) + j) =
-              v4f{st.o[j][i], st.o[j + 1][i], st.o[j + 2][i], st.o[j + 3][i]};
-    }
-    if (g == 0) {
-      lds_m[wave * 16 + c] = st.m;
-      lds_l[wave * 16 + c] = st.l;
+        for (int j = 0; j < DP / 16; j += 4)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<v4f*>(o + (DP / 16) * (4 * g + i) + j) =
+                v4f{st[q].o[j][i], st[q].o[j + 1][i], st[q].o[j + 2][i], st[q].o[j + 3][i]};
+        if (g == 0) {
+          lds_m[at] = st[q].m;
+          lds_l[at] = l;
+        }
+      }
     }
     __syncthreads();
     const bool whole = count == sp.tiles;
@@ -504,13 +534,13 @@ __global__ __launch_bounds__(64 * kMaxWaves) void attend_kernel(const AttnArgs a
     for (int x = tid; x < rows * q4; x += 64 << a.waves_shift) {
       const int rr = x / q4, d = 4 * (x - rr * q4);
       float m = lds_m[rr];
-      for (int w = 1; w < waves; ++w) m = fmaxf(m, lds_m[w * 16 + rr]);
+      for (int w = 1; w < waves; ++w) m = fmaxf(m, lds_m[w * rows_max + rr]);
       const float ms = m == -__builtin_inff() ? 0.0f : m;
       float l = 0.0f;
       v4f o = {0.0f, 0.0f, 0.0f, 0.0f};
       for (int w = 0; w < waves; ++w) {
-        const float f = __builtin_amdgcn_exp2f(lds_m[w * 16 + rr] - ms);
-        l = __builtin_fmaf(f, lds_l[w * 16 + rr], l);
+        const float f = __builtin_amdgcn_exp2f(lds_m[w * rows_max + rr] - ms);
+        l = __builtin_fmaf(f, lds_l[w * rows_max + rr], l);
         const v4f ow = *reinterpret_cast<const v4f*>(lds + (w * rows_max + rr) * LD + d);
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[i] = __builtin_fmaf(f, ow[i], o[i]);
@@ -558,7 +588,7 @@ __global__ __launch_bounds__(256) void join_kernel(const AttnArgs a, int wgs, in
   const int R = a.heads * a.qtiles;
   const int b = blockIdx.x / R, region = blockIdx.x - b * R;
   const int h = a.qtiles == 1 ? region : region / a.qtiles, qt = region - h * a.qtiles;
-  const int rows = min(16, a.G - 16 * qt), rows_max = a.G < 16 ? a.G : 16;
+  const int rows = min(a.qrows, a.G - a.qrows * qt), rows_max = a.rows_max;
   const Line ln = line_of<false>(a, wgs, b);
   const int t0 = ln.begin + region * ln.span.tiles, t1 = t0 + ln.span.tiles;
   const int w0 = t0 / ln.per, w1 = (t1 - 1) / ln.per;
@@ -610,7 +640,7 @@ __global__ __launch_bounds__(256) void join_kernel(const AttnArgs a, int wgs, in
     }
   }
   if (!on) return;
-  const int64_t at = (int64_t)b * a.Hq + h * a.G + 16 * qt + rr;
+  const int64_t at = (int64_t)b * a.Hq + h * a.G + a.qrows * qt + rr;
   const float inv = l > 0.0f ? 1.0f / l : 0.0f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) o[i] *= inv;
@@ -627,7 +657,7 @@ __global__ __launch_bounds__(256) void join_kernel(const AttnArgs a, int wgs, in
 // ---- host -------------------------------------------------------------------
 
 struct Shape {
-  int G, qtiles, rows;
+  int G, qrows, qtiles, rows;
   int64_t regions, max_len, wgs;  // wgs: workgroups of a split launch; 0: one workgroup per region
   int waves_shift;
 };
@@ -636,8 +666,11 @@ static Shape shape_of(const fp8b_kv_cache& c, int64_t B, int64_t Hq, int64_t col
                       int64_t window) {
   Shape s;
   s.G = (int)(Hq / c.heads);
-  s.qtiles = (s.G + 15) / 16;
-  s.rows = s.G < 16 ? s.G : 16;
+  // more than 16 heads: two query tiles to a wave, so K and V are read and
+  // widened once for both; up to 128 positions, where the registers allow it
+  s.qrows = s.G > 16 && c.head_dim <= 128 ? 32 : 16;
+  s.qtiles = (s.G + s.qrows - 1) / s.qrows;
+  s.rows = s.G < s.qrows ? s.G : s.qrows;
   s.regions = B * c.heads * s.qtiles;
   const int64_t room = cols * c.page_size;
   s.max_len = max_context < room ? max_context : room;
@@ -665,19 +698,23 @@ int64_t attention_workspace(const fp8b_kv_cache& c, int64_t B, int64_t Hq, int64
   return 2 * s.wgs * partial_floats(s.rows, (int)c.head_dim) * (int64_t)sizeof(float);
 }
 
-template <int DP, bool FULL, int FMT, int TERMS>
+template <int DP, bool FULL, int FMT, int TERMS, int QT>
 static int launch_one(const AttnArgs& a, unsigned grid, hipStream_t s) {
-  const int rows = a.G < 16 ? a.G : 16;
   const int waves = 1 << a.waves_shift;
-  const size_t lds = (size_t)(waves * rows * (DP + 4) + 2 * waves * 16) * sizeof(float);
-  hipLaunchKernelGGL((attend_kernel<DP, FULL, FMT, TERMS>), dim3(grid), dim3(64 * waves), lds, s, a);
+  const size_t lds = (size_t)waves * a.rows_max * (DP + 4 + 2) * sizeof(float);
+  hipLaunchKernelGGL((attend_kernel<DP, FULL, FMT, TERMS, QT>), dim3(grid), dim3(64 * waves), lds, s, a);
   return check_launch();
+}
+template <int DP, bool FULL, int QT>
+static int launch_fmt(const AttnArgs& a, int fmt, unsigned grid, hipStream_t s) {
+  if (fmt == FP8B_FMT_E5M2)
+    return a.out_f32 ? launch_one<DP, FULL, 1, 3, QT>(a, grid, s) : launch_one<DP, FULL, 1, 2, QT>(a, grid, s);
+  return a.out_f32 ? launch_one<DP, FULL, 2, 3, QT>(a, grid, s) : launch_one<DP, FULL, 2, 2, QT>(a, grid, s);
 }
 template <int DP, bool FULL>
 static int launch_dp(const AttnArgs& a, int fmt, unsigned grid, hipStream_t s) {
-  if (fmt == FP8B_FMT_E5M2)
-    return a.out_f32 ? launch_one<DP, FULL, 1, 3>(a, grid, s) : launch_one<DP, FULL, 1, 2>(a, grid, s);
-  return a.out_f32 ? launch_one<DP, FULL, 2, 3>(a, grid, s) : launch_one<DP, FULL, 2, 2>(a, grid, s);
+  if (DP <= 128 && a.qrows == 32) return launch_fmt<DP, FULL, DP <= 128 ? 2 : 1>(a, fmt, grid, s);
+  return launch_fmt<DP, FULL, 1>(a, fmt, grid, s);
 }
 
 int launch_attention(const fp8b_kv_cache& c, const Attention& p, hipStream_t s) {
@@ -697,7 +734,9 @@ int launch_attention(const fp8b_kv_cache& c, const Attention& p, hipStream_t s) 
   a.heads = (int)c.heads;
   a.D = (int)c.head_dim;
   a.G = sh.G;
+  a.qrows = sh.qrows;
   a.qtiles = sh.qtiles;
+  a.rows_max = sh.rows;
   a.table = p.table;
   a.ld_table = p.ld_table;
   a.lens = p.lens;

@@ -339,17 +339,19 @@ def test_attention_head_dims(F, D, fmt, out_dtype):
     _check_attention(F, c, lens, q, table, out_dtype=out_dtype, max_context=256)     # not split
 
 
-@pytest.mark.parametrize("Hq,H", [(1, 1), (7, 1), (16, 1), (17, 1), (40, 1), (5, 5), (28, 4), (24, 8), (32, 16),
-                                  (96, 2)])
-def test_attention_head_layouts(F, Hq, H):
+@pytest.mark.parametrize("Hq,H,D", [(1, 1, 64), (7, 1, 64), (16, 1, 64), (17, 1, 64), (40, 1, 64), (5, 5, 64),
+                                    (28, 4, 64), (24, 8, 64), (32, 16, 64), (96, 2, 64), (32, 1, 128), (33, 1, 128),
+                                    (71, 1, 128), (24, 1, 80), (20, 1, 48), (16, 1, 256), (40, 2, 256), (34, 2, 192)])
+def test_attention_head_layouts(F, Hq, H, D):
     g = W.gen(Hq, DEV)
     lens = [100, 513, 3]
     pages, table = _book(lens, 32, g)
-    c = _filled(F, pages, H, 32, 64, "e5m2", g)
-    wide = torch.randn(3, Hq + 1, 80, generator=g, device=DEV).bfloat16()
-    q = wide[:, 1:, 8:72]                                                # strided
+    c = _filled(F, pages, H, 32, D, "e5m2", g)
+    wide = torch.randn(3, Hq + 1, D + 16, generator=g, device=DEV).bfloat16()
+    q = wide[:, 1:, 8:D + 8]                                             # strided
     _check_attention(F, c, lens, q, table)
-    _check_attention(F, c, lens, q, table, max_context=200, out_dtype=torch.float32)
+    _check_attention(F, c, lens, q, table, max_context=600, out_dtype=torch.float32)
+    _check_attention(F, c, lens, q, table, max_context=4000)             # 8 waves: the most shared memory
 
 
 @pytest.mark.parametrize("S", [16, 32, 64, 256, 4096])
