@@ -38,7 +38,6 @@ using namespace fp8blk;
 constexpr int kTile = 32;       // keys a wave takes at a time
 constexpr int kSplitShift = 2;  // log2 of the waves of a workgroup of a split launch
 constexpr int kMaxWaves = 8;    // and of any
-constexpr int kDirectTiles = 128;
 constexpr int kMaxWgs = 512;    // workgroups of a split launch: 2 for each of the 256 CUs
 constexpr int kMinTiles = 8;    // tiles (all waves together) a workgroup of a split launch takes at least
 
@@ -677,18 +676,32 @@ static Shape shape_of(const fp8b_kv_cache& c, int64_t B, int64_t Hq, int64_t col
   // the most tiles a region can have: a window reaches into one more
   const int64_t seen = window > 0 && window < s.max_len ? window + kTile - 1 : s.max_len;
   const int64_t tiles = (seen + kTile - 1) / kTile;
-  if (tiles <= kDirectTiles) {
+  // A CU works through a tile of each SIMD in about 0.85 us (128 positions),
+  // so one workgroup per region takes 4 + 0.21 tiles us, whatever its waves;
+  // splitting evens that out over the 256 CUs for about 5 us of a second
+  // launch.  Measured, direct / split us, 128 positions, up to 1.5 times as
+  // many tiles as on average: 8 regions of 32 tiles 10.2 / 9.4, of 63 16.3 /
+  // 12.1, of 125 28 / 12.5; 32 of 46 12.4 / 12.4; 128 of 46 14.5 / 17.3, of 121
+  // 29 / 24; 512 of 28 19 / 25, of 121 78 / 79, of 281 166 / 159.
+  const int64_t direct = s.regions / 2 < 32 ? 32 : (s.regions / 2 < 128 ? s.regions / 2 : 128);
+  if (tiles <= direct) {
+    // As many waves as there are tiles, up to 8; fewer where that leaves each
+    // only a few tiles and there are regions enough for 12 waves a CU without
+    // (2048 regions of 5 tiles: 1 / 2 / 4 / 8 waves 14.2 / 15.2 / 18 / 30 us;
+    // 272 of 33 tiles of 64 positions: 27 / 16 / 11.2 / 9.9).
     s.wgs = 0;
     s.waves_shift = 3;
     while (s.waves_shift > 0 && ((1 << s.waves_shift) > tiles ||
                                  ((4 << s.waves_shift) > tiles && (s.regions << s.waves_shift) > 12 * 256)))
       --s.waves_shift;
   } else {
+    // Two workgroups of four waves a CU: with 4 (1024 workgroups) a third of
+    // them waits for room (131072 tokens x 8 heads 68 -> 59 us, 128 x 6000 x 8
+    // 350 -> 314 us); a piece of fewer than 8 tiles costs more to join.
     s.waves_shift = kSplitShift;
     const int64_t want = (s.regions * tiles + kMinTiles - 1) / kMinTiles;
     s.wgs = want < kMaxWgs ? want : kMaxWgs;
   }
-  // TUNE
   return s;
 }
 
