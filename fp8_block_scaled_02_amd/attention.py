@@ -65,16 +65,21 @@ def attn_lib():
     return _attn_lib
 
 
+_bf16, _f32, _i32, _i64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
+_contiguous = torch.contiguous_format
+_current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
+
 def _call(fn, dev, *args):
     """One C call on the current stream of GPU `dev`, which is made current
     for it: a default stream is NULL, which means the current device's."""
     f = getattr(_attn_lib or attn_lib(), fn)
-    if dev == torch._C._cuda_getDevice():
-        rc = f(*args, torch._C._cuda_getCurrentRawStream(dev))
+    if dev == _current_device():
+        rc = f(*args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
-            rc = f(*args, torch._C._cuda_getCurrentRawStream(dev))
-    if rc != 0:
+            rc = f(*args, _raw_stream(dev))
+    if rc:
         raise Fp8Error(fn, rc)
 
 
@@ -95,17 +100,19 @@ def _on(dev, *ts):
 def _rows(t, name):
     """(address, token stride, head stride) of bf16 [tokens, heads, D]; the
     stride of a dimension of one entry means nothing and is put in order."""
-    if t.dtype != torch.bfloat16 or t.dim() != 3 or (t.stride(2) != 1 and t.shape[2] != 1):
+    if t.dtype is not _bf16 or t.ndim != 3:
         raise ValueError(f"{name} must be 3-D bf16 [tokens, heads, head_dim], head rows contiguous")
     T, H, D = t.shape
-    st, sh, _ = t.stride()
+    st, sh, sd = t.stride()
+    if sd != 1 and D != 1:
+        raise ValueError(f"{name} must be 3-D bf16 [tokens, heads, head_dim], head rows contiguous")
     if H <= 1:
         sh = D
     return t.data_ptr(), (st if T > 1 else sh * H), sh
 
 
 def _index(t, dtype, shape, name):
-    if t.dtype != dtype or not t.is_contiguous():
+    if t.dtype is not dtype or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous {dtype}")
     if t.shape != shape:
         _shape(t, shape, name)
@@ -115,6 +122,11 @@ def _out(t, shape, name):
     if t.shape != shape:
         _shape(t, shape, name)
     return t
+
+
+def _empty_like(t):
+    """An uninitialised contiguous tensor (half the host time of torch.empty)."""
+    return torch.empty_like(t, memory_format=_contiguous)
 
 
 class KVCache:
@@ -159,13 +171,19 @@ class KVCache:
             strides.append(t.stride(0) if P > 1 else t[0].numel())
         _need(strides[0] == strides[1] and strides[2] == strides[3], "K and V pages must lie equally far apart")
         _on(k_codes.get_device(), v_codes, k_scales, v_scales)
-        self.k_codes, self.v_codes, self.k_scales, self.v_scales = k_codes, v_codes, k_scales, v_scales
+        self._tensors = k_codes, v_codes, k_scales, v_scales
         self.pages, self.heads, self.page_size, self.head_dim, self.fmt = P, H, S, D, fmt
         self.device = k_codes.device
         self._dev = k_codes.get_device()
         self._struct = _CacheStruct(k_codes.data_ptr(), v_codes.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
                                     strides[0], strides[2], P, S, H, D, _CACHE_FMT[fmt], 0)
         self._ref = ctypes.addressof(self._struct)
+
+    # read-only: the addresses were taken when the cache was made
+    k_codes = property(lambda self: self._tensors[0])
+    v_codes = property(lambda self: self._tensors[1])
+    k_scales = property(lambda self: self._tensors[2])
+    v_scales = property(lambda self: self._tensors[3])
 
 
 def _rope(D, T, cos_sin, positions, q_weight, k_weight, eps, interleaved):
@@ -174,20 +192,20 @@ def _rope(D, T, cos_sin, positions, q_weight, k_weight, eps, interleaved):
     cs = pos = qw = kw = None
     n = rot = 0
     if cos_sin is not None:
-        if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
+        if cos_sin.dtype is not _f32 or cos_sin.ndim != 2 or not cos_sin.is_contiguous():
             raise ValueError("cos_sin must be contiguous float32 [max_pos, rot_dim]")
         n, rot = cos_sin.shape
         if not 16 <= rot <= D or rot % 16:
             raise ValueError(f"rot_dim must be a multiple of 16 from 16 to {D}")
         if n < 1:
             raise ValueError("cos_sin must hold at least one position")
-        _index(positions, torch.int64, (T,), "positions")
+        _index(positions, _i64, (T,), "positions")
         cs, pos = cos_sin.data_ptr(), positions.data_ptr()
     if q_weight is not None:
-        _index(q_weight, torch.bfloat16, (D,), "q_weight")
+        _index(q_weight, _bf16, (D,), "q_weight")
         qw = q_weight.data_ptr()
     if k_weight is not None:
-        _index(k_weight, torch.bfloat16, (D,), "k_weight")
+        _index(k_weight, _bf16, (D,), "k_weight")
         kw = k_weight.data_ptr()
     return _RopeStruct(qw, kw, cs, pos, n, rot, eps, bool(interleaved))
 
@@ -206,8 +224,8 @@ def fp8_qk_norm_rope(q, k, cos_sin=None, positions=None, q_weight=None, k_weight
     if Tk != T or Dk != D:
         raise ValueError(f"k must be [{T}, Hk, {D}]")
     r = _rope(D, T, cos_sin, positions, q_weight, k_weight, eps, interleaved)
-    q_out = torch.empty_like(q, memory_format=torch.contiguous_format) if q_out is None else _out(q_out, q.shape, "q_out")
-    k_out = torch.empty_like(k, memory_format=torch.contiguous_format) if k_out is None else _out(k_out, k.shape, "k_out")
+    q_out = _empty_like(q) if q_out is None else _out(q_out, q.shape, "q_out")
+    k_out = _empty_like(k) if k_out is None else _out(k_out, k.shape, "k_out")
     qo, ko = _rows(q_out, "q_out"), _rows(k_out, "k_out")
     dev = q.get_device()
     _on(dev, k, cos_sin, positions, q_weight, k_weight, q_out, k_out)
@@ -229,7 +247,7 @@ def fp8_kv_cache_write(k, v, slots, cache: KVCache):
     cache, such as -1, writes nothing.  Slots should differ: one named twice
     holds either token's row, or a mixture.  Returns the cache."""
     T, ka, va = _kv_rows(k, v, cache)
-    _index(slots, torch.int64, (T,), "slots")
+    _index(slots, _i64, (T,), "slots")
     _on(cache._dev, k, v, slots)
     _call("fp8_kv_cache_write", cache._dev, *ka, *va, slots.data_ptr(), T, cache._ref)
     return cache
@@ -246,8 +264,8 @@ def fp8_qkv_cache_write(q, k, v, cos_sin, positions, slots, cache: KVCache, q_we
     if Tq != T or D != cache.head_dim:
         raise ValueError(f"q must be [{T}, Hq, {cache.head_dim}]")
     r = _rope(D, T, cos_sin, positions, q_weight, k_weight, eps, interleaved)
-    _index(slots, torch.int64, (T,), "slots")
-    q_out = torch.empty_like(q, memory_format=torch.contiguous_format) if q_out is None else _out(q_out, q.shape, "q_out")
+    _index(slots, _i64, (T,), "slots")
+    q_out = _empty_like(q) if q_out is None else _out(q_out, q.shape, "q_out")
     qo = _rows(q_out, "q_out")
     _on(cache._dev, q, k, v, cos_sin, positions, slots, q_weight, k_weight, q_out)
     _call("fp8_qkv_cache_write", cache._dev, *qa, *ka, *va, slots.data_ptr(), T, Hq, ctypes.addressof(r), cache._ref,
@@ -256,11 +274,13 @@ def fp8_qkv_cache_write(q, k, v, cos_sin, positions, slots, cache: KVCache, q_we
 
 
 def _table(block_table):
-    if (block_table.dtype != torch.int32 or block_table.dim() != 2 or
-            (block_table.stride(1) != 1 and block_table.shape[1] != 1)):
+    if block_table.dtype is not _i32 or block_table.ndim != 2:
         raise ValueError("block_table must be 2-D int32, rows contiguous")
     B, cols = block_table.shape
-    return B, block_table.data_ptr(), (block_table.stride(0) if B > 1 else cols), cols
+    ld, one = block_table.stride()
+    if one != 1 and cols != 1:
+        raise ValueError("block_table must be 2-D int32, rows contiguous")
+    return B, block_table.data_ptr(), (ld if B > 1 else cols), cols
 
 
 def fp8_kv_cache_read(cache: KVCache, block_table, offsets, rows: int, k_out=None, v_out=None):
@@ -269,13 +289,13 @@ def fp8_kv_cache_read(cache: KVCache, block_table, offsets, rows: int, k_out=Non
     int32 [B, cols]: each sequence's pages in order; offsets int32 [B + 1];
     rows from offsets[B] on are left as they were."""
     B, *table = _table(block_table)
-    _index(offsets, torch.int32, (B + 1,), "offsets")
+    _index(offsets, _i32, (B + 1,), "offsets")
     shape = (rows, cache.heads, cache.head_dim)
     outs = []
     for t, name in ((k_out, "k_out"), (v_out, "v_out")):
         if t is None:
             t = torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
-        _index(t, torch.bfloat16, shape, name)
+        _index(t, _bf16, shape, name)
         outs.append(t)
     k_out, v_out = outs
     _on(cache._dev, block_table, offsets, k_out, v_out)
@@ -305,21 +325,27 @@ def fp8_paged_attention(q, cache: KVCache, block_table, context_lens, scale=None
     Bt, table, ld, cols = _table(block_table)
     if Bt != B:
         raise ValueError(f"block_table must have {B} rows")
-    _index(context_lens, torch.int32, (B,), "context_lens")
-    if out_dtype == torch.bfloat16:
+    _index(context_lens, _i32, (B,), "context_lens")
+    if out_dtype is _bf16:
         od = OUT_BF16
-    elif out_dtype == torch.float32:
+    elif out_dtype is _f32:
         od = OUT_F32
     else:
         raise ValueError("out_dtype must be bfloat16 or float32")
-    if out is None:
-        out = torch.empty(shape, dtype=out_dtype, device=q.device)
-    else:
+    if out is not None:
         _index(out, out_dtype, shape, "out")
+    elif od == OUT_BF16:
+        out = _empty_like(q)
+    else:
+        out = torch.empty(shape, dtype=out_dtype, device=q.device)
     if lse is not None:
-        _index(lse, torch.float32, (B, Hq), "lse")
+        _index(lse, _f32, (B, Hq), "lse")
     if max_context is None:
         max_context = min(cols * cache.page_size, MAX_CONTEXT)
+    elif not 0 <= max_context <= MAX_CONTEXT:
+        raise ValueError(f"max_context must be from 0 to {MAX_CONTEXT}")
+    if not 0 <= window < 1 << 63:
+        raise ValueError("window must be 0 or a number of tokens")
     dev = cache._dev
     _on(dev, q, block_table, context_lens, out, lse)
     nbytes = (_attn_lib or attn_lib()).fp8_paged_attention_workspace(cache._ref, B, Hq, cols, max_context, window)

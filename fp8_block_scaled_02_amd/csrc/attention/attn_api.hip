@@ -14,6 +14,7 @@ constexpr int64_t kMaxDim = (int64_t)1 << 30;
 constexpr int64_t kMaxStride = (int64_t)1 << 40;  // keeps every 64-bit offset in range
 constexpr int64_t kMaxPage = ((int64_t)1 << 32) - 1;  // page strides: 32-bit factors of the kernels' offsets
 constexpr int64_t kMaxTokens = ((int64_t)1 << 24) - 1;  // a launch holds below 2^32 threads of 256 a workgroup
+constexpr int64_t kMaxRegions = (int64_t)1 << 22;        // below 2^32 threads of up to 512 a workgroup
 constexpr int64_t kMaxHeads = 65536;
 
 bool head_dim_ok(int64_t D) { return D >= 16 && D <= 256 && D % 16 == 0; }
@@ -70,7 +71,8 @@ int attention_sizes(const fp8b_kv_cache* c, int64_t B, int64_t Hq, int64_t cols,
   const int64_t room = cols * c->page_size;
   const int64_t tokens = max_context < room ? max_context : room;
   const int64_t regions = B * c->heads * ((Hq / c->heads + 15) / 16);
-  if (regions > kMaxTokens || regions * (tokens / 32 + 1) > INT32_MAX) return FP8B_EINVAL;
+  // (the pieces of a split launch may end up to 512 tiles past the last one)
+  if (regions >= kMaxRegions || regions * (tokens / 32 + 1) > INT32_MAX - 1024) return FP8B_EINVAL;
   return FP8B_OK;
 }
 

@@ -683,7 +683,7 @@ static Shape shape_of(const fp8b_kv_cache& c, int64_t B, int64_t Hq, int64_t col
   // many tiles as on average: 8 regions of 32 tiles 10.2 / 9.4, of 63 16.3 /
   // 12.1, of 125 28 / 12.5; 32 of 46 12.4 / 12.4; 128 of 46 14.5 / 17.3, of 121
   // 29 / 24; 512 of 28 19 / 25, of 121 78 / 79, of 281 166 / 159.
-  const int64_t direct = s.regions / 2 < 32 ? 32 : (s.regions / 2 < 128 ? s.regions / 2 : 128);
+  const int64_t direct = s.regions / 2 < 48 ? 48 : (s.regions / 2 < 128 ? s.regions / 2 : 128);
   if (tiles <= direct) {
     // As many waves as there are tiles, up to 8; fewer where that leaves each
     // only a few tiles and there are regions enough for 12 waves a CU without

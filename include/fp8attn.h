@@ -51,8 +51,9 @@ int fp8b_attn_abi_version(void);
  *
  *   k_codes, v_codes    16-byte aligned; k_scales, v_scales: 16-byte aligned.
  *   page_stride         bytes, >= heads * page_size * head_dim, a multiple
- *                       of 16; the same for K and V.
- *   scale_page_stride   floats, >= heads * page_size, a multiple of 4.
+ *                       of 16, below 2^32; the same for K and V.
+ *   scale_page_stride   floats, >= heads * page_size, a multiple of 4, below
+ *                       2^32.
  *   pages      1 .. 2^31 - 1.
  *   page_size  tokens: 16, 32, 64, ... 4096 (a power of two).
  *   heads      1 .. 1024;  head_dim 16 .. 256, a multiple of 16.
@@ -70,6 +71,7 @@ typedef struct {
  * How queries and keys are normed and rotated (host struct).  Per head x of
  * D values, all in fp32:
  *   u[i] = x[i] / sqrt(mean_j x[j]^2 + eps) * weight[i]   (weight NULL: u = x)
+ *   (the sum of squares has to be finite and the mean plus eps normal in fp32),
  *   for i < rot_dim / 2, with c = cos_sin[pos][i] and
  *   s = cos_sin[pos][rot_dim/2 + i]:
  *     (a, b) -> (a c - b s, b c + a s), where (a, b) is
@@ -97,7 +99,8 @@ typedef struct {
  * fp8_qk_norm_rope -- norm and rotate the queries and keys of T tokens.
  *
  *   q   bf16, token t's head h at q + t * q_t + h * q_h (strides in
- *       elements, multiples of 8), 16-byte aligned; k likewise with Hk heads.
+ *       elements, multiples of 8, q_t <= 2^40, q_h < 2^30), 16-byte aligned;
+ *       k likewise with Hk heads.
  *       Slices of a fused projection's output need no copy.
  *   q_out, k_out  bf16 with strides of their own, as q and k; rows apart from
  *       each other.  Either may be the very array it is computed from (the
@@ -194,8 +197,8 @@ int fp8_kv_cache_read(const fp8b_kv_cache *cache, const int32_t *table,
  *   workspace  fp8_paged_attention_workspace(...) bytes, 16-byte aligned;
  *            what it holds before the call does not matter.  Calls that may
  *            run at the same time need one each.  NULL where the size is 0.
- *   B * heads * ceil(Hq / heads / 16) < 2^24, and times (tokens / 32 + 1)
- *            < 2^31, tokens being min(max_context, cols * page_size).
+ *   B * heads * ceil(Hq / heads / 16) < 2^22, and times (tokens / 32 + 1)
+ *            < 2^31 - 1024, tokens being min(max_context, cols * page_size).
  *
  * fp8_paged_attention_workspace returns the bytes for these sizes (it
  * depends on sizes only), or a negative status for sizes that

@@ -93,7 +93,8 @@ def test_norm_rope_refusals(M, L):
     for over, rc in [(dict(T=0), OK), (dict(T=-1), EINVAL), (dict(T=1 << 24), EINVAL), (dict(Hq=0, Hk=0), EINVAL),
                      (dict(Hq=-1), EINVAL), (dict(Hk=65537), EINVAL), (dict(D=8), EINVAL), (dict(D=100), EINVAL),
                      (dict(D=512), EINVAL), (dict(rope=None), EINVAL), (dict(q=None), EINVAL), (dict(k=ODD), EALIGN),
-                     (dict(q_t=1020), EALIGN), (dict(k_h=-8), EINVAL), (dict(qo=None), EINVAL),
+                     (dict(q_t=1020), EALIGN), (dict(k_h=-8), EINVAL),
+                     (dict(q_h=1 << 30), EINVAL), (dict(k_t=1 << 41), EINVAL), (dict(qo=None), EINVAL),
                      (dict(ko=GOOD + 8), EALIGN), (dict(ko_t=12), EALIGN)]:
         assert f(*_with(args, **over)) == rc, over
     for over, rc in [(dict(rot_dim=8), EINVAL), (dict(rot_dim=144), EINVAL), (dict(rot_dim=-16), EINVAL),
@@ -158,7 +159,7 @@ def test_attention_refusals(M, L):
     f = L.fp8_paged_attention
     sizes = [(dict(B=-1), EINVAL), (dict(Hq=0), EINVAL), (dict(Hq=30), EINVAL), (dict(Hq=65544), EINVAL),
              (dict(cols=0), EINVAL), (dict(most=-1), EINVAL), (dict(most=(1 << 30) + 1), EINVAL),
-             (dict(window=-1), EINVAL), (dict(cache=None), EINVAL), (dict(B=1 << 22), EINVAL),
+             (dict(window=-1), EINVAL), (dict(cache=None), EINVAL), (dict(B=1 << 19), EINVAL),
              (dict(B=1 << 16, cols=1 << 20, ld=1 << 20, most=1 << 24), EINVAL)]
     for over, rc in sizes + [(dict(B=0), OK), (dict(dtype=2), EUNSUPPORTED), (dict(ld=999), EINVAL),
                              (dict(scale=float("nan")), EINVAL), (dict(scale=float("inf")), EINVAL),

@@ -24,7 +24,6 @@ class _HostCache(F.KVCache):
     def __init__(self):
         self.pages, self.heads, self.page_size, self.head_dim, self.fmt = 4, 2, 16, 64, "e5m2"
         self.device, self._dev, self._ref = torch.device("cpu"), -1, 0
-        self.k_codes = torch.zeros(4, 2, 16, 64, dtype=u8)
 
 
 def test_cache_layouts():
@@ -110,4 +109,8 @@ def test_attention_arguments():
     _raises("out_dtype", f, q, c, table, lens, out_dtype=torch.float16)
     _raises("out must be contiguous", f, q, c, table, lens, out=torch.zeros(3, 4, 64))
     _raises("out must have shape", f, q, c, table, lens, out=torch.zeros(3, 2, 64, dtype=bf16))
+    _raises("max_context must be", f, q, c, table, lens, max_context=-1)
+    _raises("max_context must be", f, q, c, table, lens, max_context=1 << 64)
+    _raises("window must be", f, q, c, table, lens, window=-1)
+    _raises("window must be", f, q, c, table, lens, window=1 << 64)
     _raises("lse must have shape", f, q, c, table, lens, lse=torch.zeros(3, 2))
