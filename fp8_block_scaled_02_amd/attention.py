@@ -175,6 +175,7 @@ class KVCache:
         self.pages, self.heads, self.page_size, self.head_dim, self.fmt = P, H, S, D, fmt
         self.device = k_codes.device
         self._dev = k_codes.get_device()
+        self._bf16 = torch.empty(0, dtype=torch.bfloat16, device=k_codes.device)    # makes outputs of its kind
         self._struct = _CacheStruct(k_codes.data_ptr(), v_codes.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
                                     strides[0], strides[2], P, S, H, D, _CACHE_FMT[fmt], 0)
         self._ref = ctypes.addressof(self._struct)
@@ -294,7 +295,7 @@ def fp8_kv_cache_read(cache: KVCache, block_table, offsets, rows: int, k_out=Non
     outs = []
     for t, name in ((k_out, "k_out"), (v_out, "v_out")):
         if t is None:
-            t = torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
+            t = cache._bf16.new_empty(shape)
         _index(t, _bf16, shape, name)
         outs.append(t)
     k_out, v_out = outs

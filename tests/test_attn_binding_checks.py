@@ -24,6 +24,7 @@ class _HostCache(F.KVCache):
     def __init__(self):
         self.pages, self.heads, self.page_size, self.head_dim, self.fmt = 4, 2, 16, 64, "e5m2"
         self.device, self._dev, self._ref = torch.device("cpu"), -1, 0
+        self._bf16 = torch.empty(0, dtype=bf16)
 
 
 def test_cache_layouts():
