@@ -1,5 +1,7 @@
 """The attention binding refuses misuse on the host before the library is
 called (no GPU needed): layouts and types first, then the device."""
+import ctypes
+
 import pytest
 import torch
 
@@ -19,12 +21,11 @@ def _tensors(P=4, H=2, S=16, D=64):
 
 
 class _HostCache(F.KVCache):
-    """A cache on the host, to reach the checks after the cache's own."""
+    """A cache on the host, to reach the checks after the cache's own (only its sizes are read there)."""
 
     def __init__(self):
-        self.pages, self.heads, self.page_size, self.head_dim, self.fmt = 4, 2, 16, 64, "e5m2"
-        self.device, self._dev, self._ref = torch.device("cpu"), -1, 0
-        self._bf16 = torch.empty(0, dtype=bf16)
+        self._struct = F.attention._CacheStruct(pages=4, page_size=16, heads=2, head_dim=64, fmt=F.FMT_E5M2)
+        self._ref, self._dev = ctypes.addressof(self._struct), -1
 
 
 def test_cache_layouts():
@@ -111,7 +112,11 @@ def test_attention_arguments():
     _raises("out must be contiguous", f, q, c, table, lens, out=torch.zeros(3, 4, 64))
     _raises("out must have shape", f, q, c, table, lens, out=torch.zeros(3, 2, 64, dtype=bf16))
     _raises("max_context must be", f, q, c, table, lens, max_context=-1)
-    _raises("max_context must be", f, q, c, table, lens, max_context=1 << 64)
+    _raises("max_context must be", f, q, c, table, lens, max_context=(1 << 30) + 1)
     _raises("window must be", f, q, c, table, lens, window=-1)
-    _raises("window must be", f, q, c, table, lens, window=1 << 64)
+    with pytest.raises(OverflowError):
+        f(q, c, table, lens, window=1 << 64)
+    with pytest.raises(TypeError):
+        f(q, c, table, lens, window=2.5)
+    _raises("must be a tensor", f, q, c, [[0]], lens)
     _raises("lse must have shape", f, q, c, table, lens, lse=torch.zeros(3, 2))
