@@ -136,19 +136,25 @@ class KVCache:
         _need(16 <= S <= 4096 and S & (S - 1) == 0, "page_size must be a power of two from 16 to 4096")
         _need(16 <= D <= 256 and D % 16 == 0, "head_dim must be a multiple of 16 from 16 to 256")
         strides = []
-        for t, dtype, shape, name in ((k_codes, torch.uint8, (P, H, S, D), "k_codes"),
-                                      (v_codes, torch.uint8, (P, H, S, D), "v_codes"),
-                                      (k_scales, torch.float32, (P, H, S), "k_scales"),
-                                      (v_scales, torch.float32, (P, H, S), "v_scales")):
-            _need(t.dtype == dtype, f"{name} must be {dtype}")
-            _shape(t, shape, name)
-            _need(t[0].is_contiguous(), f"{name}: a page must be contiguous")
-            _need(P == 1 or t.stride(0) >= t[0].numel(), f"{name}: pages overlap")
-            strides.append(t.stride(0) if P > 1 else t[0].numel())
+        for t, name in ((k_codes, "k_codes"), (v_codes, "v_codes"), (k_scales, "k_scales"), (v_scales, "v_scales")):
+            dtype, page = (torch.uint8, (H, S, D)) if name.endswith("codes") else (torch.float32, (H, S))
+            if t.dtype != dtype:
+                raise ValueError(f"{name} must be {dtype}")
+            if t.shape != (P, *page):
+                _shape(t, (P, *page), name)
+            if not t[0].is_contiguous():
+                raise ValueError(f"{name}: a page must be contiguous")
+            n = t[0].numel()
+            if P > 1 and t.stride(0) < n:
+                raise ValueError(f"{name}: pages overlap")
+            strides.append(t.stride(0) if P > 1 else n)
         _need(strides[0] == strides[1] and strides[2] == strides[3], "K and V pages must lie equally far apart")
+        dev = k_codes.get_device()
         for t in (k_codes, v_codes, k_scales, v_scales):
-            _need(t.is_cuda, f"every tensor must be on a GPU (found one on {t.device})")
-            _need(t.device == k_codes.device, f"every tensor must be on {k_codes.device} (found one on {t.device})")
+            if not t.is_cuda:
+                raise ValueError(f"every tensor must be on a GPU (found one on {t.device})")
+            if t.get_device() != dev:
+                raise ValueError(f"every tensor must be on cuda:{dev} (found one on {t.device})")
         self._tensors = k_codes, v_codes, k_scales, v_scales
         self.pages, self.heads, self.page_size, self.head_dim, self.fmt = P, H, S, D, fmt
         self.device = k_codes.device

@@ -156,7 +156,9 @@ __device__ __forceinline__ u32x2 quantise_row(const u32x4& raw, float& d) {
 // FMT: 0 no cache (keys to k_out), 1 E5M2, 2 E4M3.  ROPE: 0 none, 1 halves,
 // 2 interleaved.  HBM-bound (2 bytes in and 2, or 1 and a scale, out per
 // value), but only just: 8 values are one 16-byte load and some 150
-// instructions, so addresses are kept to 32-bit products.
+// instructions, so addresses are kept to 32-bit products.  Norm and rotation of
+// 4096 tokens x (64 + 8) x 128: 30.8 us, 4.98 TB/s; cache write of 32768 x 8 x
+// 128: 37.3 us, 5.46 TB/s; of one step's 32 tokens 2.3 us, which is the launch.
 template <int LPR, int ROPE, int FMT>
 __global__ __launch_bounds__(256) void qkv_kernel(const QkvArgs a) {
   constexpr int kSlots = 256 / LPR;
@@ -293,7 +295,14 @@ __global__ __launch_bounds__(256) void qkv_kernel(const QkvArgs a) {
   }
 }
 
+// From 1024 workgroups of one token group each on, a slot takes several rows
+// (4096 tokens x 72 heads: 31 us, 50 with a slot for every row; 900 tokens x 16
+// heads: 3.2 us, 4.4 with several rows a slot).  512: 512 x 72 7.0 -> 7.9 us;
+// 2048: 1500 x 72 12.1 -> 13.8.  Non-temporal stores pay from there on too
+// (rotation of 4096 x 72 heads 34 -> 30 us, but 1021 x 25 x 80 4.5 -> 4.7).
 constexpr int kManyWgs = 1024;
+// Tokens a slot takes in a large cache write: 32768 x 16 heads 46 us with 1 or
+// 2, 40 with 4, 41 with 8 (4096 x 16: 7.9 with 4, 9.8 with 8).
 constexpr int kTokenItems = 4;
 
 int launch_qkv(const Rows& q, const Rows& k, const Rows& v, int64_t T, int D, const fp8b_rope* rope, const Rows& q_out,
@@ -397,8 +406,9 @@ constexpr int kMaxReadRows = 512;   // of a workgroup: kReadTurns * 256
 // 2^slot_shift threads share a row, 16 codes each (one 16-byte load, two
 // 16-byte stores), so a workgroup takes kReadTurns * 256 / 2^slot_shift rows; K and V in
 // blockIdx.y.  Its threads first look up each row's sequence (binary search
-// over offsets) and page and leave them in LDS.  HBM-bound: 1 byte in, 2 out.
-// Rows and pieces that do not exist are read at valid addresses and not put
+// over offsets) and page and leave them in LDS.  HBM-bound: 1 byte in, 2 out:
+// 32768 tokens x 8 x 128, K and V, 43.6 us, 4.66 TB/s (one row a turn 46, four
+// 43.6, eight 52).  Rows and pieces that do not exist are read at valid addresses and not put
 // out, so that no branch comes between the loads.
 template <int FMT>
 __global__ __launch_bounds__(256) void cache_read_kernel(const ReadArgs a) {
