@@ -4,7 +4,7 @@ paged FP8 key-value cache (C ABI: include/fp8attn.h).
 As in the package itself, argument marshalling only: checks, outputs and the
 attention's workspace allocated with torch, the current torch stream of the
 tensors' device.  The calls go through a small native module
-(csrc/attention/binding.cpp), since a decode step on a few sequences is bound
+(csrc_attention/binding.cpp), since a decode step on a few sequences is bound
 by the host.  There is no fallback: if libfp8attn.so or the module is missing
 the functions raise on first use.  Nothing here records a gradient.
 """

@@ -1,7 +1,7 @@
 """Compile libfp8blk.so and libfp8attn.so (HIP, gfx950) in-tree with hipcc.
 
 The libraries are the product's compute path: every hot-path step runs in
-the kernels under csrc/ (the linear layers, libfp8blk.so) and csrc/attention/
+the kernels under csrc/ (the linear layers, libfp8blk.so) and csrc_attention/
 (the attention side of a decode step, libfp8attn.so, and the host code of its
 Python calls, _attn_binding.so, against torch's headers).  Compiled with
 packed-FP32 instructions disabled.
@@ -14,6 +14,7 @@ import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
+ATTN_CSRC = os.path.join(HERE, "csrc_attention")
 LIB = os.path.join(HERE, "libfp8blk.so")
 ATTN_LIB = os.path.join(HERE, "libfp8attn.so")
 ATTN_BINDING = os.path.join(HERE, "_attn_binding.so")
@@ -32,7 +33,7 @@ def sources():
 
 
 def attn_sources():
-    return sorted(glob.glob(os.path.join(CSRC, "attention", "*.hip")))
+    return sorted(glob.glob(os.path.join(ATTN_CSRC, "*.hip")))
 
 
 def build(verbose: bool = False) -> str:
@@ -52,7 +53,7 @@ def _compile_binding(verbose: bool) -> None:
            "-isystem", os.path.join(root, "include"),
            "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
            "-isystem", sysconfig.get_paths()["include"],
-           os.path.join(CSRC, "attention", "binding.cpp"), "-o", tmp,
+           os.path.join(ATTN_CSRC, "binding.cpp"), "-o", tmp,
            "-L" + HERE, "-lfp8attn", "-Wl,-rpath,$ORIGIN",
            "-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
     if verbose:

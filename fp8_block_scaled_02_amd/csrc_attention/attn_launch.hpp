@@ -3,7 +3,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include "../../../include/fp8attn.h"
+#include "../../include/fp8attn.h"
 
 namespace fp8attn {
 

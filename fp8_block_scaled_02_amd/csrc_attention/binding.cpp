@@ -21,7 +21,7 @@
 #include <sstream>
 #include <string>
 
-#include "../../../include/fp8attn.h"
+#include "../../include/fp8attn.h"
 
 namespace {
 

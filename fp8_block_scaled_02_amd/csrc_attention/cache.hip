@@ -1,7 +1,7 @@
 // cache.hip -- what surrounds the attention kernel on a paged FP8 cache
 // (layout: fp8b_kv_cache in include/fp8attn.h): query/key norms with the
 // position rotation, the quantising write, and reading back.
-#include "../common.hpp"
+#include "../csrc/common.hpp"
 #include "attn_launch.hpp"
 
 namespace fp8attn {

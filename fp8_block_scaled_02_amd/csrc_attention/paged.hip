@@ -35,7 +35,7 @@
 // bound of short contexts on few regions.
 #include <type_traits>
 
-#include "../common.hpp"
+#include "../csrc/common.hpp"
 #include "attn_launch.hpp"
 
 namespace fp8attn {
