@@ -389,6 +389,56 @@ def test_attention_many_sequences(F):
     _check_attention(F, c, lens, q, table, max_context=128, check=range(0, 333, 7))
 
 
+@pytest.mark.parametrize("B", [63, 64, 65, 128, 129])
+def test_attention_batches_at_a_waves_width(F, B):
+    """The lengths are scanned 64 at a time; one sequence in the middle is far longer than the rest."""
+    g = W.gen(B, DEV)
+    lens = [int(x) for x in torch.randint(0, 60, (B,), generator=g, device=DEV)]
+    lens[B // 2], lens[-1] = 4999, 333
+    pages, table = _book(lens, 16, g)
+    c = _filled(F, pages, 1, 16, 32, "e4m3", g)
+    q = torch.randn(B, 3, 32, generator=g, device=DEV).bfloat16()
+    _check_attention(F, c, lens, q, table, out_dtype=torch.float32)
+
+
+def test_attention_outputs_and_strides(F):
+    """Outputs given by the caller, one query for all rows, a table that is a slice of a wider one, no context at all."""
+    g = W.gen(16, DEV)
+    lens = [70, 300, 9]
+    pages, table = _book(lens, 16, g)
+    c = _filled(F, pages, 2, 16, 64, "e5m2", g)
+    lt = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    one = torch.randn(1, 4, 64, generator=g, device=DEV).bfloat16()
+    want = F.fp8_paged_attention(one.repeat(3, 1, 1), c, table, lt)
+    assert torch.equal(F.fp8_paged_attention(one.expand(3, 4, 64), c, table, lt), want)
+    wide = torch.full((3, table.shape[1] + 5), -9, dtype=torch.int32, device=DEV)
+    wide[:, 2:-3] = table
+    assert torch.equal(F.fp8_paged_attention(one.expand(3, 4, 64), c, wide[:, 2:-3], lt), want)
+    out, lse = torch.full((3, 4, 64), 7.0, device=DEV), torch.full((3, 4), 7.0, device=DEV)
+    got = F.fp8_paged_attention(one.expand(3, 4, 64), c, table, lt, out_dtype=torch.float32, out=out, lse=lse,
+                                max_context=0)
+    assert got.data_ptr() == out.data_ptr() and not out.any() and (lse == -np.inf).all()
+    short = F.fp8_paged_attention(one, c, table[:1, :1], lt[:1])          # one page of five
+    assert torch.equal(short, F.fp8_paged_attention(one, c, table[:1], lt[:1], max_context=16))
+
+
+def test_random_shapes(F):
+    """Sizes, layouts, masks and formats drawn together."""
+    import random
+    rng = random.Random(7)
+    for turn in range(40):
+        g = W.gen(1000 + turn, DEV)
+        H, G, D = rng.choice((1, 2, 3, 5)), rng.choice((1, 2, 3, 4, 7, 8, 16, 18, 33)), 16 * rng.randint(1, 16)
+        S, B = rng.choice((16, 32, 128)), rng.choice((1, 2, 5, 17))
+        most = rng.choice((20, 200, 2000))
+        lens = [rng.randint(0, most) for _ in range(B)]
+        pages, table = _book(lens, S, g, room=rng.choice((most, 6000)))
+        c = _filled(F, pages, H, S, D, rng.choice(("e5m2", "e4m3")), g)
+        q = (rng.choice((0.5, 3.0)) * torch.randn(B, H * G, D, generator=g, device=DEV)).bfloat16()
+        print(turn, H, G, D, S, B, most, flush=True)
+        _check_attention(F, c, lens, q, table, rng.choice((0, 0, 1, 40, 700)), rng.choice((torch.bfloat16, torch.float32)))
+
+
 def test_attention_all_empty(F):
     g = W.gen(4, DEV)
     _, table = _book([0, 0, 0], 16, g)
