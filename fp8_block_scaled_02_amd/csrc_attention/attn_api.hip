@@ -147,7 +147,7 @@ FP8B_EXPORT int fp8_kv_cache_read(const fp8b_kv_cache* cache, const int32_t* tab
   FP8B_TRY(cache_sizes(cache));
   if (B < 1 || B > kMaxDim || cols < 1 || cols > kMaxDim || ld_table < cols || ld_table > kMaxStride)
     return FP8B_EINVAL;
-  if (R < 0 || R > ((int64_t)1 << 28) - 16) return FP8B_EINVAL;
+  if (R < 0 || R > kMaxTokens) return FP8B_EINVAL;
   if (R == 0) return FP8B_OK;  // nothing is read or written; empty arrays may be NULL
   FP8B_TRY(cache_pointers(cache));
   if (!table || !offsets || !k_out || !v_out) return FP8B_EINVAL;

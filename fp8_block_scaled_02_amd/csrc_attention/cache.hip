@@ -386,36 +386,43 @@ int launch_qkv(const Rows& q, const Rows& k, const Rows& v, int64_t T, int D, co
 
 // ---- reading back ----------------------------------------------------------
 
+// x / d for x < 2^16 and inv = ceil(2^32 / d) (d = 1: inv 0): the excess of inv,
+// below d / 2^32 per unit, adds up to less than 1 / d.
+__device__ __forceinline__ int divide_by(int x, uint32_t inv) { return inv ? (int)__umulhi((uint32_t)x, inv) : x; }
+static uint32_t inverse(uint32_t d) { return d == 1 ? 0u : (uint32_t)((((uint64_t)1 << 32) + d - 1) / d); }
+
 struct ReadArgs {
   const uint8_t *k_codes, *v_codes;
   const float *k_scales, *v_scales;
-  int64_t page_stride, scale_page_stride, pages;
+  uint32_t page_stride, scale_page_stride;
+  int64_t pages;
   int page_shift, heads, D;
   const int32_t* table;
   int64_t ld_table, cols;
   const int32_t* offsets;
   int64_t B, R;
   uint16_t *k_out, *v_out;
-  uint32_t inv;    // ceil(2^32 / (D / 16)): divides a piece index by multiplication
-  int slot_shift;  // log2 of the threads that share a row
+  int rows;                       // of a workgroup
+  uint32_t inv_pieces, inv_head;  // of the pieces of a row and of a head
 };
 
-constexpr int kReadTurns = 2;       // rows a thread group takes, all loaded before any is put out
-constexpr int kMaxReadRows = 512;   // of a workgroup: kReadTurns * 256
+constexpr int kReadTurns = 2;       // pieces a thread takes, all loaded before any is put out
+constexpr int kReadPieces = 256 * kReadTurns;
 
-// 2^slot_shift threads share a row, 16 codes each (one 16-byte load, two
-// 16-byte stores), so a workgroup takes kReadTurns * 256 / 2^slot_shift rows; K and V in
-// blockIdx.y.  Its threads first look up each row's sequence (binary search
-// over offsets) and page and leave them in LDS.  HBM-bound: 1 byte in, 2 out:
-// 32768 tokens x 8 x 128, K and V, 43.6 us, 4.66 TB/s (one row a turn 46, four
-// 43.6, eight 52).  Rows and pieces that do not exist are read at valid addresses and not put
-// out, so that no branch comes between the loads.
+// A workgroup takes `rows` rows, their pieces of 16 codes (one 16-byte load,
+// two 16-byte stores) dealt to the threads in one line: as many rows as fill
+// 512 pieces, or one longer row in turns; K and V in blockIdx.y.  Its threads
+// first look up each row's sequence (binary search over offsets) and page and
+// leave them in LDS.  HBM-bound: 1 byte in, 2 out: 32768 tokens x 8 x 128, K and
+// V, 41.5 us, 4.9 TB/s (one piece a turn 46, four 43.6, eight 52).  Rows and
+// pieces that do not exist are read at valid addresses and not put out, so that
+// no branch comes between the loads.
 template <int FMT>
 __global__ __launch_bounds__(256) void cache_read_kernel(const ReadArgs a) {
-  __shared__ int row_page[kMaxReadRows];  // -1: no such row
-  __shared__ int row_place[kMaxReadRows];
+  __shared__ int row_page[kReadPieces];  // -1: no such row
+  __shared__ int row_place[kReadPieces];
   const int tid = threadIdx.x;
-  const int share = 1 << a.slot_shift, groups = 256 >> a.slot_shift, rows = kReadTurns * groups;
+  const int rows = a.rows;
   const int64_t row0 = (int64_t)blockIdx.x * rows;
   const bool is_v = blockIdx.y != 0;
   for (int x = tid; x < rows; x += 256) {
@@ -442,24 +449,23 @@ __global__ __launch_bounds__(256) void cache_read_kernel(const ReadArgs a) {
   const float* scales = is_v ? a.v_scales : a.k_scales;
   uint16_t* out = (is_v ? a.v_out : a.k_out) + row0 * a.heads * a.D;
   const int per_head = a.D / 16;
-  const int pieces = a.heads * per_head;
-  const int grp = tid >> a.slot_shift;
-  for (int p0 = tid & (share - 1); p0 < ((pieces + share - 1) & ~(share - 1)); p0 += share) {
-    const int p = min(p0, pieces - 1);
-    const int h = a.inv ? (int)__umulhi((uint32_t)p, a.inv) : p;
-    const int c = p - h * per_head;
+  const int pieces = a.heads * per_head, total = rows * pieces;
+  for (int i0 = tid; i0 < ((total + kReadPieces - 1) & ~(kReadPieces - 1)); i0 += kReadPieces) {
     u32x4 raw[kReadTurns];
     float d[kReadTurns];
-    bool ok[kReadTurns];
+    int to[kReadTurns];  // piece of the output, -1: none
 #pragma unroll
     for (int u = 0; u < kReadTurns; ++u) {
-      const int x = grp + u * groups;
-      ok[u] = row_page[x] >= 0 && p0 < pieces;
-      const int64_t page = max(row_page[x], 0);
-      const int in_page = (h << a.page_shift) + row_place[x];
-      raw[u] = __builtin_nontemporal_load(
-          reinterpret_cast<const u32x4*>(codes + (page * a.page_stride + (int64_t)in_page * a.D + 16 * c)));
-      d[u] = scales[page * a.scale_page_stride + in_page];
+      const int i = min(i0 + 256 * u, total - 1);
+      const int x = rows == 1 ? 0 : divide_by(i, a.inv_pieces);
+      const int p = i - x * pieces;
+      const int h = divide_by(p, a.inv_head);
+      to[u] = row_page[x] >= 0 && i0 + 256 * u < total ? i : -1;
+      const uint32_t page = (uint32_t)max(row_page[x], 0);
+      const uint32_t in_page = ((uint32_t)h << a.page_shift) + (uint32_t)row_place[x];
+      raw[u] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(
+          codes + ((uint64_t)page * a.page_stride + in_page * (uint32_t)a.D + 16 * (p - h * per_head))));
+      d[u] = scales[(uint64_t)page * a.scale_page_stride + in_page];
     }
 #pragma unroll
     for (int u = 0; u < kReadTurns; ++u) {
@@ -480,8 +486,8 @@ __global__ __launch_bounds__(256) void cache_read_kernel(const ReadArgs a) {
         o[i >> 1][2 * (i & 1)] = __builtin_bit_cast(uint32_t, b0);
         o[i >> 1][2 * (i & 1) + 1] = __builtin_bit_cast(uint32_t, b1);
       }
-      if (ok[u]) {
-        u32x4* q = reinterpret_cast<u32x4*>(out + (int64_t)(grp + u * groups) * a.heads * a.D + 16 * p);
+      if (to[u] >= 0) {
+        u32x4* q = reinterpret_cast<u32x4*>(out + (int64_t)16 * to[u]);
         __builtin_nontemporal_store(o[0], q);
         __builtin_nontemporal_store(o[1], q + 1);
       }
@@ -496,8 +502,8 @@ int launch_cache_read(const fp8b_kv_cache& c, const int32_t* table, int64_t ld_t
   a.v_codes = c.v_codes;
   a.k_scales = c.k_scales;
   a.v_scales = c.v_scales;
-  a.page_stride = c.page_stride;
-  a.scale_page_stride = c.scale_page_stride;
+  a.page_stride = (uint32_t)c.page_stride;
+  a.scale_page_stride = (uint32_t)c.scale_page_stride;
   a.pages = c.pages;
   a.page_shift = __builtin_ctzll((unsigned long long)c.page_size);
   a.heads = (int)c.heads;
@@ -510,16 +516,11 @@ int launch_cache_read(const fp8b_kv_cache& c, const int32_t* table, int64_t ld_t
   a.R = R;
   a.k_out = k_out;
   a.v_out = v_out;
-  const uint32_t per_head = (uint32_t)a.D / 16;
-  // p * inv >> 32 = p / per_head for p < 2^16: the excess of inv, below
-  // per_head / 2^32 per unit, stays under 1 / per_head for those p
-  a.inv = per_head == 1 ? 0u : (uint32_t)((((uint64_t)1 << 32) + per_head - 1) / per_head);
-  const int pieces = a.heads * (int)per_head;
-  int shift = 0;
-  while ((1 << shift) < pieces && shift < 8) ++shift;
-  a.slot_shift = shift;
-  const int64_t rows = kReadTurns * (256 >> shift);
-  const dim3 grid((unsigned)((R + rows - 1) / rows), 2);
+  const int pieces = a.heads * (a.D / 16);
+  a.rows = pieces < kReadPieces ? kReadPieces / pieces : 1;
+  a.inv_pieces = inverse((uint32_t)pieces);
+  a.inv_head = inverse((uint32_t)a.D / 16);
+  const dim3 grid((unsigned)((R + a.rows - 1) / a.rows), 2);
   if (c.fmt == FP8B_FMT_E5M2) hipLaunchKernelGGL(cache_read_kernel<1>, grid, dim3(256), 0, s, a);
   else hipLaunchKernelGGL(cache_read_kernel<2>, grid, dim3(256), 0, s, a);
   return check_launch();

@@ -156,7 +156,7 @@ int fp8_qkv_cache_write(const void *q, int64_t q_t, int64_t q_h,
  *            cols pages, give unspecified rows but never fault.
  *   offsets  int32 [B+1], non-decreasing, [0] = 0 (otherwise unspecified
  *            rows, no fault).  Rows from offsets[B] on are left as they were.
- *   R        rows of the outputs; 0 is a no-op.  R <= 2^28 - 16.
+ *   R        rows of the outputs; 0 is a no-op.  R < 2^24.
  *   B, cols  >= 1, <= 2^30; ld_table >= cols.
  *   k_out, v_out  bf16 contiguous [R][heads][head_dim], 16-byte aligned.
  */

@@ -142,7 +142,7 @@ def test_cache_read_refusals(M, L):
     good = _cache(M)
     args = dict(cache=_byref(good), table=GOOD, ld=7, cols=7, offsets=GOOD, B=3, R=100, k=GOOD, v=GOOD, s=None)
     f = L.fp8_kv_cache_read
-    for over, rc in [(dict(R=0), OK), (dict(R=-1), EINVAL), (dict(R=1 << 28), EINVAL), (dict(B=0), EINVAL),
+    for over, rc in [(dict(R=0), OK), (dict(R=-1), EINVAL), (dict(R=1 << 24), EINVAL), (dict(B=0), EINVAL),
                      (dict(cols=0), EINVAL), (dict(ld=6), EINVAL), (dict(table=None), EINVAL), (dict(table=ODD), EALIGN),
                      (dict(offsets=None), EINVAL), (dict(k=None), EINVAL), (dict(v=GOOD + 8), EALIGN),
                      (dict(cache=None), EINVAL)]:
