@@ -154,15 +154,14 @@ __device__ __forceinline__ u32x2 quantise_row(const u32x4& raw, float& d) {
 // (nothing to rotate, heads no more than slots) the same head of later tokens.
 //
 // FMT: 0 no cache (keys to k_out), 1 E5M2, 2 E4M3.  ROPE: 0 none, 1 halves,
-// 2 interleaved.  HBM-bound (2 bytes in and 2, or 1 and a scale, out per
-// value), but only just: 8 values are one 16-byte load and some 150
+// 2 interleaved.  STREAM: non-temporal loads.  HBM-bound (2 bytes in and 2, or
+// 1 and a scale, out per value), but only just: 8 values are one 16-byte load and some 150
 // instructions, so addresses are kept to 32-bit products.  Norm and rotation of
 // 4096 tokens x (64 + 8) x 128: 30.8 us, 4.98 TB/s; cache write of 32768 x 8 x
 // 128: 37.3 us, 5.46 TB/s; of one step's 32 tokens 2.3 us, which is the launch.
-template <int LPR, int ROPE, int FMT>
+template <int LPR, int ROPE, int FMT, bool STREAM>
 __global__ __launch_bounds__(256) void qkv_kernel(const QkvArgs a) {
   constexpr int kSlots = 256 / LPR;
-  constexpr bool kStream = ROPE == 0 && FMT != 0;  // a pure cache write: non-temporal loads (2-5% faster)
   const int lane = threadIdx.x & (LPR - 1);
   const int slot = threadIdx.x / LPR;
   const int per_token = 1 << a.slot_shift;
@@ -183,7 +182,7 @@ __global__ __launch_bounds__(256) void qkv_kernel(const QkvArgs a) {
   const uint32_t qs = 2 * (uint32_t)a.q.h, ks = 2 * (uint32_t)a.k.h, vs = 2 * (uint32_t)a.v.h;
   const int64_t qo = address(a.q_out.p) + 2 * (t * a.q_out.t + e0);
   const int64_t ko = address(a.k_out.p) + 2 * (t * a.k_out.t + e0);
-  u32x4 next = load_row<kStream>(of_kind(r, k0, v0, qp, kp, vp), of_kind(r, k0, v0, qs, ks, vs),
+  u32x4 next = load_row<STREAM>(of_kind(r, k0, v0, qp, kp, vp), of_kind(r, k0, v0, qs, ks, vs),
                                  r - of_kind(r, k0, v0, 0, k0, v0), on);
   int64_t next_slot = FMT != 0 ? a.slots[t] : 0;
 
@@ -229,7 +228,7 @@ __global__ __launch_bounds__(256) void qkv_kernel(const QkvArgs a) {
     }
     const bool last = left == 1 || t >= a.T || r >= rows;
     if (!last) {
-      next = load_row<kStream>(of_kind(r, k0, v0, qp, kp, vp), of_kind(r, k0, v0, qs, ks, vs),
+      next = load_row<STREAM>(of_kind(r, k0, v0, qp, kp, vp), of_kind(r, k0, v0, qs, ks, vs),
                                r - of_kind(r, k0, v0, 0, k0, v0), on);
       if (FMT != 0 && a.token_items > 1) next_slot = a.slots[t];
     }
@@ -256,7 +255,7 @@ __global__ __launch_bounds__(256) void qkv_kernel(const QkvArgs a) {
       }
       if (ROPE == 1) {
         float o[8];
-        if (a.rot == 8 * LPR) {
+        if (a.rot == 8 * LPR) {  // (4096 x 72 heads of 128: 32.6 us, 33.9 by the shuffles)
 #pragma unroll
           for (int i = 0; i < 8; ++i) o[i] = other_half<LPR>(f[i]);
         } else {
@@ -301,6 +300,10 @@ __global__ __launch_bounds__(256) void qkv_kernel(const QkvArgs a) {
 // 2048: 1500 x 72 12.1 -> 13.8.  Non-temporal stores pay from there on too
 // (rotation of 4096 x 72 heads 34 -> 30 us, but 1021 x 25 x 80 4.5 -> 4.7).
 constexpr int kManyWgs = 1024;
+// Rows that the last-level cache (256 MB) can still hold are read from there: a
+// write of 134 MB of rows 45.6 us with plain loads, 41.4 non-temporal; of 17 MB
+// 7.4 and 7.9.
+constexpr int64_t kStreamBytes = (int64_t)64 << 20;
 // Tokens a slot takes in a large cache write: 32768 x 16 heads 46 us with 1 or
 // 2, 40 with 4, 41 with 8 (4096 x 16: 7.9 with 4, 9.8 with 8).
 constexpr int kTokenItems = 4;
@@ -362,12 +365,16 @@ int launch_qkv(const Rows& q, const Rows& k, const Rows& v, int64_t T, int D, co
     gx = (T + (int64_t)tokens * kTokenItems - 1) / (tokens * kTokenItems);
   }
   const dim3 grid((unsigned)gx, (unsigned)gy);
-#define FP8A_QKV(L, R, F) hipLaunchKernelGGL((qkv_kernel<L, R, F>), grid, dim3(256), 0, s, a)
-#define FP8A_QKV_F(L, R)            \
-  do {                              \
-    if (fmt == 0) FP8A_QKV(L, R, 0); \
-    else if (fmt == 1) FP8A_QKV(L, R, 1); \
-    else FP8A_QKV(L, R, 2);         \
+  const bool streamed = kind == 0 && cache && 2 * T * rows * D >= kStreamBytes;
+#define FP8A_QKV(L, R, F) hipLaunchKernelGGL((qkv_kernel<L, R, F, false>), grid, dim3(256), 0, s, a)
+#define FP8A_QKV_S(L, F) hipLaunchKernelGGL((qkv_kernel<L, 0, F, true>), grid, dim3(256), 0, s, a)
+#define FP8A_QKV_F(L, R)                      \
+  do {                                        \
+    if (fmt == 0) FP8A_QKV(L, R, 0);          \
+    else if (R == 0 && streamed && fmt == 1) FP8A_QKV_S(L, 1); \
+    else if (R == 0 && streamed) FP8A_QKV_S(L, 2); \
+    else if (fmt == 1) FP8A_QKV(L, R, 1);     \
+    else FP8A_QKV(L, R, 2);                   \
   } while (0)
 #define FP8A_QKV_R(L)               \
   do {                              \
@@ -380,6 +387,7 @@ int launch_qkv(const Rows& q, const Rows& k, const Rows& v, int64_t T, int D, co
   else FP8A_QKV_R(32);
 #undef FP8A_QKV_R
 #undef FP8A_QKV_F
+#undef FP8A_QKV_S
 #undef FP8A_QKV
   return check_launch();
 }

@@ -179,6 +179,37 @@ def test_cache_write(F, H, S, D, T, fmt):
     _assert_cache(c, _expect_written(c, k, v, slots))
 
 
+@pytest.mark.parametrize("T,H,D,fmt", [(20011, 8, 128, "e5m2"), (9001, 8, 128, "e4m3"), (30011, 5, 256, "e4m3"),
+                                       (12345, 1, 80, "e5m2")])
+def test_large_write_is_the_small_writes(F, T, H, D, fmt):
+    """Calls large enough for slots that walk along tokens and for non-temporal accesses, against calls of 700
+    tokens; some tokens are padding."""
+    g = W.gen(T, DEV)
+    k, v = _rows(T, H, D, g), _rows(T, H, D, g)
+    pages = -(-T // 64) + 1
+    slots = torch.randperm(pages * 64, generator=g, device=DEV)[:T]
+    slots[::7] = -1
+    one, two = _fresh(F, pages, H, 64, D, fmt), _fresh(F, pages, H, 64, D, fmt)
+    F.fp8_kv_cache_write(k, v, slots, one)
+    for lo in range(0, T, 700):
+        F.fp8_kv_cache_write(k[lo:lo + 700], v[lo:lo + 700], slots[lo:lo + 700], two)
+    for a, b in zip((one.k_codes, one.v_codes, one.k_scales, one.v_scales),
+                    (two.k_codes, two.v_codes, two.k_scales, two.v_scales)):
+        assert torch.equal(a, b)
+
+
+def test_large_norm_rope_is_the_small_ones(F):
+    g = W.gen(17, DEV)
+    T = 4100
+    q, k = _rows(T, 20, 128, g), _rows(T, 3, 128, g)
+    tab, pos = _table(128, 99), torch.randint(0, 99, (T,), generator=g, device=DEV)
+    w = torch.rand(128, generator=g, device=DEV).bfloat16()
+    qo, ko = F.fp8_qk_norm_rope(q, k, tab, pos, w, w)
+    for lo in range(0, T, 500):
+        a, b = F.fp8_qk_norm_rope(q[lo:lo + 500], k[lo:lo + 500], tab, pos[lo:lo + 500], w, w)
+        assert torch.equal(qo[lo:lo + 500], a) and torch.equal(ko[lo:lo + 500], b)
+
+
 def test_cache_write_into_a_layer_of_a_shared_allocation(F):
     """K and V of three layers in one allocation, page by page; neighbours stay."""
     g = W.gen(9, DEV)
