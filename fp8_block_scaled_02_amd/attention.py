@@ -196,8 +196,8 @@ def fp8_qkv_cache_write(q, k, v, cos_sin, positions, slots, cache: KVCache, q_we
     """fp8_qk_norm_rope and fp8_kv_cache_write in one launch (the same bits):
     returns the queries, normed and rotated; the keys, normed and rotated,
     and the values go to the cache."""
-    return _call("qkv_write", cache._dev, cache._ref, cache._dev, q, k, v, cos_sin, positions, slots, q_weight, k_weight,
-                 eps, interleaved, q_out)
+    return _call("qkv_write", cache._dev, cache._ref, cache._dev, q, k, v, cos_sin, positions, slots, q_weight,
+                 k_weight, eps, interleaved, q_out)
 
 
 def fp8_kv_cache_read(cache: KVCache, block_table, offsets, rows: int, k_out=None, v_out=None):

@@ -139,12 +139,15 @@ fp8b_rope rope_of(int64_t D, int64_t T, const at::Tensor* cos_sin, const at::Ten
   return r;
 }
 
-// The caller's output, bf16 rows of x's shape; NULL for None.
+// The caller's output, bf16 rows of x's shape that lie apart (tokens outside
+// heads or heads outside tokens); NULL for None.
 const at::Tensor* given_rows(PyObject* o, const at::Tensor& x, const char* name) {
   const at::Tensor* t = maybe(o, name);
   if (t) {
     shape(*t, x.sizes(), name);
-    rows(*t, name);
+    const Rows r = rows(*t, name);
+    const bool apart = (r.h >= r.D && r.t >= (r.H - 1) * r.h + r.D) || (r.t >= r.D && r.h >= (r.T - 1) * r.t + r.D);
+    if (!apart && r.T > 0 && r.H > 0) refuse(std::string(name) + ": rows overlap");
   }
   return t;
 }
@@ -261,6 +264,8 @@ PyObject* cache_read(PyObject* const* a) {
   const char* names[2] = {"k_out", "v_out"};
   for (int i = 0; i < 2; ++i)
     if (given[i]) flat(*given[i], at::kBFloat16, {R, c->heads, c->head_dim}, names[i]);
+  if (given[0] && given[1] && R > 0 && given[0]->data_ptr() == given[1]->data_ptr())
+    refuse("k_out and v_out must be apart");
   on(dev, {&bt, &offsets, given[0], given[1]});
   void* stream = address(a[0]);
   at::Tensor out[2];

@@ -155,10 +155,11 @@ __device__ __forceinline__ u32x2 quantise_row(const u32x4& raw, float& d) {
 //
 // FMT: 0 no cache (keys to k_out), 1 E5M2, 2 E4M3.  ROPE: 0 none, 1 halves,
 // 2 interleaved.  STREAM: non-temporal loads.  HBM-bound (2 bytes in and 2, or
-// 1 and a scale, out per value), but only just: 8 values are one 16-byte load and some 150
-// instructions, so addresses are kept to 32-bit products.  Norm and rotation of
-// 4096 tokens x (64 + 8) x 128: 30.8 us, 4.98 TB/s; cache write of 32768 x 8 x
-// 128: 37.3 us, 5.46 TB/s; of one step's 32 tokens 2.3 us, which is the launch.
+// 1 and a scale, out per value), but only just: 8 values are one 16-byte load
+// and some 150 instructions, so addresses are kept to 32-bit products.  Norm
+// and rotation of 4096 tokens x (64 + 8) x 128: 30.8 us, 4.98 TB/s; cache write
+// of 32768 x 8 x 128: 37.3 us, 5.46 TB/s; of one step's 32 tokens 2.3 us, which
+// is the launch.
 template <int LPR, int ROPE, int FMT, bool STREAM>
 __global__ __launch_bounds__(256) void qkv_kernel(const QkvArgs a) {
   constexpr int kSlots = 256 / LPR;
@@ -202,15 +203,12 @@ __global__ __launch_bounds__(256) void qkv_kernel(const QkvArgs a) {
           // the first of a pair gets a c - b s, the second b c + a s
           sn[i] = e0 < half ? -tab[half + i0 + i] : tab[half + i0 + i];
         }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) cs[i] = 1.0f, sn[i] = 0.0f;
       }
-    } else {
+    } else if (e0 < a.rot) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        cs[i] = e0 < a.rot ? tab[(e0 >> 1) + i] : 1.0f;
-        sn[i] = e0 < a.rot ? tab[half + (e0 >> 1) + i] : 0.0f;
+        cs[i] = tab[(e0 >> 1) + i];
+        sn[i] = tab[half + (e0 >> 1) + i];
       }
     }
   }
@@ -262,10 +260,12 @@ __global__ __launch_bounds__(256) void qkv_kernel(const QkvArgs a) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) o[i] = __shfl(f[i], partner, LPR);
         }
-        // positions past rot: cos 1, sin 0
+        // positions past rot stay as they are, infinities too
+        if (e0 < a.rot) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = __builtin_fmaf(f[i], cs[i], o[i] * sn[i]);
-      } else if (ROPE == 2) {
+          for (int i = 0; i < 8; ++i) f[i] = __builtin_fmaf(f[i], cs[i], o[i] * sn[i]);
+        }
+      } else if (ROPE == 2 && e0 < a.rot) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float x = f[2 * i], y = f[2 * i + 1];

@@ -563,7 +563,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void attend_kernel(const AttnArgs a
           *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + at * a.D + d) =
               u32x2{__builtin_bit_cast(uint32_t, b0), __builtin_bit_cast(uint32_t, b1)};
         }
-        if (a.lse && d == 0) a.lse[at] = l > 0.0f ? (m + __log2f(l)) * 0.69314718056f : -__builtin_inff();
+        if (a.lse && d == 0) a.lse[at] = l == 0.0f ? -__builtin_inff() : (m + __log2f(l)) * 0.69314718056f;
       } else {
         *reinterpret_cast<v4f*>(part + (int64_t)rr * a.D + d) = o;
         if (d == 0) {
@@ -657,7 +657,7 @@ __global__ __launch_bounds__(256) void join_kernel(const AttnArgs a, int wgs, in
     *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + at * a.D + d) =
         u32x2{__builtin_bit_cast(uint32_t, b0), __builtin_bit_cast(uint32_t, b1)};
   }
-  if (a.lse && d == 0) a.lse[at] = l > 0.0f ? (m + __log2f(l)) * 0.69314718056f : -__builtin_inff();
+  if (a.lse && d == 0) a.lse[at] = l == 0.0f ? -__builtin_inff() : (m + __log2f(l)) * 0.69314718056f;
 }
 
 // ---- host -------------------------------------------------------------------

@@ -158,7 +158,8 @@ int fp8_qkv_cache_write(const void *q, int64_t q_t, int64_t q_h,
  *            rows, no fault).  Rows from offsets[B] on are left as they were.
  *   R        rows of the outputs; 0 is a no-op.  R < 2^24.
  *   B, cols  >= 1, <= 2^30; ld_table >= cols.
- *   k_out, v_out  bf16 contiguous [R][heads][head_dim], 16-byte aligned.
+ *   k_out, v_out  bf16 contiguous [R][heads][head_dim], 16-byte aligned,
+ *            apart from each other and from the inputs.
  */
 int fp8_kv_cache_read(const fp8b_kv_cache *cache, const int32_t *table,
                       int64_t ld_table, int64_t cols, const int32_t *offsets,
@@ -173,7 +174,8 @@ int fp8_kv_cache_read(const fp8b_kv_cache *cache, const int32_t *table,
  *   s_j = scale * sum_i q[b][h][i] * K[j][i]
  *   out[b][h] = sum_j e^(s_j - m) V[j] / sum_j e^(s_j - m),  m = max_j s_j
  *   lse[b][h] = m + ln(sum_j e^(s_j - m))
- * A row that sees nothing gives out 0 and lse -inf.  What lies in the pages
+ * A row that sees nothing, or only scores of -inf, gives out 0 and lse -inf;
+ * a NaN or +inf among the seen scores gives NaN.  What lies in the pages
  * outside the seen range, NaN codes or scales included, has no effect.
  * Products and sums are fp32; the weights e^(s_j - m) enter the products
  * with V split into bf16 parts that keep at least 16 (bf16 output) or 24
@@ -193,7 +195,8 @@ int fp8_kv_cache_read(const fp8b_kv_cache *cache, const int32_t *table,
  *   Hq       a multiple of cache->heads, at most 65536.
  *   scale    finite.
  *   out      contiguous [B][Hq][head_dim], bf16 or fp32 (out_dtype), 16-byte
- *            aligned.  lse: float [B][Hq] or NULL.
+ *            aligned.  lse: float [B][Hq] or NULL.  Neither may overlap the
+ *            inputs, the workspace or the other.
  *   workspace  fp8_paged_attention_workspace(...) bytes, 16-byte aligned;
  *            what it holds before the call does not matter.  Calls that may
  *            run at the same time need one each.  NULL where the size is 0.

@@ -70,6 +70,21 @@ def test_norm_rope_arguments():
     _raises("k_out must be 3-D bf16", f, q, k, tab, pos, k_out=torch.zeros(3, 2, 64))
 
 
+def test_outputs_lie_apart():
+    q, k = torch.zeros(3, 4, 64, dtype=bf16), torch.zeros(3, 2, 64, dtype=bf16)
+    f = F.fp8_qk_norm_rope
+    line = torch.zeros(4096, dtype=bf16)
+    _raises("q_out: rows overlap", f, q, k, q_out=q[:, :1].expand(3, 4, 64))
+    _raises("q_out: rows overlap", f, q, k, q_out=q[:1].expand(3, 4, 64))
+    _raises("q_out: rows overlap", f, q, k, q_out=line.as_strided((3, 4, 64), (256, 56, 1)))
+    _raises("k_out: rows overlap", f, q, k, k_out=line.as_strided((3, 2, 64), (120, 64, 1)))
+    for st in ((256, 64), (64, 192), (512, 72), (72, 256)):       # these do not: refused for the host's memory only
+        _raises("on a GPU", f, q, k, q_out=line.as_strided((3, 4, 64), (*st, 1)))
+    kv = torch.zeros(5, 2, 64, dtype=bf16)
+    _raises("apart", F.fp8_kv_cache_read, _HostCache(), torch.zeros(1, 4, dtype=i32), torch.zeros(2, dtype=i32), 5, kv,
+            kv)
+
+
 def test_cache_calls():
     c = _HostCache()
     q, k = torch.zeros(3, 4, 64, dtype=bf16), torch.zeros(3, 2, 64, dtype=bf16)

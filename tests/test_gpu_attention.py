@@ -127,6 +127,18 @@ def test_norm_of_zeros_and_position_ends(F):
     torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("D,rot,inter", [(64, 16, False), (128, 48, False), (256, 64, False), (80, 32, True)])
+def test_infinities_beyond_the_rotation_pass(F, D, rot, inter):
+    q = torch.ones(3, 2, D, device=DEV).bfloat16()
+    q[1, 0, rot:] = float("inf")
+    q[2, 1, rot + 1] = float("-inf")
+    k = q.clone()
+    tab, pos = _table(rot, 8), torch.tensor([1, 5, 7], device=DEV)
+    for o in F.fp8_qk_norm_rope(q, k, tab, pos, interleaved=inter):
+        assert torch.equal(o[..., rot:], q[..., rot:])
+        assert torch.isfinite(o[..., :rot]).all()
+
+
 # ---- writing and reading -----------------------------------------------------
 
 
@@ -524,6 +536,33 @@ def test_what_is_not_seen_has_no_effect(F, fmt, max_context):
         dirty.k_scales[bad] = float("inf")
         dirty.v_scales[bad] = float("-inf")
         assert torch.equal(F.fp8_paged_attention(q, dirty, table, lt, window=win, max_context=max_context), want)
+
+
+@pytest.mark.parametrize("max_context", [200, None])         # one workgroup a head; split and joined
+def test_nan_among_the_seen(F, max_context):
+    """A NaN in one query head, or in the K scale of a seen token, gives NaN there and nowhere else."""
+    g = W.gen(8, DEV)
+    lens = [150, 200, 37]
+    n_cols = 400
+    pages, table = _book([16 * n_cols] * 3, 16, g)
+    c = _filled(F, pages, 2, 16, 64, "e5m2", g)
+    q = torch.randn(3, 8, 64, generator=g, device=DEV).bfloat16()
+    lt = torch.tensor(lens, dtype=torch.int32, device=DEV)
+
+    def run():
+        lse = torch.empty(3, 8, device=DEV)
+        return F.fp8_paged_attention(q, c, table, lt, lse=lse, max_context=max_context), lse
+
+    want, want_l = run()
+    assert torch.isfinite(want).all() and torch.isfinite(want_l).all()
+    q[1, 5, 3] = float("nan")
+    c.k_scales[table[2, 1].long(), 0, 4] = float("nan")           # token 20 of sequence 2, KV head 0
+    bad = torch.zeros(3, 8, dtype=torch.bool, device=DEV)
+    bad[1, 5] = True
+    bad[2, :4] = True
+    out, lse = run()
+    assert torch.isnan(out[bad]).all() and torch.isnan(lse[bad]).all()
+    assert torch.equal(out[~bad], want[~bad]) and torch.equal(lse[~bad], want_l[~bad])
 
 
 def test_attention_pages_that_are_none(F):
