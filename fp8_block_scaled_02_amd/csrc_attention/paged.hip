@@ -43,10 +43,12 @@ namespace fp8attn {
 using namespace fp8blk;
 
 constexpr int kTile = 32;       // keys a wave takes at a time
-constexpr int kSplitShift = 2;  // log2 of the waves of a workgroup of a split launch
+constexpr int kSplitShift = 2;  // log2 of the waves of a workgroup that shares its regions with others
 constexpr int kMaxWaves = 8;    // and of any
-constexpr int kMaxWgs = 512;    // workgroups of a split launch: 2 for each of the 256 CUs
-constexpr int kMinTiles = 8;    // tiles (all waves together) a workgroup of a split launch takes at least
+constexpr int kMaxWgs = 512;    // pieces of the line: 2 for each of the 256 CUs
+constexpr int kMinTiles = 8;    // tiles (all waves together) of a piece of the line at least
+constexpr int kPartWgs = 256;   // workgroups that take parts of regions: 1 for each CU
+constexpr int kMinPart = 4;     // and the tiles of a part at least
 
 struct AttnArgs {
   const uint16_t* q;
@@ -67,7 +69,8 @@ struct AttnArgs {
   int out_f32;
   float* lse;
   float* ws;
-  int split;
+  int line;         // pieces of the line of all tiles; otherwise parts of each region
+  int parts_shift;  // log2 of the parts of a region
   int waves_shift;  // log2 of the waves of a workgroup
 };
 
@@ -148,6 +151,13 @@ __device__ __forceinline__ Line line_of(const AttnArgs& a, int wgs, int x) {
   return ln;
 }
 
+// Otherwise each region is cut into 2^parts_shift equal parts, a workgroup each:
+// so many tiles to a part, so a short region may have fewer.
+__device__ __forceinline__ int part_tiles(const AttnArgs& a, int tiles) {
+  const int per = (tiles + (1 << a.parts_shift) - 1) >> a.parts_shift;
+  return per > kMinPart ? per : kMinPart;
+}
+
 // Floats of a partial result: G rows of D, then G maxima, then G sums.
 __host__ __device__ inline int64_t partial_floats(int rows, int D) { return (int64_t)rows * (D + 2); }
 
@@ -161,16 +171,6 @@ __device__ __forceinline__ uint32_t widen2(uint32_t w) {
 __device__ __forceinline__ uint64_t lane_value(uint64_t v, int lane) {
   return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), lane) << 32 |
          (uint32_t)__builtin_amdgcn_readlane((int)v, lane);
-}
-
-// Over the four lanes that share lane % 16: each swap leaves one row of the
-// pair in the first result and the other in the second.
-__device__ __forceinline__ float swap_max(float v) {
-  typedef unsigned int u2 __attribute__((ext_vector_type(2)));
-  const u2 x = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  v = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
-  const u2 y = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  return fmaxf(__uint_as_float(y[0]), __uint_as_float(y[1]));
 }
 
 // A head's rows in page 0, and how far from there a half tile's (16 keys, all
@@ -253,6 +253,32 @@ struct State {
   float m, l;
   v4f o[DP / 16];
 };
+// The maximum before any score: finite, so that differences of maxima and masked
+// scores (-inf) are never NaN; no finite score is below it.
+constexpr float kLowest = -3.402823466e38f;
+
+// Maxima without the compiler's canonicalising copies (no operand is a
+// signalling NaN); a NaN operand is passed over, as by fmaxf.
+__device__ __forceinline__ float max2(float x, float y) {
+  float r;
+  asm("v_max_f32 %0, %1, %2" : "=v"(r) : "v"(x), "v"(y));
+  return r;
+}
+__device__ __forceinline__ float max3(float x, float y, float z) {
+  float r;
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(x), "v"(y), "v"(z));
+  return r;
+}
+
+// Over the four lanes that share lane % 16: each swap leaves one row of the
+// pair in the first result and the other in the second.
+__device__ __forceinline__ float swap_max(float v) {
+  typedef unsigned int u2 __attribute__((ext_vector_type(2)));
+  const u2 x = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = max2(__uint_as_float(x[0]), __uint_as_float(x[1]));
+  const u2 y = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return max2(__uint_as_float(y[0]), __uint_as_float(y[1]));
+}
 
 // s = K Q^T with scales, log2 domain, for QT tiles of 16 query heads.
 template <int DP, bool FULL, int FMT, int QT>
@@ -292,14 +318,10 @@ __device__ __forceinline__ void scores(const AttnArgs& a, const bf16x8 (&qf)[QT]
 // date.
 template <int DP>
 __device__ __forceinline__ void weights(float (&s)[8], State<DP>& st) {
-  float mx = s[0];
-#pragma unroll
-  for (int i = 1; i < 8; ++i) mx = fmaxf(mx, s[i]);
-  mx = swap_max(mx);
+  const float mx = swap_max(max2(max3(max3(max3(s[0], s[1], s[2]), s[3], s[4]), s[5], s[6]), s[7]));
   if (__any(mx > st.m)) {
-    const float m = fmaxf(st.m, mx);
-    // m is -inf only where nothing was seen yet: nothing to rescale
-    const float alpha = m == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(st.m - m);
+    const float m = max2(st.m, mx);
+    const float alpha = __builtin_amdgcn_exp2f(st.m - m);
     st.m = m;
     st.l *= alpha;
 #pragma unroll
@@ -307,10 +329,9 @@ __device__ __forceinline__ void weights(float (&s)[8], State<DP>& st) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) st.o[j][i] *= alpha;
   }
-  const float m = st.m == -__builtin_inff() ? 0.0f : st.m;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    s[i] = __builtin_amdgcn_exp2f(s[i] - m);
+    s[i] = __builtin_amdgcn_exp2f(s[i] - st.m);
     st.l += s[i];
   }
 }
@@ -329,6 +350,8 @@ __device__ __forceinline__ void accumulate(float (&p)[QT][8], const ValueRegs<DP
       for (int i = 0; i < 4; ++i) {
         const bf16x2 b = {(__bf16)p[q][2 * i], (__bf16)p[q][2 * i + 1]};
         pf[q][t][i] = __builtin_bit_cast(uint32_t, b);
+        // (as it is: the low half would be rounded a second time otherwise)
+        asm("" : "+v"(pf[q][t][i]));
         p[q][2 * i] -= __uint_as_float(pf[q][t][i] << 16);
         p[q][2 * i + 1] -= __uint_as_float(pf[q][t][i] & 0xffff0000u);
       }
@@ -448,11 +471,11 @@ __device__ __forceinline__ void run_tiles(const AttnArgs& a, const Span& sp, int
   turn(std::false_type{});
 }
 
-// One workgroup takes a piece of the line (split) or one region (not split).
-// In a piece, each region's tiles are dealt to the waves, whose results
-// are joined in LDS; a region that lies whole in the piece is put out, others
-// go to the workspace: slot 2w for the region the piece begins in, slot 2w+1
-// for the one it ends in.
+// One workgroup takes a piece of the line or a part of one region.  In a piece,
+// each region's tiles are dealt to the waves, whose results are joined in LDS; a
+// region that lies whole in the workgroup is put out, others go to the
+// workspace: of piece w of the line, slot 2w for the region it begins in, slot
+// 2w+1 for the one it ends in; of a part, the workgroup's slot.
 template <int DP, bool FULL, int FMT, int TERMS, int QT>
 __global__ __launch_bounds__(64 * kMaxWaves) void attend_kernel(const AttnArgs a) {
   extern __shared__ float lds[];
@@ -467,7 +490,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void attend_kernel(const AttnArgs a
 
   int b, region, tile, left;  // left: tiles of this piece still to do
   Span sp;
-  if (a.split) {
+  if (a.line) {
     const Line ln = line_of<true>(a, gridDim.x, blockIdx.x);
     b = ln.seq;
     if (b == a.B) return;
@@ -477,11 +500,17 @@ __global__ __launch_bounds__(64 * kMaxWaves) void attend_kernel(const AttnArgs a
     region = at / sp.tiles;
     tile = at - region * sp.tiles;
   } else {
-    b = blockIdx.x / R;
-    region = blockIdx.x - b * R;
+    const int x = blockIdx.x >> a.parts_shift;
+    b = x / R;
+    region = x - b * R;
     tile = 0;
     left = 0x7fffffff;
     sp = span_of(a, a.lens[b]);
+    if (a.parts_shift > 0) {  // (else the first page is looked up without waiting for the length)
+      left = part_tiles(a, sp.tiles);
+      tile = (blockIdx.x - (x << a.parts_shift)) * left;
+      if (tile >= sp.tiles) return;
+    }
   }
 
   for (;;) {
@@ -492,7 +521,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void attend_kernel(const AttnArgs a
     State<DP> st[QT];
 #pragma unroll
     for (int q = 0; q < QT; ++q) {
-      st[q].m = -__builtin_inff();
+      st[q].m = kLowest;
       st[q].l = 0.0f;
 #pragma unroll
       for (int j = 0; j < DP / 16; ++j) st[q].o[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
@@ -535,17 +564,19 @@ __global__ __launch_bounds__(64 * kMaxWaves) void attend_kernel(const AttnArgs a
     __syncthreads();
     const bool whole = count == sp.tiles;
     float* part = nullptr;
-    if (!whole) part = a.ws + (2 * (int64_t)blockIdx.x + (tile == 0 ? 1 : 0)) * partial_floats(rows_max, a.D);
+    if (!whole) {
+      const int64_t slot = a.line ? 2 * (int64_t)blockIdx.x + (tile == 0 ? 1 : 0) : blockIdx.x;
+      part = a.ws + slot * partial_floats(rows_max, a.D);
+    }
     const int q4 = a.D / 4;
     for (int x = tid; x < rows * q4; x += 64 << a.waves_shift) {
       const int rr = x / q4, d = 4 * (x - rr * q4);
       float m = lds_m[rr];
       for (int w = 1; w < waves; ++w) m = fmaxf(m, lds_m[w * rows_max + rr]);
-      const float ms = m == -__builtin_inff() ? 0.0f : m;
       float l = 0.0f;
       v4f o = {0.0f, 0.0f, 0.0f, 0.0f};
       for (int w = 0; w < waves; ++w) {
-        const float f = __builtin_amdgcn_exp2f(lds_m[w * rows_max + rr] - ms);
+        const float f = __builtin_amdgcn_exp2f(lds_m[w * rows_max + rr] - m);
         l = __builtin_fmaf(f, lds_l[w * rows_max + rr], l);
         const v4f ow = *reinterpret_cast<const v4f*>(lds + (w * rows_max + rr) * LD + d);
 #pragma unroll
@@ -574,7 +605,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void attend_kernel(const AttnArgs a
     }
     left -= count;
     tile = 0;
-    if (!a.split || left <= 0) return;
+    if (!a.line || left <= 0) return;
     __syncthreads();  // the next region's results go to the same LDS
     if (++region == R) {
       region = 0;
@@ -584,7 +615,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void attend_kernel(const AttnArgs a
   }
 }
 
-// Joins the partial results of the regions that several pieces share.  A
+// Joins the partial results of the regions that several workgroups share.  A
 // workgroup takes `rows_wg` rows (query heads; blockIdx.y: which) of a region,
 // D/4 threads a row and as many groups of pieces as threads are left.
 __global__ __launch_bounds__(256) void join_kernel(const AttnArgs a, int wgs, int rows_wg) {
@@ -595,27 +626,39 @@ __global__ __launch_bounds__(256) void join_kernel(const AttnArgs a, int wgs, in
   const int b = blockIdx.x / R, region = blockIdx.x - b * R;
   const int h = a.qtiles == 1 ? region : region / a.qtiles, qt = region - h * a.qtiles;
   const int rows = min(a.qrows, a.G - a.qrows * qt), rows_max = a.rows_max;
-  const Line ln = line_of<false>(a, wgs, b);
-  const int t0 = ln.begin + region * ln.span.tiles, t1 = t0 + ln.span.tiles;
-  const int w0 = t0 / ln.per, w1 = (t1 - 1) / ln.per;
-  if (w0 == w1) return;  // put out by the piece that held it whole
+  int n;           // of the partial results; number 0 is in slot first, k > 0 in next + k * step
+  int64_t first, next, step;
+  if (a.line) {
+    const Line ln = line_of<false>(a, wgs, b);
+    const int t0 = ln.begin + region * ln.span.tiles, t1 = t0 + ln.span.tiles;
+    const int w0 = t0 / ln.per;
+    n = (t1 - 1) / ln.per - w0 + 1;
+    first = 2 * (int64_t)w0 + 1;  // the first of them ends its piece in the region, the others begin theirs
+    next = 2 * (int64_t)w0;
+    step = 2;
+  } else {
+    const int tiles = span_of(a, a.lens[b]).tiles, per = part_tiles(a, tiles);
+    n = (tiles + per - 1) / per;
+    first = next = (int64_t)blockIdx.x << a.parts_shift;
+    step = 1;
+  }
+  if (n == 1) return;  // put out by the workgroup that held it whole
 
   const int64_t pf = partial_floats(rows_max, a.D);
   const int q4 = a.D / 4, groups = 256 / (q4 * rows_wg);
   const int d = 4 * (tid % q4), rr_wg = tid / q4 % rows_wg, grp = tid / q4 / rows_wg;
   const int rr = blockIdx.y * rows_wg + rr_wg;
   const bool on = grp < groups && rr < rows;
-  float m = -__builtin_inff(), l = 0.0f;
+  float m = kLowest, l = 0.0f;
   v4f o = {0.0f, 0.0f, 0.0f, 0.0f};
   if (on) {
 #pragma unroll 4
-    for (int w = w0 + grp; w <= w1; w += groups) {
-      // the first of them ends its piece in the region, the others begin theirs
-      const float* p = a.ws + (2 * (int64_t)w + (w == w0 ? 1 : 0)) * pf;
+    for (int k = grp; k < n; k += groups) {
+      const float* p = a.ws + (k == 0 ? first : next + k * step) * pf;
       const float pm = p[(int64_t)rows_max * a.D + rr], pl = p[(int64_t)rows_max * a.D + rows_max + rr];
       const v4f po = *reinterpret_cast<const v4f*>(p + (int64_t)rr * a.D + d);
-      const float nm = fmaxf(m, pm), ns = nm == -__builtin_inff() ? 0.0f : nm;
-      const float f0 = __builtin_amdgcn_exp2f(m - ns), f1 = __builtin_amdgcn_exp2f(pm - ns);
+      const float nm = fmaxf(m, pm);
+      const float f0 = __builtin_amdgcn_exp2f(m - nm), f1 = __builtin_amdgcn_exp2f(pm - nm);
       m = nm;
       l = l * f0 + pl * f1;
 #pragma unroll
@@ -632,13 +675,12 @@ __global__ __launch_bounds__(256) void join_kernel(const AttnArgs a, int wgs, in
     }
     __syncthreads();
     if (!on || grp != 0) return;
-    m = -__builtin_inff();
+    m = kLowest;
     for (int k = 0; k < groups; ++k) m = fmaxf(m, lds_ml[0][k * rows_wg + rr_wg]);
-    const float ms = m == -__builtin_inff() ? 0.0f : m;
     l = 0.0f;
     o = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     for (int k = 0; k < groups; ++k) {
-      const float f = __builtin_amdgcn_exp2f(lds_ml[0][k * rows_wg + rr_wg] - ms);
+      const float f = __builtin_amdgcn_exp2f(lds_ml[0][k * rows_wg + rr_wg] - m);
       l += f * lds_ml[1][k * rows_wg + rr_wg];
       const v4f ok = *reinterpret_cast<const v4f*>(lds + 4 * (k * rows_wg * q4 + tid));
 #pragma unroll
@@ -664,8 +706,8 @@ __global__ __launch_bounds__(256) void join_kernel(const AttnArgs a, int wgs, in
 
 struct Shape {
   int G, qrows, qtiles, rows;
-  int64_t regions, max_len, wgs;  // wgs: workgroups of a split launch; 0: one workgroup per region
-  int waves_shift;
+  int64_t regions, max_len, wgs;  // wgs: pieces of the line; 0: parts of each region
+  int waves_shift, parts_shift;
 };
 
 static Shape shape_of(const fp8b_kv_cache& c, int64_t B, int64_t Hq, int64_t cols, int64_t max_context,
@@ -685,23 +727,42 @@ static Shape shape_of(const fp8b_kv_cache& c, int64_t B, int64_t Hq, int64_t col
   // the most tiles a region can have: a window reaches into one more
   const int64_t seen = window > 0 && window < s.max_len ? window + kTile - 1 : s.max_len;
   const int64_t tiles = (seen + kTile - 1) / kTile;
-  // A CU works through a tile of each SIMD in about 0.85 us (128 positions),
-  // so one workgroup per region takes 4 + 0.21 tiles us, whatever its waves;
-  // splitting evens that out over the 256 CUs for about 5 us of a second
-  // launch.  Measured, direct / split us, 128 positions, up to 1.5 times as
-  // many tiles as on average: 8 regions of 32 tiles 10.2 / 9.4, of 63 16.3 /
-  // 12.1, of 125 28 / 12.5; 32 of 46 12.4 / 12.4; 128 of 46 14.5 / 17.3, of 121
-  // 29 / 24; 512 of 28 19 / 25, of 121 78 / 79, of 281 166 / 159.
-  const int64_t direct = s.regions / 2 < 48 ? 48 : (s.regions / 2 < 128 ? s.regions / 2 : 128);
-  if (tiles <= direct) {
-    // As many waves as there are tiles, up to 8; fewer where that leaves each
-    // only a few tiles and there are regions enough for 12 waves a CU without
-    // (2048 regions of 5 tiles: 1 / 2 / 4 / 8 waves 14.2 / 15.2 / 18 / 30 us;
-    // 272 of 33 tiles of 64 positions: 27 / 16 / 11.2 / 9.9).
-    s.wgs = 0;
-    s.waves_shift = 3;
+  // Three ways to deal out the work (us at 128 positions, lengths up to 1.5 times
+  // the average).
+  //
+  // Each region cut into as many equal parts as there are CUs for, and joined by a
+  // second launch, which costs about as much as 24 tiles in a row (12 of 256
+  // positions, 48 of 64): whole / in parts, 8 regions of 24 tiles 7.0 / 8.3, of 30
+  // 10.0 / 8.0, of 94 11.7 / 8.2; 64 of 47 14.0 / 11.1; 128 of 33 11.6 / 12.3, of 47
+  // 14.5 / 14.0.  Parts of 8 tiles at least: 8.6 and 11.0; 512 workgroups of two
+  // waves: 9.5 and 12.8, 256 of eight: 9.2 and 11.8.
+  const int body = c.head_dim <= 64 ? 64 : (c.head_dim <= 128 ? 128 : 256);
+  int parts_shift = 0;
+  while ((s.regions << (parts_shift + 1)) <= kPartWgs && (kMinPart << parts_shift) < tiles) ++parts_shift;
+  const int64_t saved = tiles - (tiles >> parts_shift);  // in a row, by the parts
+  // One workgroup per region while they are short: in a line of all tiles, cut
+  // evenly whatever the lengths, a launch costs about 5 us more but no CU waits
+  // for the longest region: whole / line, 512 regions of 28 tiles 19 / 25, of 121
+  // 78 / 79, of 281 166 / 159.
+  const int64_t whole = s.regions / 2 < 48 ? 48 : (s.regions / 2 < 128 ? s.regions / 2 : 128);
+  s.wgs = 0;
+  s.parts_shift = 0;
+  if (saved * body > 24 * 128 && tiles <= ((int64_t)64 << parts_shift)) {
+    // (in parts / line: 32 regions of 47 tiles 9.1 / 12.4, of 375 19.6 / 21.7; 64 of
+    // 188 19.7 / 20.8, of 375, 94 to a part, 33.7 / 33.1)
+    s.parts_shift = parts_shift;
+    s.waves_shift = kSplitShift;
+  } else if (tiles <= whole) {
+    // Four waves where 128 or 256 positions fill the body, else eight (64 regions of
+    // 24 tiles 4 / 8 waves 8.5 / 9.0, of 256 positions 13.4 / 14.4; 128 of 24 with 80
+    // positions 9.8 / 9.4, with 64 9.0 / 8.7), but not more than tiles; fewer where
+    // that leaves each only a few tiles and there are regions enough for 12 waves
+    // a CU without (2048 regions of 5 tiles: 1 / 2 / 4 / 8 waves 14.2 / 15.2 / 18 /
+    // 30; 272 of 33 tiles of 64 positions: 27 / 16 / 11.2 / 9.9, 512 of them 4 / 8
+    // waves 13.7 / 16.5).
+    s.waves_shift = c.head_dim == 128 || c.head_dim == 256 ? 2 : 3;
     while (s.waves_shift > 0 && ((1 << s.waves_shift) > tiles ||
-                                 ((4 << s.waves_shift) > tiles && (s.regions << s.waves_shift) > 12 * 256)))
+                                 ((5 << s.waves_shift) > tiles && (s.regions << s.waves_shift) > 12 * 256)))
       --s.waves_shift;
   } else {
     // Two workgroups of four waves a CU: with 4 (1024 workgroups) a third of
@@ -719,7 +780,8 @@ static Shape shape_of(const fp8b_kv_cache& c, int64_t B, int64_t Hq, int64_t col
 int64_t attention_workspace(const fp8b_kv_cache& c, int64_t B, int64_t Hq, int64_t cols, int64_t max_context,
                             int64_t window) {
   const Shape s = shape_of(c, B, Hq, cols, max_context, window);
-  return 2 * s.wgs * partial_floats(s.rows, (int)c.head_dim) * (int64_t)sizeof(float);
+  const int64_t slots = s.wgs > 0 ? 2 * s.wgs : (s.parts_shift > 0 ? s.regions << s.parts_shift : 0);
+  return slots * partial_floats(s.rows, (int)c.head_dim) * (int64_t)sizeof(float);
 }
 
 template <int DP, bool FULL, int FMT, int TERMS, int QT>
@@ -773,10 +835,11 @@ int launch_attention(const fp8b_kv_cache& c, const Attention& p, hipStream_t s) 
   a.out_f32 = p.out_f32;
   a.lse = p.lse;
   a.ws = p.workspace;
-  a.split = sh.wgs > 0;
+  a.line = sh.wgs > 0;
+  a.parts_shift = sh.parts_shift;
   a.waves_shift = sh.waves_shift;
   a.cols = (int)p.cols;
-  const unsigned grid = (unsigned)(sh.wgs > 0 ? sh.wgs : sh.regions);
+  const unsigned grid = (unsigned)(sh.wgs > 0 ? sh.wgs : sh.regions << sh.parts_shift);
   int rc;
   // Bodies of 64, 128 and 256 positions; one that D fills asks nothing about D
   // (2-5% faster on short contexts, 1% on long ones).  192 positions go through
@@ -787,12 +850,12 @@ int launch_attention(const fp8b_kv_cache& c, const Attention& p, hipStream_t s) 
   else if (a.D < 128) rc = launch_dp<128, false>(a, c.fmt, grid, s);
   else if (a.D == 256) rc = launch_dp<256, true>(a, c.fmt, grid, s);
   else rc = launch_dp<256, false>(a, c.fmt, grid, s);
-  if (rc != FP8B_OK || !a.split) return rc;
+  if (rc != FP8B_OK || (!a.line && a.parts_shift == 0)) return rc;
   // Few pieces to a region: its rows side by side in a workgroup (128 x 6000 x 8
   // heads 313 us, 325 with a row each).  Many: one row, the threads shared out
   // over the pieces (131072 x 8 heads 60 us, 69 with the rows side by side).
   const int fit = 256 / (a.D / 4);
-  const int rows_wg = sh.wgs <= 4 * sh.regions ? (sh.rows < fit ? sh.rows : fit) : 1;
+  const int rows_wg = grid <= 4 * sh.regions ? (sh.rows < fit ? sh.rows : fit) : 1;
   const dim3 jgrid((unsigned)sh.regions, (unsigned)((sh.rows + rows_wg - 1) / rows_wg));
   hipLaunchKernelGGL(join_kernel, jgrid, dim3(256), 0, s, a, (int)grid, rows_wg);
   return check_launch();

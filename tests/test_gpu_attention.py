@@ -421,6 +421,21 @@ def test_attention_long_context_is_split_and_joined(F):
     _check_attention(F, c, lens, q, table, max_context=4096)
 
 
+@pytest.mark.parametrize("fmt", ["e5m2", "e4m3"])
+@pytest.mark.parametrize("Hq,H,D,window", [(8, 2, 128, 0), (4, 1, 64, 1700), (9, 3, 80, 0), (3, 1, 256, 0), (20, 1, 128, 0),
+                                           (8, 2, 128, 1500)])
+def test_attention_of_regions_in_parts(F, Hq, H, D, window, fmt):
+    """Few regions of some length: each in equal parts, also where lengths leave most parts nothing."""
+    g = W.gen(21, DEV)
+    lens = [2000, 0, 1, 31, 33, 127, 129, 130, 640, 1999]
+    pages, table = _book([2000] * len(lens), 32, g)
+    c = _filled(F, pages, H, 32, D, fmt, g)
+    q = torch.randn(len(lens), Hq, D, generator=g, device=DEV).bfloat16()
+    _check_attention(F, c, lens, q, table, window=window, out_dtype=torch.float32)
+    _check_attention(F, c, lens[:1], q[:1], table[:1], window=window)
+    _check_attention(F, c, lens[2:5], q[2:5], table[2:5], window=window, max_context=1100)
+
+
 def test_attention_many_sequences(F):
     """More sequences than a wave has lanes, and more regions than workgroups."""
     g = W.gen(3, DEV)
