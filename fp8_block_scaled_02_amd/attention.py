@@ -62,6 +62,9 @@ def attn_lib():
         L.fp8_paged_attention.restype = ci
         L.fp8_paged_attention.argtypes = rows + [vp, vp, i64, i64, vp, i64, i64, i64, i64, ctypes.c_float, vp, ci, vp,
                                                  vp, vp]
+        L.fp8_attention_step.restype = ci
+        L.fp8_attention_step.argtypes = (rows + rows + rows + [vp, i64, i64, vp, vp, vp, i64, i64, vp, i64, i64,
+                                                               ctypes.c_float] + rows + [vp, ci, vp, vp, vp])
         _attn_lib = L
     return _attn_lib
 
@@ -102,7 +105,7 @@ def _call(fn, dev, *args):
 
 
 _C_NAMES = {"norm_rope": "fp8_qk_norm_rope", "cache_write": "fp8_kv_cache_write", "qkv_write": "fp8_qkv_cache_write",
-            "cache_read": "fp8_kv_cache_read", "attention": "fp8_paged_attention"}
+            "cache_read": "fp8_kv_cache_read", "attention": "fp8_paged_attention", "step": "fp8_attention_step"}
 
 
 class KVCache:
@@ -231,7 +234,9 @@ def attention_step(q, k, v, cos_sin, positions, slots, cache: KVCache, block_tab
     """The attention side of one decode step, between the q/k/v projection
     and the output projection: norm and rotate the new token's queries and
     keys, quantise its K and V into the cache, attend.  context_lens counts
-    the new token.  Returns out [B, Hq, D]."""
-    q = fp8_qkv_cache_write(q, k, v, cos_sin, positions, slots, cache, q_weight, k_weight, eps, interleaved)
-    return fp8_paged_attention(q, cache, block_table, context_lens, scale, window, out_dtype,
-                               max_context=max_context)
+    the new token.  Every argument is checked before anything is written.
+    Returns out [B, Hq, D]."""
+    if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
+        raise ValueError("out_dtype must be bfloat16 or float32")
+    return _call("step", cache._dev, cache._ref, cache._dev, q, k, v, cos_sin, positions, slots, q_weight, k_weight, eps,
+                 interleaved, block_table, context_lens, scale, window, out_dtype is torch.float32, max_context)

@@ -62,6 +62,25 @@ fp8attn::Rows rows(const void* p, int64_t t, int64_t h, int64_t heads) {
   return {static_cast<const uint16_t*>(p), t, h, (int)heads};
 }
 
+// The arrays of a fused write.
+struct QkvWrite {
+  fp8attn::Rows q, k, v, q_out;
+};
+int qkv_write_check(const QkvWrite& w, const int64_t* slots, const fp8b_rope* rope, const fp8b_kv_cache* cache) {
+  int rc = rope_check(rope, cache->head_dim);
+  for (const fp8attn::Rows* r : {&w.q, &w.k, &w.v, &w.q_out})
+    if (rc == FP8B_OK) rc = rows_check(r->p, r->t, r->h);
+  if (rc == FP8B_OK) rc = cache_pointers(cache);
+  if (rc != FP8B_OK) return rc;
+  if (!slots) return FP8B_EINVAL;
+  return aligned(slots, 8) ? FP8B_OK : FP8B_EALIGN;
+}
+int qkv_write(const QkvWrite& w, const int64_t* slots, int64_t T, const fp8b_rope* rope, const fp8b_kv_cache* cache,
+              void* stream) {
+  return fp8attn::launch_qkv(w.q, w.k, w.v, T, (int)cache->head_dim, rope, w.q_out, rows(nullptr, 0, 0, 0), slots,
+                             cache, as_stream(stream));
+}
+
 int attention_sizes(const fp8b_kv_cache* c, int64_t B, int64_t Hq, int64_t cols, int64_t max_context,
                     int64_t window) {
   const int rc = cache_sizes(c);
@@ -74,6 +93,24 @@ int attention_sizes(const fp8b_kv_cache* c, int64_t B, int64_t Hq, int64_t cols,
   // (the pieces of a split launch may end up to 512 tiles past the last one)
   if (regions >= kMaxRegions || regions * (tokens / 32 + 1) > INT32_MAX - 1024) return FP8B_EINVAL;
   return FP8B_OK;
+}
+
+int attention_check(const fp8attn::Attention& a, const fp8b_kv_cache* c, int out_dtype) {
+  if (out_dtype != FP8B_OUT_F32 && out_dtype != FP8B_OUT_BF16) return FP8B_EUNSUPPORTED;
+  const int rc = attention_sizes(c, a.B, a.Hq, a.cols, a.max_context, a.window);
+  if (rc != FP8B_OK) return rc;
+  return isfinite(a.scale) && a.ld_table >= a.cols && a.ld_table <= kMaxStride ? FP8B_OK : FP8B_EINVAL;
+}
+int attention_pointers(const fp8attn::Attention& a, const fp8b_kv_cache* c) {
+  int rc = rows_check(a.q, a.q_b, a.q_h);
+  if (rc == FP8B_OK) rc = cache_pointers(c);
+  if (rc != FP8B_OK) return rc;
+  if (!a.table || !a.lens || !a.out) return FP8B_EINVAL;
+  if (!aligned(a.table, 4) || !aligned(a.lens, 4) || !aligned(a.out, 16) || !aligned(a.lse, 4) ||
+      !aligned(a.workspace, 16))
+    return FP8B_EALIGN;
+  const bool needed = fp8attn::attention_workspace(*c, a.B, a.Hq, a.cols, a.max_context, a.window) > 0;
+  return a.workspace || !needed ? FP8B_OK : FP8B_EINVAL;
 }
 
 }  // namespace
@@ -128,17 +165,10 @@ FP8B_EXPORT int fp8_qkv_cache_write(const void* q, int64_t q_t, int64_t q_h, con
   FP8B_TRY(cache_sizes(cache));
   if (T < 0 || T > kMaxTokens || Hq < 1 || Hq > kMaxHeads) return FP8B_EINVAL;
   if (T == 0) return FP8B_OK;  // nothing is read or written; empty arrays may be NULL
-  FP8B_TRY(rope_check(rope, cache->head_dim));
-  FP8B_TRY(rows_check(q, q_t, q_h));
-  FP8B_TRY(rows_check(k, k_t, k_h));
-  FP8B_TRY(rows_check(v, v_t, v_h));
-  FP8B_TRY(rows_check(q_out, qo_t, qo_h));
-  FP8B_TRY(cache_pointers(cache));
-  if (!slots) return FP8B_EINVAL;
-  if (!aligned(slots, 8)) return FP8B_EALIGN;
-  return fp8attn::launch_qkv(rows(q, q_t, q_h, Hq), rows(k, k_t, k_h, cache->heads), rows(v, v_t, v_h, cache->heads),
-                             T, (int)cache->head_dim, rope, rows(q_out, qo_t, qo_h, Hq), rows(nullptr, 0, 0, 0), slots,
-                             cache, as_stream(stream));
+  const QkvWrite w = {rows(q, q_t, q_h, Hq), rows(k, k_t, k_h, cache->heads), rows(v, v_t, v_h, cache->heads),
+                      rows(q_out, qo_t, qo_h, Hq)};
+  FP8B_TRY(qkv_write_check(w, slots, rope, cache));
+  return qkv_write(w, slots, T, rope, cache, stream);
 }
 
 FP8B_EXPORT int fp8_kv_cache_read(const fp8b_kv_cache* cache, const int32_t* table, int64_t ld_table, int64_t cols,
@@ -166,33 +196,31 @@ FP8B_EXPORT int fp8_paged_attention(const void* q, int64_t q_b, int64_t q_h, con
                                     const int32_t* table, int64_t ld_table, int64_t cols, const int32_t* lens,
                                     int64_t B, int64_t Hq, int64_t max_context, int64_t window, float scale, void* out,
                                     int out_dtype, float* lse, void* workspace, void* stream) {
-  if (out_dtype != FP8B_OUT_F32 && out_dtype != FP8B_OUT_BF16) return FP8B_EUNSUPPORTED;
-  FP8B_TRY(attention_sizes(cache, B, Hq, cols, max_context, window));
-  if (!isfinite(scale) || ld_table < cols || ld_table > kMaxStride) return FP8B_EINVAL;
+  const fp8attn::Attention a = {static_cast<const uint16_t*>(q), q_b, q_h, table, ld_table, cols, lens, B, Hq,
+                                max_context, window, scale, out, out_dtype == FP8B_OUT_F32, lse,
+                                static_cast<float*>(workspace)};
+  FP8B_TRY(attention_check(a, cache, out_dtype));
   if (B == 0) return FP8B_OK;  // nothing is read or written; empty arrays may be NULL
-  FP8B_TRY(rows_check(q, q_b, q_h));
-  FP8B_TRY(cache_pointers(cache));
-  if (!table || !lens || !out) return FP8B_EINVAL;
-  if (!aligned(table, 4) || !aligned(lens, 4) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(workspace, 16))
-    return FP8B_EALIGN;
-  if (!workspace && fp8attn::attention_workspace(*cache, B, Hq, cols, max_context, window) > 0) return FP8B_EINVAL;
-  fp8attn::Attention a{};
-  a.q = static_cast<const uint16_t*>(q);
-  a.q_b = q_b;
-  a.q_h = q_h;
-  a.table = table;
-  a.ld_table = ld_table;
-  a.cols = cols;
-  a.lens = lens;
-  a.B = B;
-  a.Hq = Hq;
-  a.max_context = max_context;
-  a.window = window;
-  a.scale = scale;
-  a.out = out;
-  a.out_f32 = out_dtype == FP8B_OUT_F32;
-  a.lse = lse;
-  a.workspace = static_cast<float*>(workspace);
+  FP8B_TRY(attention_pointers(a, cache));
+  return fp8attn::launch_attention(*cache, a, as_stream(stream));
+}
+
+FP8B_EXPORT int fp8_attention_step(const void* q, int64_t q_b, int64_t q_h, const void* k, int64_t k_b, int64_t k_h,
+                                   const void* v, int64_t v_b, int64_t v_h, const int64_t* slots, int64_t B,
+                                   int64_t Hq, const fp8b_rope* rope, const fp8b_kv_cache* cache,
+                                   const int32_t* table, int64_t ld_table, int64_t cols, const int32_t* lens,
+                                   int64_t max_context, int64_t window, float scale, void* q_out, int64_t qo_b,
+                                   int64_t qo_h, void* out, int out_dtype, float* lse, void* workspace, void* stream) {
+  const fp8attn::Attention a = {static_cast<const uint16_t*>(q_out), qo_b, qo_h, table, ld_table, cols, lens, B, Hq,
+                                max_context, window, scale, out, out_dtype == FP8B_OUT_F32, lse,
+                                static_cast<float*>(workspace)};
+  FP8B_TRY(attention_check(a, cache, out_dtype));
+  if (B == 0) return FP8B_OK;  // nothing is read or written; empty arrays may be NULL
+  const QkvWrite w = {rows(q, q_b, q_h, Hq), rows(k, k_b, k_h, cache->heads), rows(v, v_b, v_h, cache->heads),
+                      rows(q_out, qo_b, qo_h, Hq)};
+  FP8B_TRY(qkv_write_check(w, slots, rope, cache));
+  FP8B_TRY(attention_pointers(a, cache));
+  FP8B_TRY(qkv_write(w, slots, B, rope, cache, stream));
   return fp8attn::launch_attention(*cache, a, as_stream(stream));
 }
 

@@ -214,29 +214,41 @@ PyObject* cache_write(PyObject* const* a) {
   }));
 }
 
+// What a fused write takes, from (q, k, v, cos_sin, positions, slots, q_weight,
+// k_weight, eps, interleaved).
+struct QkvWrite {
+  const at::Tensor &q, &k, &v, &slots;
+  const at::Tensor *cs, *pos, *qw, *kw;
+  Rows qr, kr, vr;
+  fp8b_rope r;
+  const int64_t* s;
+  QkvWrite(const fp8b_kv_cache* c, PyObject* const* a)
+      : q(tensor(a[0], "q")), k(tensor(a[1], "k")), v(tensor(a[2], "v")), slots(tensor(a[5], "slots")),
+        cs(maybe(a[3], "cos_sin")), pos(maybe(a[4], "positions")), qw(maybe(a[6], "q_weight")),
+        kw(maybe(a[7], "k_weight")), qr(rows(q, "q")) {
+    kv_rows(k, v, c, kr, vr);
+    if (qr.T != kr.T || qr.D != c->head_dim)
+      refuse("q must be [" + std::to_string(kr.T) + ", Hq, " + std::to_string(c->head_dim) + "]");
+    r = rope_of(qr.D, qr.T, cs, pos, qw, kw, number(a[8]), truth(a[9]));
+    s = static_cast<const int64_t*>(flat(slots, at::kLong, {qr.T}, "slots"));
+  }
+  void all_on(int64_t dev) const { on(dev, {&q, &k, &v, cs, pos, &slots, qw, kw}); }
+};
+
 // (stream, cache, dev, q, k, v, cos_sin, positions, slots, q_weight, k_weight, eps, interleaved, q_out) -> q_out
 PyObject* qkv_write(PyObject* const* a) {
   const fp8b_kv_cache* c = cache_of(a[1]);
   const int64_t dev = integer(a[2]);
-  const at::Tensor &q = tensor(a[3], "q"), &k = tensor(a[4], "k"), &v = tensor(a[5], "v");
-  const Rows qr = rows(q, "q");
-  Rows kr, vr;
-  kv_rows(k, v, c, kr, vr);
-  if (qr.T != kr.T || qr.D != c->head_dim)
-    refuse("q must be [" + std::to_string(kr.T) + ", Hq, " + std::to_string(c->head_dim) + "]");
-  const at::Tensor *cs = maybe(a[6], "cos_sin"), *pos = maybe(a[7], "positions"), *qw = maybe(a[9], "q_weight"),
-                   *kw = maybe(a[10], "k_weight");
-  const at::Tensor& slots = tensor(a[8], "slots");
-  const fp8b_rope r = rope_of(qr.D, qr.T, cs, pos, qw, kw, number(a[11]), truth(a[12]));
-  const void* s = flat(slots, at::kLong, {qr.T}, "slots");
-  const at::Tensor* gq = given_rows(a[13], q, "q_out");
-  on(dev, {&q, &k, &v, cs, pos, &slots, qw, kw, gq});
+  const QkvWrite w(c, a + 3);
+  const at::Tensor* gq = given_rows(a[13], w.q, "q_out");
+  w.all_on(dev);
+  on(dev, {gq});
   void* stream = address(a[0]);
-  const at::Tensor qo = gq ? *gq : at::empty(q.sizes(), q.options());
-  const Rows qor = rows(qo, "q_out");
+  const at::Tensor qo = gq ? *gq : at::empty(w.q.sizes(), w.q.options());
+  const Rows o = rows(qo, "q_out");
   const int rc = launch([&] {
-    return fp8_qkv_cache_write(qr.p, qr.t, qr.h, kr.p, kr.t, kr.h, vr.p, vr.t, vr.h, static_cast<const int64_t*>(s),
-                               qr.T, qr.H, &r, c, qor.p, qor.t, qor.h, stream);
+    return fp8_qkv_cache_write(w.qr.p, w.qr.t, w.qr.h, w.kr.p, w.kr.t, w.kr.h, w.vr.p, w.vr.t, w.vr.h, w.s, w.qr.T,
+                               w.qr.H, &w.r, c, o.p, o.t, o.h, stream);
   });
   return rc ? status(rc) : THPVariable_Wrap(qo);
 }
@@ -278,44 +290,83 @@ PyObject* cache_read(PyObject* const* a) {
   return rc ? status(rc) : pair(out[0], out[1]);
 }
 
+// What an attention takes beside its queries r, from (block_table, context_lens,
+// scale, window, fp32) and max_context.
+struct Attention {
+  const at::Tensor &bt, &lens;
+  Table t;
+  const int32_t* lp;
+  double scale;
+  int64_t window, most;
+  at::ScalarType type;
+  Attention(const fp8b_kv_cache* c, const Rows& r, PyObject* const* a, PyObject* max_context)
+      : bt(tensor(a[0], "block_table")), lens(tensor(a[1], "context_lens")) {
+    constexpr int64_t kMaxContext = (int64_t)1 << 30;
+    if (r.D != c->head_dim) refuse("q must be [B, Hq, " + std::to_string(c->head_dim) + "]");
+    if (r.H < 1 || r.H % c->heads != 0)
+      refuse("query heads must be a multiple of the cache's " + std::to_string(c->heads));
+    t = table_of(bt);
+    if (t.B != r.T) refuse("block_table must have " + std::to_string(r.T) + " rows");
+    lp = static_cast<const int32_t*>(flat(lens, at::kInt, {r.T}, "context_lens"));
+    scale = a[2] == Py_None ? 1.0 / std::sqrt((double)r.D) : number(a[2]);
+    window = integer(a[3]);
+    type = truth(a[4]) ? at::kFloat : at::kBFloat16;
+    most = max_context == Py_None ? std::min(t.cols * c->page_size, kMaxContext) : integer(max_context);
+    if (most < 0 || most > kMaxContext) refuse("max_context must be from 0 to " + std::to_string(kMaxContext));
+    if (window < 0) refuse("window must be 0 or a number of tokens");
+  }
+  int dtype() const { return type == at::kFloat ? FP8B_OUT_F32 : FP8B_OUT_BF16; }
+};
+// Of `bytes` on the current stream, like the call that uses it.
+at::Tensor workspace(int64_t bytes, const at::Tensor& q) {
+  return bytes > 0 ? at::empty({bytes}, q.options().dtype(at::kByte)) : at::Tensor();
+}
+
 // (stream, cache, dev, q, block_table, context_lens, scale, window, fp32, out, lse, max_context) -> out
 PyObject* attention(PyObject* const* a) {
-  constexpr int64_t kMaxContext = (int64_t)1 << 30;
   const fp8b_kv_cache* c = cache_of(a[1]);
   const int64_t dev = integer(a[2]);
-  const at::Tensor &q = tensor(a[3], "q"), &bt = tensor(a[4], "block_table"), &lens = tensor(a[5], "context_lens");
+  const at::Tensor& q = tensor(a[3], "q");
   const Rows r = rows(q, "q");
-  if (r.D != c->head_dim) refuse("q must be [B, Hq, " + std::to_string(c->head_dim) + "]");
-  if (r.H < 1 || r.H % c->heads != 0)
-    refuse("query heads must be a multiple of the cache's " + std::to_string(c->heads));
-  const Table t = table_of(bt);
-  if (t.B != r.T) refuse("block_table must have " + std::to_string(r.T) + " rows");
-  const void* lp = flat(lens, at::kInt, {r.T}, "context_lens");
-  const double scale = a[6] == Py_None ? 1.0 / std::sqrt((double)r.D) : number(a[6]);
-  const int64_t window = integer(a[7]);
-  const bool f32 = truth(a[8]);
-  const at::ScalarType type = f32 ? at::kFloat : at::kBFloat16;
+  const Attention x(c, r, a + 4, a[11]);
   const at::Tensor *given = maybe(a[9], "out"), *lse = maybe(a[10], "lse");
-  if (given) flat(*given, type, {r.T, r.H, r.D}, "out");
-  void* lsep = lse ? flat(*lse, at::kFloat, {r.T, r.H}, "lse") : nullptr;
-  int64_t most = kMaxContext;
-  if (a[11] == Py_None) most = std::min(t.cols * c->page_size, kMaxContext);
-  else most = integer(a[11]);
-  if (most < 0 || most > kMaxContext) refuse("max_context must be from 0 to " + std::to_string(kMaxContext));
-  if (window < 0) refuse("window must be 0 or a number of tokens");
-  on(dev, {&q, &bt, &lens, given, lse});
-  const int64_t bytes = fp8_paged_attention_workspace(c, r.T, r.H, t.cols, most, window);
+  if (given) flat(*given, x.type, {r.T, r.H, r.D}, "out");
+  float* lsep = lse ? static_cast<float*>(flat(*lse, at::kFloat, {r.T, r.H}, "lse")) : nullptr;
+  on(dev, {&q, &x.bt, &x.lens, given, lse});
+  const int64_t bytes = fp8_paged_attention_workspace(c, r.T, r.H, x.t.cols, x.most, x.window);
   if (bytes < 0) return status(bytes);
   void* stream = address(a[0]);
-  const at::Tensor out = given ? *given : at::empty({r.T, r.H, r.D}, q.options().dtype(type));
-  // on the current stream, like the call that uses it
-  at::Tensor ws;
-  if (bytes > 0) ws = at::empty({bytes}, q.options().dtype(at::kByte));
+  const at::Tensor out = given ? *given : at::empty({r.T, r.H, r.D}, q.options().dtype(x.type));
+  const at::Tensor ws = workspace(bytes, q);
   void *outp = out.data_ptr(), *wsp = bytes > 0 ? ws.data_ptr() : nullptr;
   const int rc = launch([&] {
-    return fp8_paged_attention(r.p, r.t, r.h, c, t.p, t.ld, t.cols, static_cast<const int32_t*>(lp), r.T, r.H, most,
-                               window, (float)scale, outp, f32 ? FP8B_OUT_F32 : FP8B_OUT_BF16,
-                               static_cast<float*>(lsep), wsp, stream);
+    return fp8_paged_attention(r.p, r.t, r.h, c, x.t.p, x.t.ld, x.t.cols, x.lp, r.T, r.H, x.most, x.window,
+                               (float)x.scale, outp, x.dtype(), lsep, wsp, stream);
+  });
+  return rc ? status(rc) : THPVariable_Wrap(out);
+}
+
+// (stream, cache, dev, q, k, v, cos_sin, positions, slots, q_weight, k_weight, eps, interleaved, block_table,
+// context_lens, scale, window, fp32, max_context) -> out
+PyObject* step(PyObject* const* a) {
+  const fp8b_kv_cache* c = cache_of(a[1]);
+  const int64_t dev = integer(a[2]);
+  const QkvWrite w(c, a + 3);
+  const Rows& r = w.qr;
+  const Attention x(c, r, a + 13, a[18]);
+  w.all_on(dev);
+  on(dev, {&x.bt, &x.lens});
+  const int64_t bytes = fp8_paged_attention_workspace(c, r.T, r.H, x.t.cols, x.most, x.window);
+  if (bytes < 0) return status(bytes);
+  void* stream = address(a[0]);
+  const at::Tensor qo = at::empty({r.T, r.H, r.D}, w.q.options());
+  const at::Tensor out = at::empty({r.T, r.H, r.D}, w.q.options().dtype(x.type));
+  const at::Tensor ws = workspace(bytes, w.q);
+  void *qop = qo.data_ptr(), *outp = out.data_ptr(), *wsp = bytes > 0 ? ws.data_ptr() : nullptr;
+  const int rc = launch([&] {
+    return fp8_attention_step(r.p, r.t, r.h, w.kr.p, w.kr.t, w.kr.h, w.vr.p, w.vr.t, w.vr.h, w.s, r.T, r.H, &w.r, c,
+                              x.t.p, x.t.ld, x.t.cols, x.lp, x.most, x.window, (float)x.scale, qop, r.H * r.D, r.D,
+                              outp, x.dtype(), nullptr, wsp, stream);
   });
   return rc ? status(rc) : THPVariable_Wrap(out);
 }
@@ -343,7 +394,8 @@ PyMethodDef method(const char* name) {
 
 PyMethodDef methods[] = {method<norm_rope, 11>("norm_rope"),   method<cache_write, 6>("cache_write"),
                          method<qkv_write, 14>("qkv_write"),   method<cache_read, 8>("cache_read"),
-                         method<attention, 12>("attention"),   {nullptr, nullptr, 0, nullptr}};
+                         method<attention, 12>("attention"),   method<step, 19>("step"),
+                         {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_attn_binding", "Host side of attention.py's calls.", -1, methods,
                       nullptr, nullptr, nullptr, nullptr};

@@ -217,6 +217,24 @@ int fp8_paged_attention(const void *q, int64_t q_b, int64_t q_h,
                         int64_t window, float scale, void *out, int out_dtype,
                         float *lse, void *workspace, void *stream);
 
+/*
+ * fp8_attention_step -- the attention side of a decode step, B sequences with
+ * one new token each: fp8_qkv_cache_write of the tokens (T = B), then
+ * fp8_paged_attention of the queries in q_out; lens counts the new tokens.
+ * Bit-identical to the two calls, with every argument checked before anything
+ * is written.  The workspace is fp8_paged_attention's for the same sizes.
+ */
+int fp8_attention_step(const void *q, int64_t q_b, int64_t q_h, const void *k,
+                       int64_t k_b, int64_t k_h, const void *v, int64_t v_b,
+                       int64_t v_h, const int64_t *slots, int64_t B,
+                       int64_t Hq, const fp8b_rope *rope,
+                       const fp8b_kv_cache *cache, const int32_t *table,
+                       int64_t ld_table, int64_t cols, const int32_t *lens,
+                       int64_t max_context, int64_t window, float scale,
+                       void *q_out, int64_t qo_b, int64_t qo_h, void *out,
+                       int out_dtype, float *lse, void *workspace,
+                       void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -11,7 +11,7 @@ ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 HEADER = os.path.join(ROOT, "include", "fp8attn.h")
 
 ENTRIES = ["fp8b_attn_abi_version", "fp8_qk_norm_rope", "fp8_kv_cache_write", "fp8_qkv_cache_write",
-           "fp8_kv_cache_read", "fp8_paged_attention_workspace", "fp8_paged_attention"]
+           "fp8_kv_cache_read", "fp8_paged_attention_workspace", "fp8_paged_attention", "fp8_attention_step"]
 OK, EINVAL, EALIGN, EUNSUPPORTED = 0, -1, -2, -3
 GOOD, ODD = 1 << 20, (1 << 20) + 2       # never dereferenced here
 
@@ -179,6 +179,29 @@ def test_attention_refusals(M, L):
         assert f(*_with(args, cache=_byref(bad))) == rc, over
         assert w(*_with(base, cache=_byref(bad))) == rc, over
     for over, rc in BAD_POINTERS:
+        bad = _cache(M, **over)
+        assert f(*_with(args, cache=_byref(bad))) == rc, over
+
+
+def test_step_refusals(M, L):
+    good = _cache(M)
+    rope = M._RopeStruct(GOOD, GOOD, GOOD, GOOD, 100, 64, 1e-6, 0)
+    args = dict(q=GOOD, q_b=4096, q_h=128, k=GOOD, k_b=1024, k_h=128, v=GOOD, v_b=1024, v_h=128, slots=GOOD, B=3, Hq=32,
+                rope=_byref(rope), cache=_byref(good), table=GOOD, ld=1000, cols=1000, lens=GOOD, most=16000, window=0,
+                scale=0.1, q_out=GOOD, qo_b=4096, qo_h=128, out=GOOD, dtype=1, lse=None, ws=GOOD, s=None)
+    f = L.fp8_attention_step
+    bad_rope = M._RopeStruct(GOOD, GOOD, GOOD, GOOD, 100, 136, 1e-6, 0)
+    for over, rc in [(dict(B=0), OK), (dict(B=-1), EINVAL), (dict(B=1 << 19), EINVAL), (dict(Hq=30), EINVAL),
+                     (dict(cols=0), EINVAL), (dict(ld=999), EINVAL), (dict(most=-1), EINVAL), (dict(window=-1), EINVAL),
+                     (dict(scale=float("nan")), EINVAL), (dict(dtype=2), EUNSUPPORTED), (dict(cache=None), EINVAL),
+                     (dict(rope=None), EINVAL), (dict(rope=_byref(bad_rope)), EINVAL),
+                     (dict(q=None), EINVAL), (dict(k=ODD), EALIGN), (dict(v_h=4), EALIGN), (dict(slots=None), EINVAL),
+                     (dict(slots=ODD), EALIGN), (dict(q_out=None), EINVAL), (dict(qo_b=-8), EINVAL),
+                     (dict(table=None), EINVAL), (dict(lens=None), EINVAL), (dict(out=None), EINVAL),
+                     (dict(out=GOOD + 4), EALIGN), (dict(lse=ODD), EALIGN), (dict(ws=None), EINVAL),
+                     (dict(ws=GOOD + 8), EALIGN)]:
+        assert f(*_with(args, **over)) == rc, over
+    for over, rc in BAD_CACHES + BAD_POINTERS:
         bad = _cache(M, **over)
         assert f(*_with(args, cache=_byref(bad))) == rc, over
 

@@ -135,3 +135,23 @@ def test_attention_arguments():
         f(q, c, table, lens, window=2.5)
     _raises("must be a tensor", f, q, c, [[0]], lens)
     _raises("lse must have shape", f, q, c, table, lens, lse=torch.zeros(3, 2))
+
+
+def test_step_arguments():
+    """Both halves' checks, the device last."""
+    c = _HostCache()
+    q, k, v = torch.zeros(3, 4, 64, dtype=bf16), torch.zeros(3, 2, 64, dtype=bf16), torch.zeros(3, 2, 64, dtype=bf16)
+    tab, pos, slots = torch.zeros(10, 64), torch.zeros(3, dtype=i64), torch.zeros(3, dtype=i64)
+    bt, lens = torch.zeros(3, 4, dtype=i32), torch.ones(3, dtype=i32)
+    f = F.attention_step
+    _raises("on a GPU", f, q, k, v, tab, pos, slots, c, bt, lens)
+    _raises("q must be", f, q[:2], k, v, tab, pos, slots, c, bt, lens)
+    _raises("query heads", f, q[:, :3], k, v, tab, pos, slots, c, bt, lens)
+    _raises("v must have shape", f, q, k, v[:, :1], tab, pos, slots, c, bt, lens)
+    _raises("go together", f, q, k, v, None, pos, slots, c, bt, lens)
+    _raises("slots must be", f, q, k, v, tab, pos, slots.int(), c, bt, lens)
+    _raises("block_table must have 3 rows", f, q, k, v, tab, pos, slots, c, bt[:2], lens)
+    _raises("context_lens must be", f, q, k, v, tab, pos, slots, c, bt, lens.long())
+    _raises("window", f, q, k, v, tab, pos, slots, c, bt, lens, window=-1)
+    _raises("max_context", f, q, k, v, tab, pos, slots, c, bt, lens, max_context=-1)
+    _raises("out_dtype", f, q, k, v, tab, pos, slots, c, bt, lens, out_dtype=torch.float16)

@@ -681,6 +681,31 @@ def test_steps_in_a_row(F, fmt):
         s.place()
 
 
+@pytest.mark.parametrize("B,most", [(5, 100), (2, 2500), (40, 700), (70, 4200)])
+def test_step_is_the_two_calls(F, B, most):
+    g = W.gen(23, DEV)
+    s = _Step(F, g, B=B, most=most)
+    for k in (dict(), dict(window=50), dict(out_dtype=torch.float32, scale=0.3), dict(max_context=60)):
+        got = s.run(**k)
+        codes = s.c.k_codes.clone()
+        q = F.fp8_qkv_cache_write(s.q, s.k, s.v, s.tab, s.pos, s.slots, s.c, s.w, s.w, 1e-6)
+        assert torch.equal(s.c.k_codes, codes)
+        assert torch.equal(F.fp8_paged_attention(q, s.c, s.table, s.lt, **k), got)
+
+
+def test_a_refused_step_writes_nothing(F):
+    s = _Step(F, W.gen(24, DEV), B=3)
+    s.c.k_codes.fill_(0x5A)
+    for k in (dict(window=-1), dict(scale=float("nan")), dict(max_context=-1), dict(out_dtype=torch.float16)):
+        with pytest.raises((ValueError, F.Fp8Error)):
+            s.run(**k)
+    s.table = s.table[:2]
+    with pytest.raises(ValueError):
+        s.run()
+    torch.cuda.synchronize()
+    assert (s.c.k_codes == 0x5A).all()
+
+
 def test_same_call_same_bits(F):
     g = W.gen(13, DEV)
     s = _Step(F, g, B=9, most=5000)
