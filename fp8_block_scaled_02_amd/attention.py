@@ -238,5 +238,5 @@ def attention_step(q, k, v, cos_sin, positions, slots, cache: KVCache, block_tab
     Returns out [B, Hq, D]."""
     if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
         raise ValueError("out_dtype must be bfloat16 or float32")
-    return _call("step", cache._dev, cache._ref, cache._dev, q, k, v, cos_sin, positions, slots, q_weight, k_weight, eps,
-                 interleaved, block_table, context_lens, scale, window, out_dtype is torch.float32, max_context)
+    return _call("step", cache._dev, cache._ref, cache._dev, q, k, v, cos_sin, positions, slots, q_weight, k_weight,
+                 eps, interleaved, block_table, context_lens, scale, window, out_dtype is torch.float32, max_context)

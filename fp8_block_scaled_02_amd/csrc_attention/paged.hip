@@ -28,11 +28,11 @@
 // output's own rounding; the further MFMAs are hidden behind the loads.
 //
 // Measured (128 positions, E5M2): 128 sequences x 6000 tokens x 8 heads for 64
-// query heads 300 us (5.3 TB/s; a copy of 200 MB runs at 5.4), 131072 tokens x
-// 8 heads 56 us (4.9 TB/s), 32 x 2048 x 8 31 us, 129 tokens x 8 5.2 us.  A tile
-// takes 267 vector instructions and 24 MFMAs, about 0.83 us of a SIMD that has
-// one wave: at the memory's rate a third of the vector units' time, but the
-// bound of short contexts on few regions.
+// query heads 299 us (5.3 TB/s; a copy of 200 MB runs at 5.4), 131072 tokens x
+// 8 heads 56 us (4.9 TB/s), 32 x 2048 x 8 31 us, 8 x 1000 x 8 11 us, 129 tokens
+// x 8 5.2 us.  A tile takes 253 vector instructions and 24 MFMAs, about 0.8 us
+// of a SIMD that has one wave: at the memory's rate a third of the vector units'
+// time.  Short contexts are bound by each workgroup's chain of loads.
 #include <type_traits>
 
 #include "../csrc/common.hpp"

@@ -422,8 +422,8 @@ def test_attention_long_context_is_split_and_joined(F):
 
 
 @pytest.mark.parametrize("fmt", ["e5m2", "e4m3"])
-@pytest.mark.parametrize("Hq,H,D,window", [(8, 2, 128, 0), (4, 1, 64, 1700), (9, 3, 80, 0), (3, 1, 256, 0), (20, 1, 128, 0),
-                                           (8, 2, 128, 1500)])
+@pytest.mark.parametrize("Hq,H,D,window", [(8, 2, 128, 0), (4, 1, 64, 1700), (9, 3, 80, 0), (3, 1, 256, 0),
+                                           (20, 1, 128, 0), (8, 2, 128, 1500)])
 def test_attention_of_regions_in_parts(F, Hq, H, D, window, fmt):
     """Few regions of some length: each in equal parts, also where lengths leave most parts nothing."""
     g = W.gen(21, DEV)
