@@ -23,9 +23,10 @@
 //                 v_cvt_scalef32_pk_bf16 widens the pair.
 //
 // Codes are exact in bf16 and Q is bf16, so S is exact but for fp32 sums.
-// The weights (times the V scale) are split into 2 bf16 terms for bf16
-// output and 3 for fp32 output: one term alone would be as coarse as the
-// output's own rounding; the further MFMAs are hidden behind the loads.
+// The weights (times the V scale) are split into 3 bf16 terms, which hold all
+// 24 bits of them: nothing before the output's own rounding is coarser than
+// fp32 (2 terms, 16 bits, gave bf16 outputs that are off by a rounding where V
+// lies within 2^-16 of a tie).
 //
 // Measured (128 positions, E5M2): 128 sequences x 6000 tokens x 8 heads for 64
 // query heads 299 us (5.3 TB/s; a copy of 200 MB runs at 5.4), 131072 tokens x
@@ -43,6 +44,7 @@ namespace fp8attn {
 using namespace fp8blk;
 
 constexpr int kTile = 32;       // keys a wave takes at a time
+constexpr int kTerms = 3;       // bf16 terms of a weight
 constexpr int kSplitShift = 2;  // log2 of the waves of a workgroup that shares its regions with others
 constexpr int kMaxWaves = 8;    // and of any
 constexpr int kMaxWgs = 512;    // pieces of the line: 2 for each of the 256 CUs
@@ -337,15 +339,15 @@ __device__ __forceinline__ void weights(float (&s)[8], State<DP>& st) {
 }
 
 // O += P V, p the weights times the V scales.
-template <int DP, int FMT, int TERMS, int QT>
+template <int DP, int FMT, int QT>
 __device__ __forceinline__ void accumulate(float (&p)[QT][8], const ValueRegs<DP>& v, State<DP> (&st)[QT]) {
   typedef uint32_t frag __attribute__((ext_vector_type(4)));
-  // p = sum of TERMS bf16 terms, each the rounded rest of those before
-  frag pf[QT][TERMS];
+  // p = sum of kTerms bf16 terms, each the rounded rest of those before
+  frag pf[QT][kTerms];
 #pragma unroll
   for (int q = 0; q < QT; ++q)
 #pragma unroll
-    for (int t = 0; t < TERMS; ++t)
+    for (int t = 0; t < kTerms; ++t)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const bf16x2 b = {(__bf16)p[q][2 * i], (__bf16)p[q][2 * i + 1]};
@@ -379,7 +381,7 @@ __device__ __forceinline__ void accumulate(float (&p)[QT][8], const ValueRegs<DP
 #pragma unroll
       for (int q = 0; q < QT; ++q)
 #pragma unroll
-        for (int t = 0; t < TERMS; ++t)
+        for (int t = 0; t < kTerms; ++t)
           st[q].o[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
               __builtin_bit_cast(bf16x8, vf), __builtin_bit_cast(bf16x8, pf[q][t]), st[q].o[j], 0, 0, 0);
     }
@@ -393,7 +395,7 @@ __device__ __forceinline__ void accumulate(float (&p)[QT][8], const ValueRegs<DP
 // The page of each half tile is looked up 32 tiles ahead, one per lane.  Past
 // the last token a half may lie anywhere in the cache (ids are clamped): what
 // is read there is masked.
-template <int DP, bool FULL, int FMT, int TERMS, int QT>
+template <int DP, bool FULL, int FMT, int QT>
 __device__ __forceinline__ void run_tiles(const AttnArgs& a, const Span& sp, int b, int h,
                                           const bf16x8 (&qf)[QT][DP / 32], int t, int end, State<DP> (&st)[QT]) {
   const int lane = threadIdx.x & 63, g = lane >> 4;
@@ -459,7 +461,7 @@ __device__ __forceinline__ void run_tiles(const AttnArgs& a, const Span& sp, int
 #pragma unroll
       for (int i = 0; i < 8; ++i) s[q][i] *= v.s[i >> 2][i & 3];
     }
-    accumulate<DP, FMT, TERMS, QT>(s, v, st);
+    accumulate<DP, FMT, QT>(s, v, st);
     if (MORE) load_values<DP, FULL>(a, at, hf, v);
   };
 
@@ -476,7 +478,7 @@ __device__ __forceinline__ void run_tiles(const AttnArgs& a, const Span& sp, int
 // region that lies whole in the workgroup is put out, others go to the
 // workspace: of piece w of the line, slot 2w for the region it begins in, slot
 // 2w+1 for the one it ends in; of a part, the workgroup's slot.
-template <int DP, bool FULL, int FMT, int TERMS, int QT>
+template <int DP, bool FULL, int FMT, int QT>
 __global__ __launch_bounds__(64 * kMaxWaves) void attend_kernel(const AttnArgs a) {
   extern __shared__ float lds[];
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
@@ -539,7 +541,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void attend_kernel(const AttnArgs a
           qf[q][j] = __builtin_bit_cast(bf16x8, w);
         }
       }
-      run_tiles<DP, FULL, FMT, TERMS, QT>(a, sp, b, h, qf, tile + wave, tile + count, st);
+      run_tiles<DP, FULL, FMT, QT>(a, sp, b, h, qf, tile + wave, tile + count, st);
     }
 #pragma unroll
     for (int q = 0; q < QT; ++q) {
@@ -784,18 +786,16 @@ int64_t attention_workspace(const fp8b_kv_cache& c, int64_t B, int64_t Hq, int64
   return slots * partial_floats(s.rows, (int)c.head_dim) * (int64_t)sizeof(float);
 }
 
-template <int DP, bool FULL, int FMT, int TERMS, int QT>
+template <int DP, bool FULL, int FMT, int QT>
 static int launch_one(const AttnArgs& a, unsigned grid, hipStream_t s) {
   const int waves = 1 << a.waves_shift;
   const size_t lds = (size_t)waves * a.rows_max * (DP + 4 + 2) * sizeof(float);
-  hipLaunchKernelGGL((attend_kernel<DP, FULL, FMT, TERMS, QT>), dim3(grid), dim3(64 * waves), lds, s, a);
+  hipLaunchKernelGGL((attend_kernel<DP, FULL, FMT, QT>), dim3(grid), dim3(64 * waves), lds, s, a);
   return check_launch();
 }
 template <int DP, bool FULL, int QT>
 static int launch_fmt(const AttnArgs& a, int fmt, unsigned grid, hipStream_t s) {
-  if (fmt == FP8B_FMT_E5M2)
-    return a.out_f32 ? launch_one<DP, FULL, 1, 3, QT>(a, grid, s) : launch_one<DP, FULL, 1, 2, QT>(a, grid, s);
-  return a.out_f32 ? launch_one<DP, FULL, 2, 3, QT>(a, grid, s) : launch_one<DP, FULL, 2, 2, QT>(a, grid, s);
+  return fmt == FP8B_FMT_E5M2 ? launch_one<DP, FULL, 1, QT>(a, grid, s) : launch_one<DP, FULL, 2, QT>(a, grid, s);
 }
 template <int DP, bool FULL>
 static int launch_dp(const AttnArgs& a, int fmt, unsigned grid, hipStream_t s) {

@@ -178,9 +178,8 @@ int fp8_kv_cache_read(const fp8b_kv_cache *cache, const int32_t *table,
  * a NaN or +inf among the seen scores gives NaN.  What lies in the pages
  * outside the seen range, NaN codes or scales included, has no effect.
  * Products and sums are fp32; the weights e^(s_j - m) enter the products
- * with V split into bf16 parts that keep at least 16 (bf16 output) or 24
- * (fp32 output) significant bits, as long as the product of a weight and
- * its V scale is at least 2^-100.  Sums are taken in a fixed order: the
+ * with V split into bf16 parts that keep at least 24 significant bits, as
+ * long as the product of a weight and its V scale is at least 2^-100.  Sums are taken in a fixed order: the
  * same call gives the same bits.
  *
  *   q        bf16, row b's head h at q + b * q_b + h * q_h (elements,
