@@ -137,10 +137,11 @@ __device__ __forceinline__ u32x2 quantise_row(const u32x4& raw, float& d) {
   const BlockDivisor bd = make_divisor(amax, d);
   divide_block(f, v, bd);
   // With a normal d the quotients end at kMax (1 + 2^-23), which rounds to
-  // kMax: only a subnormal d, rounded coarsely, needs the clamp.
+  // kMax: only a subnormal d, rounded coarsely, needs the clamp.  By comparisons:
+  // NaN passes, as it does on the other path (fminf and fmaxf would drop it).
   if (!bd.fast) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = fminf(fmaxf(v[i], -kMax), kMax);
+    for (int i = 0; i < 8; ++i) v[i] = v[i] > kMax ? kMax : (v[i] < -kMax ? -kMax : v[i]);
   }
   if (FMT == 1) return u32x2{pack4_e5m2(v[0], v[1], v[2], v[3]), pack4_e5m2(v[4], v[5], v[6], v[7])};
   return u32x2{pack4_e4m3(v[0], v[1], v[2], v[3]), pack4_e4m3(v[4], v[5], v[6], v[7])};

@@ -117,7 +117,9 @@ int fp8_qk_norm_rope(const void *q, int64_t q_t, int64_t q_h, const void *k,
 /*
  * fp8_kv_cache_write -- quantise keys and values as they enter the cache:
  * per token and head, d = fp32(amax / Fmax) (1 if amax = 0; Fmax 57344 or
- * 448), codes = E(clamp(fp32(x / d), +-Fmax)), d to the scale.
+ * 448), codes = E(clamp(fp32(x / d), +-Fmax)), d to the scale.  A NaN in a
+ * row becomes a NaN code and leaves the row's other values as they would be
+ * without it; an infinity makes the scale NaN.
  *
  *   k, v    bf16, token t's head h at k + t * k_t + h * k_h (elements,
  *           multiples of 8), 16-byte aligned.

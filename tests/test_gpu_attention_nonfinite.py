@@ -68,3 +68,22 @@ def test_a_step_on_nan_keys_gives_nan(F, magnitude, fmt):
     got = step(bad)
     assert torch.isfinite(want).all() and torch.isnan(got[1, 4:]).all()
     assert torch.equal(got[0], want[0]) and torch.equal(got[1, :4], want[1, :4])
+
+
+@pytest.mark.parametrize("fmt", ["e5m2", "e4m3"])
+@pytest.mark.parametrize("value", [float("inf"), float("-inf")])
+def test_an_infinity_makes_the_rows_scale_nan(F, value, fmt):
+    g = W.gen(6, DEV)
+    c, clean = _fresh(F, 1, 2, 16, 64, fmt), _fresh(F, 1, 2, 16, 64, fmt)
+    rows = _rows(16, 2, 64, g)
+    bad = rows.clone()
+    bad[3, 1, 5] = value
+    slots = torch.arange(16, device=DEV)
+    F.fp8_kv_cache_write(rows, rows, slots, clean)
+    F.fp8_kv_cache_write(bad, bad, slots, c)
+    at = torch.zeros(1, 2, 16, dtype=torch.bool, device=DEV)
+    at[0, 1, 3] = True
+    for a, b in ((c.k_scales, clean.k_scales), (c.v_scales, clean.v_scales)):
+        assert torch.isnan(a[at]).all() and torch.equal(a[~at], b[~at])
+    for a, b in ((c.k_codes, clean.k_codes), (c.v_codes, clean.v_codes)):
+        assert torch.equal(a[~at], b[~at])
