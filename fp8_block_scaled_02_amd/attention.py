@@ -207,7 +207,8 @@ def fp8_kv_cache_read(cache: KVCache, block_table, offsets, rows: int, k_out=Non
     """The cache back as bf16: sequence b's tokens are rows offsets[b] to
     offsets[b + 1] of k_out, v_out [rows, heads, head_dim].  block_table
     int32 [B, cols]: each sequence's pages in order; offsets int32 [B + 1];
-    rows from offsets[B] on are left as they were."""
+    rows from offsets[B] on are left as they were.  Outputs given by the
+    caller share no memory with each other, the inputs or the cache."""
     return _call("cache_read", cache._dev, cache._ref, cache._dev, block_table, offsets, rows, k_out, v_out)
 
 

@@ -18,6 +18,7 @@
 #include <cmath>
 #include <exception>
 #include <initializer_list>
+#include <numeric>
 #include <sstream>
 #include <string>
 
@@ -152,6 +153,49 @@ const at::Tensor* given_rows(PyObject* o, const at::Tensor& x, const char* name)
   return t;
 }
 
+// The bytes of an array: rows of `len` bytes, n[0] x n[1] of them, s[0] and s[1] apart.
+struct Area {
+  int64_t p, n[2], s[2], len;
+  bool empty() const { return n[0] < 1 || n[1] < 1 || len < 1; }
+  int64_t end() const { return p + (n[0] - 1) * s[0] + (n[1] - 1) * s[1] + len; }
+  int outer() const { return s[0] * (n[0] > 1) >= s[1] * (n[1] > 1) ? 0 : 1; }
+};
+int64_t number_of(const void* p) { return (int64_t)reinterpret_cast<uintptr_t>(p); }
+Area area(const void* p, int64_t bytes) { return {number_of(p), {1, 1}, {0, 0}, bytes}; }
+Area area(const at::Tensor& t) { return area(t.data_ptr(), t.numel() * (int64_t)t.element_size()); }  // contiguous
+
+// Blocks of la and lb bytes, delta apart, each repeated at distances that g divides.
+bool between(int64_t delta, int64_t g, int64_t la, int64_t lb) {
+  if (g == 0) return false;
+  const int64_t r = (delta % g + g) % g;
+  return r >= la && r + lb <= g;
+}
+// Whether two arrays have no byte in common: one ends before the other begins,
+// or they are slices of one allocation whose rows, or blocks of rows, take
+// turns.  (Arrays that are interlaced in another way count as not apart.)
+bool apart(const Area& a, const Area& b) {
+  if (a.empty() || b.empty() || a.end() <= b.p || b.end() <= a.p) return true;
+  int64_t all = 0, outer = 0;
+  for (const Area* x : {&a, &b}) {
+    for (int i = 0; i < 2; ++i)
+      if (x->n[i] > 1) all = std::gcd(all, x->s[i]);
+    if (x->n[x->outer()] > 1) outer = std::gcd(outer, x->s[x->outer()]);
+  }
+  auto block = [](const Area& x) { return x.len + (x.n[1 - x.outer()] - 1) * x.s[1 - x.outer()]; };
+  return between(b.p - a.p, all, a.len, b.len) || between(b.p - a.p, outer, block(a), block(b));
+}
+void keep_apart(const Area& a, const Area& b, const char* x, const char* y) {
+  if (!apart(a, b)) refuse(std::string(x) + " and " + y + " must lie apart");
+}
+// An output and the cache.
+void off_cache(const Area& x, const char* name, const fp8b_kv_cache* c) {
+  const int64_t rows = c->heads * c->page_size;
+  for (const uint8_t* p : {c->k_codes, c->v_codes})
+    keep_apart(x, {number_of(p), {c->pages, 1}, {c->page_stride, 0}, rows * c->head_dim}, name, "the cache");
+  for (const float* p : {c->k_scales, c->v_scales})
+    keep_apart(x, {number_of(p), {c->pages, 1}, {4 * c->scale_page_stride, 0}, 4 * rows}, name, "the cache");
+}
+
 // A C call with other Python threads let in: a launch waits while its queue is full.
 struct Unlocked {
   PyThreadState* s = PyEval_SaveThread();
@@ -263,6 +307,7 @@ Table table_of(const at::Tensor& t) {
   const int64_t B = t.size(0), cols = t.size(1);
   return {static_cast<const int32_t*>(t.data_ptr()), B, B > 1 ? t.stride(0) : cols, cols};
 }
+Area area(const Table& t) { return {number_of(t.p), {t.B, 1}, {4 * t.ld, 0}, 4 * t.cols}; }
 
 // (stream, cache, dev, block_table, offsets, rows, k_out, v_out) -> (k_out, v_out)
 PyObject* cache_read(PyObject* const* a) {
@@ -276,8 +321,14 @@ PyObject* cache_read(PyObject* const* a) {
   const char* names[2] = {"k_out", "v_out"};
   for (int i = 0; i < 2; ++i)
     if (given[i]) flat(*given[i], at::kBFloat16, {R, c->heads, c->head_dim}, names[i]);
-  if (given[0] && given[1] && R > 0 && given[0]->data_ptr() == given[1]->data_ptr())
-    refuse("k_out and v_out must be apart");
+  for (int i = 0; i < 2; ++i)
+    if (given[i]) {
+      const Area o = area(*given[i]);
+      if (i == 0 && given[1]) keep_apart(o, area(*given[1]), names[0], names[1]);
+      keep_apart(o, area(t), names[i], "block_table");
+      keep_apart(o, area(offsets), names[i], "offsets");
+      off_cache(o, names[i], c);
+    }
   on(dev, {&bt, &offsets, given[0], given[1]});
   void* stream = address(a[0]);
   at::Tensor out[2];
