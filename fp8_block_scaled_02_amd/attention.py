@@ -179,8 +179,9 @@ def fp8_qk_norm_rope(q, k, cos_sin=None, positions=None, q_weight=None, k_weight
     rotation by the position, in one pass: q [T, Hq, D] and k [T, Hk, D]
     bf16 with any token and head strides (multiples of 8), cos_sin float32
     [max_pos, rot_dim] (cosines, then sines, of each position), positions
-    int64 [T], weights bf16 [D].  Returns (q_out, k_out) bf16; an output may
-    be its input."""
+    int64 [T], weights bf16 [D].  Returns (q_out, k_out) bf16; an output
+    given by the caller may be the very rows it is made from, and otherwise
+    shares no memory with any other argument."""
     return _call("norm_rope", q.get_device(), q, k, cos_sin, positions, q_weight, k_weight, eps, interleaved, q_out,
                  k_out)
 
@@ -198,7 +199,8 @@ def fp8_qkv_cache_write(q, k, v, cos_sin, positions, slots, cache: KVCache, q_we
                         interleaved=False, q_out=None):
     """fp8_qk_norm_rope and fp8_kv_cache_write in one launch (the same bits):
     returns the queries, normed and rotated; the keys, normed and rotated,
-    and the values go to the cache."""
+    and the values go to the cache.  q_out may be q's very rows, and otherwise
+    shares no memory with any other argument."""
     return _call("qkv_write", cache._dev, cache._ref, cache._dev, q, k, v, cos_sin, positions, slots, q_weight,
                  k_weight, eps, interleaved, q_out)
 

@@ -164,6 +164,8 @@ int64_t number_of(const void* p) { return (int64_t)reinterpret_cast<uintptr_t>(p
 Area area(const void* p, int64_t bytes) { return {number_of(p), {1, 1}, {0, 0}, bytes}; }
 Area area(const at::Tensor& t) { return area(t.data_ptr(), t.numel() * (int64_t)t.element_size()); }  // contiguous
 
+Area area(const Rows& r) { return {number_of(r.p), {r.T, r.H}, {2 * r.t, 2 * r.h}, 2 * r.D}; }
+
 // Blocks of la and lb bytes, delta apart, each repeated at distances that g divides.
 bool between(int64_t delta, int64_t g, int64_t la, int64_t lb) {
   if (g == 0) return false;
@@ -186,6 +188,13 @@ bool apart(const Area& a, const Area& b) {
 }
 void keep_apart(const Area& a, const Area& b, const char* x, const char* y) {
   if (!apart(a, b)) refuse(std::string(x) + " and " + y + " must lie apart");
+}
+void keep_apart(const Area& a, const at::Tensor* b, const char* x, const char* y) {
+  if (b) keep_apart(a, area(*b), x, y);
+}
+// Rows given for an output and the rows it is made from: the same ones, or apart.
+void same_or_apart(const Rows& a, const Rows& b, const char* x, const char* y) {
+  if (a.p != b.p || a.t != b.t || a.h != b.h) keep_apart(area(a), area(b), x, y);
 }
 // An output and the cache.
 void off_cache(const Area& x, const char* name, const fp8b_kv_cache* c) {
@@ -225,6 +234,23 @@ PyObject* norm_rope(PyObject* const* a) {
                    *kw = maybe(a[6], "k_weight");
   const fp8b_rope r = rope_of(qr.D, qr.T, cs, pos, qw, kw, number(a[7]), truth(a[8]));
   const at::Tensor *gq = given_rows(a[9], q, "q_out"), *gk = given_rows(a[10], k, "k_out");
+  const struct {
+    const at::Tensor* t;
+    const char* name;
+    const Rows &own, &other;
+    const char *own_name, *other_name;
+  } given[2] = {{gq, "q_out", qr, kr, "q", "k"}, {gk, "k_out", kr, qr, "k", "q"}};
+  for (const auto& g : given)
+    if (g.t) {
+      const Rows o = rows(*g.t, g.name);
+      same_or_apart(o, g.own, g.name, g.own_name);
+      keep_apart(area(o), area(g.other), g.name, g.other_name);
+      keep_apart(area(o), cs, g.name, "cos_sin");
+      keep_apart(area(o), pos, g.name, "positions");
+      keep_apart(area(o), qw, g.name, "q_weight");
+      keep_apart(area(o), kw, g.name, "k_weight");
+      if (g.t == gq && gk) keep_apart(area(o), area(rows(*gk, "k_out")), g.name, "k_out");
+    }
   on(q.get_device(), {&k, cs, pos, qw, kw, gq, gk});
   void* stream = address(a[0]);
   const at::Tensor qo = gq ? *gq : at::empty(q.sizes(), q.options());
@@ -285,6 +311,19 @@ PyObject* qkv_write(PyObject* const* a) {
   const int64_t dev = integer(a[2]);
   const QkvWrite w(c, a + 3);
   const at::Tensor* gq = given_rows(a[13], w.q, "q_out");
+  if (gq) {
+    const Rows o = rows(*gq, "q_out");
+    const Area x = area(o);
+    same_or_apart(o, w.qr, "q_out", "q");
+    keep_apart(x, area(w.kr), "q_out", "k");
+    keep_apart(x, area(w.vr), "q_out", "v");
+    keep_apart(x, w.cs, "q_out", "cos_sin");
+    keep_apart(x, w.pos, "q_out", "positions");
+    keep_apart(x, &w.slots, "q_out", "slots");
+    keep_apart(x, w.qw, "q_out", "q_weight");
+    keep_apart(x, w.kw, "q_out", "k_weight");
+    off_cache(x, "q_out", c);
+  }
   w.all_on(dev);
   on(dev, {gq});
   void* stream = address(a[0]);

@@ -138,7 +138,8 @@ int fp8_kv_cache_write(const void *k, int64_t k_t, int64_t k_h, const void *v,
  * and rotated to q_out, keys normed, rotated, rounded to bf16 and quantised
  * into the cache, values quantised into the cache.  Bit-identical to
  * fp8_qk_norm_rope followed by fp8_kv_cache_write.  Queries of tokens whose
- * slot is outside the cache are written all the same.
+ * slot is outside the cache are written all the same.  q_out may be q itself
+ * (the same address and strides) and may not overlap any input otherwise.
  */
 int fp8_qkv_cache_write(const void *q, int64_t q_t, int64_t q_h,
                         const void *k, int64_t k_t, int64_t k_h,

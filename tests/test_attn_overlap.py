@@ -66,3 +66,118 @@ def test_read_outputs_in_the_cache():
     c = _At(codes[:, :2048].view(4, 2, 16, 64), codes[:, 2048:4096].view(4, 2, 16, 64), c.k_scales, c.v_scales)
     _apart(f, c, table, offs, 1, codes[1, 4096:].view(bf16).view(1, 2, 64))
     _not_apart("k_out and the cache", f, c, table, offs, 1, codes[1, 4080:4336].view(bf16).view(1, 2, 64))
+
+
+def _projection(T=5, Hq=4, H=2, D=64):
+    """q, k, v as slices of one projection's output, and that with room on both sides."""
+    n = (Hq + 2 * H) * D
+    wide = torch.zeros(T + 2, n, dtype=bf16)
+    y = wide[1:T + 1]
+    return [y[:, a * D:b * D].view(T, b - a, D) for a, b in ((0, Hq), (Hq, Hq + H), (Hq + H, Hq + 2 * H))], wide
+
+
+def test_rope_outputs():
+    (q, k, v), wide = _projection()
+    f = F.fp8_qk_norm_rope
+    other = torch.zeros(5, 6, 64, dtype=bf16)
+    _apart(f, q, k, q_out=q, k_out=k)                           # in place
+    _apart(f, q, k, k_out=v)                                    # over the values: the caller's choice
+    _apart(f, q, k, q_out=other[:, :4], k_out=other[:, 4:])
+    _not_apart("k_out and q", f, q, k, k_out=q[:, :2])
+    _not_apart("q_out and q", f, q, k, q_out=wide.flatten().as_strided(q.shape, q.stride(), q.storage_offset() + 8))
+    _not_apart("q_out and q", f, q, k, q_out=wide[:5, :256].view(5, 4, 64))        # a token earlier
+    _not_apart("q_out and k", f, torch.zeros_like(q), k, q_out=wide[1:6, 128:384].view(5, 4, 64))
+    _not_apart("q_out and k_out", f, q, k, q_out=other[:, :4], k_out=other[:, 3:5])
+    same = torch.zeros(5, 2, 64, dtype=bf16)
+    _not_apart("q_out and k_out", f, k, v, q_out=same, k_out=same)
+    _not_apart("q_out and k", f, k, v, q_out=v)
+    tab, pos = torch.zeros(10, 64), torch.zeros(5, dtype=i64)
+    _not_apart("k_out and cos_sin", f, q, k, tab, pos, k_out=tab.view(bf16).flatten()[:640].view(5, 2, 64))
+    w = torch.zeros(6 * 128, dtype=bf16)
+    _not_apart("k_out and q_weight", f, q, k, None, None, w[32:96], k_out=w[64:704].view(5, 2, 64))
+    _not_apart("k_out and k_weight", f, q, k, None, None, None, w[640:704], k_out=w[64:704].view(5, 2, 64))
+    _apart(f, q, k, None, None, w[:64], w[704:], k_out=w[64:704].view(5, 2, 64))
+
+
+def test_rope_outputs_head_by_head():
+    """q and k of each head side by side, [T, H, 3, D]; heads outside tokens, [3, H, T, D]."""
+    f = F.fp8_qk_norm_rope
+    y = torch.zeros(5, 4, 3, 64, dtype=bf16)
+    q, k = y[:, :, 0], y[:, :, 1]
+    _apart(f, q, k, q_out=q, k_out=k)
+    _apart(f, q, k, q_out=y[:, :, 2])
+    _not_apart("q_out and k", f, q, k, q_out=k)
+    z = torch.zeros(4, 3, 5, 64, dtype=bf16)
+    q, k = (z[:, i].transpose(0, 1) for i in (0, 1))
+    _apart(f, q, k, q_out=q, k_out=k)
+    _not_apart("k_out and q", f, q, k, k_out=q)
+
+
+def test_rope_outputs_drawn():
+    """Strided rows in one buffer against a count of the bytes they share: rows that do share some are always
+    refused, and rows of one projection that do not are never."""
+    import random
+    rng, refused, taken = random.Random(3), 0, 0
+    buf = torch.zeros(1 << 14, dtype=bf16)
+    for _ in range(400):
+        T, H, D = rng.randint(1, 4), rng.randint(1, 3), 16 * rng.randint(1, 3)
+        h = D + 8 * rng.randint(0, 9)
+        t = H * h + 8 * rng.randint(0, 20)
+        if rng.random() < 0.3:
+            h, t = T * h + 8 * rng.randint(0, 20), h
+        shape = (T, H, D)
+        if rng.random() < 0.5:
+            h2, t2 = h, t
+        else:
+            h2 = D + 8 * rng.randint(0, 9)
+            t2 = H * h2 + 8 * rng.randint(0, 20)
+        k = buf.as_strided(shape, (t, h, 1), 8 * rng.randint(0, 60))
+        out = buf.as_strided(shape, (t2, h2, 1), 8 * rng.randint(0, 60))
+        q = torch.zeros(shape, dtype=bf16)
+        buf.zero_()
+        k.fill_(1.0)
+        shared = bool((out == 1).any())
+        with pytest.raises(ValueError) as e:
+            F.fp8_qk_norm_rope(q, k, q_out=out)
+        if "must lie apart" in str(e.value):
+            refused += 1
+            one_layout = (t, h) == (t2, h2) and T > 1 and H > 1
+            assert shared or not one_layout or _turns_differ(k, out)
+        else:
+            taken += 1
+            assert "on a GPU" in str(e.value) and not shared
+    assert refused > 50 and taken > 50
+
+
+def _turns_differ(a, b):
+    """Rows of one layout that neither take turns row by row nor block by block (a token's heads, or a head's tokens)."""
+    import math
+    d = b.storage_offset() - a.storage_offset()
+    (T, H, D), (t, h) = a.shape, a.stride()[:2]
+    g = math.gcd(t, h)
+    outer, block = (t, (H - 1) * h + D) if t >= h else (h, (T - 1) * t + D)
+    return not (D <= d % g <= g - D) and not (block <= d % outer <= outer - block)
+
+
+def test_fused_write_queries():
+    (q, k, v), wide = _projection()
+    c = _cache()
+    tab, pos, slots = torch.zeros(10, 64), torch.zeros(5, dtype=i64), torch.zeros(5, dtype=i64)
+    w = torch.zeros(64, dtype=bf16)
+
+    def f(out, q=q, k=k, v=v, c=c, pos=pos, slots=slots, w=None):
+        return F.fp8_qkv_cache_write(q, k, v, tab, pos, slots, c, w, w, q_out=out)
+
+    _apart(f, None)
+    _apart(f, q)
+    _apart(f, torch.zeros(5, 4, 64, dtype=bf16), w=w)
+    _not_apart("q_out and q", f, wide[:5, :256].view(5, 4, 64))
+    _not_apart("q_out and k", f, wide[1:6, 256:].view(5, 4, 64))
+    _not_apart("q_out and v", f, wide[1:6, 256:].view(5, 4, 64), k=torch.zeros_like(k))
+    line = torch.zeros(4096, dtype=i64)
+    out = line[16:16 + 320].view(bf16).view(5, 4, 64)
+    _not_apart("q_out and positions", f, out, pos=line[12:17])
+    _not_apart("q_out and slots", f, out, slots=line[335:340])
+    _not_apart("q_out and q_weight", f, out, w=line[:17].view(bf16)[4:68])
+    _apart(f, out, pos=line[11:16], slots=line[336:341], w=line[:16].view(bf16))
+    _not_apart("q_out and the cache", f, c.v_codes.flatten()[1024:1024 + 2560].view(bf16).view(5, 4, 64))
