@@ -224,7 +224,8 @@ def fp8_paged_attention(q, cache: KVCache, block_table, context_lens, scale=None
     tokens.  max_context, if given, cuts longer lengths: a tight value saves
     the splitting of short contexts.  Returns out [B, Hq, D] (bf16 or
     fp32); lse, if given (float32 [B, Hq]), receives the log of the sum of
-    exponentials, -inf for an empty row."""
+    exponentials, -inf for an empty row.  out and lse given by the caller
+    share no memory with each other, the inputs or the cache."""
     if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
         raise ValueError("out_dtype must be bfloat16 or float32")
     return _call("attention", cache._dev, cache._ref, cache._dev, q, block_table, context_lens, scale, window,

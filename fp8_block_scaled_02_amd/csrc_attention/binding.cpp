@@ -21,6 +21,7 @@
 #include <numeric>
 #include <sstream>
 #include <string>
+#include <utility>
 
 #include "../../include/fp8attn.h"
 
@@ -422,6 +423,16 @@ PyObject* attention(PyObject* const* a) {
   const at::Tensor *given = maybe(a[9], "out"), *lse = maybe(a[10], "lse");
   if (given) flat(*given, x.type, {r.T, r.H, r.D}, "out");
   float* lsep = lse ? static_cast<float*>(flat(*lse, at::kFloat, {r.T, r.H}, "lse")) : nullptr;
+  const std::pair<const at::Tensor*, const char*> outs[2] = {{given, "out"}, {lse, "lse"}};
+  for (const auto& [t, name] : outs)
+    if (t) {
+      const Area o = area(*t);
+      if (t == given) keep_apart(o, lse, name, "lse");
+      keep_apart(o, area(r), name, "q");
+      keep_apart(o, area(x.t), name, "block_table");
+      keep_apart(o, &x.lens, name, "context_lens");
+      off_cache(o, name, c);
+    }
   on(dev, {&q, &x.bt, &x.lens, given, lse});
   const int64_t bytes = fp8_paged_attention_workspace(c, r.T, r.H, x.t.cols, x.most, x.window);
   if (bytes < 0) return status(bytes);

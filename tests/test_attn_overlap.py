@@ -181,3 +181,30 @@ def test_fused_write_queries():
     _not_apart("q_out and q_weight", f, out, w=line[:17].view(bf16)[4:68])
     _apart(f, out, pos=line[11:16], slots=line[336:341], w=line[:16].view(bf16))
     _not_apart("q_out and the cache", f, c.v_codes.flatten()[1024:1024 + 2560].view(bf16).view(5, 4, 64))
+
+
+def test_attention_outputs():
+    c = _cache()
+    line = torch.zeros(8192, dtype=f32)
+    table, lens = torch.zeros(3, 5, dtype=i32), torch.zeros(3, dtype=i32)
+    q = torch.zeros(3, 4, 64, dtype=bf16)
+
+    def f(q=q, table=table, lens=lens, **k):
+        return F.fp8_paged_attention(q, c, table, lens, **k)
+
+    out = line[64:64 + 384].view(bf16).view(3, 4, 64)
+    out32 = line[64:64 + 768].view(3, 4, 64)
+    _apart(f, out=out, lse=line[52:64].view(3, 4))
+    _apart(f, out=out, lse=line[448:460].view(3, 4))
+    _not_apart("out and lse", f, out=out, lse=line[53:65].view(3, 4))
+    _not_apart("out and lse", f, out=out32, out_dtype=f32, lse=line[831:843].view(3, 4))
+    _not_apart("out and q", f, q=out, out=out)
+    _not_apart("out and q", f, q=line[440:440 + 384].view(bf16).view(3, 4, 64), out=out)
+    _not_apart("lse and q", f, q=out, lse=line[440:452].view(3, 4))
+    _not_apart("out and block_table", f, out=out, table=line[50:65].view(i32).view(3, 5))
+    _not_apart("lse and block_table", f, lse=line[60:72].view(3, 4), table=line[50:65].view(i32).view(3, 5))
+    _not_apart("out and context_lens", f, out=out, lens=line[447:450].view(i32))
+    _not_apart("lse and the cache", f, lse=c.k_scales.flatten()[4:16].view(3, 4))
+    _not_apart("out and the cache", f, out=c.k_codes.flatten()[2048:2048 + 1536].view(bf16).view(3, 4, 64))
+    y = torch.zeros(3, 8 * 64, dtype=bf16)
+    _apart(f, q=y[:, :256].view(3, 4, 64), out=torch.zeros(3, 4, 64, dtype=bf16))
