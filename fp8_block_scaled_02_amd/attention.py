@@ -118,7 +118,8 @@ class KVCache:
     are arbitrary until written; what is not read through a length has no
     effect); from_tensors() takes tensors the caller keeps, whose pages may
     lie any distance apart, the same for K and V (one layer of a larger
-    allocation, K and V side by side)."""
+    allocation, K and V side by side).  A cache in which any of the four share
+    memory can be read but not written."""
 
     def __init__(self, pages, page_size, heads, head_dim, fmt="e5m2", device="cuda"):
         codes = [torch.empty(pages, heads, page_size, head_dim, dtype=torch.uint8, device=device) for _ in range(2)]

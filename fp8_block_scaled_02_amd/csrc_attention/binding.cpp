@@ -197,13 +197,28 @@ void keep_apart(const Area& a, const at::Tensor* b, const char* x, const char* y
 void same_or_apart(const Rows& a, const Rows& b, const char* x, const char* y) {
   if (a.p != b.p || a.t != b.t || a.h != b.h) keep_apart(area(a), area(b), x, y);
 }
+// The arrays of a cache.
+struct CacheAreas {
+  Area a[4];
+  explicit CacheAreas(const fp8b_kv_cache* c) {
+    const int64_t rows = c->heads * c->page_size;
+    for (int i = 0; i < 2; ++i) {
+      a[i] = {number_of(i ? c->v_codes : c->k_codes), {c->pages, 1}, {c->page_stride, 0}, rows * c->head_dim};
+      a[2 + i] = {number_of(i ? c->v_scales : c->k_scales), {c->pages, 1}, {4 * c->scale_page_stride, 0}, 4 * rows};
+    }
+  }
+};
 // An output and the cache.
 void off_cache(const Area& x, const char* name, const fp8b_kv_cache* c) {
-  const int64_t rows = c->heads * c->page_size;
-  for (const uint8_t* p : {c->k_codes, c->v_codes})
-    keep_apart(x, {number_of(p), {c->pages, 1}, {c->page_stride, 0}, rows * c->head_dim}, name, "the cache");
-  for (const float* p : {c->k_scales, c->v_scales})
-    keep_apart(x, {number_of(p), {c->pages, 1}, {4 * c->scale_page_stride, 0}, 4 * rows}, name, "the cache");
+  for (const Area& y : CacheAreas(c).a) keep_apart(x, y, name, "the cache");
+}
+// A cache to be written: the places of K and V, codes and scales.  (One that is only read may share them.)
+void writable(const fp8b_kv_cache* c) {
+  if (!c->k_codes) return;  // (refused by the call)
+  const CacheAreas x(c);
+  const char* names[4] = {"k_codes", "v_codes", "k_scales", "v_scales"};
+  for (int i = 1; i < 4; ++i)
+    for (int j = 0; j < i; ++j) keep_apart(x.a[j], x.a[i], names[j], names[i]);
 }
 
 // A C call with other Python threads let in: a launch waits while its queue is full.
@@ -277,6 +292,7 @@ PyObject* cache_write(PyObject* const* a) {
   const at::Tensor &k = tensor(a[3], "k"), &v = tensor(a[4], "v"), &slots = tensor(a[5], "slots");
   Rows kr, vr;
   kv_rows(k, v, c, kr, vr);
+  writable(c);
   const void* s = flat(slots, at::kLong, {kr.T}, "slots");
   on(integer(a[2]), {&k, &v, &slots});
   void* stream = address(a[0]);
@@ -298,6 +314,7 @@ struct QkvWrite {
         cs(maybe(a[3], "cos_sin")), pos(maybe(a[4], "positions")), qw(maybe(a[6], "q_weight")),
         kw(maybe(a[7], "k_weight")), qr(rows(q, "q")) {
     kv_rows(k, v, c, kr, vr);
+    writable(c);
     if (qr.T != kr.T || qr.D != c->head_dim)
       refuse("q must be [" + std::to_string(kr.T) + ", Hq, " + std::to_string(c->head_dim) + "]");
     r = rope_of(qr.D, qr.T, cs, pos, qw, kw, number(a[8]), truth(a[9]));

@@ -50,6 +50,8 @@ int fp8b_attn_abi_version(void);
  * page strides let layers, or K and V, share one allocation.
  *
  *   k_codes, v_codes    16-byte aligned; k_scales, v_scales: 16-byte aligned.
+ *                       Apart from one another, pages interlaced or not, in
+ *                       a cache that is written.
  *   page_stride         bytes, >= heads * page_size * head_dim, a multiple
  *                       of 16, below 2^32; the same for K and V.
  *   scale_page_stride   floats, >= heads * page_size, a multiple of 4, below

@@ -208,3 +208,34 @@ def test_attention_outputs():
     _not_apart("out and the cache", f, out=c.k_codes.flatten()[2048:2048 + 1536].view(bf16).view(3, 4, 64))
     y = torch.zeros(3, 8 * 64, dtype=bf16)
     _apart(f, q=y[:, :256].view(3, 4, 64), out=torch.zeros(3, 4, 64, dtype=bf16))
+
+
+def test_writes_into_a_cache_that_shares_its_places():
+    q, k = torch.zeros(3, 4, 64, dtype=bf16), torch.zeros(3, 2, 64, dtype=bf16)
+    tab, pos, slots = torch.zeros(10, 64), torch.zeros(3, dtype=i64), torch.zeros(3, dtype=i64)
+    bt, lens, offs = torch.zeros(3, 4, dtype=i32), torch.ones(3, dtype=i32), torch.zeros(4, dtype=i32)
+    writes = (lambda c: F.fp8_kv_cache_write(k, k, slots, c),
+              lambda c: F.fp8_qkv_cache_write(q, k, k, tab, pos, slots, c),
+              lambda c: F.attention_step(q, k, k, tab, pos, slots, c, bt, lens))
+    codes, scales = torch.zeros(4, 3, 2, 2, 16, 64, dtype=u8), torch.zeros(4, 3, 2, 2, 16)
+
+    def layer(i, j, x=0, y=1):
+        return _At(codes[:, i, x], codes[:, j, y], scales[:, i, x], scales[:, j, y])
+
+    packed = torch.zeros(4, 2 * 2048 + 2 * 128, dtype=u8)          # a page: K, V, their scales
+    parts = [packed[:, a:a + n] for a, n in ((0, 2048), (2048, 2048), (4096, 128), (4224, 128))]
+    parts = [x.view(4, 2, 16, 64) for x in parts[:2]] + [x.view(f32).view(4, 2, 16) for x in parts[2:]]
+    flat = codes.flatten()
+    shifted = [flat[a:a + 8192].view(4, 2, 16, 64) for a in (0, 8176)]
+    for w in writes:
+        for good in (layer(0, 0), layer(1, 1), layer(2, 1), _cache(1), _At(*parts)):
+            _apart(w, good)
+        _not_apart("k_codes and v_codes", w, layer(1, 1, 0, 0))
+        _not_apart("k_codes and v_codes", w, _At(*shifted, torch.zeros(4, 2, 16), torch.zeros(4, 2, 16)))
+        c = _cache()
+        _not_apart("k_scales and v_scales", w, _At(c.k_codes, c.v_codes, c.k_scales, c.k_scales))
+        _not_apart("v_codes and k_scales", w,
+                   _At(c.k_codes, c.v_codes, c.v_codes.flatten()[:512].view(f32).view(4, 2, 16), c.v_scales))
+    one = layer(1, 1, 0, 0)                                        # reading is left alone
+    _apart(F.fp8_paged_attention, q, one, bt, lens)
+    _apart(F.fp8_kv_cache_read, one, bt, offs, 5)
