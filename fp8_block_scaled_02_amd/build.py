@@ -37,9 +37,12 @@ def attn_sources():
 
 
 def build(verbose: bool = False) -> str:
+    """libfp8blk.so first: it needs hipcc alone, and is there also where the
+    binding's compiler or torch's headers are not."""
+    _compile(LIB, sources(), verbose)
     _compile(ATTN_LIB, attn_sources(), verbose)
     _compile_binding(verbose)
-    return _compile(LIB, sources(), verbose)
+    return LIB
 
 
 def _compile_binding(verbose: bool) -> None:
