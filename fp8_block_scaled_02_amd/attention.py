@@ -70,12 +70,12 @@ def attn_lib():
 
 
 _native = None
-_current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+_current_device = _raw_stream = None    # torch's device calls, looked up with the native module
 
 
 def _load():
     """The native module of the calls below (raises if it has not been built)."""
-    global _native
+    global _native, _current_device, _raw_stream
     if _native is None:
         attn_lib()
         try:
@@ -83,6 +83,7 @@ def _load():
         except ImportError as e:
             raise ImportError(f"{e}: build it with `python -m fp8_block_scaled_02_amd.build` "
                               "(there is no Python fallback)") from e
+        _current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
         _native = _attn_binding
     return _native
 

@@ -40,3 +40,15 @@ def test_the_linear_library_needs_hipcc_alone(compilers):
     with pytest.raises(FileNotFoundError):
         build.build()
     assert (out / "libfp8blk.so").exists()
+
+
+def test_import_without_a_gpu_build_of_torch():
+    """The linear layers' module imports where torch has no device calls; the attention's calls look them up on first
+    use."""
+    code = ("import torch\n"
+            "for n in ('_cuda_getDevice', '_cuda_getCurrentRawStream'):\n"
+            "    if hasattr(torch._C, n): delattr(torch._C, n)\n"
+            "import fp8_block_scaled_02_amd as F\n"
+            "F.lib()\n")
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr
