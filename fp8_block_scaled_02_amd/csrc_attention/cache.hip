@@ -57,24 +57,6 @@ __device__ __forceinline__ float row_max_nonneg(float v) {
   return __uint_as_float(u);
 }
 
-// The value LPR / 2 lanes away (a whole head's rotation partner): half-row
-// mirror and quad reversal (4), row rotation (8), row swap (16).
-template <int LPR>
-__device__ __forceinline__ float other_half(float v) {
-  int x = __float_as_int(v);
-  if (LPR == 8) {
-    x = __builtin_amdgcn_update_dpp(0, x, 0x141, 0xF, 0xF, false);
-    x = __builtin_amdgcn_update_dpp(0, x, 0x1B, 0xF, 0xF, false);
-  } else if (LPR == 16) {
-    x = __builtin_amdgcn_update_dpp(0, x, 0x128, 0xF, 0xF, false);
-  } else {
-    typedef unsigned int u2 __attribute__((ext_vector_type(2)));
-    const u2 y = __builtin_amdgcn_permlane16_swap((uint32_t)x, (uint32_t)x, false, false);
-    x = (int)((threadIdx.x & 16) ? y[0] : y[1]);
-  }
-  return __int_as_float(x);
-}
-
 __device__ __forceinline__ void unpack8(const u32x4& w, float (&f)[8]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -254,13 +236,8 @@ __global__ __launch_bounds__(256) void qkv_kernel(const QkvArgs a) {
       }
       if (ROPE == 1) {
         float o[8];
-        if (a.rot == 8 * LPR) {  // (4096 x 72 heads of 128: 32.6 us, 33.9 by the shuffles)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) o[i] = other_half<LPR>(f[i]);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) o[i] = __shfl(f[i], partner, LPR);
-        }
+        for (int i = 0; i < 8; ++i) o[i] = __shfl(f[i], partner, LPR);
         // positions past rot stay as they are, infinities too
         if (e0 < a.rot) {
 #pragma unroll
