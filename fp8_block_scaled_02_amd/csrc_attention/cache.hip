@@ -29,7 +29,6 @@ struct QkvArgs {
   int page_shift;
   int slot_shift;  // log2 of the row slots of a workgroup that one token takes
   int items, token_items;  // rows of a slot; token_items > 1: they are of that many tokens
-  bool stream;             // non-temporal stores
 };
 
 // Sum and maximum over the LPR (8, 16 or 32) adjacent lanes of a row: quad
@@ -95,13 +94,6 @@ __device__ __forceinline__ u32x4 load_row(int64_t p, uint32_t step, int h, bool 
   u32x4 w = {0, 0, 0, 0};
   if (on) w = STREAM ? __builtin_nontemporal_load(x) : *x;
   return w;
-}
-
-// Rows of a large call are read by a later kernel, from memory: non-temporal.
-template <typename T>
-__device__ __forceinline__ void store(global_ptr<T> p, T v, bool stream) {
-  if (stream) __builtin_nontemporal_store(v, p);
-  else *p = v;
 }
 
 // Codes and scale of a row of bf16 values (the quantiser of fp8_kv_quant and
@@ -255,7 +247,7 @@ __global__ __launch_bounds__(256) void qkv_kernel(const QkvArgs a) {
     }
     if (FMT == 0 || rr < k0) {
       const uint32_t step = 2 * (uint32_t)(rr < k0 ? a.q_out.h : a.k_out.h);
-      if (on) store((global_ptr<u32x4>)((rr < k0 ? qo : ko) + (int64_t)((uint64_t)(uint32_t)h * step)), raw, a.stream);
+      if (on) *(global_ptr<u32x4>)((rr < k0 ? qo : ko) + (int64_t)((uint64_t)(uint32_t)h * step)) = raw;
     } else if (sl >= 0 && sl < a.total_slots) {
       float d;
       const u32x2 codes = quantise_row<LPR, FMT>(raw, d);
@@ -265,7 +257,7 @@ __global__ __launch_bounds__(256) void qkv_kernel(const QkvArgs a) {
                          (int64_t)((uint64_t)page * a.page_stride + in_page * (uint32_t)a.D);
       const int64_t sp = (rr < v0 ? address(a.k_scales) : address(a.v_scales)) +
                          4 * (int64_t)((uint64_t)page * a.scale_page_stride + in_page);
-      if (on) store((global_ptr<u32x2>)(cp + e0), codes, a.stream);
+      if (on) *(global_ptr<u32x2>)(cp + e0) = codes;
       if (lane == 0) *(global_ptr<float>)sp = d;
     }
     if (last) return;
@@ -275,8 +267,7 @@ __global__ __launch_bounds__(256) void qkv_kernel(const QkvArgs a) {
 // From 1024 workgroups of one token group each on, a slot takes several rows
 // (4096 tokens x 72 heads: 31 us, 50 with a slot for every row; 900 tokens x 16
 // heads: 3.2 us, 4.4 with several rows a slot).  512: 512 x 72 7.0 -> 7.9 us;
-// 2048: 1500 x 72 12.1 -> 13.8.  Non-temporal stores pay from there on too
-// (rotation of 4096 x 72 heads 34 -> 30 us, but 1021 x 25 x 80 4.5 -> 4.7).
+// 2048: 1500 x 72 12.1 -> 13.8.
 constexpr int kManyWgs = 1024;
 // Rows that the last-level cache (256 MB) can still hold are read from there: a
 // write of 134 MB of rows 45.6 us with plain loads, 41.4 non-temporal; of 17 MB
@@ -334,7 +325,6 @@ int launch_qkv(const Rows& q, const Rows& k, const Rows& v, int64_t T, int D, co
   int64_t gx = (T + tokens - 1) / tokens, gy = 1;
   a.items = turns;
   a.token_items = 1;
-  a.stream = gx >= kManyWgs;
   if (gx < kManyWgs) {  // few tokens: every row a slot of its own
     gy = turns;
     a.items = 1;
