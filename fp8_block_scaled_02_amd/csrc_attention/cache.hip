@@ -132,9 +132,11 @@ __device__ __forceinline__ u32x2 quantise_row(const u32x4& raw, float& d) {
 // 2 interleaved.  STREAM: non-temporal loads.  HBM-bound (2 bytes in and 2, or
 // 1 and a scale, out per value), but only just: 8 values are one 16-byte load
 // and some 150 instructions, so addresses are kept to 32-bit products.  Norm
-// and rotation of 4096 tokens x (64 + 8) x 128: 30.8 us, 4.98 TB/s; cache write
-// of 32768 x 8 x 128: 37.3 us, 5.46 TB/s; of one step's 32 tokens 2.3 us, which
-// is the launch.
+// and rotation of 4096 tokens x (64 + 8) x 128: 30.6 us, 5.0 TB/s; with the cache
+// write of their keys and values 35.5 us (40.9 in two calls); cache write of 32768 x
+// 8 x 128: 40 us, 5.1 TB/s; of one step's 32 tokens 2.3 us, which is the launch.
+// (Times in this file: us a call in a replayed graph of calls on three sets of
+// inputs in turn.)
 template <int LPR, int ROPE, int FMT, bool STREAM>
 __global__ __launch_bounds__(256) void qkv_kernel(const QkvArgs a) {
   constexpr int kSlots = 256 / LPR;
@@ -265,16 +267,16 @@ __global__ __launch_bounds__(256) void qkv_kernel(const QkvArgs a) {
 }
 
 // From 1024 workgroups of one token group each on, a slot takes several rows
-// (4096 tokens x 72 heads: 31 us, 50 with a slot for every row; 900 tokens x 16
-// heads: 3.2 us, 4.4 with several rows a slot).  512: 512 x 72 7.0 -> 7.9 us;
-// 2048: 1500 x 72 12.1 -> 13.8.
+// (rotation of 4096 x 72 heads: 31 us, 40 with a slot for every row; write of 900
+// tokens x 8 heads: 3.2 us, 4.5 with several rows a slot).  512: rotation of 512 x 72
+// 7.0 -> 8.0 us; 2048: 1500 x 72 12.1 -> 13.9.
 constexpr int kManyWgs = 1024;
 // Rows that the last-level cache (256 MB) can still hold are read from there: a
-// write of 134 MB of rows 45.6 us with plain loads, 41.4 non-temporal; of 17 MB
-// 7.4 and 7.9.
+// write of 134 MB of rows (32768 x 8 heads) 45.4 us with plain loads, 42.0
+// non-temporal; of 17 MB 7.5 and 7.9.
 constexpr int64_t kStreamBytes = (int64_t)64 << 20;
-// Tokens a slot takes in a large cache write: 32768 x 16 heads 46 us with 1 or
-// 2, 40 with 4, 41 with 8 (4096 x 16: 7.9 with 4, 9.8 with 8).
+// Tokens a slot takes in a large cache write: 32768 x 8 heads 44.6 us with 1, 39.7
+// with 2, 39.4 with 4, 39.9 with 8; 4096 x 8 7.2, -, 7.3, 8.9.
 constexpr int kTokenItems = 4;
 
 int launch_qkv(const Rows& q, const Rows& k, const Rows& v, int64_t T, int D, const fp8b_rope* rope, const Rows& q_out,
@@ -390,7 +392,7 @@ constexpr int kReadPieces = 256 * kReadTurns;
 // 512 pieces, or one longer row in turns; K and V in blockIdx.y.  Its threads
 // first look up each row's sequence (binary search over offsets) and page and
 // leave them in LDS.  HBM-bound: 1 byte in, 2 out: 32768 tokens x 8 x 128, K and
-// V, 41.5 us, 4.9 TB/s (one piece a turn 46, four 43.6, eight 52).  Rows and
+// V, 41.2 us, 4.9 TB/s (one piece a turn 42.9, four 43.7, eight 44.8).  Rows and
 // pieces that do not exist are read at valid addresses and not put out, so that
 // no branch comes between the loads.
 template <int FMT>

@@ -28,11 +28,16 @@
 // fp32 (2 terms, 16 bits, gave bf16 outputs that are off by a rounding where V
 // lies within 2^-16 of a tie).
 //
-// Measured (128 positions, E5M2): 128 sequences x 6000 tokens x 8 heads for 64
-// query heads 299 us (5.3 TB/s; a copy of 200 MB runs at 5.4), 131072 tokens x
-// 8 heads 56 us (4.9 TB/s), 32 x 2048 x 8 31 us, 8 x 1000 x 8 11 us, 129 tokens
-// x 8 5.2 us.  A tile takes 253 vector instructions and 24 MFMAs, about 0.8 us
-// of a SIMD that has one wave: at the memory's rate a third of the vector units'
+// Times in this file: us a call on the GPU in a replayed graph of calls on three
+// sets of inputs in turn, E5M2 and bf16 output if nothing else is said; a copy of
+// 200 MB runs at 5.4 TB/s.
+//
+// Measured (128 positions, lengths from half to one and a half times the average):
+// 128 sequences x 6000 tokens x 8 heads for 64 query heads 306 us (5.2 TB/s), one of
+// 131072 tokens x 8 heads 60 (4.6 TB/s), 32 x 2048 x 8 33 (27, 4.6 TB/s, when all are
+// equally long: a workgroup a region waits for the longest), 8 x 1000 x 8 11.3, 129
+// tokens x 8 5.4.  A tile takes 281 vector instructions and 32 MFMAs, about 0.75 us of
+// a SIMD that has one wave: at the memory's rate two fifths of the vector units'
 // time.  Short contexts are bound by each workgroup's chain of loads.
 #include <type_traits>
 
@@ -390,8 +395,7 @@ __device__ __forceinline__ void accumulate(float (&p)[QT][8], const ValueRegs<DP
 
 // A wave's tiles t, t + waves, ... below `end` (relative to the span's first)
 // of one region.  The next tile's keys are loaded as soon as this one's are
-// used, its values likewise, so a tile is always in flight (two of them, for
-// 60 more registers, measured no faster).
+// used, its values likewise, so a tile is always in flight.
 // The page of each half tile is looked up 32 tiles ahead, one per lane.  Past
 // the last token a half may lie anywhere in the cache (ids are clamped): what
 // is read there is masked.
@@ -718,8 +722,8 @@ static Shape shape_of(const fp8b_kv_cache& c, int64_t B, int64_t Hq, int64_t col
   s.G = (int)(Hq / c.heads);
   // more than 16 heads: two query tiles to a wave, so K and V are read and
   // widened once for both; up to 128 positions, where the registers allow it
-  // (32 x 4096 x 4 KV heads, 24 heads each: 44 us, 53 one tile at a time; 1 KV
-  // head of 48: 40 and 45)
+  // (32 x 4096 tokens x 4 KV heads, 24 heads each: 45.6 us, 54.4 one tile at a
+  // time; 32 x 8192 x 1 KV head of 48, E4M3: 41.9 and 46.7)
   s.qrows = s.G > 16 && c.head_dim <= 128 ? 32 : 16;
   s.qtiles = (s.G + s.qrows - 1) / s.qrows;
   s.rows = s.G < s.qrows ? s.G : s.qrows;
@@ -729,49 +733,49 @@ static Shape shape_of(const fp8b_kv_cache& c, int64_t B, int64_t Hq, int64_t col
   // the most tiles a region can have: a window reaches into one more
   const int64_t seen = window > 0 && window < s.max_len ? window + kTile - 1 : s.max_len;
   const int64_t tiles = (seen + kTile - 1) / kTile;
-  // Three ways to deal out the work (us at 128 positions, lengths up to 1.5 times
-  // the average).
+  // Three ways to deal out the work (128 positions; tiles: the most of a region).
   //
   // Each region cut into as many equal parts as there are CUs for, and joined by a
-  // second launch, which costs about as much as 24 tiles in a row (12 of 256
-  // positions, 48 of 64): whole / in parts, 8 regions of 24 tiles 7.0 / 8.3, of 30
-  // 10.0 / 8.0, of 94 11.7 / 8.2; 64 of 47 14.0 / 11.1; 128 of 33 11.6 / 12.3, of 47
-  // 14.5 / 14.0.  Parts of 8 tiles at least: 8.6 and 11.0; 512 workgroups of two
-  // waves: 9.5 and 12.8, 256 of eight: 9.2 and 11.8.
+  // second launch, which costs about as much as 20 tiles in a row; cut from 24 on
+  // (12 of 256 positions, 48 of 64): whole / in parts, 8 regions of 16 tiles 7.0 /
+  // 7.9, of 20 7.8 / 7.7, of 24 8.5 / 7.7, of 94 22.6 / 9.4; 64 of 45 13.8 / 11.3; 128
+  // of 33 11.8 / 12.6, of 47 14.3 / 14.1.  Half as many parts: 8 of 94 9.7, 64 of 45
+  // 12.5; as many workgroups of eight waves 9.3 and 12.1, twice as many of two 10.5 and
+  // 11.7.
   const int body = c.head_dim <= 64 ? 64 : (c.head_dim <= 128 ? 128 : 256);
   int parts_shift = 0;
   while ((s.regions << (parts_shift + 1)) <= kPartWgs && (kMinPart << parts_shift) < tiles) ++parts_shift;
   const int64_t saved = tiles - (tiles >> parts_shift);  // in a row, by the parts
   // One workgroup per region while they are short: in a line of all tiles, cut
-  // evenly whatever the lengths, a launch costs about 5 us more but no CU waits
-  // for the longest region: whole / line, 512 regions of 28 tiles 19 / 25, of 121
-  // 78 / 79, of 281 166 / 159.
+  // evenly whatever the lengths, a launch costs about 6 us more but no CU waits
+  // for the longest region: whole / line, 512 regions of 29 tiles 19.4 / 25.9, of
+  // 122 83.6 / 82.8, of 279 177 / 166.
   const int64_t whole = s.regions / 2 < 48 ? 48 : (s.regions / 2 < 128 ? s.regions / 2 : 128);
   s.wgs = 0;
   s.parts_shift = 0;
   if (saved * body > 24 * 128 && tiles <= ((int64_t)64 << parts_shift)) {
-    // (in parts / line: 32 regions of 47 tiles 9.1 / 12.4, of 375 19.6 / 21.7; 64 of
-    // 188 19.7 / 20.8, of 375, 94 to a part, 33.7 / 33.1)
+    // (in parts / line: 32 regions of 43 tiles 9.6 / 13.1, of 354 19.7 / 22.6; 64 of
+    // 178 19.8 / 21.5, of 314, 79 to a part, 33.7 / 33.3)
     s.parts_shift = parts_shift;
     s.waves_shift = kSplitShift;
   } else if (tiles <= whole) {
     // Four waves where 128 or 256 positions fill the body, else eight (64 regions of
-    // 24 tiles 4 / 8 waves 8.5 / 9.0, of 256 positions 13.4 / 14.4; 128 of 24 with 80
-    // positions 9.8 / 9.4, with 64 9.0 / 8.7), but not more than tiles; fewer where
+    // 23 tiles 4 / 8 waves 8.6 / 9.4, of 256 positions 13.7 / 14.6; 128 of 23 with 80
+    // positions 10.7 / 9.9, with 64 8.1 / 7.8), but not more than tiles; fewer where
     // that leaves each only a few tiles and there are regions enough for 12 waves
-    // a CU without (2048 regions of 5 tiles: 1 / 2 / 4 / 8 waves 14.2 / 15.2 / 18 /
-    // 30; 272 of 33 tiles of 64 positions: 27 / 16 / 11.2 / 9.9, 512 of them 4 / 8
-    // waves 13.7 / 16.5).
+    // a CU without (2048 regions of 5 tiles: 1 / 2 / 4 / 8 waves 14.6 / 15.7 / 18.4 /
+    // 31.1).  Eight waves fill a CU: 272 regions of 33 tiles of 64 positions, E4M3, fp32
+    // output, take 26.4 / 16.1 / 11.2 / 10.0 where a third of them is empty, but 26.4 /
+    // 20.4 / 13.5 / 16.4 where none is (16 of them wait for the other 256), 512 of them
+    // 4 / 8 waves 15.8 / 18.4.
     s.waves_shift = c.head_dim == 128 || c.head_dim == 256 ? 2 : 3;
     while (s.waves_shift > 0 && ((1 << s.waves_shift) > tiles ||
                                  ((5 << s.waves_shift) > tiles && (s.regions << s.waves_shift) > 12 * 256)))
       --s.waves_shift;
   } else {
-    // Two workgroups of four waves a CU: with 4 (1024 workgroups) a third of
-    // them waits for room (131072 tokens x 8 heads 68 -> 59 us, 128 x 6000 x 8
-    // 350 -> 314 us); a piece of fewer than 8 tiles costs more to join.  Of two
-    // or eight waves: 60.1 and 61.3 us against 59.1 (32 x 2048 x 8 heads 33.1
-    // and 37.5 against 32.5).
+    // Two workgroups of four waves a CU: 131072 tokens x 8 heads 60.4 us, with four a
+    // CU (a fourth of them waits for room) 63.5, with one 58.1; 128 x 6000 x 8 309, 309
+    // and 305.  Of two or eight waves 61.6 and 62.9, 311 and 309 (four: 60.1, 305).
     s.waves_shift = kSplitShift;
     const int64_t want = (s.regions * tiles + kMinTiles - 1) / kMinTiles;
     s.wgs = want < kMaxWgs ? want : kMaxWgs;
@@ -842,8 +846,9 @@ int launch_attention(const fp8b_kv_cache& c, const Attention& p, hipStream_t s) 
   const unsigned grid = (unsigned)(sh.wgs > 0 ? sh.wgs : sh.regions << sh.parts_shift);
   int rc;
   // Bodies of 64, 128 and 256 positions; one that D fills asks nothing about D
-  // (2-5% faster on short contexts, 1% on long ones).  192 positions go through
-  // the 256 body (88.6 us): a body of their own spills (158 us).
+  // (8 x 1000 tokens x 8 heads 11.4 us, 12.2 by the other; 131072 60.0 and 60.5).  192
+  // positions go through the 256 body (32 x 4096 x 8 heads 90.6 us, 256 positions
+  // 117): a body of their own spills about 100 registers.
   if (a.D == 64) rc = launch_dp<64, true>(a, c.fmt, grid, s);
   else if (a.D < 64) rc = launch_dp<64, false>(a, c.fmt, grid, s);
   else if (a.D == 128) rc = launch_dp<128, true>(a, c.fmt, grid, s);
@@ -852,8 +857,8 @@ int launch_attention(const fp8b_kv_cache& c, const Attention& p, hipStream_t s) 
   else rc = launch_dp<256, false>(a, c.fmt, grid, s);
   if (rc != FP8B_OK || (!a.line && a.parts_shift == 0)) return rc;
   // Few pieces to a region: its rows side by side in a workgroup (128 x 6000 x 8
-  // heads 313 us, 325 with a row each).  Many: one row, the threads shared out
-  // over the pieces (131072 x 8 heads 60 us, 69 with the rows side by side).
+  // heads 306 us, 318 with a row each).  Many: one row, the threads shared out
+  // over the pieces (131072 x 8 heads 60.3 us, 69.9 with the rows side by side).
   const int fit = 256 / (a.D / 4);
   const int rows_wg = grid <= 4 * sh.regions ? (sh.rows < fit ? sh.rows : fit) : 1;
   const dim3 jgrid((unsigned)sh.regions, (unsigned)((sh.rows + rows_wg - 1) / rows_wg));
