@@ -180,7 +180,9 @@ int fp8_kv_cache_read(const fp8b_kv_cache *cache, const int32_t *table,
  *   out[b][h] = sum_j e^(s_j - m) V[j] / sum_j e^(s_j - m),  m = max_j s_j
  *   lse[b][h] = m + ln(sum_j e^(s_j - m))
  * A row that sees nothing, or only scores of -inf, gives out 0 and lse -inf;
- * a NaN or +inf among the seen scores gives NaN.  What lies in the pages
+ * a NaN or +inf among the seen scores gives NaN.  A V code of a seen token
+ * that is not finite makes its position of the KV head's rows NaN or
+ * infinite, a V scale all their positions.  What lies in the pages
  * outside the seen range, NaN codes or scales included, has no effect.
  * Products and sums are fp32; the weights e^(s_j - m) enter the products
  * with V split into bf16 parts that keep at least 24 significant bits, as
@@ -191,7 +193,9 @@ int fp8_kv_cache_read(const fp8b_kv_cache *cache, const int32_t *table,
  *            multiples of 8), 16-byte aligned.  It includes the new token
  *            only through lens: write its K and V first.
  *   table, ld_table, cols, B  as for fp8_kv_cache_read; B >= 0 (0 is a
- *            no-op).  Only the pages of seen tokens are looked up.
+ *            no-op).  All cols entries of a row have to be readable; entries
+ *            beyond the seen tokens' pages may be read, and the pages they
+ *            name loaded (ids are clamped), without effect on the results.
  *   lens     int32 [B].
  *   max_context  0 .. 2^30: lengths beyond it, or beyond cols * page_size, are
  *            cut to it; a tight value saves the splitting of short contexts.

@@ -87,3 +87,31 @@ def test_an_infinity_makes_the_rows_scale_nan(F, value, fmt):
         assert torch.isnan(a[at]).all() and torch.equal(a[~at], b[~at])
     for a, b in ((c.k_codes, clean.k_codes), (c.v_codes, clean.v_codes)):
         assert torch.equal(a[~at], b[~at])
+
+
+@pytest.mark.parametrize("max_context", [300, None])          # whole regions; parts
+def test_values_that_are_not_finite_stay_in_their_position(F, max_context):
+    """An infinite V code of a seen token: that position of its KV head's rows is not finite, all else is the same;
+    an infinite V scale: every position of them."""
+    g = W.gen(8, DEV)
+    H, D, S, n = 2, 128, 16, 290
+    c = F.KVCache(20, S, H, D, "e5m2", DEV)
+    F.fp8_kv_cache_write(_rows(320, H, D, g), _rows(320, H, D, g), torch.arange(320, device=DEV), c)
+    q = _rows(1, 6, D, g)
+    table = torch.zeros(1, 200, dtype=torch.int32, device=DEV)
+    table[0, :20] = torch.arange(20, device=DEV)
+    lens = torch.tensor([n], dtype=torch.int32, device=DEV)
+
+    def run():
+        return F.fp8_paged_attention(q, c, table, lens, out_dtype=torch.float32, max_context=max_context)[0]
+
+    want = run()
+    c.v_codes[9, 1, 3, 77] = 0x7C
+    got = run()
+    bad = torch.zeros(6, D, dtype=torch.bool, device=DEV)
+    bad[3:, 77] = True
+    assert not torch.isfinite(got[bad]).any() and torch.equal(got[~bad], want[~bad])
+    c.v_codes[9, 1, 3, 77] = 0
+    c.v_scales[9, 1, 3] = float("inf")
+    got = run()
+    assert not torch.isfinite(got[3:]).any() and torch.equal(got[:3], want[:3])
