@@ -236,13 +236,14 @@ def fp8_paged_attention(q, cache: KVCache, block_table, context_lens, scale=None
 
 def attention_step(q, k, v, cos_sin, positions, slots, cache: KVCache, block_table, context_lens, q_weight=None,
                    k_weight=None, eps=1e-6, interleaved=False, scale=None, window: int = 0, out_dtype=torch.bfloat16,
-                   max_context=None):
+                   max_context=None, out=None, lse=None):
     """The attention side of one decode step, between the q/k/v projection
     and the output projection: norm and rotate the new token's queries and
     keys, quantise its K and V into the cache, attend.  context_lens counts
     the new token.  Every argument is checked before anything is written.
-    Returns out [B, Hq, D]."""
+    Returns out [B, Hq, D]; out and lse are as fp8_paged_attention's."""
     if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
         raise ValueError("out_dtype must be bfloat16 or float32")
     return _call("step", cache._dev, cache._ref, cache._dev, q, k, v, cos_sin, positions, slots, q_weight, k_weight,
-                 eps, interleaved, block_table, context_lens, scale, window, out_dtype is torch.float32, max_context)
+                 eps, interleaved, block_table, context_lens, scale, window, out_dtype is torch.float32, max_context, out,
+                 lse)

@@ -320,6 +320,16 @@ struct QkvWrite {
     r = rope_of(qr.D, qr.T, cs, pos, qw, kw, number(a[8]), truth(a[9]));
     s = static_cast<const int64_t*>(flat(slots, at::kLong, {qr.T}, "slots"));
   }
+  // An output and what is read beside q.
+  void keep_off(const Area& x, const char* name) const {
+    keep_apart(x, area(kr), name, "k");
+    keep_apart(x, area(vr), name, "v");
+    keep_apart(x, cs, name, "cos_sin");
+    keep_apart(x, pos, name, "positions");
+    keep_apart(x, &slots, name, "slots");
+    keep_apart(x, qw, name, "q_weight");
+    keep_apart(x, kw, name, "k_weight");
+  }
   void all_on(int64_t dev) const { on(dev, {&q, &k, &v, cs, pos, &slots, qw, kw}); }
 };
 
@@ -333,13 +343,7 @@ PyObject* qkv_write(PyObject* const* a) {
     const Rows o = rows(*gq, "q_out");
     const Area x = area(o);
     same_or_apart(o, w.qr, "q_out", "q");
-    keep_apart(x, area(w.kr), "q_out", "k");
-    keep_apart(x, area(w.vr), "q_out", "v");
-    keep_apart(x, w.cs, "q_out", "cos_sin");
-    keep_apart(x, w.pos, "q_out", "positions");
-    keep_apart(x, &w.slots, "q_out", "slots");
-    keep_apart(x, w.qw, "q_out", "q_weight");
-    keep_apart(x, w.kw, "q_out", "k_weight");
+    w.keep_off(x, "q_out");
     off_cache(x, "q_out", c);
   }
   w.all_on(dev);
@@ -425,6 +429,26 @@ struct Attention {
   }
   int dtype() const { return type == at::kFloat ? FP8B_OUT_F32 : FP8B_OUT_BF16; }
 };
+// Outputs given by the caller, from (out, lse): their checks but the device.
+struct Given {
+  const at::Tensor *out, *lse;
+  float* lse_p;
+  Given(const fp8b_kv_cache* c, const Rows& r, const Attention& x, PyObject* const* a)
+      : out(maybe(a[0], "out")), lse(maybe(a[1], "lse")) {
+    if (out) flat(*out, x.type, {r.T, r.H, r.D}, "out");
+    lse_p = lse ? static_cast<float*>(flat(*lse, at::kFloat, {r.T, r.H}, "lse")) : nullptr;
+    const std::pair<const at::Tensor*, const char*> outs[2] = {{out, "out"}, {lse, "lse"}};
+    for (const auto& [t, name] : outs)
+      if (t) {
+        const Area o = area(*t);
+        if (t == out) keep_apart(o, lse, name, "lse");
+        keep_apart(o, area(r), name, "q");
+        keep_apart(o, area(x.t), name, "block_table");
+        keep_apart(o, &x.lens, name, "context_lens");
+        off_cache(o, name, c);
+      }
+  }
+};
 // Of `bytes` on the current stream, like the call that uses it.
 at::Tensor workspace(int64_t bytes, const at::Tensor& q) {
   return bytes > 0 ? at::empty({bytes}, q.options().dtype(at::kByte)) : at::Tensor();
@@ -437,54 +461,45 @@ PyObject* attention(PyObject* const* a) {
   const at::Tensor& q = tensor(a[3], "q");
   const Rows r = rows(q, "q");
   const Attention x(c, r, a + 4, a[11]);
-  const at::Tensor *given = maybe(a[9], "out"), *lse = maybe(a[10], "lse");
-  if (given) flat(*given, x.type, {r.T, r.H, r.D}, "out");
-  float* lsep = lse ? static_cast<float*>(flat(*lse, at::kFloat, {r.T, r.H}, "lse")) : nullptr;
-  const std::pair<const at::Tensor*, const char*> outs[2] = {{given, "out"}, {lse, "lse"}};
-  for (const auto& [t, name] : outs)
-    if (t) {
-      const Area o = area(*t);
-      if (t == given) keep_apart(o, lse, name, "lse");
-      keep_apart(o, area(r), name, "q");
-      keep_apart(o, area(x.t), name, "block_table");
-      keep_apart(o, &x.lens, name, "context_lens");
-      off_cache(o, name, c);
-    }
-  on(dev, {&q, &x.bt, &x.lens, given, lse});
+  const Given given(c, r, x, a + 9);
+  on(dev, {&q, &x.bt, &x.lens, given.out, given.lse});
   const int64_t bytes = fp8_paged_attention_workspace(c, r.T, r.H, x.t.cols, x.most, x.window);
   if (bytes < 0) return status(bytes);
   void* stream = address(a[0]);
-  const at::Tensor out = given ? *given : at::empty({r.T, r.H, r.D}, q.options().dtype(x.type));
+  const at::Tensor out = given.out ? *given.out : at::empty({r.T, r.H, r.D}, q.options().dtype(x.type));
   const at::Tensor ws = workspace(bytes, q);
   void *outp = out.data_ptr(), *wsp = bytes > 0 ? ws.data_ptr() : nullptr;
   const int rc = launch([&] {
     return fp8_paged_attention(r.p, r.t, r.h, c, x.t.p, x.t.ld, x.t.cols, x.lp, r.T, r.H, x.most, x.window,
-                               (float)x.scale, outp, x.dtype(), lsep, wsp, stream);
+                               (float)x.scale, outp, x.dtype(), given.lse_p, wsp, stream);
   });
   return rc ? status(rc) : THPVariable_Wrap(out);
 }
 
 // (stream, cache, dev, q, k, v, cos_sin, positions, slots, q_weight, k_weight, eps, interleaved, block_table,
-// context_lens, scale, window, fp32, max_context) -> out
+// context_lens, scale, window, fp32, max_context, out, lse) -> out
 PyObject* step(PyObject* const* a) {
   const fp8b_kv_cache* c = cache_of(a[1]);
   const int64_t dev = integer(a[2]);
   const QkvWrite w(c, a + 3);
   const Rows& r = w.qr;
   const Attention x(c, r, a + 13, a[18]);
+  const Given given(c, r, x, a + 19);
+  for (const auto& [t, name] : {std::pair{given.out, "out"}, std::pair{given.lse, "lse"}})
+    if (t) w.keep_off(area(*t), name);
   w.all_on(dev);
-  on(dev, {&x.bt, &x.lens});
+  on(dev, {&x.bt, &x.lens, given.out, given.lse});
   const int64_t bytes = fp8_paged_attention_workspace(c, r.T, r.H, x.t.cols, x.most, x.window);
   if (bytes < 0) return status(bytes);
   void* stream = address(a[0]);
   const at::Tensor qo = at::empty({r.T, r.H, r.D}, w.q.options());
-  const at::Tensor out = at::empty({r.T, r.H, r.D}, w.q.options().dtype(x.type));
+  const at::Tensor out = given.out ? *given.out : at::empty({r.T, r.H, r.D}, w.q.options().dtype(x.type));
   const at::Tensor ws = workspace(bytes, w.q);
   void *qop = qo.data_ptr(), *outp = out.data_ptr(), *wsp = bytes > 0 ? ws.data_ptr() : nullptr;
   const int rc = launch([&] {
     return fp8_attention_step(r.p, r.t, r.h, w.kr.p, w.kr.t, w.kr.h, w.vr.p, w.vr.t, w.vr.h, w.s, r.T, r.H, &w.r, c,
                               x.t.p, x.t.ld, x.t.cols, x.lp, x.most, x.window, (float)x.scale, qop, r.H * r.D, r.D,
-                              outp, x.dtype(), nullptr, wsp, stream);
+                              outp, x.dtype(), given.lse_p, wsp, stream);
   });
   return rc ? status(rc) : THPVariable_Wrap(out);
 }
@@ -512,7 +527,7 @@ PyMethodDef method(const char* name) {
 
 PyMethodDef methods[] = {method<norm_rope, 11>("norm_rope"),   method<cache_write, 6>("cache_write"),
                          method<qkv_write, 14>("qkv_write"),   method<cache_read, 8>("cache_read"),
-                         method<attention, 12>("attention"),   method<step, 19>("step"),
+                         method<attention, 12>("attention"),   method<step, 21>("step"),
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_attn_binding", "Host side of attention.py's calls.", -1, methods,

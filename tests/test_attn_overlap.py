@@ -239,3 +239,28 @@ def test_writes_into_a_cache_that_shares_its_places():
     one = layer(1, 1, 0, 0)                                        # reading is left alone
     _apart(F.fp8_paged_attention, q, one, bt, lens)
     _apart(F.fp8_kv_cache_read, one, bt, offs, 5)
+
+
+def test_step_outputs():
+    c = _cache()
+    q, k = torch.zeros(3, 4, 64, dtype=bf16), torch.zeros(3, 2, 64, dtype=bf16)
+    tab, pos, slots = torch.zeros(10, 64), torch.zeros(3, dtype=i64), torch.zeros(3, dtype=i64)
+    bt, lens, w = torch.zeros(3, 4, dtype=i32), torch.ones(3, dtype=i32), torch.zeros(64, dtype=bf16)
+    out, lse = torch.zeros(3, 4, 64, dtype=bf16), torch.zeros(3, 4)
+
+    def f(q=q, k=k, pos=pos, slots=slots, bt=bt, w=w, **x):
+        return F.attention_step(q, k, k, tab, pos, slots, c, bt, lens, w, w, **x)
+
+    _apart(f, out=out, lse=lse)
+    _not_apart("out and q", f, q=out, out=out)
+    _not_apart("out and k", f, k=out.flatten()[:384].view(3, 2, 64), out=out)
+    _not_apart("out and slots", f, slots=out.flatten()[:12].view(i64), out=out)
+    _not_apart("out and q_weight", f, w=out.flatten()[64:128], out=out)
+    _not_apart("lse and positions", f, pos=lse.flatten()[:6].view(i64), lse=lse)
+    _not_apart("lse and cos_sin", f, lse=tab.flatten()[:12].view(3, 4))
+    _not_apart("lse and block_table", f, bt=lse.view(i32), lse=lse)
+    _not_apart("out and the cache", f, out=c.v_codes.flatten()[:1536].view(bf16).view(3, 4, 64))
+    with pytest.raises(ValueError, match="out must be contiguous"):
+        f(out=out.float())
+    with pytest.raises(ValueError, match="lse must have shape"):
+        f(lse=lse[:2])
