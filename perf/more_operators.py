@@ -1,0 +1,491 @@
+"""Timing cases of expert routing and of the W8A8 layers in 8-bit integers:
+the router with its plan and gradient, token rows to the experts and back with
+their gradients, the row quantiser, the integer linear layer, the experts'
+products, and the whole expert layer.
+
+Where `own` is false, run() computes each operator in elementary torch
+operations; where it is true it calls the library.
+"""
+import math
+import random
+
+import torch
+
+own = False
+
+TYPES = {"bf16": torch.bfloat16, "fp32": torch.float32}
+BYTES = {"bf16": 2, "fp32": 4}
+
+
+def listed():
+    return [
+        # the router of one decode step of 32 sequences, 8 of 256 experts
+        dict(name="route_step", op="route", T=32, E=256, k=8, dtype="bf16", renorm=True, padded=False, grad=False),
+        # a training batch's router with its gradient: fp32 logits, weights
+        # from the softmax over all experts, every seventh token padding
+        dict(name="route_train", op="route", T=16384, E=256, k=8, dtype="fp32", renorm=False, padded=True, grad=True),
+        # rows to the experts and back and both gradients: few experts, odd
+        # width, fp32, tokens that go nowhere
+        dict(name="rows_odd", op="rows", T=1021, E=20, k=3, N=1001, dtype="fp32", padded=True),
+        # the same for 4096 tokens of 7168 channels, 8 of 256 experts
+        dict(name="rows_train", op="rows", T=4096, E=256, k=8, N=7168, dtype="bf16", padded=False),
+        # the activations of a small decode batch
+        dict(name="quant_step", op="quant", M=8, K=8192, dtype="bf16"),
+        # the activations of a prompt
+        dict(name="quant_prompt", op="quant", M=4096, K=7168, dtype="bf16"),
+        # one token through a layer: the weights' bytes count
+        dict(name="linear_one", op="linear", M=1, K=8192, N=28672, bias=False, dtype="bf16", out="bf16"),
+        # sizes that fill no tile, bias, fp32 in and out
+        dict(name="linear_odd", op="linear", M=101, K=1480, N=1001, bias=True, dtype="fp32", out="fp32"),
+        # a prompt through a layer: the products count
+        dict(name="linear_prompt", op="linear", M=4096, K=7168, N=18432, bias=False, dtype="bf16", out="bf16"),
+        # the experts' products of 8 tokens: at most 64 of 256 experts are read
+        dict(name="experts_step", op="experts", T=8, E=256, k=8, K=7168, N=2048, out="bf16"),
+        # the same of a prompt, with the skew that routers have: the largest
+        dict(name="experts_prompt", op="experts", T=4096, E=256, k=8, K=7168, N=2048, out="bf16"),
+        # the whole expert layer of a decode step, some sequences padding
+        dict(name="layer_step", op="layer", T=32, E=256, k=8, K=7168, N=2048, dtype="bf16", padded=True),
+    ]
+
+
+def _log(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def draw(rng):
+    ls = listed()
+    most = {n: max(work(c)[n] for c in ls) for n in ("bytes", "flops")}
+    weights = max(c["E"] * c["N"] * c["K"] for c in ls if c["op"] in ("experts", "layer"))
+    while True:
+        op = rng.choice(("route", "rows", "quant", "linear", "linear", "experts", "layer"))
+        E = _log(rng, 4, 512)
+        k = rng.randint(1, min(E, 12))
+        dtype = rng.choice(("bf16", "bf16", "fp32"))
+        out = rng.choice(("bf16", "bf16", "fp32"))
+        padded = rng.random() < 0.5
+        if op == "route":
+            c = dict(op=op, T=_log(rng, 1, 32768), E=E, k=k, dtype=dtype, renorm=rng.random() < 0.5, padded=padded,
+                     grad=rng.random() < 0.5)
+        elif op == "rows":
+            c = dict(op=op, T=_log(rng, 1, 16384), E=E, k=k, N=_log(rng, 16, 8192), dtype=dtype, padded=padded)
+        elif op == "quant":
+            c = dict(op=op, M=_log(rng, 1, 16384), K=_log(rng, 16, 32768), dtype=dtype)
+        elif op == "linear":
+            c = dict(op=op, M=_log(rng, 1, 8192), K=_log(rng, 64, 16384), N=_log(rng, 16, 32768),
+                     bias=rng.random() < 0.5, dtype=dtype, out=out)
+        elif op == "experts":
+            c = dict(op=op, T=_log(rng, 1, 4096), E=E, k=k, K=_log(rng, 64, 8192), N=_log(rng, 64, 8192), out=out)
+        else:
+            c = dict(op=op, T=_log(rng, 1, 4096), E=E, k=k, K=_log(rng, 64, 8192), N=_log(rng, 64, 8192), dtype=dtype,
+                     padded=padded)
+        # an odd size is as good as the next multiple of 16: most real ones are such multiples
+        for n in ("N", "K"):
+            if n in c and rng.random() < 0.6:
+                c[n] = -(-c[n] // 16) * 16
+        w = work(c)
+        big = op in ("experts", "layer") and c["E"] * c["N"] * c["K"] > weights
+        if not big and all(w[n] <= most[n] for n in most):
+            return c
+
+
+def _live(case):
+    """Tokens that are no padding."""
+    T = case["T"]
+    return T - len(range(3, T, 7)) if case.get("padded") else T
+
+
+def _active(case):
+    """Experts that rows fall on, on average: one of rank r is chosen by a
+    token where N(0, 1) passes c + ln r, with c such that k of them are."""
+    def chances(c):
+        return [0.5 * math.erfc((c + math.log(r)) / math.sqrt(2.0)) for r in range(1, case["E"] + 1)]
+
+    lo, hi = -40.0, 40.0
+    for _ in range(60):
+        c = (lo + hi) / 2
+        lo, hi = (c, hi) if sum(chances(c)) > case["k"] else (lo, c)
+    return sum(1 - (1 - p) ** _live(case) for p in chances(lo))
+
+
+def work(case):
+    op = case["op"]
+    if op == "quant":
+        M, K = case["M"], case["K"]
+        return dict(bytes=M * K * (BYTES[case["dtype"]] + 1) + 4 * M, flops=3 * M * K)
+    if op == "linear":
+        M, K, N = case["M"], case["K"], case["N"]
+        return dict(bytes=M * K * BYTES[case["dtype"]] + N * K + 4 * N * (2 if case["bias"] else 1) +
+                    M * N * BYTES[case["out"]], flops=2 * M * N * K)
+    T, E, k = case["T"], case["E"], case["k"]
+    R = _live(case) * k
+    if op == "route":
+        b = BYTES[case["dtype"]]
+        n = T * E * b + T * k * 16 + 4 * E
+        if case["grad"]:
+            n += T * E * b * (1 if case["renorm"] else 2) + T * k * 12
+        return dict(bytes=n, flops=T * E * (4 if case["grad"] else 2))
+    N = case["N"]
+    if op == "rows":
+        b = BYTES[case["dtype"]]
+        return dict(bytes=b * N * (4 * T + 5 * R) + 8 * R + 12 * T * k, flops=6 * R * N)
+    K = case["K"]
+    n = _active(case) * (N * K + 4 * N)
+    if op == "experts":
+        n += T * K + 8 * R + R * N * BYTES[case["out"]]
+    else:
+        n += T * K * BYTES[case["dtype"]] + T * E * BYTES[case["dtype"]] + 16 * T * k + T * N * 2
+    return dict(bytes=n, flops=2 * R * N * K)
+
+
+# ---- inputs -----------------------------------------------------------------
+
+
+def _logits(case, g):
+    """A router's logits: spread between tokens, some experts in more demand
+    (falling with their rank); padding tokens have no expert."""
+    T, E = case["T"], case["E"]
+    rank = torch.randperm(E, generator=g, device="cuda") + 1
+    z = torch.randn(T, E, generator=g, device="cuda") - torch.log(rank.float())
+    if case.get("padded"):
+        z[3::7] = -math.inf
+    return z.to(TYPES[case.get("dtype", "fp32")])
+
+
+def _acts(M, K, g, dtype):
+    """Activations with a few outlier channels."""
+    x = torch.randn(M, K, generator=g, device="cuda")
+    x[:, torch.randperm(K, generator=g, device="cuda")[:max(1, K // 200)]] *= 50.0
+    return x.to(TYPES[dtype])
+
+
+def _codes(shape, g):
+    """Weight codes and their channels' scales, as a checkpoint holds them."""
+    w = torch.empty(shape, dtype=torch.int8, device="cuda")
+    for i in range(0, shape[0], 4096 if len(shape) == 2 else 16):
+        part = w[i:i + (4096 if len(shape) == 2 else 16)]
+        part.copy_((32.0 * torch.randn(part.shape, generator=g, device="cuda")).round_().clamp_(-127, 127))
+    s = 0.02 / 32.0 * torch.exp2(2 * torch.rand(shape[:-1], generator=g, device="cuda") - 1)
+    return w, s
+
+
+def _sorted(experts, E):
+    """Rows in the order of (expert, token, slot) of experts [T, k], -1 for none."""
+    T, k = experts.shape
+    flat = experts.flatten().long()
+    order = torch.argsort(torch.where(flat < 0, E, flat), stable=True)
+    count = torch.bincount(flat[flat >= 0], minlength=E)
+    offsets = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    offsets[1:] = count.cumsum(0)
+    rows = torch.empty(T * k, dtype=torch.int32, device="cuda")
+    rows[order] = torch.arange(T * k, dtype=torch.int32, device="cuda")
+    return dict(offsets=offsets, row_index=(order // k).int(),
+                token_rows=torch.where(flat < 0, -1, rows).view(T, k).int().contiguous())
+
+
+def prepare(case, seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    op = case["op"]
+    s = dict(case)
+    if op == "route":
+        s["logits"] = _logits(case, g)
+        if case["grad"]:
+            s["dgates"] = torch.randn(case["T"], case["k"], generator=g, device="cuda")
+    elif op == "rows":
+        T, k, N, dt = case["T"], case["k"], case["N"], TYPES[case["dtype"]]
+        z = _logits(case, g).float()
+        top = z.topk(k, 1)
+        s |= _sorted(torch.where(top.values == -math.inf, -1, top.indices).int(), case["E"])
+        s["gates"] = torch.where(top.values == -math.inf, 0.0, torch.softmax(top.values, 1)).nan_to_num(0.0)
+        for n, rows in (("x", T), ("y", T * k), ("dout", T), ("drows", T * k)):
+            s[n] = torch.randn(rows, N, generator=g, device="cuda").to(dt)
+        # rows behind the last expert's stay as they are
+        s["rows"], s["dy"] = (torch.zeros(T * k, N, dtype=dt, device="cuda") for _ in range(2))
+    elif op == "quant":
+        s["x"] = _acts(case["M"], case["K"], g, case["dtype"])
+    elif op == "linear":
+        s["x"] = _acts(case["M"], case["K"], g, case["dtype"])
+        s["w"], s["sw"] = _codes((case["N"], case["K"]), g)
+        s["b"] = torch.randn(case["N"], generator=g, device="cuda") if case["bias"] else None
+    else:
+        s["w"], s["sw"] = _codes((case["E"], case["N"], case["K"]), g)
+        z = _logits(case, g)
+        if op == "layer":
+            s["logits"] = z
+            s["x"] = _acts(case["T"], case["K"], g, case["dtype"])
+        else:
+            s |= _sorted(z.topk(case["k"], 1).indices.int(), case["E"])
+            # rows lie whole 128-byte lines apart, as the quantiser lays them out
+            codes, s["sa"] = _codes((case["T"], case["K"]), g)
+            s["a"] = codes.new_zeros(case["T"], -(-case["K"] // 128) * 128)[:, :case["K"]].copy_(codes)
+    if own and "w" in s:
+        import fp8_block_scaled_02_amd as F
+        s["w"] = F.int8_weight_pack(s["w"])
+    return s
+
+
+# ---- the plain form ---------------------------------------------------------
+
+
+def _plain_route(logits, k, renorm):
+    z = logits.float()
+    value, e = torch.sort(z, dim=1, descending=True, stable=True)
+    value, e = value[:, :k], e[:, :k]
+    none = value == -math.inf
+    top = torch.where(none[:, :1], 0.0, value[:, :1])
+    p = torch.exp(value - top)
+    total = (p if renorm else torch.exp(z - top)).sum(1, keepdim=True)
+    gates = torch.where(none, 0.0, p / torch.where(total == 0, 1.0, total))
+    experts = torch.where(none, -1, e).int()
+    # a row's place: rows of the experts before it, then those of earlier tokens and slots
+    E = z.shape[1]
+    flat = experts.flatten().long()
+    order = torch.sort(torch.where(flat < 0, E, flat), stable=True).indices
+    rank = torch.empty_like(order)
+    rank[order] = torch.arange(order.numel(), device=order.device)
+    count = torch.zeros(E + 1, dtype=torch.int64, device=z.device)
+    count.index_add_(0, flat + 1, (flat >= 0).long())
+    return dict(gates=gates, experts=experts, offsets=count.cumsum(0).int(), row_index=(order // k).int(),
+                token_rows=torch.where(flat < 0, -1, rank).view_as(experts).int())
+
+
+def _plain_route_backward(dgates, logits, gates, experts, renorm):
+    kept = experts >= 0
+    dot = torch.where(kept, gates * dgates, 0.0).sum(1, keepdim=True)
+    # one place more for the slots that have no expert
+    d = torch.zeros(logits.shape[0], logits.shape[1] + 1, device=logits.device)
+    e = torch.where(kept, experts, logits.shape[1]).long()
+    if renorm:
+        d.scatter_(1, e, gates * (dgates - dot))
+        d = d[:, :-1]
+    else:
+        z = logits.float()
+        top = z.amax(1, keepdim=True)
+        p = torch.exp(z - torch.where(top == -math.inf, 0.0, top))
+        total = p.sum(1, keepdim=True)
+        d.scatter_(1, e, gates * dgates)
+        d = d[:, :-1] - p / torch.where(total == 0, 1.0, total) * dot
+    return d.to(logits.dtype)
+
+
+def _plain_combine(y, token_rows, gates, dtype):
+    kept = token_rows >= 0
+    rows = y[token_rows.clamp(min=0).long()].float()
+    return torch.where(kept[..., None], rows * gates[..., None], 0.0).sum(1).to(dtype)
+
+
+def _plain_quant(x):
+    x = x.float()
+    amax = x.abs().amax(1)
+    d = torch.where(amax == 0, 1.0, amax / torch.full_like(amax, 127.0))
+    return torch.round(x / d[:, None]), d
+
+
+def _plain_experts(a, sa, w, sw, offsets, row_index):
+    """The experts that have rows, one after the other."""
+    y = torch.zeros(row_index.numel(), w.shape[1], device=w.device)
+    ends = offsets.tolist()
+    for e in range(w.shape[0]):
+        if ends[e] < ends[e + 1]:
+            t = row_index[ends[e]:ends[e + 1]].long()
+            y[ends[e]:ends[e + 1]] = torch.matmul(a[t].float(), w[e].float().t()) * sa[t][:, None] * sw[e]
+    return y
+
+
+def _route_out(r):
+    # (rows behind the last expert's have no token)
+    live = torch.arange(r["row_index"].numel(), device=r["offsets"].device) < r["offsets"][-1]
+    return [r["gates"], r["experts"], r["offsets"], torch.where(live, r["row_index"], -1), r["token_rows"]]
+
+
+def _plain(s):
+    op = s["op"]
+    if op == "route":
+        r = _plain_route(s["logits"], s["k"], s["renorm"])
+        out = _route_out(r)
+        if s["grad"]:
+            out.append(_plain_route_backward(s["dgates"], s["logits"], r["gates"], r["experts"], s["renorm"]))
+        return out
+    if op == "rows":
+        dt, tr = s["x"].dtype, s["token_rows"]
+        kept = tr >= 0
+        live = torch.arange(s["rows"].shape[0], device=tr.device) < s["offsets"][-1]
+        rows = torch.where(live[:, None], s["x"][s["row_index"].long()], s["rows"])
+        out = _plain_combine(s["y"], tr, s["gates"], dt)
+        at = tr.clamp(min=0).long()
+        dout = s["dout"].float()[:, None]
+        dgates = torch.where(kept, (dout * s["y"][at].float()).sum(-1), 0.0)
+        # slots that have no row write to one more, which is left out
+        dy = torch.cat((s["dy"], s["dy"][:1]))
+        dy[torch.where(kept, tr, dy.shape[0] - 1).long()] = (s["gates"][..., None] * dout).to(dt)
+        dx = _plain_combine(s["drows"], tr, torch.ones_like(s["gates"]), dt)
+        return [rows, out, dy[:-1], dgates, dx]
+    if op == "quant":
+        codes, d = _plain_quant(s["x"])
+        return [codes.to(torch.int8), d]
+    if op == "linear":
+        a, sa = _plain_quant(s["x"])
+        y = torch.matmul(a, s["w"].float().t()) * sa[:, None] * s["sw"]
+        return (y + s["b"] if s["bias"] else y).to(TYPES[s["out"]])
+    if op == "experts":
+        return _plain_experts(s["a"], s["sa"], s["w"], s["sw"], s["offsets"], s["row_index"]).to(TYPES[s["out"]])
+    r = _plain_route(s["logits"], s["k"], True)
+    a, sa = _plain_quant(s["x"])
+    y = _plain_experts(a, sa, s["w"], s["sw"], r["offsets"], r["row_index"])
+    return [_plain_combine(y, r["token_rows"], r["gates"], torch.bfloat16)] + _route_out(r)
+
+
+# ---- the library's calls ----------------------------------------------------
+
+
+def _own_route_out(r):
+    return [r.gates, r.experts, r.expert_offsets, r.row_index, r.token_rows]
+
+
+def _own(s):
+    import fp8_block_scaled_02_amd as F
+    op = s["op"]
+    if op == "route":
+        r = F.moe_route(s["logits"], s["k"], s["renorm"])
+        out = _own_route_out(r)
+        if s["grad"]:
+            out.append(F.moe_route_backward(s["dgates"], s["logits"], r.gates, r.experts, s["renorm"]))
+        return out
+    if op == "rows":
+        rows = F.moe_gather(s["x"], s["row_index"], s["offsets"], out=s["rows"])
+        out = F.moe_combine(s["y"], s["token_rows"], s["gates"])
+        dy, dgates = F.moe_combine_backward(s["dout"], s["y"], s["token_rows"], s["gates"], dy=s["dy"])
+        dx = F.moe_gather_backward(s["drows"], s["token_rows"])
+        return [rows, out, dy, dgates, dx]
+    if op == "quant":
+        return F.int8_quant(s["x"])
+    if op == "linear":
+        return F.int8_linear(s["x"], s["w"], s["sw"], s["b"], TYPES[s["out"]])
+    if op == "experts":
+        return F.int8_grouped_gemm(s["a"], s["sa"], s["row_index"], s["offsets"], s["w"], s["sw"], TYPES[s["out"]])
+    out, r = F.int8_moe_forward(s["x"], s["logits"], s["k"], s["w"], s["sw"])
+    return [out] + _own_route_out(r)
+
+
+def run(state):
+    return _own(state) if own else _plain(state)
+
+
+# ---- the definition in 64 bits ----------------------------------------------
+
+
+def _exact_plan(z, k):
+    """For each token its experts in order of logit, then of number; the rows
+    of each expert in order of token and slot."""
+    T, E = z.shape
+    # a logit's standing: how many logits of its token are larger, or equal with a lower number
+    number = torch.arange(E, device="cuda")
+    experts = torch.full((T, k), -1, dtype=torch.int64, device="cuda")
+    for lo in range(0, T, 512):
+        part = z[lo:lo + 512]
+        before = torch.zeros(part.shape, dtype=torch.int64, device="cuda")
+        for e in range(E):
+            before += (part[:, e:e + 1] > part) | ((part[:, e:e + 1] == part) & (e < number))
+        t, e = ((before < k) & (part > -math.inf)).nonzero(as_tuple=True)
+        experts[lo + t, before[t, e]] = e
+    flat = experts.flatten()
+    held = flat.new_zeros(E + 1)
+    row_index = torch.full((T * k,), -1, dtype=torch.int64, device="cuda")
+    token_rows = torch.full((T * k,), -1, dtype=torch.int64, device="cuda")
+    at = 0
+    for e in range(E):
+        mine = (flat == e).nonzero()[:, 0]
+        n = mine.numel()
+        row_index[at:at + n] = mine // k
+        token_rows[mine] = torch.arange(at, at + n, device="cuda")
+        at += n
+        held[e + 1] = at
+    return experts, held, row_index, token_rows.view(T, k)
+
+
+def _exact_gates(z, experts, renorm):
+    kept = experts >= 0
+    chosen = torch.where(kept, z.gather(1, experts.clamp(min=0)), -math.inf)
+    lse = torch.logsumexp(chosen if renorm else z, 1, keepdim=True)
+    return torch.where(kept, torch.exp(chosen - lse), 0.0)
+
+
+def _exact_quant(x):
+    x = x.double()
+    amax = x.abs().max(1).values
+    d = (amax / 127).float().double()
+    d[amax == 0] = 1.0
+    # a code is the whole number nearest to the fp32 quotient
+    return (x / d[:, None]).float().double().round(), d
+
+
+def exact(case, seed):
+    global own
+    was, own = own, False                       # the inputs as they are, without the library's layouts
+    try:
+        s = prepare(case, seed)
+    finally:
+        own = was
+    op = case["op"]
+    if op == "quant":
+        codes, d = _exact_quant(s["x"])
+        return [codes.to(torch.int8), d]
+    if op == "linear":
+        a, d = _exact_quant(s["x"])
+        y = (s["w"].double() @ a.t().contiguous()).t() * d[:, None] * s["sw"].double()
+        return y + s["b"].double() if case["bias"] else y
+    k = case["k"]
+    if op == "rows":
+        tr, g, dout = s["token_rows"].long(), s["gates"].double(), s["dout"].double()
+        n = int(s["offsets"][-1])
+        rows, dy = s["rows"].double(), s["dy"].double()
+        rows[:n] = s["x"].double()[s["row_index"][:n].long()]
+        out, dx = torch.zeros_like(dout), torch.zeros_like(dout)
+        dgates = torch.zeros_like(g)
+        for j in range(k):
+            t = (tr[:, j] >= 0).nonzero()[:, 0]
+            r = tr[t, j]
+            out[t] += g[t, j:j + 1] * s["y"][r].double()
+            dx[t] += s["drows"][r].double()
+            dy[r] = g[t, j:j + 1] * dout[t]
+            dgates[t, j] = (dout[t] * s["y"][r].double()).sum(1)
+        return [rows, out, dy, dgates, dx]
+    if op == "experts":
+        out = torch.zeros(s["row_index"].numel(), case["N"], dtype=torch.float64, device="cuda")
+        offs = s["offsets"].tolist()
+        for e in range(case["E"]):
+            t = s["row_index"][offs[e]:offs[e + 1]].long()
+            if t.numel():
+                y = s["w"][e].double() @ s["a"][t].double().t().contiguous()
+                out[offs[e]:offs[e + 1]] = y.t() * s["sa"][t].double()[:, None] * s["sw"][e].double()
+        return out
+    z = s["logits"].double()
+    renorm = op == "layer" or case["renorm"]
+    experts, held, row_index, token_rows = _exact_plan(z, k)
+    gates = _exact_gates(z, experts, renorm)
+    plan = [gates] + [v.int() for v in (experts, held, row_index, token_rows)]
+    if op == "layer":
+        a, d = _exact_quant(s["x"])
+        out = torch.zeros(case["T"], case["N"], dtype=torch.float64, device="cuda")
+        ends = held.tolist()
+        for e in range(case["E"]):
+            t = row_index[ends[e]:ends[e + 1]]
+            if t.numel():
+                y = (s["w"][e].double() @ a[t].t().contiguous()).t() * d[t][:, None] * s["sw"][e].double()
+                g = (gates[t] * (experts[t] == e)).sum(1, keepdim=True)
+                out[t] += g * y
+        return [out] + plan
+    if case["grad"]:
+        dg = s["dgates"].double()
+        hot = torch.zeros(case["T"], case["E"] + 1, dtype=torch.float64, device="cuda")
+        hot.scatter_(1, torch.where(experts < 0, case["E"], experts), gates * dg)
+        hot = hot[:, :-1]
+        total = hot.sum(1, keepdim=True)
+        # the share of the softmax: over the chosen experts, or over all
+        if renorm:
+            share = torch.zeros(case["T"], case["E"] + 1, dtype=torch.float64, device="cuda")
+            share = share.scatter_(1, torch.where(experts < 0, case["E"], experts), gates)[:, :-1]
+        else:
+            share = torch.softmax(z, 1).nan_to_num(0.0)
+        plan.append(hot - share * total)
+    return plan
