@@ -352,7 +352,7 @@ def _own(s):
             out.append(F.moe_route_backward(s["dgates"], s["logits"], r.gates, r.experts, s["renorm"]))
         return out
     if op == "rows":
-        rows = F.moe_gather(s["x"], s["row_index"], s["offsets"], out=s["rows"])
+        rows = F.moe_gather(s["x"], s["token_rows"], out=s["rows"])
         out = F.moe_combine(s["y"], s["token_rows"], s["gates"])
         dy, dgates = F.moe_combine_backward(s["dout"], s["y"], s["token_rows"], s["gates"], dy=s["dy"])
         dx = F.moe_gather_backward(s["drows"], s["token_rows"])
