@@ -562,3 +562,6 @@ def fp8b_stream_probe(kind: int, x: torch.Tensor, q: torch.Tensor, scales: torch
 from .attention import (  # noqa: E402
     KVCache, attention_step, attn_lib, fp8_kv_cache_read, fp8_kv_cache_write, fp8_paged_attention, fp8_qk_norm_rope,
     fp8_qkv_cache_write)
+from .moe import (  # noqa: E402
+    Routing, int8_gemm, int8_grouped_gemm, int8_linear, int8_moe_forward, int8_quant, int8_weight_pack, moe_combine,
+    moe_combine_backward, moe_gather, moe_gather_backward, moe_lib, moe_route, moe_route_backward, moe_sort)
