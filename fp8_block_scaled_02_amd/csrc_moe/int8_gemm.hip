@@ -202,11 +202,221 @@ __global__ __launch_bounds__(kStreamThreads) void grouped_stream_kernel(Product 
   stream_tile<MI, P, BF16>(p, r, (int64_t)(blockIdx.x % tiles_n) * P, wide);
 }
 
+// ---- tiles ------------------------------------------------------------------
+
+typedef __attribute__((address_space(3))) void lds_void;
+typedef const __attribute__((address_space(1))) void global_void;
+
+constexpr int kStep = 128;  // codes of K a step
+
+// LDS byte of 16-byte chunk `ch` (0 .. 7) of row r of a tile of 128-byte rows;
+// chunks are swapped by bits 1-3 of the row, which keeps the fragment reads
+// free of bank conflicts.
+__device__ __forceinline__ int lds_at(int r, int ch) { return r * kStep + ((ch ^ ((r >> 1) & 7)) << 4); }
+
+// All but the last N loads from memory have arrived, and all reads of LDS.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (0 << 8) | ((N >> 4) << 14));
+}
+
+// A raw buffer over the 4 GiB from base.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_at(const void* base) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, (int)0xFFFFFFFFu, 0x00020000);
+}
+__device__ __forceinline__ v4i load16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+  const auto v = __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0);
+  return v4i{(int)v[0], (int)v[1], (int)v[2], (int)v[3]};
+}
+// 16 bytes a lane from memory to 1 KB of LDS, not through registers.
+__device__ __forceinline__ void load_lds(__amdgpu_buffer_rsrc_t r, uint32_t off, uint32_t step_off, int8_t* lds) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)lds, 16, off, step_off, 0, 0);
+}
+
+// WM x 4 waves, each with 16 MI rows of a and 16 NJ of the weights.
+template <int MI_, int WM_, int NJ_>
+struct Cfg {
+  static constexpr int MI = MI_, WM = WM_, NJ = NJ_;
+  static constexpr int kWaves = 4 * WM, kThreads = 64 * kWaves;
+  static constexpr int kRows = 16 * MI * WM, kCols = 64 * NJ;
+  static constexpr int kA = kRows / 8 / kWaves;  // pieces of 8 rows of a that a wave brings in a step
+  static_assert(kRows % (8 * kWaves) == 0, "pieces split evenly");
+};
+
+// The codes of a wave's weight rows in one step.
+template <int NJ>
+struct Weights {
+  v4i w[2][NJ];
+};
+
+#ifndef SGB
+#define SGB 2
+#endif
+template <class C, bool BF16>
+__device__ __forceinline__ void tile(const Product& p, const Rows& r, int64_t panel0, bool wide) {
+  constexpr int MI = C::MI, NJ = C::NJ;
+  __shared__ __attribute__((aligned(16))) int8_t st0[C::kRows * kStep];
+  __shared__ __attribute__((aligned(16))) int8_t st1[C::kRows * kStep];
+  __shared__ __attribute__((aligned(16))) int8_t st2[C::kRows * kStep];
+  __shared__ __attribute__((aligned(16))) int8_t st3[C::kRows * kStep];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wn = wave & 3, wm = wave >> 2;
+  const int l16 = lane & 15, g = lane >> 4;
+  const int64_t panels = (p.N + 15) / 16;
+  const int steps = (int)((p.K + kStep - 1) / kStep);
+  const int8_t* abase = p.a + (r.index ? 0 : r.m0 * p.lda);
+  uint32_t aoff[C::kA];
+#pragma unroll
+  for (int q = 0; q < C::kA; ++q) {
+    const int row = 8 * (wave + C::kWaves * q) + (lane >> 3);
+    const int64_t t = r.index ? r.token(row) : min(row, r.rows - 1);
+    aoff[q] = (uint32_t)(t * p.lda) + 16 * ((lane & 7) ^ ((row >> 1) & 7));
+  }
+  const int64_t first = panel0 + wn * NJ;
+  uint32_t woff[NJ];
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) woff[j] = (uint32_t)(min(first + j, panels - 1) * 1024) + 16 * lane;
+  const int64_t chunk = panels * 1024;
+  auto load_w = [&](v4i (&w)[NJ], int c) {
+    const __amdgpu_buffer_rsrc_t b = buffer_at(r.w + c * chunk);
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) w[j] = load16(b, woff[j]);
+  };
+  const __amdgpu_buffer_rsrc_t abuf = buffer_at(abase);
+  auto issue = [&](int8_t* st, int t) {
+#pragma unroll
+    for (int q = 0; q < C::kA; ++q)
+      load_lds(abuf, aoff[q], (uint32_t)(t * kStep), st + 1024 * (wave + C::kWaves * q));
+  };
+  v4i acc[MI][NJ];
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) acc[i][j] = v4i{0, 0, 0, 0};
+  const int x_lo = lds_at(16 * MI * wm + l16, g);
+  // Step t multiplies stage t % 4 by the weights of set t % 2: the first
+  // chunk's products, then the second's, each chunk's registers loaded again
+  // for step t + 2 as soon as its products are issued.
+  auto step = [&](int t, const int8_t* cur, Weights<NJ>& w, int8_t* refill, bool more_a, bool more_w, bool full) {
+    // this wave's part of stage t is in LDS; what may still fly is younger:
+    // the stages of t + 1 and t + 2, the weights of t and t + 1
+    if (full) wait_loads<4 * NJ + 2 * C::kA>(); else wait_loads<0>();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    if (more_a) issue(refill, t + 3);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int8_t* x = cur + (h ? x_lo ^ 64 : x_lo);
+#pragma unroll
+      for (int i = 0; i < MI; ++i) {
+        const v4i v = *reinterpret_cast<const v4i*>(x + 2048 * i);
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) acc[i][j] = mfma(w.w[h][j], v, acc[i][j]);
+      }
+      if (more_w) load_w(w.w[h], 2 * (t + 2) + h);
+    }
+    // LDS reads SGB fragments ahead of the products
+    if (SGB > 0) {
+      __builtin_amdgcn_sched_group_barrier(0x020, C::kA, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, SGB, 0);
+#pragma unroll
+      for (int i = 0; i < 2 * MI; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, NJ, 0);
+        if (i + SGB < 2 * MI) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        if (more_w && (i == MI - 1 || i == 2 * MI - 1)) __builtin_amdgcn_sched_group_barrier(0x020, NJ, 0);
+      }
+    }
+  };
+  Weights<NJ> w0, w1;
+  // (the loads of steps that are not there read the last one's again: with a
+  // branch the compiler would not know how many loads are in flight at the
+  // head of the loop, and wait for all)
+  const int last = steps - 1;
+  issue(st0, 0);
+  issue(st1, min(1, last));
+  load_w(w0.w[0], 0);
+  load_w(w0.w[1], 1);
+  issue(st2, min(2, last));
+  load_w(w1.w[0], 2 * min(1, last));
+  load_w(w1.w[1], 2 * min(1, last) + 1);
+  int t = 0;
+  for (; t + 7 <= steps; t += 4) {
+    step(t, st0, w0, st3, true, true, true);
+    step(t + 1, st1, w1, st0, true, true, true);
+    step(t + 2, st2, w0, st1, true, true, true);
+    step(t + 3, st3, w1, st2, true, true, true);
+  }
+  // one to six more
+  auto tail = [&](int u, const int8_t* cur, Weights<NJ>& w, int8_t* refill) {
+    if (u < steps) step(u, cur, w, refill, u + 3 < steps, u + 2 < steps, u + 2 < steps);
+  };
+  tail(t, st0, w0, st3);
+  tail(t + 1, st1, w1, st0);
+  tail(t + 2, st2, w0, st1);
+  tail(t + 3, st3, w1, st2);
+  tail(t + 4, st0, w0, st3);
+  tail(t + 5, st1, w1, st0);
+  wait_loads<0>();
+#pragma unroll
+  for (int i = 0; i < MI; ++i) {
+    const int m = 16 * (MI * wm + i) + l16;
+    if (m >= r.rows) continue;
+    const float sa = p.sa[r.token(m)];
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      const int64_t n = (first + j) * 16 + 4 * g;
+      if (n < p.N) store4<BF16>(p.y.p, (r.m0 + m) * p.y.ld, n, p.N, acc[i][j], sa, r.sw, p.bias, wide);
+    }
+  }
+}
+
+// Output tile of workgroup `id`: workgroups go round the 8 XCDs in turn, so
+// each XCD gets a run of tiles, in groups of 8 tiles of rows, so that the
+// workgroups of an XCD share rows and weights in its L2.
+__device__ __forceinline__ void tile_of(int id, int tiles_m, int tiles_n, int& tm, int& tn) {
+  const int n = tiles_m * tiles_n;
+  if (n % 8 == 0) id = id % 8 * (n / 8) + id / 8;
+  constexpr int kGroup = 8;
+  const int per = kGroup * tiles_n, group = id / per, first = group * kGroup;
+  const int rows = min(tiles_m - first, kGroup), in = id - group * per;
+  tm = first + in % rows;
+  tn = in / rows;
+}
+
+template <class C, bool BF16, int OCC>
+__global__ __launch_bounds__(C::kThreads, OCC) void tile_kernel(Product p, int64_t M, int tiles_m, int tiles_n,
+                                                                bool wide) {
+  int tm, tn;
+  tile_of(blockIdx.x, tiles_m, tiles_n, tm, tn);
+  const int64_t m0 = (int64_t)tm * C::kRows;
+  const Rows r{nullptr, M, m0, (int)min((int64_t)C::kRows, M - m0), p.w, p.sw};
+  tile<C, BF16>(p, r, (int64_t)tn * C::NJ * 4, wide);
+}
+
 bool wide_rows(const Mat& y) { return reinterpret_cast<uintptr_t>(y.p) % 16 == 0 && y.ld % 4 == 0; }
 
 }  // namespace
 
+template <class C, int OCC>
+int launch_tiles(const Product& p, int64_t M, hipStream_t s) {
+  const int64_t tiles_m = (M + C::kRows - 1) / C::kRows, tiles_n = (p.N + C::kCols - 1) / C::kCols;
+  if (tiles_m * tiles_n > (1 << 22)) return FP8B_EINVAL;
+  auto go = [&](auto b) {
+    hipLaunchKernelGGL((tile_kernel<C, decltype(b)::value, OCC>), dim3((unsigned)(tiles_m * tiles_n)), dim3(C::kThreads),
+                       0, s, p, M, (int)tiles_m, (int)tiles_n, wide_rows(p.y));
+    return check_launch();
+  };
+  return p.y.bf16 ? go(std::true_type{}) : go(std::false_type{});
+}
+
+#ifndef BIG
+#define BIG Cfg<8, 1, 4>, 2
+#endif
 int launch_gemm(const Product& p, int64_t M, hipStream_t s) {
+  if (M > 128) return launch_tiles<BIG>(p, M, s);
+  if (M > 64) return launch_tiles<Cfg<8, 1, 4>, 2>(p, M, s);
   constexpr int MI = 4, P = 4;
   const int64_t tiles_n = (p.N + 16 * P - 1) / (16 * P), tiles = tiles_n * ((M + 16 * MI - 1) / (16 * MI));
   if (tiles > (1 << 22)) return FP8B_EINVAL;
