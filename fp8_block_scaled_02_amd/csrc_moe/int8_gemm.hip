@@ -21,6 +21,7 @@
 
 namespace fp8moe {
 
+using fp8blk::bf16x2;
 using fp8blk::f32_to_bf16_bits;
 using fp8blk::u32x2;
 using fp8blk::u32x4;
@@ -33,10 +34,14 @@ __device__ __forceinline__ v4i mfma(v4i w, v4i x, v4i c) {
   return __builtin_amdgcn_mfma_i32_16x16x64_i8(w, x, c, 0, 0, 0);
 }
 
+// How y can be written, by its address and leading dimension: one value at a
+// time, four (8 bytes of bf16, 16 of fp32), or 16 bytes of either.
+enum class Stores { values, fours, lines };
+
 // Four columns n .. n+3 of row y (those below N), from their sums.
 template <bool BF16>
 __device__ __forceinline__ void store4(void* y, int64_t row, int64_t n, int64_t N, const v4i acc, float sa,
-                                       const float* __restrict__ sw, const float* __restrict__ bias, bool wide) {
+                                       const float* __restrict__ sw, const float* __restrict__ bias, Stores store) {
   float v[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -46,7 +51,7 @@ __device__ __forceinline__ void store4(void* y, int64_t row, int64_t n, int64_t 
   }
   if constexpr (BF16) {
     uint16_t* p = static_cast<uint16_t*>(y) + row + n;
-    if (wide && n + 4 <= N) {
+    if (store != Stores::values && n + 4 <= N) {
       *reinterpret_cast<u32x2*>(p) = u32x2{f32_to_bf16_bits(v[0]) | f32_to_bf16_bits(v[1]) << 16,
                                            f32_to_bf16_bits(v[2]) | f32_to_bf16_bits(v[3]) << 16};
     } else {
@@ -56,7 +61,7 @@ __device__ __forceinline__ void store4(void* y, int64_t row, int64_t n, int64_t 
     }
   } else {
     float* p = static_cast<float*>(y) + row + n;
-    if (wide && n + 4 <= N) {
+    if (store != Stores::values && n + 4 <= N) {
       *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
     } else {
 #pragma unroll
@@ -83,35 +88,64 @@ struct Rows {
 
 constexpr int kStreamThreads = 512, kStreamWaves = 8;
 
+__device__ __forceinline__ v4i load_once(const int8_t* p) {
+  return __builtin_nontemporal_load(reinterpret_cast<const v4i*>(p));
+}
+
+// sums: MI * P KB of LDS.
 template <int MI, int P, bool BF16>
-__device__ __forceinline__ void stream_tile(const Product& p, const Rows& r, int64_t panel0, bool wide) {
-  __shared__ int sums[MI * P * 4 * 64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l16 = lane & 15, g = lane >> 4;
+__device__ __forceinline__ void stream_tile(const Product& p, const Rows& r, int64_t panel0, Stores store, int* sums) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l16 = lane & 15,
+            g = lane >> 4;
   const int64_t panels = (p.N + 15) / 16;
   const int chunks = (int)((p.K + 127) / 128) * 2;
   const int8_t* ap[MI];
-  const int8_t* wp[P];
+  uint32_t woff[P];
 #pragma unroll
   for (int i = 0; i < MI; ++i) ap[i] = p.a + r.token(16 * i + l16) * p.lda + 16 * g;
 #pragma unroll
-  for (int j = 0; j < P; ++j) wp[j] = r.w + min(panel0 + j, panels - 1) * 1024 + 16 * lane;
+  for (int j = 0; j < P; ++j) woff[j] = (uint32_t)(min(panel0 + j, panels - 1) * 1024) + 16 * lane;
+  for (int i = threadIdx.x; i < MI * P * 256; i += kStreamThreads) sums[i] = 0;
   v4i acc[MI][P];
 #pragma unroll
   for (int i = 0; i < MI; ++i)
 #pragma unroll
     for (int j = 0; j < P; ++j) acc[i][j] = v4i{0, 0, 0, 0};
-  for (int c = wave; c < chunks; c += kStreamWaves) {
-    v4i x[MI], w[P];
+  // a ring of U chunks in flight; a chunk past the wave's last reads that one
+  // again, and is not multiplied
+  constexpr int U = P == 1 ? 3 : 2;
+  v4i x[U][MI], w[U][P];
+  auto fetch = [&](int u, int c) {
+    c = min(c, chunks - 1);
+    const int8_t* base = r.w + (int64_t)c * panels * 1024;
 #pragma unroll
-    for (int i = 0; i < MI; ++i) x[i] = *reinterpret_cast<const v4i*>(ap[i] + (int64_t)c * 64);
+    for (int j = 0; j < P; ++j) w[u][j] = load_once(base + woff[j]);
 #pragma unroll
-    for (int j = 0; j < P; ++j) w[j] = *reinterpret_cast<const v4i*>(wp[j] + (int64_t)c * panels * 1024);
+    for (int i = 0; i < MI; ++i) x[u][i] = *reinterpret_cast<const v4i*>(ap[i] + (int64_t)c * 64);
+  };
 #pragma unroll
-    for (int i = 0; i < MI; ++i)
+  for (int u = 0; u < U; ++u) fetch(u, wave + u * kStreamWaves);
+  const int mine = (chunks - wave + kStreamWaves - 1) / kStreamWaves;  // chunks of this wave
+  int c = wave, n = 0;
+  for (; n + U <= mine; n += U) {
 #pragma unroll
-      for (int j = 0; j < P; ++j) acc[i][j] = mfma(w[j], x[i], acc[i][j]);
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int j = 0; j < P; ++j) acc[i][j] = mfma(w[u][j], x[u][i], acc[i][j]);
+      fetch(u, c + (u + U) * kStreamWaves);
+    }
+    c += U * kStreamWaves;
   }
-  for (int i = threadIdx.x; i < MI * P * 256; i += kStreamThreads) sums[i] = 0;
+#pragma unroll
+  for (int u = 0; u < U - 1; ++u)
+    if (n + u < mine) {
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int j = 0; j < P; ++j) acc[i][j] = mfma(w[u][j], x[u][i], acc[i][j]);
+    }
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < MI; ++i)
@@ -128,78 +162,92 @@ __device__ __forceinline__ void stream_tile(const Product& p, const Rows& r, int
       v4i v;
 #pragma unroll
       for (int q = 0; q < 4; ++q) v[q] = sums[(f * 4 + q) * 64 + lane];
-      store4<BF16>(p.y.p, (r.m0 + m) * p.y.ld, n, p.N, v, p.sa[r.token(m)], r.sw, p.bias, wide);
+      store4<BF16>(p.y.p, (r.m0 + m) * p.y.ld, n, p.N, v, p.sa[r.token(m)], r.sw, p.bias, store);
     }
   }
 }
 
 template <int MI, int P, bool BF16>
-__global__ __launch_bounds__(kStreamThreads) void stream_kernel(Product p, int64_t M, int tiles_n, bool wide) {
-  const int tn = blockIdx.x % tiles_n;
-  const int64_t m0 = (int64_t)(blockIdx.x / tiles_n) * 16 * MI;
-  const Rows r{nullptr, M, m0, (int)min((int64_t)16 * MI, M - m0), p.w, p.sw};
-  stream_tile<MI, P, BF16>(p, r, (int64_t)tn * P, wide);
+__global__ __launch_bounds__(kStreamThreads) void stream_kernel(Product p, int64_t M, Stores store) {
+  __shared__ int sums[MI * P * 256];
+  const Rows r{nullptr, M, 0, (int)M, p.w, p.sw};
+  stream_tile<MI, P, BF16>(p, r, (int64_t)blockIdx.x * P, store, sums);
 }
 
-// The expert that tile `tile` of BM rows belongs to, counted over the experts
-// in turn, and its rows; false past the last one.  Every thread of a workgroup
-// of THREADS calls it.
+// What a workgroup of a grouped product has: rows of one expert.
+struct Item {
+  int expert, first, rows;
+};
+
+// Inclusive sum over a wave: within rows of 16 lanes, then the rows' last lanes
+// to the rows behind them.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int dpp_add(int v) {
+  return v + __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);
+}
+__device__ __forceinline__ int wave_scan(int v) {
+  v = dpp_add<0x111, 0xF>(v);
+  v = dpp_add<0x112, 0xF>(v);
+  v = dpp_add<0x114, 0xF>(v);
+  v = dpp_add<0x118, 0xF>(v);
+  v = dpp_add<0x142, 0xA>(v);
+  return dpp_add<0x143, 0xC>(v);
+}
+
+// Rows of expert e, whatever offsets holds.
+__device__ __forceinline__ int2 rows_of(const int32_t* __restrict__ offsets, int e, int64_t R) {
+  const int lo = max(0, min(offsets[e], (int)R));
+  return make_int2(lo, max(lo, min(offsets[e + 1], (int)R)) - lo);
+}
+
+// Piece `at` of BM rows or fewer, counted over the experts in turn; false past
+// the last.  Every thread of a workgroup of THREADS calls it.
 template <int BM, int THREADS>
-__device__ __forceinline__ bool find_expert(const int32_t* __restrict__ offsets, int E, int64_t R, int tile, int& expert,
-                                            int& first, int& rows) {
-  __shared__ int wave_sum[THREADS / 64];
-  __shared__ int found[3];
+__device__ __forceinline__ bool find_item(const int32_t* __restrict__ offsets, int E, int64_t R, int at, Item& item) {
+  constexpr int kW = THREADS / 64;
+  static_assert(1024 <= 2 * THREADS, "the two turns' sums are not written again");
+  __shared__ int sum[2][kW];
+  __shared__ Item found;
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
-  if (tid == 0) found[0] = -1;
-  int base = 0;
-  for (int e0 = 0; e0 < E; e0 += THREADS) {
+  int base = 0, turn = 0;
+  for (int e0 = 0; e0 < E && base <= at; e0 += THREADS, turn ^= 1) {
     const int e = e0 + tid;
-    int lo = 0, n = 0;
-    if (e < E) {
-      lo = max(0, min(offsets[e], (int)R));
-      n = max(lo, min(offsets[e + 1], (int)R)) - lo;
-    }
-    const int mine = (n + BM - 1) / BM;
-    int sum = mine;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int o = __shfl_up(sum, d);
-      sum += lane >= d ? o : 0;
-    }
+    const int2 rows = e < E ? rows_of(offsets, e, R) : make_int2(0, 0);
+    const int mine = (rows.y + BM - 1) / BM, scan = wave_scan(mine);
+    if (lane == 63) sum[turn][w] = scan;
     __syncthreads();
-    if (lane == 63) wave_sum[w] = sum;
-    __syncthreads();
-    int before = base, all = 0;
+    int earlier = base;
 #pragma unroll
-    for (int i = 0; i < THREADS / 64; ++i) {
-      before += i < w ? wave_sum[i] : 0;
-      all += wave_sum[i];
+    for (int i = 0; i < kW; ++i) {
+      earlier += i < w ? sum[turn][i] : 0;
+      base += sum[turn][i];
     }
-    const int at = tile - (before + sum - mine);
-    if (at >= 0 && at < mine) {
-      found[0] = e;
-      found[1] = lo + at * BM;
-      found[2] = min(BM, n - at * BM);
-    }
-    base += all;
+    const int in = at - (earlier + scan - mine);
+    if (in >= 0 && in < mine) found = Item{e, rows.x + in * BM, min(BM, rows.y - in * BM)};
   }
+  if (base <= at) return false;  // the same in every thread
   __syncthreads();
-  expert = found[0];
-  first = found[1];
-  rows = found[2];
-  return expert >= 0;
+  // the same in every lane, which addresses in scalar registers have to be
+  item.expert = __builtin_amdgcn_readfirstlane(found.expert);
+  item.first = __builtin_amdgcn_readfirstlane(found.first);
+  item.rows = __builtin_amdgcn_readfirstlane(found.rows);
+  return true;
+}
+
+__device__ __forceinline__ Rows item_rows(const Product& p, const Item& it, int64_t T, const int32_t* index) {
+  const int64_t bytes = (p.N + 15) / 16 * 16 * ((p.K + 127) / 128 * 128);
+  return Rows{index, T, it.first, it.rows, p.w + it.expert * bytes, p.sw + (int64_t)it.expert * p.N};
 }
 
 template <int MI, int P, bool BF16>
 __global__ __launch_bounds__(kStreamThreads) void grouped_stream_kernel(Product p, int64_t T,
                                                                         const int32_t* __restrict__ index,
                                                                         const int32_t* __restrict__ offsets, int64_t R,
-                                                                        int E, int tiles_n, bool wide) {
-  int e, first, rows;
-  if (!find_expert<16 * MI, kStreamThreads>(offsets, E, R, blockIdx.x / tiles_n, e, first, rows)) return;
-  const int64_t bytes = (p.N + 15) / 16 * 16 * ((p.K + 127) / 128 * 128);
-  const Rows r{index, T, first, rows, p.w + e * bytes, p.sw + (int64_t)e * p.N};
-  stream_tile<MI, P, BF16>(p, r, (int64_t)(blockIdx.x % tiles_n) * P, wide);
+                                                                        int E, int tiles_n, Stores store) {
+  __shared__ int sums[MI * P * 256];
+  Item it;
+  if (!find_item<16 * MI, kStreamThreads>(offsets, E, R, blockIdx.x / tiles_n, it)) return;
+  stream_tile<MI, P, BF16>(p, item_rows(p, it, T, index), (int64_t)(blockIdx.x % tiles_n) * P, store, sums);
 }
 
 // ---- tiles ------------------------------------------------------------------
@@ -225,8 +273,9 @@ __device__ __forceinline__ void wait_loads() {
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_at(const void* base) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, (int)0xFFFFFFFFu, 0x00020000);
 }
+template <bool ONCE>
 __device__ __forceinline__ v4i load16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
-  const auto v = __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0);
+  const auto v = __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, ONCE ? 2 : 0);  // 2: non-temporal
   return v4i{(int)v[0], (int)v[1], (int)v[2], (int)v[3]};
 }
 // 16 bytes a lane from memory to 1 KB of LDS, not through registers.
@@ -235,14 +284,28 @@ __device__ __forceinline__ void load_lds(__amdgpu_buffer_rsrc_t r, uint32_t off,
 }
 
 // WM x 4 waves, each with 16 MI rows of a and 16 NJ of the weights.
-template <int MI_, int WM_, int NJ_>
+// SETS sets of weight registers: a step's weights are asked for SETS steps ahead.
+template <int MI_, int WM_, int NJ_, int SETS_ = 2>
 struct Cfg {
-  static constexpr int MI = MI_, WM = WM_, NJ = NJ_;
+  static constexpr int MI = MI_, WM = WM_, NJ = NJ_, SETS = SETS_;
   static constexpr int kWaves = 4 * WM, kThreads = 64 * kWaves;
   static constexpr int kRows = 16 * MI * WM, kCols = 64 * NJ;
   static constexpr int kA = kRows / 8 / kWaves;  // pieces of 8 rows of a that a wave brings in a step
   static_assert(kRows % (8 * kWaves) == 0, "pieces split evenly");
 };
+
+// The upper half (odd rows of 16 lanes) of a changes places with the lower half
+// (even rows) of b.
+__device__ __forceinline__ void swap32(uint32_t& a, uint32_t& b) {
+  const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+  a = r[0];
+  b = r[1];
+}
+__device__ __forceinline__ void swap16(uint32_t& a, uint32_t& b) {
+  const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+  a = r[0];
+  b = r[1];
+}
 
 // The codes of a wave's weight rows in one step.
 template <int NJ>
@@ -250,17 +313,114 @@ struct Weights {
   v4i w[2][NJ];
 };
 
-#ifndef SGB
-#define SGB 2
-#endif
-template <class C, bool BF16>
-__device__ __forceinline__ void tile(const Product& p, const Rows& r, int64_t panel0, bool wide) {
-  constexpr int MI = C::MI, NJ = C::NJ;
-  __shared__ __attribute__((aligned(16))) int8_t st0[C::kRows * kStep];
-  __shared__ __attribute__((aligned(16))) int8_t st1[C::kRows * kStep];
-  __shared__ __attribute__((aligned(16))) int8_t st2[C::kRows * kStep];
-  __shared__ __attribute__((aligned(16))) int8_t st3[C::kRows * kStep];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+constexpr int kAhead = 2;  // LDS reads ahead of the products: 480 us with 2 to 4 at 4096 x 7168 -> 18432, 512 with 1
+
+// A wave's sums to rows i0 .. i0 + 16 MI - 1 of y, columns from panel `first`
+// on.  Lane 16 g + l16 has four columns of row l16 of every panel, 8 bytes of
+// bf16; where whole pieces are stored the four lanes of a row change places
+// first (v_permlane*_swap), so that each has 16 bytes or more in a row and a
+// store instruction fills 64 bytes of a line or more.
+template <int MI, int NJ, bool BF16>
+__device__ __forceinline__ void store_tile(const Product& p, const Rows& r, int i0, int64_t first,
+                                           const v4i (&acc)[MI][NJ], Stores how) {
+  static_assert(NJ == 2 || NJ == 4, "transposed by twos or fours");
+  const int lane = threadIdx.x & 63, l16 = lane & 15, g = lane >> 4;
+  if (first * 16 >= p.N) return;
+  float scale[NJ][4], bias[NJ][4];
+#pragma unroll
+  for (int j = 0; j < NJ; ++j)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int64_t n = min((first + j) * 16 + 4 * g + q, p.N - 1);
+      scale[j][q] = r.sw[n];
+      bias[j][q] = p.bias ? p.bias[n] : 0.0f;
+    }
+  const bool whole = how == Stores::lines && (first + NJ) * 16 <= p.N;
+#pragma unroll
+  for (int i = 0; i < MI; ++i) {
+    const int m = i0 + 16 * i + l16;
+    const float sa = p.sa[r.token(m)];
+    const int64_t row = (r.m0 + m) * p.y.ld;
+    constexpr int D = BF16 ? 2 : 4;  // dwords of four columns
+    uint32_t d[NJ][D];
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      float v[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        v[q] = (float)acc[i][j][q] * (sa * scale[j][q]);
+        if (p.bias) v[q] += bias[j][q];
+      }
+      if constexpr (BF16) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const bf16x2 two = {(__bf16)v[2 * q], (__bf16)v[2 * q + 1]};
+          d[j][q] = __builtin_bit_cast(uint32_t, two);
+        }
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) d[j][q] = __float_as_uint(v[q]);
+      }
+    }
+    char* y = static_cast<char*>(p.y.p) + (row + first * 16) * (BF16 ? 2 : 4);
+    if (whole) {
+#pragma unroll
+      for (int q = 0; q < D; ++q) {
+        if constexpr (NJ == 4) {
+          swap32(d[0][q], d[2][q]);
+          swap32(d[1][q], d[3][q]);
+          swap16(d[0][q], d[1][q]);
+          swap16(d[2][q], d[3][q]);
+        } else {
+          swap16(d[0][q], d[1][q]);
+        }
+      }
+      // four panels: lane g has panel g, d[j] its columns 4 j ..; two: lane g
+      // has columns 8 (g / 2) .. of panel g % 2, d[j] four of them
+      const int at = NJ == 4 ? 16 * g : 16 * (g & 1) + 8 * (g >> 1);
+      if (m < r.rows) {
+        u32x4* to = reinterpret_cast<u32x4*>(y + at * (BF16 ? 2 : 4));
+#pragma unroll
+        for (int v = 0; v < NJ * D / 4; ++v)
+          to[v] = BF16 ? u32x4{d[2 * v][0], d[2 * v][1], d[2 * v + 1][0], d[2 * v + 1][1]}
+                       : u32x4{d[v][0], d[v][1], d[v][D - 2], d[v][D - 1]};
+      }
+    } else if (m < r.rows) {
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        const int64_t n = (first + j) * 16 + 4 * g;
+        char* to = y + (16 * j + 4 * g) * (BF16 ? 2 : 4);
+        if (how != Stores::values && n + 4 <= p.N) {
+          if constexpr (BF16)
+            *reinterpret_cast<u32x2*>(to) = u32x2{d[j][0], d[j][1]};
+          else
+            *reinterpret_cast<u32x4*>(to) = u32x4{d[j][0], d[j][1], d[j][2], d[j][3]};
+        } else {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (n + q < p.N) {
+              if constexpr (BF16)
+                reinterpret_cast<uint16_t*>(to)[q] = (uint16_t)(d[j][q / 2] >> (16 * (q & 1)));
+              else
+                reinterpret_cast<uint32_t*>(to)[q] = d[j][q];
+            }
+        }
+      }
+    }
+  }
+}
+
+// st0 .. st3: the stages, C::kRows * kStep bytes of LDS each, arrays of their
+// own (so that the compiler can tell which of them a load to LDS writes).
+template <class C, bool BF16, bool ONCE = false>
+__device__ __forceinline__ void tile(const Product& p, const Rows& r, int64_t panel0, Stores store, int8_t* st0,
+                                     int8_t* st1, int8_t* st2, int8_t* st3) {
+  constexpr int MI = C::MI, NJ = C::NJ, SETS = C::SETS;
+  // (made anew for every tile: what follows from it is not kept from tile to
+  // tile in registers that the products need)
+  int lane = threadIdx.x & 63;
+  asm volatile("" : "+v"(lane));
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wn = wave & 3, wm = wave >> 2;
   const int l16 = lane & 15, g = lane >> 4;
   const int64_t panels = (p.N + 15) / 16;
@@ -281,7 +441,7 @@ __device__ __forceinline__ void tile(const Product& p, const Rows& r, int64_t pa
   auto load_w = [&](v4i (&w)[NJ], int c) {
     const __amdgpu_buffer_rsrc_t b = buffer_at(r.w + c * chunk);
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) w[j] = load16(b, woff[j]);
+    for (int j = 0; j < NJ; ++j) w[j] = load16<ONCE>(b, woff[j]);
   };
   const __amdgpu_buffer_rsrc_t abuf = buffer_at(abase);
   auto issue = [&](int8_t* st, int t) {
@@ -295,13 +455,13 @@ __device__ __forceinline__ void tile(const Product& p, const Rows& r, int64_t pa
 #pragma unroll
     for (int j = 0; j < NJ; ++j) acc[i][j] = v4i{0, 0, 0, 0};
   const int x_lo = lds_at(16 * MI * wm + l16, g);
-  // Step t multiplies stage t % 4 by the weights of set t % 2: the first
+  // Step t multiplies stage t % 4 by the weights of set t % SETS: the first
   // chunk's products, then the second's, each chunk's registers loaded again
-  // for step t + 2 as soon as its products are issued.
+  // for step t + SETS as soon as its products are issued.
   auto step = [&](int t, const int8_t* cur, Weights<NJ>& w, int8_t* refill, bool more_a, bool more_w, bool full) {
     // this wave's part of stage t is in LDS; what may still fly is younger:
-    // the stages of t + 1 and t + 2, the weights of t and t + 1
-    if (full) wait_loads<4 * NJ + 2 * C::kA>(); else wait_loads<0>();
+    // the stages of t + 1 and t + 2, the weights from t on
+    if (full) wait_loads<2 * SETS * NJ + 2 * C::kA>(); else wait_loads<0>();
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
@@ -315,32 +475,35 @@ __device__ __forceinline__ void tile(const Product& p, const Rows& r, int64_t pa
 #pragma unroll
         for (int j = 0; j < NJ; ++j) acc[i][j] = mfma(w.w[h][j], v, acc[i][j]);
       }
-      if (more_w) load_w(w.w[h], 2 * (t + 2) + h);
+      if (more_w) load_w(w.w[h], 2 * (t + SETS) + h);
     }
-    // LDS reads SGB fragments ahead of the products
-    if (SGB > 0) {
-      __builtin_amdgcn_sched_group_barrier(0x020, C::kA, 0);
-      __builtin_amdgcn_sched_group_barrier(0x100, SGB, 0);
+    // the order of the step's instructions: loads to LDS (0x20), LDS reads
+    // (0x100), products (0x8), and the loads of weights behind each chunk
+    __builtin_amdgcn_sched_group_barrier(0x020, C::kA, 0);
+    __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
 #pragma unroll
-      for (int i = 0; i < 2 * MI; ++i) {
-        __builtin_amdgcn_sched_group_barrier(0x008, NJ, 0);
-        if (i + SGB < 2 * MI) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-        if (more_w && (i == MI - 1 || i == 2 * MI - 1)) __builtin_amdgcn_sched_group_barrier(0x020, NJ, 0);
-      }
+    for (int i = 0; i < 2 * MI; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x008, NJ, 0);
+      if (i + kAhead < 2 * MI) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      if (more_w && (i == MI - 1 || i == 2 * MI - 1)) __builtin_amdgcn_sched_group_barrier(0x020, NJ, 0);
     }
   };
-  Weights<NJ> w0, w1;
+  Weights<NJ> sets[SETS];
+  Weights<NJ>&w0 = sets[0], &w1 = sets[SETS - 1];
   // (the loads of steps that are not there read the last one's again: with a
   // branch the compiler would not know how many loads are in flight at the
   // head of the loop, and wait for all)
   const int last = steps - 1;
   issue(st0, 0);
   issue(st1, min(1, last));
+  if (SETS == 1) issue(st2, min(2, last));
   load_w(w0.w[0], 0);
   load_w(w0.w[1], 1);
-  issue(st2, min(2, last));
-  load_w(w1.w[0], 2 * min(1, last));
-  load_w(w1.w[1], 2 * min(1, last) + 1);
+  if (SETS == 2) {
+    issue(st2, min(2, last));
+    load_w(w1.w[0], 2 * min(1, last));
+    load_w(w1.w[1], 2 * min(1, last) + 1);
+  }
   int t = 0;
   for (; t + 7 <= steps; t += 4) {
     step(t, st0, w0, st3, true, true, true);
@@ -350,7 +513,7 @@ __device__ __forceinline__ void tile(const Product& p, const Rows& r, int64_t pa
   }
   // one to six more
   auto tail = [&](int u, const int8_t* cur, Weights<NJ>& w, int8_t* refill) {
-    if (u < steps) step(u, cur, w, refill, u + 3 < steps, u + 2 < steps, u + 2 < steps);
+    if (u < steps) step(u, cur, w, refill, u + 3 < steps, u + SETS < steps, u + 2 < steps);
   };
   tail(t, st0, w0, st3);
   tail(t + 1, st1, w1, st0);
@@ -359,17 +522,7 @@ __device__ __forceinline__ void tile(const Product& p, const Rows& r, int64_t pa
   tail(t + 4, st0, w0, st3);
   tail(t + 5, st1, w1, st0);
   wait_loads<0>();
-#pragma unroll
-  for (int i = 0; i < MI; ++i) {
-    const int m = 16 * (MI * wm + i) + l16;
-    if (m >= r.rows) continue;
-    const float sa = p.sa[r.token(m)];
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-      const int64_t n = (first + j) * 16 + 4 * g;
-      if (n < p.N) store4<BF16>(p.y.p, (r.m0 + m) * p.y.ld, n, p.N, acc[i][j], sa, r.sw, p.bias, wide);
-    }
-  }
+  store_tile<MI, NJ, BF16>(p, r, 16 * MI * wm, first, acc, store);
 }
 
 // Output tile of workgroup `id`: workgroups go round the 8 XCDs in turn, so
@@ -387,17 +540,133 @@ __device__ __forceinline__ void tile_of(int id, int tiles_m, int tiles_n, int& t
 
 template <class C, bool BF16, int OCC>
 __global__ __launch_bounds__(C::kThreads, OCC) void tile_kernel(Product p, int64_t M, int tiles_m, int tiles_n,
-                                                                bool wide) {
+                                                                Stores store) {
   int tm, tn;
   tile_of(blockIdx.x, tiles_m, tiles_n, tm, tn);
   const int64_t m0 = (int64_t)tm * C::kRows;
   const Rows r{nullptr, M, m0, (int)min((int64_t)C::kRows, M - m0), p.w, p.sw};
-  tile<C, BF16>(p, r, (int64_t)tn * C::NJ * 4, wide);
+  __shared__ __attribute__((aligned(16))) int8_t st0[C::kRows * kStep];
+  __shared__ __attribute__((aligned(16))) int8_t st1[C::kRows * kStep];
+  __shared__ __attribute__((aligned(16))) int8_t st2[C::kRows * kStep];
+  __shared__ __attribute__((aligned(16))) int8_t st3[C::kRows * kStep];
+  tile<C, BF16>(p, r, (int64_t)tn * C::NJ * 4, store, st0, st1, st2, st3);
 }
 
-bool wide_rows(const Mat& y) { return reinterpret_cast<uintptr_t>(y.p) % 16 == 0 && y.ld % 4 == 0; }
+// The pieces of a plan, in LDS: experts' rows cut into whole tiles of BM rows
+// and last pieces of more than kLittle rows (kind 0), and last pieces of up to
+// kLittle rows (kind 1), which are bound by their weights.
+constexpr int kLittle = 32;
+struct Pieces {
+  int lo[1025];         // first row of an expert, and the end
+  int before[2][1024];  // pieces of a kind before an expert's
+  int sum[2][4];
+  Item found;
+};
+template <int BM>
+__device__ __forceinline__ int pieces_of(int n, int kind) {
+  const int rest = n % BM;
+  return kind ? rest > 0 && rest <= kLittle : n / BM + (rest > kLittle);
+}
+// Every thread of a workgroup of 256; the kinds' numbers.
+template <int BM>
+__device__ __forceinline__ int2 count_pieces(Pieces& s, const int32_t* __restrict__ offsets, int E, int64_t R) {
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+  for (int e = tid; e <= E; e += 256) s.lo[e] = max(0, min(offsets[e], (int)R));
+  __syncthreads();
+  int base[2] = {0, 0};
+  for (int e0 = 0; e0 < E; e0 += 256) {
+    const int e = e0 + tid;
+    const int n = e < E ? max(0, s.lo[e + 1] - s.lo[e]) : 0;
+    int mine[2], scan[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      mine[k] = pieces_of<BM>(n, k);
+      scan[k] = wave_scan(mine[k]);
+      if (lane == 63) s.sum[k][w] = scan[k];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      int earlier = base[k];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        earlier += i < w ? s.sum[k][i] : 0;
+        base[k] += s.sum[k][i];
+      }
+      if (e < E) s.before[k][e] = earlier + scan[k] - mine[k];
+    }
+    __syncthreads();
+  }
+  return make_int2(__builtin_amdgcn_readfirstlane(base[0]), __builtin_amdgcn_readfirstlane(base[1]));
+}
+// Piece `rank` of a kind.  Every thread of the workgroup.
+template <int BM>
+__device__ __forceinline__ Item find_piece(Pieces& s, int E, int kind, int rank) {
+  for (int e = threadIdx.x; e < E; e += 256) {
+    const int n = max(0, s.lo[e + 1] - s.lo[e]), in = rank - s.before[kind][e];
+    if (in >= 0 && in < pieces_of<BM>(n, kind)) {
+      const int piece = kind ? n / BM : in;
+      s.found = Item{e, s.lo[e] + piece * BM, min(BM, n - piece * BM)};
+    }
+  }
+  __syncthreads();
+  // the same in every lane, which addresses in scalar registers have to be
+  const Item it{__builtin_amdgcn_readfirstlane(s.found.expert), __builtin_amdgcn_readfirstlane(s.found.first),
+                __builtin_amdgcn_readfirstlane(s.found.rows)};
+  __syncthreads();
+  return it;
+}
 
-}  // namespace
+// Workgroups go round the 8 XCDs in turn.  Each XCD takes an eighth of the
+// pieces of kind 0 (times the columns, 64 NJ at a time), then an eighth of
+// kind 1, in groups of 8 pieces whose products for all columns follow each
+// other, so that what runs at a time on an XCD shares rows and weights in its
+// L2.  Both kinds at a time on a compute unit were no faster (870 us one after
+// the other, 893 mixed; 4096 tokens, 8 of 256 experts by a skewed router,
+// 7168 -> 2048): the loads of one wait behind the other's.  Workgroups past
+// the last piece end at once.
+template <int NJ, bool BF16>
+__global__ __launch_bounds__(256, 2) void grouped_tile_kernel(Product p, int64_t T, const int32_t* __restrict__ index,
+                                                              const int32_t* __restrict__ offsets, int64_t R, int E,
+                                                              int tiles_n, Stores store) {
+  using C = Cfg<8, 1, NJ>;
+  __shared__ __attribute__((aligned(16))) int8_t st0[C::kRows * kStep];
+  __shared__ __attribute__((aligned(16))) int8_t st1[C::kRows * kStep];
+  __shared__ __attribute__((aligned(16))) int8_t st2[C::kRows * kStep];
+  __shared__ __attribute__((aligned(16))) int8_t st3[C::kRows * kStep];
+  __shared__ Pieces pieces;
+  const int2 all = count_pieces<C::kRows>(pieces, offsets, E, R);
+  const int xcd = blockIdx.x & 7;
+  int64_t i = blockIdx.x >> 3;
+  const int64_t items0 = (int64_t)all.x * tiles_n, items1 = (int64_t)all.y * tiles_n;
+  int64_t begin = items0 * xcd / 8, end = items0 * (xcd + 1) / 8;
+  const int kind = i >= end - begin;
+  if (kind) {
+    i -= end - begin;
+    begin = items1 * xcd / 8;
+    end = items1 * (xcd + 1) / 8;
+  }
+  i += begin;
+  if (i >= end) return;
+  const int64_t per = 8 * (int64_t)tiles_n;
+  const int group = (int)(i / per), in = (int)(i - group * per), rows = min(8, (kind ? all.y : all.x) - 8 * group);
+  const int tn = in / rows;
+  const Item it = find_piece<C::kRows>(pieces, E, kind, 8 * group + in - tn * rows);
+  const Rows r = item_rows(p, it, T, index);
+  const int64_t panel0 = (int64_t)tn * NJ * 4;
+  if (kind)
+    tile<Cfg<2, 1, NJ>, BF16, true>(p, r, panel0, store, st0, st1, st2, st3);
+  else if (it.rows <= 64)
+    tile<Cfg<4, 1, NJ>, BF16>(p, r, panel0, store, st0, st1, st2, st3);
+  else
+    tile<C, BF16>(p, r, panel0, store, st0, st1, st2, st3);
+}
+
+Stores stores_of(const Mat& y) {
+  const uintptr_t p = reinterpret_cast<uintptr_t>(y.p);
+  if (p % 16 == 0 && y.ld % (y.bf16 ? 8 : 4) == 0) return Stores::lines;
+  return p % (y.bf16 ? 8 : 16) == 0 && y.ld % 4 == 0 ? Stores::fours : Stores::values;
+}
 
 template <class C, int OCC>
 int launch_tiles(const Product& p, int64_t M, hipStream_t s) {
@@ -405,39 +674,97 @@ int launch_tiles(const Product& p, int64_t M, hipStream_t s) {
   if (tiles_m * tiles_n > (1 << 22)) return FP8B_EINVAL;
   auto go = [&](auto b) {
     hipLaunchKernelGGL((tile_kernel<C, decltype(b)::value, OCC>), dim3((unsigned)(tiles_m * tiles_n)), dim3(C::kThreads),
-                       0, s, p, M, (int)tiles_m, (int)tiles_n, wide_rows(p.y));
+                       0, s, p, M, (int)tiles_m, (int)tiles_n, stores_of(p.y));
     return check_launch();
   };
   return p.y.bf16 ? go(std::true_type{}) : go(std::false_type{});
 }
 
-#ifndef BIG
-#define BIG Cfg<8, 1, 4>, 2
-#endif
-int launch_gemm(const Product& p, int64_t M, hipStream_t s) {
-  if (M > 128) return launch_tiles<BIG>(p, M, s);
-  if (M > 64) return launch_tiles<Cfg<8, 1, 4>, 2>(p, M, s);
-  constexpr int MI = 4, P = 4;
-  const int64_t tiles_n = (p.N + 16 * P - 1) / (16 * P), tiles = tiles_n * ((M + 16 * MI - 1) / (16 * MI));
-  if (tiles > (1 << 22)) return FP8B_EINVAL;
-  auto go = [&](auto b) {
-    hipLaunchKernelGGL((stream_kernel<MI, P, decltype(b)::value>), dim3((unsigned)tiles), dim3(kStreamThreads), 0, s, p,
-                       M, (int)tiles_n, wide_rows(p.y));
+// Panels of a streaming workgroup: as many as keep the fullest compute unit
+// the emptiest, for that many panels there are.
+int stream_panels(int64_t panels) {
+  constexpr int64_t kUnits = 256;
+  int best = 1;
+  int64_t least = INT64_MAX;
+  for (int P = 1; P <= 8; ++P) {
+    const int64_t groups = (panels + P - 1) / P, most = (groups + kUnits - 1) / kUnits * P;
+    if (most <= least) {
+      least = most;
+      best = P;
+    }
+  }
+  return best;
+}
+
+int launch_stream(const Product& p, int64_t M, hipStream_t s) {
+  const int64_t panels = (p.N + 15) / 16;
+  const int P = stream_panels(panels);
+  auto go = [&](auto mi, auto pp, auto b) {
+    constexpr int MI = decltype(mi)::value, PP = decltype(pp)::value;
+    hipLaunchKernelGGL((stream_kernel<MI, PP, decltype(b)::value>), dim3((unsigned)((panels + PP - 1) / PP)),
+                       dim3(kStreamThreads), 0, s, p, M, stores_of(p.y));
     return check_launch();
   };
-  return p.y.bf16 ? go(std::true_type{}) : go(std::false_type{});
+  auto with_type = [&](auto mi, auto pp) {
+    return p.y.bf16 ? go(mi, pp, std::true_type{}) : go(mi, pp, std::false_type{});
+  };
+  auto with_rows = [&](auto pp) {
+    if (M <= 16) return with_type(std::integral_constant<int, 1>{}, pp);
+    if (M <= 32) return with_type(std::integral_constant<int, 2>{}, pp);
+    return with_type(std::integral_constant<int, 4>{}, pp);
+  };
+  switch (P) {
+    case 1: return with_rows(std::integral_constant<int, 1>{});
+    case 2: return with_rows(std::integral_constant<int, 2>{});
+    case 3: return with_rows(std::integral_constant<int, 3>{});
+    case 4: return with_rows(std::integral_constant<int, 4>{});
+    case 5: return with_rows(std::integral_constant<int, 5>{});
+    case 6: return with_rows(std::integral_constant<int, 6>{});
+    case 7: return with_rows(std::integral_constant<int, 7>{});
+    default: return with_rows(std::integral_constant<int, 8>{});
+  }
+}
+
+}  // namespace
+
+// Which shape of tiles: the largest one that gives every compute unit work.
+// Measured (us; 128 x 256, 128 x 128, 64 x 128 and 32 x 128 rows x columns):
+//   4096 x 7168 -> 18432   413 505 658 947     1024 x 7168 -> 18432  138 147 179 279
+//   2048 x 4096 -> 4096     37  36  40  57     512 x 4096 -> 4096     44  27  17  18
+//   128 x 8192 -> 28672     81  57  66  92     128 x 4096 -> 4096     43  26  16  12
+// Up to 32 rows the weights are streamed: 38.8 us for 32 x 8192 -> 28672,
+// 41.2 by tiles of 32 rows.
+int launch_gemm(const Product& p, int64_t M, hipStream_t s) {
+  if (M <= 32) return launch_stream(p, M, s);
+  auto tiles = [&](int64_t rows, int64_t cols) { return (M + rows - 1) / rows * ((p.N + cols - 1) / cols); };
+  if (tiles(128, 256) >= 256) return launch_tiles<Cfg<8, 1, 4>, 2>(p, M, s);
+  if (M > 64 && M <= 128 && tiles(128, 128) >= 128) return launch_tiles<Cfg<8, 1, 2>, 2>(p, M, s);
+  if (tiles(64, 128) >= 192) return launch_tiles<Cfg<4, 1, 2>, 3>(p, M, s);
+  return launch_tiles<Cfg<2, 1, 2>, 4>(p, M, s);
 }
 
 int launch_grouped(const Product& p, int64_t T, const int32_t* row_index, const int32_t* offsets, int64_t R, int E,
                    hipStream_t s) {
-  constexpr int MI = 4, P = 4;
-  // no more tiles than full ones and one begun per expert, nor than rows
-  const int64_t tiles_n = (p.N + 16 * P - 1) / (16 * P), tiles_m = std::min(R, R / (16 * MI) + E);
-  const int64_t tiles = tiles_n * tiles_m;
-  if (tiles > (1 << 22)) return FP8B_EINVAL;
+  constexpr int NJ = 4, kRows = Cfg<8, 1, NJ>::kRows, kCols = Cfg<8, 1, NJ>::kCols;
+  const Stores store = stores_of(p.y);
+  // no more pieces than full ones and one begun per expert, nor than rows
+  auto pieces = [&](int64_t rows) { return std::min(R, R / rows + E); };
   auto go = [&](auto b) {
-    hipLaunchKernelGGL((grouped_stream_kernel<MI, P, decltype(b)::value>), dim3((unsigned)tiles), dim3(kStreamThreads),
-                       0, s, p, T, row_index, offsets, R, E, (int)tiles_n, wide_rows(p.y));
+    constexpr bool BF16 = decltype(b)::value;
+    const int64_t tiles_n = (p.N + kCols - 1) / kCols, tiles = pieces(kRows) * tiles_n;
+    // Tiles of 256 columns that would leave compute units without work: panels
+    // by two instead (8 experts' 7168 -> 2048 31 us against 43; from 32 experts
+    // on tiles are faster, 47 against 51).
+    if (tiles < 256) {
+      constexpr int MI = 1, P = 2;
+      const int64_t columns = (p.N + 16 * P - 1) / (16 * P);
+      hipLaunchKernelGGL((grouped_stream_kernel<MI, P, BF16>), dim3((unsigned)(columns * pieces(16 * MI))),
+                         dim3(kStreamThreads), 0, s, p, T, row_index, offsets, R, E, (int)columns, store);
+    } else {
+      // both kinds' shares of an XCD may be one more than an eighth
+      hipLaunchKernelGGL((grouped_tile_kernel<NJ, BF16>), dim3((unsigned)((tiles + 7) / 8 * 8 + 16)), dim3(256), 0, s, p,
+                         T, row_index, offsets, R, E, (int)tiles_n, store);
+    }
     return check_launch();
   };
   return p.y.bf16 ? go(std::true_type{}) : go(std::false_type{});

@@ -19,6 +19,8 @@ constexpr int64_t kMaxSlots = (int64_t)1 << 28;
 constexpr int64_t kMaxK = 131071;                  // (2^17 - 1) products of at most 2^14 in 32 bits
 constexpr int64_t kMaxN = (int64_t)1 << 25;
 constexpr int64_t kMaxCodes = (int64_t)1 << 46;    // bytes of packed weights
+constexpr int64_t kMaxOut = (int64_t)1 << 36;      // values of a product: launches of less than 2^32 threads
+constexpr int64_t kMaxExpertRows = (int64_t)1 << 30;  // rows of all experts' weights, for the same
 
 bool type_ok(int t) { return t == FP8B_OUT_F32 || t == FP8B_OUT_BF16; }
 int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
@@ -191,7 +193,7 @@ FP8B_EXPORT int int8_gemm(const int8_t* a, int64_t ld_a, const float* a_scales, 
                           const float* w_scales, const float* bias, int64_t M, int64_t N, int64_t K, void* y,
                           int64_t ld_y, int out_dtype, void* stream) {
   FP8B_TRY(product_sizes(N, K, out_dtype));
-  if (M < 0 || M >= kMaxTokens) return FP8B_EINVAL;
+  if (M < 0 || M >= kMaxTokens || M * N > kMaxOut) return FP8B_EINVAL;
   if (M == 0) return FP8B_OK;
   const fp8moe::Product p{a, ld_a, a_scales, w_packed, w_scales, bias, N, K, mat(y, out_dtype, ld_y)};
   FP8B_TRY(product_check(p));
@@ -205,7 +207,9 @@ FP8B_EXPORT int int8_grouped_gemm(const int8_t* a, int64_t ld_a, const float* a_
   FP8B_TRY(product_sizes(N, K, out_dtype));
   if (E < 1 || E > 1024 || R < 0 || R >= kMaxTokens || T < 1 || T >= kMaxTokens || (!row_index && T != R && R > 0))
     return FP8B_EINVAL;
-  if (up(N, 16) * up(K, 128) >= kMaxCodes / E) return FP8B_EINVAL;
+  if (up(N, 16) * up(K, 128) >= kMaxCodes / E || R * N > kMaxOut || E * N > kMaxExpertRows) return FP8B_EINVAL;
+  // the rows of a are reached by 32-bit offsets
+  if (T * ld_a >= (int64_t)1 << 32) return FP8B_EINVAL;
   if (R == 0) return FP8B_OK;
   const fp8moe::Product p{a, ld_a, a_scales, w_packed, w_scales, nullptr, N, K, mat(y, out_dtype, ld_y)};
   FP8B_TRY(product_check(p));

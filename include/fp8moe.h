@@ -196,8 +196,8 @@ int int8_weight_pack(const int8_t *w, int64_t G, int64_t N, int64_t K,
  *             read, and do not count.
  *   a_scales  float [M];  w_scales float [N];  bias float [N] or NULL.
  *   w_packed  from int8_weight_pack, 16-byte aligned.
- *   M >= 0 (0 is a no-op), < 2^24; 1 <= N <= 2^25; 1 <= K <= 131071;
- *   ld_a < 2^24.
+ *   M >= 0 (0 is a no-op), < 2^24; 1 <= N <= 2^25; M * N <= 2^36;
+ *   1 <= K <= 131071; ld_a < 2^24.
  *   y         [M][ld_y] of out_dtype.
  */
 int int8_gemm(const int8_t *a, int64_t ld_a, const float *a_scales,
@@ -216,7 +216,8 @@ int int8_gemm(const int8_t *a, int64_t ld_a, const float *a_scales,
  *   expert_offsets  int32 [E+1], non-decreasing within 0 .. R; others, or
  *                   tokens outside [0, T), give unspecified rows of y but
  *                   never fault.
- *   T >= 1; 0 <= R < 2^24 (0 is a no-op); 1 <= E <= 1024.
+ *   T >= 1, T * ld_a < 2^32 (rows are gathered with 32-bit offsets);
+ *   0 <= R < 2^24 (0 is a no-op); 1 <= E <= 1024; R * N <= 2^36; E * N <= 2^30.
  *   w_packed  of E matrices;  w_scales float [E][N].
  */
 int int8_grouped_gemm(const int8_t *a, int64_t ld_a, const float *a_scales,
