@@ -14,7 +14,7 @@ inline hipStream_t as_stream(void* s) { return static_cast<hipStream_t>(s); }
 constexpr int64_t kMaxLd = (int64_t)1 << 40;       // row numbers below 2^30 times this stay in 64 bits
 constexpr int64_t kMaxTokens = (int64_t)1 << 24;
 constexpr int64_t kMaxRows = (int64_t)1 << 30;
-constexpr int64_t kMaxCols = (int64_t)1 << 30;
+constexpr int64_t kMaxCols = (int64_t)1 << 29;    // of a row: 32-bit byte offsets, with room behind it
 constexpr int64_t kMaxSlots = (int64_t)1 << 28;
 constexpr int64_t kMaxK = 131071;                  // (2^17 - 1) products of at most 2^14 in 32 bits
 constexpr int64_t kMaxN = (int64_t)1 << 25;
@@ -87,7 +87,7 @@ FP8B_EXPORT int fp8b_moe_abi_version(void) { return FP8B_MOE_ABI_VERSION; }
 FP8B_EXPORT int64_t moe_sort_workspace(int64_t T, int64_t E, int64_t k) {
   FP8B_TRY(sort_sizes(T, E, k));
   const int64_t blocks = fp8moe::sort_blocks(T);
-  return blocks > 1 ? blocks * E * (int64_t)sizeof(int32_t) : 0;
+  return blocks > 1 ? blocks * up(E, 4) * (int64_t)sizeof(int32_t) : 0;
 }
 
 FP8B_EXPORT int moe_route(const void* logits, int dtype, int64_t ld, int64_t T, int64_t E, int64_t k, int renormalize,

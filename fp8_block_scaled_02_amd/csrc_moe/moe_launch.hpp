@@ -23,7 +23,7 @@ struct Plan {
   int32_t *experts, *offsets, *row_index, *token_rows;
 };
 
-// Workgroups of a sort that count apart; each takes E words of workspace (1: none needed).
+// Workgroups of a sort that count apart; each takes E words of workspace, rounded up to 4 (1: none needed).
 int64_t sort_blocks(int64_t T);
 int launch_route(const Mat& logits, int64_t T, int E, int k, bool renormalize, float* gates, const Plan& p, int32_t* ws,
                  hipStream_t s);

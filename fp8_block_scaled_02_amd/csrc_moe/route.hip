@@ -29,9 +29,10 @@ using fp8blk::f32_to_bf16_bits;
 
 namespace {
 
-constexpr int kThreads = 512, kWaves = kThreads / 64;
+constexpr int kThreads = 1024;     // of a workgroup that chooses
+constexpr int kPlace = 512, kWaves = kPlace / 64;  // of one that places
 constexpr int kMaxE = 1024;
-constexpr int kBlockTokens = 32;   // tokens a workgroup chooses for at a time with 16 lanes to each
+constexpr int kBlockTokens = 64;   // tokens a workgroup chooses for at a time with 16 lanes to each
 constexpr int64_t kMaxBlocks = 256;
 
 // ---- reductions over the G lanes of a token ---------------------------------
@@ -94,6 +95,22 @@ __device__ __forceinline__ void store(void* p, int64_t i, float v) {
 
 // ---- choosing ---------------------------------------------------------------
 
+__device__ __forceinline__ float of_key(uint32_t k) {
+  if (k == 0xFFFFFFFFu) return __builtin_nanf("");
+  return __uint_as_float(k >> 31 ? k & 0x7FFFFFFFu : ~k);
+}
+
+// exp(d) for d <= 0 (or NaN), 0 below the normal range: the product with
+// log2(e) in two parts, so that the error stays at a few 2^-24 for any d.
+__device__ __forceinline__ float exp_term(float d) {
+  constexpr float kHi = 1.44269502f, kLo = 1.92596303e-8f, kLn2 = 0.693147182f;
+  d = d < -200.0f ? -200.0f : d;
+  const float t = d * kHi;
+  const float rest = __builtin_fmaf(d, kHi, -t) + d * kLo;
+  const float p = __builtin_amdgcn_exp2f(t);
+  return __builtin_fmaf(p, rest * kLn2, p);
+}
+
 struct Route {
   const void* logits;
   int64_t ld, T;
@@ -105,13 +122,7 @@ struct Sort {
   int E, k;
   int64_t per_block;  // tokens of a workgroup
   Plan p;
-  int32_t* hist;      // [workgroups][E]
-};
-
-// The chosen ones of a token (lanes of the same wave write and read them).
-struct Chosen {
-  float value[64];
-  int expert[64];
+  int32_t* hist;      // [workgroups][E], rows a multiple of 4 apart
 };
 
 __device__ __forceinline__ void wave_sync() {
@@ -119,10 +130,11 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_wave_barrier();
 }
 
-// Token t by the G lanes that call it; its experts are counted in `count`.
+// Token t by the G lanes that call it; its experts are counted in `count`, and
+// left in `local` too where that is given.
 template <bool BF16, int G, int V>
-__device__ __forceinline__ void choose(const Route& r, int64_t t, int32_t* __restrict__ experts, Chosen& c,
-                                       int* count) {
+__device__ __forceinline__ void choose(const Route& r, int64_t t, int32_t* __restrict__ experts, int* count,
+                                       int* local) {
   const int l = threadIdx.x % G;
   float x[V];
   uint32_t key[V];
@@ -130,84 +142,163 @@ __device__ __forceinline__ void choose(const Route& r, int64_t t, int32_t* __res
   for (int i = 0; i < V; ++i) x[i] = l + i * G < r.E ? load<BF16>(r.logits, t * r.ld + l + i * G) : -__builtin_inff();
 #pragma unroll
   for (int i = 0; i < V; ++i) key[i] = key_of(x[i]);
-  int n = 0;  // experts chosen
-  for (; n < r.k; ++n) {
-    uint32_t top = key[0];
+  // the lane's best, the lower expert among equals
+  uint32_t best = 0;
+  int slot = 0;
+  auto rescan = [&] {
+    best = key[0];
+    slot = 0;
 #pragma unroll
-    for (int i = 1; i < V; ++i) top = max(top, key[i]);
-    const uint32_t best = max_of<G>(top);
-    if (best == 0) break;  // the same in all G lanes
-    uint32_t at = 0xFFFFFFFFu;
+    for (int i = 1; i < V; ++i)
+      if (key[i] > best) {
+        best = key[i];
+        slot = i;
+      }
+  };
+  rescan();
+  // lane j % G keeps the token's choice j, its word j / G
+  constexpr int W = 64 / G;
+  uint32_t mine[W];
+  int expert[W];
 #pragma unroll
-    for (int i = V - 1; i >= 0; --i) at = key[i] == best ? (uint32_t)(l + i * G) : at;
-    const uint32_t e = min_of<G>(at);
+  for (int w = 0; w < W; ++w) {
+    mine[w] = 0;
+    expert[w] = -1;
+  }
+  uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      if ((uint32_t)(l + i * G) == e) {
-        key[i] = 0;
-        c.value[n] = x[i];
-        c.expert[n] = (int)e;
+  for (int w = 0; w < W; ++w) {
+    for (int j = w * G; j < min(r.k, (w + 1) * G); ++j) {
+      const uint32_t most = max_of<G>(best);
+      if (most == 0) break;  // the same in all G lanes
+      const uint32_t e = min_of<G>(best == most ? (uint32_t)(l + slot * G) : 0xFFFFFFFFu);
+      if (j == 0) top = most;
+      if (l == j - w * G) {
+        mine[w] = most;
+        expert[w] = (int)e;
+      }
+      if (best == most && (uint32_t)(l + slot * G) == e) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) key[i] = i == slot ? 0 : key[i];
+        rescan();
       }
     }
   }
-  wave_sync();
-  const float m = n > 0 ? c.value[0] : 0.0f;
-  float sum = 0.0f;
-  if (r.renormalize) {
-    for (int j = l; j < n; j += G) sum += expf(c.value[j] - m);
-  } else {
+  const float m = top != 0 ? of_key(top) : 0.0f;
+  float sum = 0.0f, p[W];
 #pragma unroll
-    for (int i = 0; i < V; ++i) sum += expf(x[i] - m);  // -inf adds 0
+  for (int w = 0; w < W; ++w) {
+    p[w] = expert[w] >= 0 ? expf(of_key(mine[w]) - m) : 0.0f;
+    sum += p[w];
+  }
+  if (!r.renormalize) {
+    sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) sum += exp_term(x[i] - m);  // -inf adds 0
   }
   sum = sum_of<G>(sum);
-  for (int j = l; j < r.k; j += G) {
-    const int e = j < n ? c.expert[j] : -1;
-    r.gates[t * r.k + j] = j < n ? expf(c.value[j] - m) / sum : 0.0f;
-    experts[t * r.k + j] = e;
-    if (e >= 0) atomicAdd(&count[e], 1);
+#pragma unroll
+  for (int w = 0; w < W; ++w) {
+    const int j = w * G + l;
+    if (j < r.k) {
+      r.gates[t * r.k + j] = expert[w] >= 0 ? p[w] / sum : 0.0f;
+      experts[t * r.k + j] = expert[w];
+      if (local) local[t * r.k + j] = expert[w];
+      if (expert[w] >= 0) atomicAdd(&count[expert[w]], 1);
+    }
   }
-  wave_sync();  // c is written again for the next token
 }
 
 // ---- placing ----------------------------------------------------------------
 
 struct PlaceLds {
   int count[kWaves][kMaxE];  // rows of an expert in a wave's part, then where the next one goes
-  int total[kThreads], before[kThreads];
+  int4 all[kPlace], before[kPlace];
   int scan[kWaves];
 };
 
-// Workgroup b of nb, every thread of it.
-__device__ __forceinline__ void place(const Sort& s, int b, int nb, PlaceLds& lds) {
+// Rows of each expert in all workgroups and in those before b, left in
+// all[e], before[e] (as arrays of int): columns of four experts to a thread,
+// the workgroups' counts dealt to the threads that have the same ones.
+__device__ __forceinline__ void add_up(const Sort& s, int b, int nb, PlaceLds& lds) {
+  const int columns = (s.E + 3) / 4;
+  const int shift = 32 - __builtin_clz(columns) - ((columns & (columns - 1)) == 0);  // columns <= 2^shift
+  const int parts = min(kPlace >> shift, 16);
+  const int q = threadIdx.x & ((1 << shift) - 1), part = threadIdx.x >> shift;
+  int4 all = make_int4(0, 0, 0, 0), before = all;
+  if (q < columns && part < parts) {
+    const int4* h = reinterpret_cast<const int4*>(s.hist) + q;
+#pragma unroll 16
+    for (int i = part; i < nb; i += parts) {
+      const int4 v = h[(int64_t)i * columns];
+      const int in = i < b ? -1 : 0;
+      all = make_int4(all.x + v.x, all.y + v.y, all.z + v.z, all.w + v.w);
+      before = make_int4(before.x + (v.x & in), before.y + (v.y & in), before.z + (v.z & in), before.w + (v.w & in));
+    }
+  }
+  if (part < parts) {
+    lds.all[threadIdx.x] = all;
+    lds.before[threadIdx.x] = before;
+  }
+  __syncthreads();
+  int sum[2][2];
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int e = threadIdx.x + u * kPlace;
+    sum[u][0] = sum[u][1] = 0;
+    if (e < s.E) {
+#pragma unroll 4
+      for (int i = 0; i < parts; ++i) {
+        sum[u][0] += reinterpret_cast<const int*>(lds.all)[(i << (shift + 2)) + e];
+        sum[u][1] += reinterpret_cast<const int*>(lds.before)[(i << (shift + 2)) + e];
+      }
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int e = threadIdx.x + u * kPlace;
+    if (e < s.E) {
+      reinterpret_cast<int*>(lds.all)[e] = sum[u][0];
+      reinterpret_cast<int*>(lds.before)[e] = sum[u][1];
+    }
+  }
+}
+
+// Workgroup b of nb, the first kPlace threads of it (the others only keep the
+// barriers).  slots: the workgroup's experts.
+template <bool ALONE>
+__device__ __forceinline__ void place(const Sort& s, int b, int nb, const int32_t* slots, PlaceLds& lds) {
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, E = s.E;
+  const bool works = tid < kPlace;
   const int64_t first = (int64_t)b * s.per_block * s.k;
   const int64_t n = min(s.per_block, s.T - b * s.per_block) * s.k;  // slots of this workgroup
-  const int64_t part = (n + kWaves * 64 - 1) / (kWaves * 64) * 64;  // and of a wave
-  const int64_t lo = min(n, w * part), hi = min(n, lo + part);
-  for (int i = tid; i < kWaves * E; i += kThreads) lds.count[i / E][i % E] = 0;
+  const int64_t part = (n + kPlace - 1) / kPlace * 64;               // and of a wave
+  const int64_t lo = works ? min(n, w * part) : n, hi = min(n, lo + part);
+  if (works)
+    for (int e = tid; e < E; e += kPlace)
+#pragma unroll
+      for (int i = 0; i < kWaves; ++i) lds.count[i][e] = 0;
+  if (!ALONE) add_up(s, b, nb, lds);
   __syncthreads();
   for (int64_t i = lo + lane; i < hi; i += 64) {
-    const int e = s.p.experts[first + i];
+    const int e = slots[i];
     if ((unsigned)e < (unsigned)E) atomicAdd(&lds.count[w][e], 1);
   }
   __syncthreads();
-  // in parts of kThreads experts: all rows of an expert, and those of it before this workgroup
-  int64_t base = 0;  // rows of the experts before the part
-  for (int e0 = 0; e0 < E; e0 += kThreads) {
+  int64_t base = 0;  // rows of the experts before those of this turn
+  for (int e0 = 0; e0 < E; e0 += kPlace) {
     const int e = e0 + tid;
+    const bool have = works && e < E;
     int all = 0, before = 0;
-    if (nb > 1) {
-      if (e < E) {
-#pragma unroll 8
-        for (int i = 0; i < nb; ++i) {
-          const int h = s.hist[(int64_t)i * E + e];
-          all += h;
-          before += i < b ? h : 0;
-        }
-      }
-    } else if (e < E) {
+    if (have) {
+      if (ALONE) {
 #pragma unroll
-      for (int i = 0; i < kWaves; ++i) all += lds.count[i][e];
+        for (int i = 0; i < kWaves; ++i) all += lds.count[i][e];
+      } else {
+        all = reinterpret_cast<const int*>(lds.all)[e];
+        before = reinterpret_cast<const int*>(lds.before)[e];
+      }
     }
     int sum = all;  // inclusive scan over the wave's experts
 #pragma unroll
@@ -215,7 +306,7 @@ __device__ __forceinline__ void place(const Sort& s, int b, int nb, PlaceLds& ld
       const int o = __shfl_up(sum, d);
       sum += lane >= d ? o : 0;
     }
-    if (lane == 63) lds.scan[w] = sum;
+    if (works && lane == 63) lds.scan[w] = sum;
     __syncthreads();
     int earlier = 0, whole = 0;
 #pragma unroll
@@ -224,7 +315,7 @@ __device__ __forceinline__ void place(const Sort& s, int b, int nb, PlaceLds& ld
       whole += lds.scan[i];
     }
     const int64_t start = base + earlier + sum - all;
-    if (e < E) {
+    if (have) {
       if (b == 0) s.p.offsets[e] = (int)start;
       int at = (int)start + before;
 #pragma unroll
@@ -240,11 +331,11 @@ __device__ __forceinline__ void place(const Sort& s, int b, int nb, PlaceLds& ld
   if (b == 0 && tid == 0) s.p.offsets[E] = (int)base;
   // rows that no slot has: this workgroup's share
   const int64_t R = s.T * s.k;
-  for (int64_t r = base + (int64_t)b * kThreads + tid; r < R; r += (int64_t)nb * kThreads) s.p.row_index[r] = -1;
+  for (int64_t r = base + (int64_t)b * blockDim.x + tid; r < R; r += (int64_t)nb * blockDim.x) s.p.row_index[r] = -1;
   const int bits = 32 - __builtin_clz(E);  // E <= 2^bits - 1 tells an empty slot from the experts
   for (int64_t i0 = lo; i0 < hi; i0 += 64) {
     const int64_t i = i0 + lane;
-    int e = i < hi ? s.p.experts[first + i] : -1;
+    int e = i < hi ? slots[i] : -1;
     if ((unsigned)e >= (unsigned)E) e = E;
     uint64_t same = ~0ull;
     for (int j = 0; j < bits; ++j) {
@@ -263,51 +354,53 @@ __device__ __forceinline__ void place(const Sort& s, int b, int nb, PlaceLds& ld
   }
 }
 
-template <bool BF16, int G, int V>
+__device__ __forceinline__ void write_counts(const Sort& s, const int* count, int threads) {
+  const int stride = (s.E + 3) / 4 * 4;
+  for (int e = threadIdx.x; e < stride; e += threads)
+    s.hist[(int64_t)blockIdx.x * stride + e] = e < s.E ? count[e] : 0;
+}
+
+// ALONE: one workgroup has all tokens, chooses and places.
+template <bool BF16, int G, int V, bool ALONE>
 __global__ __launch_bounds__(kThreads) void route_kernel(Route r, Sort s) {
   constexpr int kGroups = kThreads / G;
-  __shared__ Chosen chosen[kGroups];
-  __shared__ PlaceLds lds;
-  int* count = lds.count[0];
+  __shared__ int count[kMaxE];
+  __shared__ int slots[ALONE ? kBlockTokens * 64 : 1];
   for (int e = threadIdx.x; e < r.E; e += kThreads) count[e] = 0;
   __syncthreads();
-  const int g = threadIdx.x / G;
   const int64_t end = min(r.T, (int64_t)(blockIdx.x + 1) * s.per_block);
-  // every wave goes round as often as its first token needs: the lanes of a
-  // wave stay together, groups past the end repeat the last token
-  for (int64_t t0 = (int64_t)blockIdx.x * s.per_block; t0 < end; t0 += kGroups) {
-    const int64_t t = t0 + g;
-    if (t < end) choose<BF16, G, V>(r, t, s.p.experts, chosen[g], count);
-  }
+  for (int64_t t = (int64_t)blockIdx.x * s.per_block + threadIdx.x / G; t < end; t += kGroups)
+    choose<BF16, G, V>(r, t, s.p.experts, count, ALONE ? slots : nullptr);
   __syncthreads();
-  if (gridDim.x == 1) {
-    __threadfence_block();
-    place(s, 0, 1, lds);
+  if constexpr (ALONE) {
+    __shared__ PlaceLds lds;
+    place<true>(s, 0, 1, slots, lds);
   } else {
-    for (int e = threadIdx.x; e < r.E; e += kThreads) s.hist[(int64_t)blockIdx.x * r.E + e] = count[e];
+    write_counts(s, count, kThreads);
   }
 }
 
-__global__ __launch_bounds__(kThreads) void count_kernel(Sort s) {
+__global__ __launch_bounds__(kPlace) void count_kernel(Sort s) {
   __shared__ int count[kMaxE];
-  for (int e = threadIdx.x; e < s.E; e += kThreads) count[e] = 0;
+  for (int e = threadIdx.x; e < s.E; e += kPlace) count[e] = 0;
   __syncthreads();
   const int64_t first = (int64_t)blockIdx.x * s.per_block, last = min(s.T, first + s.per_block);
-  for (int64_t i = first * s.k + threadIdx.x; i < last * s.k; i += kThreads) {
+  for (int64_t i = first * s.k + threadIdx.x; i < last * s.k; i += kPlace) {
     const int e = s.p.experts[i];
     if ((unsigned)e < (unsigned)s.E) atomicAdd(&count[e], 1);
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < s.E; e += kThreads) s.hist[(int64_t)blockIdx.x * s.E + e] = count[e];
+  write_counts(s, count, kPlace);
 }
 
-__global__ __launch_bounds__(kThreads) void place_kernel(Sort s) {
+template <bool ALONE>
+__global__ __launch_bounds__(kPlace) void place_kernel(Sort s) {
   __shared__ PlaceLds lds;
-  place(s, blockIdx.x, gridDim.x, lds);
+  place<ALONE>(s, blockIdx.x, gridDim.x, s.p.experts + (int64_t)blockIdx.x * s.per_block * s.k, lds);
 }
 
-__global__ __launch_bounds__(kThreads) void no_tokens_kernel(int32_t* offsets, int E) {
-  for (int e = threadIdx.x; e <= E; e += kThreads) offsets[e] = 0;
+__global__ __launch_bounds__(kPlace) void no_tokens_kernel(int32_t* offsets, int E) {
+  for (int e = threadIdx.x; e <= E; e += kPlace) offsets[e] = 0;
 }
 
 // ---- the weights' gradient --------------------------------------------------
@@ -317,9 +410,11 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const float* __rest
                                                              int64_t ld, const float* __restrict__ gates,
                                                              const int32_t* __restrict__ experts, int64_t T, int E,
                                                              int k, int renormalize, void* dlogits, int64_t ld_d) {
+  __shared__ float rows[256 / G][G * V];
   const int l = threadIdx.x % G;
   const int64_t t = (int64_t)blockIdx.x * (256 / G) + threadIdx.x / G;
   if (t >= T) return;
+  float* row = rows[threadIdx.x / G];
   float x[V], p[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
@@ -337,8 +432,7 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const float* __rest
     for (int i = 0; i < V; ++i) top = max(top, key_of(x[i]));
     top = max_of<G>(top);
     if (top != 0) {
-      const float m = top == 0xFFFFFFFFu ? __builtin_nanf("")
-                                         : __uint_as_float(top >> 31 ? top & 0x7FFFFFFFu : ~top);
+      const float m = of_key(top);
       float sum = 0.0f;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
@@ -350,18 +444,23 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const float* __rest
       for (int i = 0; i < V; ++i) p[i] = -(p[i] / sum) * dot;
     }
   }
-  for (int j = 0; j < k; ++j) {
-    const int e = experts[t * k + j];
-    if ((unsigned)e < (unsigned)E && e % G == l) {
-      const float g = gates[t * k + j], dg = dgates[t * k + j];
-      const float add = renormalize ? g * (dg - dot) : g * dg;
+  // the chosen experts' terms through LDS (an expert that is named more than
+  // once gets their sum, in the order of the slots: lanes of one instruction
+  // add in their order)
 #pragma unroll
-      for (int i = 0; i < V; ++i) p[i] += e / G == i ? add : 0.0f;
+  for (int i = 0; i < V; ++i) row[l + i * G] = p[i];
+  wave_sync();
+  for (int j = l; j < k; j += G) {
+    const int e = experts[t * k + j];
+    if ((unsigned)e < (unsigned)E) {
+      const float g = gates[t * k + j], dg = dgates[t * k + j];
+      unsafeAtomicAdd(&row[e], renormalize ? g * (dg - dot) : g * dg);
     }
   }
+  wave_sync();
 #pragma unroll
   for (int i = 0; i < V; ++i)
-    if (l + i * G < E) store<BF16>(dlogits, t * ld_d + l + i * G, p[i]);
+    if (l + i * G < E) store<BF16>(dlogits, t * ld_d + l + i * G, row[l + i * G]);
 }
 
 Sort sort_of(int64_t T, int E, int k, const Plan& p, int32_t* ws) {
@@ -370,7 +469,7 @@ Sort sort_of(int64_t T, int E, int k, const Plan& p, int32_t* ws) {
 }
 
 int no_tokens(int32_t* offsets, int E, hipStream_t s) {
-  hipLaunchKernelGGL(no_tokens_kernel, dim3(1), dim3(kThreads), 0, s, offsets, E);
+  hipLaunchKernelGGL(no_tokens_kernel, dim3(1), dim3(kPlace), 0, s, offsets, E);
   return check_launch();
 }
 
@@ -398,12 +497,15 @@ int launch_route(const Mat& logits, int64_t T, int E, int k, bool renormalize, f
   const Sort sort = sort_of(T, E, k, p, ws);
   const unsigned blocks = (unsigned)((T + sort.per_block - 1) / sort.per_block);
   const Route r{logits.p, logits.ld, T, E, k, renormalize, gates};
-  int rc = by_width(logits.bf16, E, [&](auto b, auto G, auto V) {
-    hipLaunchKernelGGL((route_kernel<b.value, G.value, V.value>), dim3(blocks), dim3(kThreads), 0, s, r, sort);
+  const int rc = by_width(logits.bf16, E, [&](auto b, auto G, auto V) {
+    if (blocks == 1)
+      hipLaunchKernelGGL((route_kernel<b.value, G.value, V.value, true>), dim3(1), dim3(kThreads), 0, s, r, sort);
+    else
+      hipLaunchKernelGGL((route_kernel<b.value, G.value, V.value, false>), dim3(blocks), dim3(kThreads), 0, s, r, sort);
     return check_launch();
   });
   if (rc != FP8B_OK || blocks == 1) return rc;
-  hipLaunchKernelGGL(place_kernel, dim3(blocks), dim3(kThreads), 0, s, sort);
+  hipLaunchKernelGGL(place_kernel<false>, dim3(blocks), dim3(kPlace), 0, s, sort);
   return check_launch();
 }
 
@@ -411,11 +513,13 @@ int launch_sort(int64_t T, int E, int k, const Plan& p, int32_t* ws, hipStream_t
   if (T == 0) return no_tokens(p.offsets, E, s);
   const Sort sort = sort_of(T, E, k, p, ws);
   const unsigned blocks = (unsigned)((T + sort.per_block - 1) / sort.per_block);
-  if (blocks > 1) {
-    hipLaunchKernelGGL(count_kernel, dim3(blocks), dim3(kThreads), 0, s, sort);
-    if (const int rc = check_launch()) return rc;
+  if (blocks == 1) {
+    hipLaunchKernelGGL(place_kernel<true>, dim3(1), dim3(kPlace), 0, s, sort);
+    return check_launch();
   }
-  hipLaunchKernelGGL(place_kernel, dim3(blocks), dim3(kThreads), 0, s, sort);
+  hipLaunchKernelGGL(count_kernel, dim3(blocks), dim3(kPlace), 0, s, sort);
+  if (const int rc = check_launch()) return rc;
+  hipLaunchKernelGGL(place_kernel<false>, dim3(blocks), dim3(kPlace), 0, s, sort);
   return check_launch();
 }
 

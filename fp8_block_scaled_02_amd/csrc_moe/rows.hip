@@ -1,10 +1,16 @@
 // rows.hip -- token rows to their experts and back, and both gradients.
 //
-// Every kernel goes by tokens: a workgroup has one token's slots and a piece
-// of its columns, so that a token's own row (x, out, dout) is read or written
-// once and each routed row is touched once.  All are bound by memory.  Rows
-// are moved 16 bytes at a time where every row starts on 16 bytes and the
-// columns fill them, else one value at a time.
+// Every kernel goes by tokens: a workgroup has one token's slots and all its
+// columns, so that a token's own row (x, out, dout) is read or written once,
+// each routed row is touched once, and a slot's gradient is summed where it is
+// made, in a fixed order.  All are bound by memory.
+//
+// Rows are reached through buffer descriptors of their own, whose length is
+// that of the row, or none where a slot has no row: loads past it give zeros
+// and stores past it do nothing, so there is no branch between the loads of a
+// token's slots and all of them are in flight together.  16 bytes at a time
+// where rows start on 4 bytes, else one value at a time.
+#include <algorithm>
 #include <type_traits>
 
 #include "../csrc/common.hpp"
@@ -14,66 +20,79 @@ namespace fp8moe {
 
 using fp8blk::bf16_bits_to_f32;
 using fp8blk::f32_to_bf16_bits;
-using fp8blk::u32x2;
 using fp8blk::u32x4;
 
 namespace {
 
-constexpr int kThreads = 256, kWaves = kThreads / 64;
+constexpr int kMaxThreads = 1024, kMaxWaves = kMaxThreads / 64;
+constexpr int kSlots = 8;  // slots whose rows are in flight at a time
 
-// W values of one type as they lie in memory.
-template <bool BF16, int W>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t row_at(const void* p, int64_t offset, int64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(static_cast<char*>(const_cast<void*>(p)) + offset, 0, (int)(uint32_t)bytes,
+                                           0x00020000);
+}
+
+template <bool BF16>
+constexpr int kSize = BF16 ? 2 : 4;
+
+// C consecutive values as they lie in memory: 16-byte words, or one value.
+template <bool BF16, int C>
 struct Raw {
-  static constexpr int kBytes = W * (BF16 ? 2 : 4);
-  using Word = std::conditional_t<BF16 && W == 1, uint16_t, uint32_t>;
-  static constexpr int kWords = kBytes / (int)sizeof(Word);
-  alignas(kBytes % 16 == 0 ? 16 : sizeof(Word)) Word w[kWords];
+  static constexpr int kWords = C == 1 ? 1 : C * kSize<BF16> / 4;
+  uint32_t w[kWords];
 };
-template <bool BF16, int W>
-__device__ __forceinline__ Raw<BF16, W> load(const void* p, int64_t i) {
-  Raw<BF16, W> r;
-  const char* a = static_cast<const char*>(p) + i * (BF16 ? 2 : 4);
-  if constexpr (Raw<BF16, W>::kBytes % 16 == 0) {
-#pragma unroll
-    for (int q = 0; q < Raw<BF16, W>::kBytes / 16; ++q)
-      *reinterpret_cast<u32x4*>(r.w + 4 * q) = *reinterpret_cast<const u32x4*>(a + 16 * q);
+template <bool BF16, int C>
+__device__ __forceinline__ Raw<BF16, C> load(__amdgpu_buffer_rsrc_t r, int64_t c) {
+  Raw<BF16, C> v;
+  const uint32_t at = (uint32_t)c * kSize<BF16>;
+  if constexpr (C == 1) {
+    v.w[0] = BF16 ? (uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, at, 0, 0)
+                  : (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(r, at, 0, 0);
   } else {
-    static_assert(W == 1, "16 bytes or one value");
-    r.w[0] = *reinterpret_cast<const typename Raw<BF16, W>::Word*>(a);
-  }
-  return r;
-}
-template <bool BF16, int W>
-__device__ __forceinline__ void store(void* p, int64_t i, const Raw<BF16, W>& r) {
-  char* a = static_cast<char*>(p) + i * (BF16 ? 2 : 4);
-  if constexpr (Raw<BF16, W>::kBytes % 16 == 0) {
 #pragma unroll
-    for (int q = 0; q < Raw<BF16, W>::kBytes / 16; ++q)
-      *reinterpret_cast<u32x4*>(a + 16 * q) = *reinterpret_cast<const u32x4*>(r.w + 4 * q);
+    for (int q = 0; q < Raw<BF16, C>::kWords / 4; ++q) {
+      const auto u = __builtin_amdgcn_raw_buffer_load_b128(r, at + 16 * q, 0, 0);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v.w[4 * q + i] = u[i];
+    }
+  }
+  return v;
+}
+template <bool BF16, int C>
+__device__ __forceinline__ void store(__amdgpu_buffer_rsrc_t r, int64_t c, const Raw<BF16, C>& v) {
+  const uint32_t at = (uint32_t)c * kSize<BF16>;
+  if constexpr (C == 1) {
+    if constexpr (BF16)
+      __builtin_amdgcn_raw_buffer_store_b16((unsigned short)v.w[0], r, at, 0, 0);
+    else
+      __builtin_amdgcn_raw_buffer_store_b32(v.w[0], r, at, 0, 0);
   } else {
-    *reinterpret_cast<typename Raw<BF16, W>::Word*>(a) = r.w[0];
+#pragma unroll
+    for (int q = 0; q < Raw<BF16, C>::kWords / 4; ++q)
+      __builtin_amdgcn_raw_buffer_store_b128(u32x4{v.w[4 * q], v.w[4 * q + 1], v.w[4 * q + 2], v.w[4 * q + 3]}, r,
+                                             at + 16 * q, 0, 0);
   }
 }
-template <bool BF16, int W>
-__device__ __forceinline__ float value(const Raw<BF16, W>& r, int i) {
+template <bool BF16, int C>
+__device__ __forceinline__ float value(const Raw<BF16, C>& r, int i) {
   if constexpr (!BF16)
     return __uint_as_float(r.w[i]);
-  else if constexpr (W == 1)
+  else if constexpr (C == 1)
     return bf16_bits_to_f32(r.w[0]);
   else
     return i & 1 ? __uint_as_float(r.w[i / 2] & 0xffff0000u) : __uint_as_float(r.w[i / 2] << 16);
 }
-template <bool BF16, int W>
-__device__ __forceinline__ Raw<BF16, W> raw(const float (&v)[W]) {
-  Raw<BF16, W> r;
+template <bool BF16, int C>
+__device__ __forceinline__ Raw<BF16, C> raw(const float (&v)[C]) {
+  Raw<BF16, C> r;
   if constexpr (!BF16) {
 #pragma unroll
-    for (int i = 0; i < W; ++i) r.w[i] = __float_as_uint(v[i]);
-  } else if constexpr (W == 1) {
-    r.w[0] = (uint16_t)f32_to_bf16_bits(v[0]);
+    for (int i = 0; i < C; ++i) r.w[i] = __float_as_uint(v[i]);
+  } else if constexpr (C == 1) {
+    r.w[0] = f32_to_bf16_bits(v[0]);
   } else {
 #pragma unroll
-    for (int i = 0; i < W / 2; ++i) r.w[i] = f32_to_bf16_bits(v[2 * i]) | (f32_to_bf16_bits(v[2 * i + 1]) << 16);
+    for (int i = 0; i < C / 2; ++i) r.w[i] = f32_to_bf16_bits(v[2 * i]) | f32_to_bf16_bits(v[2 * i + 1]) << 16;
   }
   return r;
 }
@@ -84,161 +103,204 @@ __device__ __forceinline__ int64_t row_of(const int32_t* token_rows, int64_t slo
   return r >= 0 && r < R ? r : -1;
 }
 
-template <bool BF16, int W>
-__global__ __launch_bounds__(kThreads) void gather_kernel(const void* x, int64_t ld_x, int64_t N,
-                                                          const int32_t* __restrict__ token_rows, int k, int64_t R,
-                                                          void* rows, int64_t ld_r) {
+// Columns of a token in pieces of C: f(first column, whole pieces of C) for U
+// pieces of a thread at a time, then one column at a time behind the last
+// whole piece.  Pieces past the last are past the descriptors' end.
+template <int C, int U, class F, class G>
+__device__ __forceinline__ void columns(int64_t N, F whole, G single) {
+  const int64_t n = N / C, step = (int64_t)blockDim.x;
+  for (int64_t v = threadIdx.x; v < n; v += U * step) whole(v * C, step * C);
+  if (C > 1)
+    for (int64_t c = n * C + threadIdx.x; c < N; c += step) single(c);
+}
+
+// Pieces of a thread at a time: two, one where eight of fp32 would not fit the
+// registers.
+template <bool BF16, int C>
+constexpr int kPieces = !BF16 && C == 8 ? 1 : 2;
+
+template <bool BF16, int C>
+__global__ __launch_bounds__(kMaxThreads) void gather_kernel(const void* x, int64_t ld_x, int64_t N,
+                                                             const int32_t* __restrict__ token_rows, int k, int64_t R,
+                                                             void* rows, int64_t ld_r) {
+  constexpr int S = kSize<BF16>, U = kPieces<BF16, C>;
   const int64_t t = blockIdx.x;
-  for (int64_t c = ((int64_t)blockIdx.y * kThreads + threadIdx.x) * W; c < N; c += (int64_t)gridDim.y * kThreads * W) {
-    const Raw<BF16, W> v = load<BF16, W>(x, t * ld_x + c);
+  auto go = [&](auto cc, auto uu, int64_t c, int64_t step) {
+    constexpr int CC = decltype(cc)::value, UU = decltype(uu)::value;
+    const __amdgpu_buffer_rsrc_t from = row_at(x, t * ld_x * S, N / CC * CC * S);
+    Raw<BF16, CC> v[UU];
+#pragma unroll
+    for (int u = 0; u < UU; ++u) v[u] = load<BF16, CC>(from, c + u * step);
     for (int j = 0; j < k; ++j) {
       const int64_t r = row_of(token_rows, t * k + j, R);
-      if (r >= 0) store<BF16, W>(rows, r * ld_r + c, v);
+      const __amdgpu_buffer_rsrc_t to = row_at(rows, r * ld_r * S, r >= 0 ? N / CC * CC * S : 0);
+#pragma unroll
+      for (int u = 0; u < UU; ++u) store<BF16, CC>(to, c + u * step, v[u]);
     }
-  }
+  };
+  using One = std::integral_constant<int, 1>;
+  columns<C, U>(
+      N, [&](int64_t c, int64_t step) { go(std::integral_constant<int, C>{}, std::integral_constant<int, U>{}, c, step); },
+      [&](int64_t c) { go(One{}, One{}, c, 0); });
 }
 
-template <bool YB, bool OB, int W>
-__global__ __launch_bounds__(kThreads) void combine_kernel(const void* y, int64_t ld_y, int64_t R, int64_t N,
-                                                           const int32_t* __restrict__ token_rows,
-                                                           const float* __restrict__ gates, int k, void* out,
-                                                           int64_t ld_o) {
+template <bool YB, bool OB, int C>
+__global__ __launch_bounds__(kMaxThreads) void combine_kernel(const void* y, int64_t ld_y, int64_t R, int64_t N,
+                                                              const int32_t* __restrict__ token_rows,
+                                                              const float* __restrict__ gates, int k, void* out,
+                                                              int64_t ld_o) {
+  constexpr int U = kPieces<YB, C>;
   const int64_t t = blockIdx.x;
-  for (int64_t c = ((int64_t)blockIdx.y * kThreads + threadIdx.x) * W; c < N; c += (int64_t)gridDim.y * kThreads * W) {
-    float acc[W];
+  auto go = [&](auto cc, auto uu, int64_t c, int64_t step) {
+    constexpr int CC = decltype(cc)::value, UU = decltype(uu)::value;
+    float acc[UU][CC];
 #pragma unroll
-    for (int i = 0; i < W; ++i) acc[i] = 0.0f;
-    // slots in batches whose loads are all issued before the first is used
-    constexpr int B = 8;
-    for (int j0 = 0; j0 < k; j0 += B) {
-      Raw<YB, W> v[B];
-      float g[B];
-      bool have[B];
+    for (int u = 0; u < UU; ++u)
 #pragma unroll
-      for (int j = 0; j < B; ++j) {
+      for (int i = 0; i < CC; ++i) acc[u][i] = 0.0f;
+    for (int j0 = 0; j0 < k; j0 += kSlots) {
+      Raw<YB, CC> v[kSlots][UU];
+      float g[kSlots];
+#pragma unroll
+      for (int j = 0; j < kSlots; ++j) {
         const int64_t r = j0 + j < k ? row_of(token_rows, t * k + j0 + j, R) : -1;
-        have[j] = r >= 0;
-        if (have[j]) {
-          g[j] = gates ? gates[t * k + j0 + j] : 1.0f;
-          v[j] = load<YB, W>(y, r * ld_y + c);
-        }
+        g[j] = r < 0 ? 0.0f : gates ? gates[t * k + j0 + j] : 1.0f;
+        const __amdgpu_buffer_rsrc_t from = row_at(y, r * ld_y * kSize<YB>, r >= 0 ? N / CC * CC * kSize<YB> : 0);
+#pragma unroll
+        for (int u = 0; u < UU; ++u) v[j][u] = load<YB, CC>(from, c + u * step);
       }
 #pragma unroll
-      for (int j = 0; j < B; ++j)
-        if (have[j]) {
+      for (int j = 0; j < kSlots; ++j)
 #pragma unroll
-          for (int i = 0; i < W; ++i) acc[i] = __builtin_fmaf(g[j], value<YB, W>(v[j], i), acc[i]);
-        }
+        for (int u = 0; u < UU; ++u)
+#pragma unroll
+          for (int i = 0; i < CC; ++i) acc[u][i] = __builtin_fmaf(g[j], value<YB, CC>(v[j][u], i), acc[u][i]);
     }
-    store<OB, W>(out, t * ld_o + c, raw<OB, W>(acc));
-  }
+    const __amdgpu_buffer_rsrc_t to = row_at(out, t * ld_o * kSize<OB>, N / CC * CC * kSize<OB>);
+#pragma unroll
+    for (int u = 0; u < UU; ++u) store<OB, CC>(to, c + u * step, raw<OB, CC>(acc[u]));
+  };
+  using One = std::integral_constant<int, 1>;
+  columns<C, U>(
+      N, [&](int64_t c, int64_t step) { go(std::integral_constant<int, C>{}, std::integral_constant<int, U>{}, c, step); },
+      [&](int64_t c) { go(One{}, One{}, c, 0); });
 }
 
-// One workgroup has a token's whole row, so that its sums need no others'.
-template <bool YB, bool OB, int W>
-__global__ __launch_bounds__(kThreads) void combine_backward_kernel(const void* dout, int64_t ld_o, const void* y,
-                                                                    int64_t ld_y, int64_t R, int64_t N,
-                                                                    const int32_t* __restrict__ token_rows,
-                                                                    const float* __restrict__ gates, int k, void* dy,
-                                                                    int64_t ld_dy, float* __restrict__ dgates) {
-  constexpr int B = 8;
-  __shared__ float part[kWaves][B];
+template <bool YB, bool OB, int C>
+__global__ __launch_bounds__(kMaxThreads) void combine_backward_kernel(
+    const void* dout, int64_t ld_o, const void* y, int64_t ld_y, int64_t R, int64_t N,
+    const int32_t* __restrict__ token_rows, const float* __restrict__ gates, int k, void* dy, int64_t ld_dy,
+    float* __restrict__ dgates) {
+  constexpr int U = kPieces<YB, C>;
+  __shared__ float part[kMaxWaves][kSlots];
   const int64_t t = blockIdx.x;
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  for (int j0 = 0; j0 < k; j0 += B) {
-    int64_t r[B];
-    float g[B], sum[B];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, waves = blockDim.x >> 6;
+  for (int j0 = 0; j0 < k; j0 += kSlots) {
+    int64_t r[kSlots];
+    float g[kSlots], sum[kSlots];
 #pragma unroll
-    for (int j = 0; j < B; ++j) {
+    for (int j = 0; j < kSlots; ++j) {
       r[j] = j0 + j < k ? row_of(token_rows, t * k + j0 + j, R) : -1;
-      g[j] = r[j] >= 0 ? gates[t * k + j0 + j] : 0.0f;
+      g[j] = r[j] < 0 ? 0.0f : gates[t * k + j0 + j];
       sum[j] = 0.0f;
     }
-    for (int64_t c = (int64_t)threadIdx.x * W; c < N; c += kThreads * W) {
-      const Raw<OB, W> d = load<OB, W>(dout, t * ld_o + c);
-      Raw<YB, W> v[B];
+    auto go = [&](auto cc, auto uu, int64_t c, int64_t step) {
+      constexpr int CC = decltype(cc)::value, UU = decltype(uu)::value;
+      const int64_t bytes = N / CC * CC * kSize<YB>;
+      const __amdgpu_buffer_rsrc_t grad = row_at(dout, t * ld_o * kSize<OB>, N / CC * CC * kSize<OB>);
+      Raw<OB, CC> d[UU];
+      Raw<YB, CC> v[kSlots][UU];
 #pragma unroll
-      for (int j = 0; j < B; ++j)
-        if (r[j] >= 0) v[j] = load<YB, W>(y, r[j] * ld_y + c);
+      for (int u = 0; u < UU; ++u) d[u] = load<OB, CC>(grad, c + u * step);
 #pragma unroll
-      for (int j = 0; j < B; ++j)
-        if (r[j] >= 0) {
-          float o[W];
+      for (int j = 0; j < kSlots; ++j)
 #pragma unroll
-          for (int i = 0; i < W; ++i) {
-            const float di = value<OB, W>(d, i);
+        for (int u = 0; u < UU; ++u)
+          v[j][u] = load<YB, CC>(row_at(y, r[j] * ld_y * kSize<YB>, r[j] >= 0 ? bytes : 0), c + u * step);
+#pragma unroll
+      for (int j = 0; j < kSlots; ++j)
+#pragma unroll
+        for (int u = 0; u < UU; ++u) {
+          float o[CC];
+#pragma unroll
+          for (int i = 0; i < CC; ++i) {
+            const float di = value<OB, CC>(d[u], i);
             o[i] = g[j] * di;
-            sum[j] = __builtin_fmaf(di, value<YB, W>(v[j], i), sum[j]);
+            // (a slot without a row has zeros here, whatever dout holds)
+            sum[j] = __builtin_fmaf(r[j] >= 0 ? di : 0.0f, value<YB, CC>(v[j][u], i), sum[j]);
           }
-          store<YB, W>(dy, r[j] * ld_dy + c, raw<YB, W>(o));
+          store<YB, CC>(row_at(dy, r[j] * ld_dy * kSize<YB>, r[j] >= 0 ? bytes : 0), c + u * step, raw<YB, CC>(o));
         }
-    }
+    };
+    using One = std::integral_constant<int, 1>;
+    columns<C, U>(
+        N,
+        [&](int64_t c, int64_t step) { go(std::integral_constant<int, C>{}, std::integral_constant<int, U>{}, c, step); },
+        [&](int64_t c) { go(One{}, One{}, c, 0); });
 #pragma unroll
-    for (int j = 0; j < B; ++j) {
+    for (int j = 0; j < kSlots; ++j) {
 #pragma unroll
       for (int m = 32; m >= 1; m >>= 1) sum[j] += __shfl_xor(sum[j], m);
       if (lane == 0) part[w][j] = sum[j];
     }
     __syncthreads();
-    if (threadIdx.x < B && j0 + (int)threadIdx.x < k) {
+    if (threadIdx.x < kSlots && j0 + (int)threadIdx.x < k) {
       float s = 0.0f;
-#pragma unroll
-      for (int i = 0; i < kWaves; ++i) s += part[i][threadIdx.x];
+      for (int i = 0; i < waves; ++i) s += part[i][threadIdx.x];
       dgates[t * k + j0 + threadIdx.x] = s;
     }
     __syncthreads();
   }
 }
 
-bool wide(const Mat& m) { return reinterpret_cast<uintptr_t>(m.p) % 16 == 0 && m.ld % (m.bf16 ? 8 : 4) == 0; }
-
-// Columns in pieces of a workgroup: enough workgroups that few tokens fill the card.
-dim3 grid_of(int64_t T, int64_t N, int W) {
-  const int64_t pieces = (N + (int64_t)kThreads * W - 1) / ((int64_t)kThreads * W);
-  return dim3((unsigned)T, (unsigned)(pieces < 1024 ? pieces : 1024));
+bool wide(const Mat& m) {
+  return reinterpret_cast<uintptr_t>(m.p) % 4 == 0 && m.ld * (m.bf16 ? 2 : 4) % 4 == 0;
 }
 
-// f(y is bf16, out is bf16, wide)
+// Threads of a workgroup: each has two pieces of a row where that fills them.
+unsigned threads_of(int64_t N, int C) {
+  const int64_t pieces = (N / C + 1) / 2;
+  return (unsigned)std::min<int64_t>(kMaxThreads, std::max<int64_t>(64, (pieces + 63) / 64 * 64));
+}
+
+// f(y is bf16, out is bf16, columns of a piece)
 template <class F>
 int by_type(bool yb, bool ob, bool w, F f) {
+  auto with = [&](auto y, auto o) {
+    constexpr int C = decltype(y)::value || decltype(o)::value ? 8 : 4;
+    return w ? f(y, o, std::integral_constant<int, C>{}) : f(y, o, std::integral_constant<int, 1>{});
+  };
   using T = std::true_type;
   using N = std::false_type;
-  if (w) return yb ? (ob ? f(T{}, T{}, T{}) : f(T{}, N{}, T{})) : (ob ? f(N{}, T{}, T{}) : f(N{}, N{}, T{}));
-  return yb ? (ob ? f(T{}, T{}, N{}) : f(T{}, N{}, N{})) : (ob ? f(N{}, T{}, N{}) : f(N{}, N{}, N{}));
+  return yb ? (ob ? with(T{}, T{}) : with(T{}, N{})) : (ob ? with(N{}, T{}) : with(N{}, N{}));
 }
 
 }  // namespace
 
 int launch_gather(const Mat& x, int64_t T, int64_t N, const int32_t* token_rows, int k, int64_t R, const Mat& rows,
                   hipStream_t s) {
-  const int W = x.bf16 ? 8 : 4;
-  const bool w = wide(x) && wide(rows) && N % W == 0;
-  return by_type(x.bf16, x.bf16, w, [&](auto b, auto, auto wd) {
-    constexpr int kW = wd.value ? (b.value ? 8 : 4) : 1;
-    hipLaunchKernelGGL((gather_kernel<b.value, kW>), grid_of(T, N, kW), dim3(kThreads), 0, s, x.p, x.ld, N, token_rows,
-                       k, R, rows.p, rows.ld);
+  return by_type(x.bf16, x.bf16, wide(x) && wide(rows), [&](auto b, auto, auto c) {
+    hipLaunchKernelGGL((gather_kernel<b.value, c.value>), dim3((unsigned)T), dim3(threads_of(N, c.value)), 0, s, x.p, x.ld,
+                       N, token_rows, k, R, rows.p, rows.ld);
     return check_launch();
   });
 }
 
 int launch_combine(const Mat& y, int64_t R, int64_t N, const int32_t* token_rows, const float* gates, int64_t T, int k,
                    const Mat& out, hipStream_t s) {
-  const bool w = (R == 0 || wide(y)) && wide(out) && N % (y.bf16 || out.bf16 ? 8 : 4) == 0;
-  return by_type(y.bf16, out.bf16, w, [&](auto yb, auto ob, auto wd) {
-    constexpr int kW = wd.value ? (yb.value || ob.value ? 8 : 4) : 1;
-    hipLaunchKernelGGL((combine_kernel<yb.value, ob.value, kW>), grid_of(T, N, kW), dim3(kThreads), 0, s, y.p, y.ld, R,
-                       N, token_rows, gates, k, out.p, out.ld);
+  return by_type(y.bf16, out.bf16, wide(y) && wide(out), [&](auto yb, auto ob, auto c) {
+    hipLaunchKernelGGL((combine_kernel<yb.value, ob.value, c.value>), dim3((unsigned)T), dim3(threads_of(N, c.value)), 0, s,
+                       y.p, y.ld, R, N, token_rows, gates, k, out.p, out.ld);
     return check_launch();
   });
 }
 
 int launch_combine_backward(const Mat& dout, const Mat& y, int64_t R, int64_t N, const int32_t* token_rows,
                             const float* gates, int64_t T, int k, const Mat& dy, float* dgates, hipStream_t s) {
-  const bool w = (R == 0 || (wide(y) && wide(dy))) && wide(dout) && N % (y.bf16 || dout.bf16 ? 8 : 4) == 0;
-  return by_type(y.bf16, dout.bf16, w, [&](auto yb, auto ob, auto wd) {
-    constexpr int kW = wd.value ? (yb.value || ob.value ? 8 : 4) : 1;
-    hipLaunchKernelGGL((combine_backward_kernel<yb.value, ob.value, kW>), dim3((unsigned)T), dim3(kThreads), 0, s,
-                       dout.p, dout.ld, y.p, y.ld, R, N, token_rows, gates, k, dy.p, dy.ld, dgates);
+  return by_type(y.bf16, dout.bf16, wide(y) && wide(dy) && wide(dout), [&](auto yb, auto ob, auto c) {
+    hipLaunchKernelGGL((combine_backward_kernel<yb.value, ob.value, c.value>), dim3((unsigned)T),
+                       dim3(threads_of(N, c.value)), 0, s, dout.p, dout.ld, y.p, y.ld, R, N, token_rows, gates, k, dy.p,
+                       dy.ld, dgates);
     return check_launch();
   });
 }

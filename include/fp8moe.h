@@ -112,7 +112,7 @@ int moe_route_backward(const float *dgates, const void *logits, int dtype,
  *   rows[token_rows[t][j]] = x[t].
  *   Rows that no slot names are left as they were.
  *
- *   x [T][ld_x], rows [R][ld_r], both of `dtype`;  N >= 1 columns, < 2^30;
+ *   x [T][ld_x], rows [R][ld_r], both of `dtype`;  N >= 1 columns, < 2^29;
  *   token_rows outside [0, R) count as -1 (no row); no row is named twice.
  *   T < 2^24; 0 <= R < 2^30; 1 <= k <= 64.
  */
@@ -161,7 +161,7 @@ int moe_combine_backward(const void *dout, int out_dtype, int64_t ld_o,
  *
  *   x       fp32 or bf16 [M][ld_x].
  *   codes   int8 [M][ld_c];  scales float [M].
- *   M >= 0 (0 is a no-op), < 2^24; K >= 1, < 2^30.
+ *   M >= 0 (0 is a no-op), < 2^24; K >= 1, < 2^29.
  */
 int int8_quant(const void *x, int dtype, int64_t M, int64_t K, int64_t ld_x,
                int8_t *codes, int64_t ld_c, float *scales, void *stream);
