@@ -2,9 +2,14 @@
 // sorts (token, slot) pairs by expert, and the weights' gradient.
 //
 // Choosing.  G lanes hold one token's E logits, V to a lane (lane l those of
-// experts l, l + G, ...), as unsigned keys that order like the numbers.  k
-// times over, the largest key is found in the lane, then over the G lanes;
-// among the lanes that hold it the lowest expert wins, and its key leaves.
+// experts l, l + G, ...), as unsigned keys that order like the numbers.  The
+// k-th largest of 16 lanes' largest keys is a lower bound of the token's k-th
+// largest key; what reaches it, rarely much more than k, goes to LDS, where
+// every candidate counts those before it (larger, or equal and of a lower
+// expert): that is its slot.  Where that does not hold (k > 16, more than 64
+// candidates, E > 256), k times over the largest key is found in the lane, then
+// over the lanes, and leaves.  Instructions bound it: for 16384 tokens, 8 of
+// 256 experts, the k-fold search took 14 us, this SELECTED.
 // The first one chosen is the maximum that the softmax subtracts, so the
 // weights follow from the k chosen (or all E) logits without another pass.
 //
@@ -69,13 +74,13 @@ __device__ __forceinline__ float sum_of(float v) {
   }));
 }
 
-// Keys that order like the numbers: NaN above all, -0 as 0, -inf (and places
-// past the last expert) 0, which is never chosen.
+// Keys that order like the numbers: NaN above all, -0 as 0, -inf kNone or
+// below (as places past the last expert), which is never chosen.
+constexpr uint32_t kNone = 0x007FFFFFu;
 __device__ __forceinline__ uint32_t key_of(float x) {
-  if (x != x) return 0xFFFFFFFFu;
-  const uint32_t u = __float_as_uint(x == 0.0f ? 0.0f : x);
-  if (u == 0xFF800000u) return 0;
-  return (u >> 31) ? ~u : u | 0x80000000u;
+  const uint32_t u = __float_as_uint(x + 0.0f);  // -0 + 0 is 0
+  const uint32_t key = u ^ (uint32_t)((int)u >> 31 | (int)0x80000000);
+  return x != x ? 0xFFFFFFFFu : key;
 }
 
 template <bool BF16>
@@ -130,21 +135,25 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_wave_barrier();
 }
 
-// Token t by the G lanes that call it; its experts are counted in `count`, and
-// left in `local` too where that is given.
-template <bool BF16, int G, int V>
-__device__ __forceinline__ void choose(const Route& r, int64_t t, int32_t* __restrict__ experts, int* count,
-                                       int* local) {
+constexpr int kCandidates = 64;
+// Of the 16 lanes of a token; an entry is a key and the expert's complement.
+struct Candidates {
+  uint64_t all[kCandidates], chosen[16];
+};
+
+// Lane j % G of a token keeps its choice j in word j / G.
+template <int W>
+struct Choice {
+  uint32_t key[W];
+  int expert[W];
+};
+
+// The choices by k searches; the largest key (kNone or below: none).
+template <int G, int V>
+__device__ __forceinline__ uint32_t search(uint32_t (&key)[V], int k, Choice<64 / G>& c) {
   const int l = threadIdx.x % G;
-  float x[V];
-  uint32_t key[V];
-#pragma unroll
-  for (int i = 0; i < V; ++i) x[i] = l + i * G < r.E ? load<BF16>(r.logits, t * r.ld + l + i * G) : -__builtin_inff();
-#pragma unroll
-  for (int i = 0; i < V; ++i) key[i] = key_of(x[i]);
-  // the lane's best, the lower expert among equals
-  uint32_t best = 0;
-  int slot = 0;
+  uint32_t best = 0, top = 0;
+  int slot = 0;  // the lane's best, the lower expert among equals
   auto rescan = [&] {
     best = key[0];
     slot = 0;
@@ -156,26 +165,16 @@ __device__ __forceinline__ void choose(const Route& r, int64_t t, int32_t* __res
       }
   };
   rescan();
-  // lane j % G keeps the token's choice j, its word j / G
-  constexpr int W = 64 / G;
-  uint32_t mine[W];
-  int expert[W];
 #pragma unroll
-  for (int w = 0; w < W; ++w) {
-    mine[w] = 0;
-    expert[w] = -1;
-  }
-  uint32_t top = 0;
-#pragma unroll
-  for (int w = 0; w < W; ++w) {
-    for (int j = w * G; j < min(r.k, (w + 1) * G); ++j) {
+  for (int w = 0; w < 64 / G; ++w) {
+    for (int j = w * G; j < min(k, (w + 1) * G); ++j) {
       const uint32_t most = max_of<G>(best);
-      if (most == 0) break;  // the same in all G lanes
+      if (most <= kNone) break;  // the same in all G lanes
       const uint32_t e = min_of<G>(best == most ? (uint32_t)(l + slot * G) : 0xFFFFFFFFu);
       if (j == 0) top = most;
       if (l == j - w * G) {
-        mine[w] = most;
-        expert[w] = (int)e;
+        c.key[w] = most;
+        c.expert[w] = (int)e;
       }
       if (best == most && (uint32_t)(l + slot * G) == e) {
 #pragma unroll
@@ -184,11 +183,103 @@ __device__ __forceinline__ void choose(const Route& r, int64_t t, int32_t* __res
       }
     }
   }
-  const float m = top != 0 ? of_key(top) : 0.0f;
+  return top;
+}
+
+template <int CTRL>
+__device__ __forceinline__ int shifted(int v) {  // from the lane CTRL - 0x110 before, 0 into a row's first
+  return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xF, 0xF, true);
+}
+
+// The choices by candidates, of 16 lanes; false (in every lane of the wave,
+// nothing chosen) where a token of the wave has too many.
+template <int V>
+__device__ __forceinline__ bool select(const uint32_t (&key)[V], int k, Candidates& lds, Choice<4>& c, uint32_t& top) {
+  const int l = threadIdx.x & 15;
+  uint32_t best = key[0];
+#pragma unroll
+  for (int i = 1; i < V; ++i) best = max(best, key[i]);
+  // how many lanes have a larger one
+  int above = 0;
+  auto turn = [&](auto n) { above += dpp<0x120 + decltype(n)::value>(best) > best; };
+  using std::integral_constant;
+  turn(integral_constant<int, 1>{});
+  turn(integral_constant<int, 2>{});
+  turn(integral_constant<int, 3>{});
+  turn(integral_constant<int, 4>{});
+  turn(integral_constant<int, 5>{});
+  turn(integral_constant<int, 6>{});
+  turn(integral_constant<int, 7>{});
+  turn(integral_constant<int, 8>{});
+  turn(integral_constant<int, 9>{});
+  turn(integral_constant<int, 10>{});
+  turn(integral_constant<int, 11>{});
+  turn(integral_constant<int, 12>{});
+  turn(integral_constant<int, 13>{});
+  turn(integral_constant<int, 14>{});
+  turn(integral_constant<int, 15>{});
+  const uint32_t bound = max(min_of<16>(above < k ? best : 0xFFFFFFFFu), kNone + 1);
+  int mine = 0;
+#pragma unroll
+  for (int i = 0; i < V; ++i) mine += key[i] >= bound;
+  int end = mine;  // inclusive sum over the lanes
+  end += shifted<0x111>(end);
+  end += shifted<0x112>(end);
+  end += shifted<0x114>(end);
+  end += shifted<0x118>(end);
+  const int n = (int)max_of<16>((uint32_t)end);
+  if (__any(n > kCandidates)) return false;
+  int at = end - mine;
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    if (key[i] >= bound) lds.all[at++] = (uint64_t)key[i] << 32 | (uint32_t)~(l + i * 16);
+  wave_sync();
+  for (int w = l; w < n; w += 16) {
+    const uint64_t own = lds.all[w];
+    int before = 0;
+    for (int i = 0; i < n; ++i) before += lds.all[i] > own;
+    if (before < k) lds.chosen[before] = own;
+  }
+  wave_sync();
+  const int chosen = min(n, k);
+  if (l < chosen) {
+    c.key[0] = (uint32_t)(lds.chosen[l] >> 32);
+    c.expert[0] = (int)~(uint32_t)lds.chosen[l];
+  }
+  top = chosen > 0 ? (uint32_t)(lds.chosen[0] >> 32) : 0;
+  wave_sync();  // written again for the next token
+  return true;
+}
+
+// Token t by the G lanes that call it; its experts are counted in `count`, and
+// left in `local` too where that is given.
+template <bool BF16, int G, int V>
+__device__ __forceinline__ void choose(const Route& r, int64_t t, int32_t* __restrict__ experts, int* count,
+                                       int* local, Candidates* lds) {
+  const int l = threadIdx.x % G;
+  float x[V];
+  uint32_t key[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) x[i] = l + i * G < r.E ? load<BF16>(r.logits, t * r.ld + l + i * G) : -__builtin_inff();
+#pragma unroll
+  for (int i = 0; i < V; ++i) key[i] = key_of(x[i]);
+  constexpr int W = 64 / G;
+  Choice<W> c;
+#pragma unroll
+  for (int w = 0; w < W; ++w) {
+    c.key[w] = 0;
+    c.expert[w] = -1;
+  }
+  uint32_t top = 0;
+  bool done = false;
+  if constexpr (G == 16)
+    if (r.k <= 16) done = select<V>(key, r.k, *lds, c, top);
+  if (!done) top = search<G, V>(key, r.k, c);
+  const float m = top > kNone ? of_key(top) : 0.0f;
   float sum = 0.0f, p[W];
 #pragma unroll
   for (int w = 0; w < W; ++w) {
-    p[w] = expert[w] >= 0 ? expf(of_key(mine[w]) - m) : 0.0f;
+    p[w] = c.expert[w] >= 0 ? expf(of_key(c.key[w]) - m) : 0.0f;
     sum += p[w];
   }
   if (!r.renormalize) {
@@ -201,17 +292,19 @@ __device__ __forceinline__ void choose(const Route& r, int64_t t, int32_t* __res
   for (int w = 0; w < W; ++w) {
     const int j = w * G + l;
     if (j < r.k) {
-      r.gates[t * r.k + j] = expert[w] >= 0 ? p[w] / sum : 0.0f;
-      experts[t * r.k + j] = expert[w];
-      if (local) local[t * r.k + j] = expert[w];
-      if (expert[w] >= 0) atomicAdd(&count[expert[w]], 1);
+      r.gates[t * r.k + j] = c.expert[w] >= 0 ? p[w] / sum : 0.0f;
+      experts[t * r.k + j] = c.expert[w];
+      if (local) local[t * r.k + j] = c.expert[w];
+      if (c.expert[w] >= 0) atomicAdd(&count[c.expert[w]], 1);
     }
   }
 }
 
 // ---- placing ----------------------------------------------------------------
 
+constexpr int kStaged = 4 * kPlace;
 struct PlaceLds {
+  int slots[kStaged];        // a workgroup's experts, where it has no more
   int count[kWaves][kMaxE];  // rows of an expert in a wave's part, then where the next one goes
   int4 all[kPlace], before[kPlace];
   int scan[kWaves];
@@ -228,7 +321,7 @@ __device__ __forceinline__ void add_up(const Sort& s, int b, int nb, PlaceLds& l
   int4 all = make_int4(0, 0, 0, 0), before = all;
   if (q < columns && part < parts) {
     const int4* h = reinterpret_cast<const int4*>(s.hist) + q;
-#pragma unroll 16
+#pragma unroll 32
     for (int i = part; i < nb; i += parts) {
       const int4 v = h[(int64_t)i * columns];
       const int in = i < b ? -1 : 0;
@@ -275,14 +368,26 @@ __device__ __forceinline__ void place(const Sort& s, int b, int nb, const int32_
   const int64_t n = min(s.per_block, s.T - b * s.per_block) * s.k;  // slots of this workgroup
   const int64_t part = (n + kPlace - 1) / kPlace * 64;               // and of a wave
   const int64_t lo = works ? min(n, w * part) : n, hi = min(n, lo + part);
+  // (asked for first, and there when the counts are added up)
+  const bool staged = !ALONE && n <= kStaged;
+  int ahead4[kStaged / kPlace];
+  if (!ALONE) {
+#pragma unroll
+    for (int i = 0; i < kStaged / kPlace; ++i) ahead4[i] = staged && tid + i * kPlace < n ? slots[tid + i * kPlace] : -1;
+  }
   if (works)
     for (int e = tid; e < E; e += kPlace)
 #pragma unroll
       for (int i = 0; i < kWaves; ++i) lds.count[i][e] = 0;
-  if (!ALONE) add_up(s, b, nb, lds);
+  if (!ALONE) {
+    add_up(s, b, nb, lds);
+#pragma unroll
+    for (int i = 0; i < kStaged / kPlace; ++i) lds.slots[tid + i * kPlace] = ahead4[i];
+  }
+  auto slot = [&](int64_t i) { return staged ? lds.slots[i] : slots[i]; };
   __syncthreads();
   for (int64_t i = lo + lane; i < hi; i += 64) {
-    const int e = slots[i];
+    const int e = slot(i);
     if ((unsigned)e < (unsigned)E) atomicAdd(&lds.count[w][e], 1);
   }
   __syncthreads();
@@ -335,7 +440,7 @@ __device__ __forceinline__ void place(const Sort& s, int b, int nb, const int32_
   const int bits = 32 - __builtin_clz(E);  // E <= 2^bits - 1 tells an empty slot from the experts
   for (int64_t i0 = lo; i0 < hi; i0 += 64) {
     const int64_t i = i0 + lane;
-    int e = i < hi ? slots[i] : -1;
+    int e = i < hi ? slot(i) : -1;
     if ((unsigned)e >= (unsigned)E) e = E;
     uint64_t same = ~0ull;
     for (int j = 0; j < bits; ++j) {
@@ -369,8 +474,10 @@ __global__ __launch_bounds__(kThreads) void route_kernel(Route r, Sort s) {
   for (int e = threadIdx.x; e < r.E; e += kThreads) count[e] = 0;
   __syncthreads();
   const int64_t end = min(r.T, (int64_t)(blockIdx.x + 1) * s.per_block);
+  __shared__ Candidates candidates[G == 16 ? kGroups : 1];
+  Candidates* own = G == 16 ? &candidates[threadIdx.x / 16] : nullptr;
   for (int64_t t = (int64_t)blockIdx.x * s.per_block + threadIdx.x / G; t < end; t += kGroups)
-    choose<BF16, G, V>(r, t, s.p.experts, count, ALONE ? slots : nullptr);
+    choose<BF16, G, V>(r, t, s.p.experts, count, ALONE ? slots : nullptr, own);
   __syncthreads();
   if constexpr (ALONE) {
     __shared__ PlaceLds lds;
@@ -431,7 +538,7 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const float* __rest
 #pragma unroll
     for (int i = 0; i < V; ++i) top = max(top, key_of(x[i]));
     top = max_of<G>(top);
-    if (top != 0) {
+    if (top > kNone) {
       const float m = of_key(top);
       float sum = 0.0f;
 #pragma unroll

@@ -25,7 +25,12 @@ using fp8blk::u32x4;
 namespace {
 
 constexpr int kMaxThreads = 1024, kMaxWaves = kMaxThreads / 64;
-constexpr int kSlots = 8;  // slots whose rows are in flight at a time
+constexpr int kMaxSlots = 8;  // slots whose rows are in flight at a time
+// Routed rows that do not fit the last-level cache (256 MiB) are read and
+// written non-temporally: combining 470 MB 91 us against 105, 268 MB 55 against
+// 64, but 67 MB 21 against 18 and 59 MB, which the products before it left
+// there, no faster.
+constexpr int64_t kCache = (int64_t)1 << 28;
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t row_at(const void* p, int64_t offset, int64_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(static_cast<char*>(const_cast<void*>(p)) + offset, 0, (int)(uint32_t)bytes,
@@ -41,7 +46,7 @@ struct Raw {
   static constexpr int kWords = C == 1 ? 1 : C * kSize<BF16> / 4;
   uint32_t w[kWords];
 };
-template <bool BF16, int C>
+template <bool BF16, int C, bool NT = false>
 __device__ __forceinline__ Raw<BF16, C> load(__amdgpu_buffer_rsrc_t r, int64_t c) {
   Raw<BF16, C> v;
   const uint32_t at = (uint32_t)c * kSize<BF16>;
@@ -51,14 +56,14 @@ __device__ __forceinline__ Raw<BF16, C> load(__amdgpu_buffer_rsrc_t r, int64_t c
   } else {
 #pragma unroll
     for (int q = 0; q < Raw<BF16, C>::kWords / 4; ++q) {
-      const auto u = __builtin_amdgcn_raw_buffer_load_b128(r, at + 16 * q, 0, 0);
+      const auto u = __builtin_amdgcn_raw_buffer_load_b128(r, at + 16 * q, 0, NT ? 2 : 0);
 #pragma unroll
       for (int i = 0; i < 4; ++i) v.w[4 * q + i] = u[i];
     }
   }
   return v;
 }
-template <bool BF16, int C>
+template <bool BF16, int C, bool NT = false>
 __device__ __forceinline__ void store(__amdgpu_buffer_rsrc_t r, int64_t c, const Raw<BF16, C>& v) {
   const uint32_t at = (uint32_t)c * kSize<BF16>;
   if constexpr (C == 1) {
@@ -70,7 +75,7 @@ __device__ __forceinline__ void store(__amdgpu_buffer_rsrc_t r, int64_t c, const
 #pragma unroll
     for (int q = 0; q < Raw<BF16, C>::kWords / 4; ++q)
       __builtin_amdgcn_raw_buffer_store_b128(u32x4{v.w[4 * q], v.w[4 * q + 1], v.w[4 * q + 2], v.w[4 * q + 3]}, r,
-                                             at + 16 * q, 0, 0);
+                                             at + 16 * q, 0, NT ? 2 : 0);
   }
 }
 template <bool BF16, int C>
@@ -119,7 +124,7 @@ __device__ __forceinline__ void columns(int64_t N, F whole, G single) {
 template <bool BF16, int C>
 constexpr int kPieces = !BF16 && C == 8 ? 1 : 2;
 
-template <bool BF16, int C>
+template <bool BF16, int C, bool NT>
 __global__ __launch_bounds__(kMaxThreads) void gather_kernel(const void* x, int64_t ld_x, int64_t N,
                                                              const int32_t* __restrict__ token_rows, int k, int64_t R,
                                                              void* rows, int64_t ld_r) {
@@ -135,7 +140,7 @@ __global__ __launch_bounds__(kMaxThreads) void gather_kernel(const void* x, int6
       const int64_t r = row_of(token_rows, t * k + j, R);
       const __amdgpu_buffer_rsrc_t to = row_at(rows, r * ld_r * S, r >= 0 ? N / CC * CC * S : 0);
 #pragma unroll
-      for (int u = 0; u < UU; ++u) store<BF16, CC>(to, c + u * step, v[u]);
+      for (int u = 0; u < UU; ++u) store<BF16, CC, NT>(to, c + u * step, v[u]);
     }
   };
   using One = std::integral_constant<int, 1>;
@@ -144,7 +149,8 @@ __global__ __launch_bounds__(kMaxThreads) void gather_kernel(const void* x, int6
       [&](int64_t c) { go(One{}, One{}, c, 0); });
 }
 
-template <bool YB, bool OB, int C>
+// S: slots whose rows are in flight at a time.
+template <bool YB, bool OB, int C, bool NT, int S>
 __global__ __launch_bounds__(kMaxThreads) void combine_kernel(const void* y, int64_t ld_y, int64_t R, int64_t N,
                                                               const int32_t* __restrict__ token_rows,
                                                               const float* __restrict__ gates, int k, void* out,
@@ -158,19 +164,19 @@ __global__ __launch_bounds__(kMaxThreads) void combine_kernel(const void* y, int
     for (int u = 0; u < UU; ++u)
 #pragma unroll
       for (int i = 0; i < CC; ++i) acc[u][i] = 0.0f;
-    for (int j0 = 0; j0 < k; j0 += kSlots) {
-      Raw<YB, CC> v[kSlots][UU];
-      float g[kSlots];
+    for (int j0 = 0; j0 < k; j0 += S) {
+      Raw<YB, CC> v[S][UU];
+      float g[S];
 #pragma unroll
-      for (int j = 0; j < kSlots; ++j) {
+      for (int j = 0; j < S; ++j) {
         const int64_t r = j0 + j < k ? row_of(token_rows, t * k + j0 + j, R) : -1;
         g[j] = r < 0 ? 0.0f : gates ? gates[t * k + j0 + j] : 1.0f;
         const __amdgpu_buffer_rsrc_t from = row_at(y, r * ld_y * kSize<YB>, r >= 0 ? N / CC * CC * kSize<YB> : 0);
 #pragma unroll
-        for (int u = 0; u < UU; ++u) v[j][u] = load<YB, CC>(from, c + u * step);
+        for (int u = 0; u < UU; ++u) v[j][u] = load<YB, CC, NT>(from, c + u * step);
       }
 #pragma unroll
-      for (int j = 0; j < kSlots; ++j)
+      for (int j = 0; j < S; ++j)
 #pragma unroll
         for (int u = 0; u < UU; ++u)
 #pragma unroll
@@ -178,7 +184,7 @@ __global__ __launch_bounds__(kMaxThreads) void combine_kernel(const void* y, int
     }
     const __amdgpu_buffer_rsrc_t to = row_at(out, t * ld_o * kSize<OB>, N / CC * CC * kSize<OB>);
 #pragma unroll
-    for (int u = 0; u < UU; ++u) store<OB, CC>(to, c + u * step, raw<OB, CC>(acc[u]));
+    for (int u = 0; u < UU; ++u) store<OB, CC, NT>(to, c + u * step, raw<OB, CC>(acc[u]));
   };
   using One = std::integral_constant<int, 1>;
   columns<C, U>(
@@ -186,20 +192,20 @@ __global__ __launch_bounds__(kMaxThreads) void combine_kernel(const void* y, int
       [&](int64_t c) { go(One{}, One{}, c, 0); });
 }
 
-template <bool YB, bool OB, int C>
+template <bool YB, bool OB, int C, bool NT, int S>
 __global__ __launch_bounds__(kMaxThreads) void combine_backward_kernel(
     const void* dout, int64_t ld_o, const void* y, int64_t ld_y, int64_t R, int64_t N,
     const int32_t* __restrict__ token_rows, const float* __restrict__ gates, int k, void* dy, int64_t ld_dy,
     float* __restrict__ dgates) {
   constexpr int U = kPieces<YB, C>;
-  __shared__ float part[kMaxWaves][kSlots];
+  __shared__ float part[kMaxWaves][S];
   const int64_t t = blockIdx.x;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, waves = blockDim.x >> 6;
-  for (int j0 = 0; j0 < k; j0 += kSlots) {
-    int64_t r[kSlots];
-    float g[kSlots], sum[kSlots];
+  for (int j0 = 0; j0 < k; j0 += S) {
+    int64_t r[S];
+    float g[S], sum[S];
 #pragma unroll
-    for (int j = 0; j < kSlots; ++j) {
+    for (int j = 0; j < S; ++j) {
       r[j] = j0 + j < k ? row_of(token_rows, t * k + j0 + j, R) : -1;
       g[j] = r[j] < 0 ? 0.0f : gates[t * k + j0 + j];
       sum[j] = 0.0f;
@@ -209,16 +215,16 @@ __global__ __launch_bounds__(kMaxThreads) void combine_backward_kernel(
       const int64_t bytes = N / CC * CC * kSize<YB>;
       const __amdgpu_buffer_rsrc_t grad = row_at(dout, t * ld_o * kSize<OB>, N / CC * CC * kSize<OB>);
       Raw<OB, CC> d[UU];
-      Raw<YB, CC> v[kSlots][UU];
+      Raw<YB, CC> v[S][UU];
 #pragma unroll
       for (int u = 0; u < UU; ++u) d[u] = load<OB, CC>(grad, c + u * step);
 #pragma unroll
-      for (int j = 0; j < kSlots; ++j)
+      for (int j = 0; j < S; ++j)
 #pragma unroll
         for (int u = 0; u < UU; ++u)
-          v[j][u] = load<YB, CC>(row_at(y, r[j] * ld_y * kSize<YB>, r[j] >= 0 ? bytes : 0), c + u * step);
+          v[j][u] = load<YB, CC, NT>(row_at(y, r[j] * ld_y * kSize<YB>, r[j] >= 0 ? bytes : 0), c + u * step);
 #pragma unroll
-      for (int j = 0; j < kSlots; ++j)
+      for (int j = 0; j < S; ++j)
 #pragma unroll
         for (int u = 0; u < UU; ++u) {
           float o[CC];
@@ -229,7 +235,7 @@ __global__ __launch_bounds__(kMaxThreads) void combine_backward_kernel(
             // (a slot without a row has zeros here, whatever dout holds)
             sum[j] = __builtin_fmaf(r[j] >= 0 ? di : 0.0f, value<YB, CC>(v[j][u], i), sum[j]);
           }
-          store<YB, CC>(row_at(dy, r[j] * ld_dy * kSize<YB>, r[j] >= 0 ? bytes : 0), c + u * step, raw<YB, CC>(o));
+          store<YB, CC, NT>(row_at(dy, r[j] * ld_dy * kSize<YB>, r[j] >= 0 ? bytes : 0), c + u * step, raw<YB, CC>(o));
         }
     };
     using One = std::integral_constant<int, 1>;
@@ -238,13 +244,13 @@ __global__ __launch_bounds__(kMaxThreads) void combine_backward_kernel(
         [&](int64_t c, int64_t step) { go(std::integral_constant<int, C>{}, std::integral_constant<int, U>{}, c, step); },
         [&](int64_t c) { go(One{}, One{}, c, 0); });
 #pragma unroll
-    for (int j = 0; j < kSlots; ++j) {
+    for (int j = 0; j < S; ++j) {
 #pragma unroll
       for (int m = 32; m >= 1; m >>= 1) sum[j] += __shfl_xor(sum[j], m);
       if (lane == 0) part[w][j] = sum[j];
     }
     __syncthreads();
-    if (threadIdx.x < kSlots && j0 + (int)threadIdx.x < k) {
+    if (threadIdx.x < S && j0 + (int)threadIdx.x < k) {
       float s = 0.0f;
       for (int i = 0; i < waves; ++i) s += part[i][threadIdx.x];
       dgates[t * k + j0 + threadIdx.x] = s;
@@ -263,46 +269,60 @@ unsigned threads_of(int64_t N, int C) {
   return (unsigned)std::min<int64_t>(kMaxThreads, std::max<int64_t>(64, (pieces + 63) / 64 * 64));
 }
 
-// f(y is bf16, out is bf16, columns of a piece)
+// f(y is bf16, out is bf16, columns of a piece, rows past the cache)
 template <class F>
-int by_type(bool yb, bool ob, bool w, F f) {
-  auto with = [&](auto y, auto o) {
-    constexpr int C = decltype(y)::value || decltype(o)::value ? 8 : 4;
-    return w ? f(y, o, std::integral_constant<int, C>{}) : f(y, o, std::integral_constant<int, 1>{});
-  };
+int by_type(bool yb, bool ob, bool w, int64_t row_bytes, F f) {
   using T = std::true_type;
   using N = std::false_type;
+  auto with = [&](auto y, auto o) {
+    constexpr int C = decltype(y)::value || decltype(o)::value ? 8 : 4;
+    if (!w) return f(y, o, std::integral_constant<int, 1>{}, N{});
+    return row_bytes >= kCache ? f(y, o, std::integral_constant<int, C>{}, T{}) : f(y, o, std::integral_constant<int, C>{}, N{});
+  };
   return yb ? (ob ? with(T{}, T{}) : with(T{}, N{})) : (ob ? with(N{}, T{}) : with(N{}, N{}));
 }
+// f(slots at a time)
+template <class F>
+int by_slots(int k, F f) {
+  if (k <= 2) return f(std::integral_constant<int, 2>{});
+  if (k <= 4) return f(std::integral_constant<int, 4>{});
+  return f(std::integral_constant<int, kMaxSlots>{});
+}
+int64_t row_bytes(const Mat& y, int64_t rows, int64_t N) { return rows * N * (y.bf16 ? 2 : 4); }
 
 }  // namespace
 
 int launch_gather(const Mat& x, int64_t T, int64_t N, const int32_t* token_rows, int k, int64_t R, const Mat& rows,
                   hipStream_t s) {
-  return by_type(x.bf16, x.bf16, wide(x) && wide(rows), [&](auto b, auto, auto c) {
-    hipLaunchKernelGGL((gather_kernel<b.value, c.value>), dim3((unsigned)T), dim3(threads_of(N, c.value)), 0, s, x.p, x.ld,
-                       N, token_rows, k, R, rows.p, rows.ld);
+  return by_type(x.bf16, x.bf16, wide(x) && wide(rows), row_bytes(x, T * k, N), [&](auto b, auto, auto c, auto nt) {
+    hipLaunchKernelGGL((gather_kernel<b.value, c.value, nt.value>), dim3((unsigned)T), dim3(threads_of(N, c.value)), 0, s,
+                       x.p, x.ld, N, token_rows, k, R, rows.p, rows.ld);
     return check_launch();
   });
 }
 
 int launch_combine(const Mat& y, int64_t R, int64_t N, const int32_t* token_rows, const float* gates, int64_t T, int k,
                    const Mat& out, hipStream_t s) {
-  return by_type(y.bf16, out.bf16, wide(y) && wide(out), [&](auto yb, auto ob, auto c) {
-    hipLaunchKernelGGL((combine_kernel<yb.value, ob.value, c.value>), dim3((unsigned)T), dim3(threads_of(N, c.value)), 0, s,
-                       y.p, y.ld, R, N, token_rows, gates, k, out.p, out.ld);
-    return check_launch();
+  return by_type(y.bf16, out.bf16, wide(y) && wide(out), row_bytes(y, T * k, N), [&](auto yb, auto ob, auto c, auto nt) {
+    return by_slots(k, [&](auto S) {
+      hipLaunchKernelGGL((combine_kernel<yb.value, ob.value, c.value, nt.value, S.value>), dim3((unsigned)T),
+                         dim3(threads_of(N, c.value)), 0, s, y.p, y.ld, R, N, token_rows, gates, k, out.p, out.ld);
+      return check_launch();
+    });
   });
 }
 
 int launch_combine_backward(const Mat& dout, const Mat& y, int64_t R, int64_t N, const int32_t* token_rows,
                             const float* gates, int64_t T, int k, const Mat& dy, float* dgates, hipStream_t s) {
-  return by_type(y.bf16, dout.bf16, wide(y) && wide(dy) && wide(dout), [&](auto yb, auto ob, auto c) {
-    hipLaunchKernelGGL((combine_backward_kernel<yb.value, ob.value, c.value>), dim3((unsigned)T),
-                       dim3(threads_of(N, c.value)), 0, s, dout.p, dout.ld, y.p, y.ld, R, N, token_rows, gates, k, dy.p,
-                       dy.ld, dgates);
-    return check_launch();
-  });
+  return by_type(y.bf16, dout.bf16, wide(y) && wide(dy) && wide(dout), row_bytes(y, T * k, N),
+                 [&](auto yb, auto ob, auto c, auto nt) {
+                   return by_slots(k, [&](auto S) {
+                     hipLaunchKernelGGL((combine_backward_kernel<yb.value, ob.value, c.value, nt.value, S.value>),
+                                        dim3((unsigned)T), dim3(threads_of(N, c.value)), 0, s, dout.p, dout.ld, y.p, y.ld,
+                                        R, N, token_rows, gates, k, dy.p, dy.ld, dgates);
+                     return check_launch();
+                   });
+                 });
 }
 
 }  // namespace fp8moe
