@@ -24,61 +24,86 @@ namespace {
 
 constexpr int kThreads = 256, kWaves = kThreads / 64;
 
-// W values of a row from column c on, as fp32; columns from K on are 0.
-template <bool BF16, int W>
-__device__ __forceinline__ void load(const void* row, int64_t c, float (&v)[W]) {
+__device__ __forceinline__ u32x4 words(const void* p) {
+  struct __attribute__((packed, aligned(4))) Words { u32x4 w; };  // rows start on 4 bytes
+  return static_cast<const Words*>(p)->w;
+}
+
+// W values of a row of K from column c < K on, as fp32; columns past the last
+// are 0.  TAIL: there may be such columns (the branch costs 2 us of 17.5 at
+// 4096 x 7168).
+template <bool BF16, int W, bool TAIL>
+__device__ __forceinline__ void load(const void* row, int64_t c, int64_t K, float (&v)[W]) {
+  auto one = [&](int64_t at) {
+    return BF16 ? fp8blk::bf16_bits_to_f32(static_cast<const uint16_t*>(row)[at]) : static_cast<const float*>(row)[at];
+  };
   if constexpr (W == 1) {
-    v[0] = BF16 ? fp8blk::bf16_bits_to_f32(static_cast<const uint16_t*>(row)[c]) : static_cast<const float*>(row)[c];
-  } else if constexpr (BF16) {
-    static_assert(W == 8, "16 bytes");
-    const u32x4 u = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(row) + c);
+    v[0] = one(c);
+  } else if (!TAIL || c + W <= K) {
+    static_assert(W == 8, "a piece");
+    const char* p = static_cast<const char*>(row) + c * (BF16 ? 2 : 4);
+    if constexpr (BF16) {
+      const u32x4 u = words(p);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(i & 1 ? u[i / 2] & 0xffff0000u : u[i / 2] << 16);
+      for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(i & 1 ? u[i / 2] & 0xffff0000u : u[i / 2] << 16);
+    } else {
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const u32x4 u = words(p + 16 * q);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[4 * q + i] = __uint_as_float(u[i]);
+      }
+    }
   } else {
 #pragma unroll
-    for (int q = 0; q < W / 4; ++q) {
-      const u32x4 u = *reinterpret_cast<const u32x4*>(static_cast<const float*>(row) + c + 4 * q);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[4 * q + i] = __uint_as_float(u[i]);
-    }
+    for (int i = 0; i < W; ++i) v[i] = c + i < K ? one(c + i) : 0.0f;
   }
 }
 
-template <int W>
-__device__ __forceinline__ void quantise(const float (&v)[W], const BlockDivisor& b, bool finite, int8_t* out) {
+template <int W, bool TAIL>
+__device__ __forceinline__ void quantise(const float (&v)[W], const BlockDivisor& b, bool finite, int8_t* out, int64_t c,
+                                         int64_t K) {
   float q[W];
   divide_block<W>(v, q, b);
-  int c[W];
+  int n[W];
 #pragma unroll
-  for (int i = 0; i < W; ++i) c[i] = finite ? (int)rintf(q[i]) : 0;
+  for (int i = 0; i < W; ++i) n[i] = finite ? (int)rintf(q[i]) : 0;
   if constexpr (W == 1) {
-    out[0] = (int8_t)c[0];
-  } else {
+    out[c] = (int8_t)n[0];
+  } else if (!TAIL || c + W <= K) {
     u32x2 o;
 #pragma unroll
     for (int h = 0; h < 2; ++h)
-      o[h] = (c[4 * h] & 0xff) | (c[4 * h + 1] & 0xff) << 8 | (c[4 * h + 2] & 0xff) << 16 |
-             (uint32_t)c[4 * h + 3] << 24;
-    *reinterpret_cast<u32x2*>(out) = o;
+      o[h] = (n[4 * h] & 0xff) | (n[4 * h + 1] & 0xff) << 8 | (n[4 * h + 2] & 0xff) << 16 |
+             (uint32_t)n[4 * h + 3] << 24;
+    *reinterpret_cast<u32x2*>(out + c) = o;
+  } else {
+#pragma unroll
+    for (int i = 0; i < W; ++i)
+      if (c + i < K) out[c + i] = (int8_t)n[i];
   }
 }
 
-// One workgroup per row; the first H pieces of W values a thread stay in
-// registers, longer rows are read again.
-template <bool BF16, int W, int H>
-__global__ __launch_bounds__(kThreads) void quant_kernel(const void* x, int64_t K, int64_t ld_x, int8_t* codes,
-                                                         int64_t ld_c, float* scales) {
-  __shared__ uint32_t part[kWaves];
-  const int64_t m = blockIdx.x;
+// LANES threads to a row (rows of fewer than a workgroup's threads share one);
+// the first H pieces of W values a thread stay in registers, longer rows are
+// read again.
+template <bool BF16, int W, int LANES, int H, bool TAIL>
+__global__ __launch_bounds__(LANES < kThreads ? kThreads : LANES) void quant_kernel(const void* x, int64_t M, int64_t K,
+                                                                                    int64_t ld_x, int8_t* codes,
+                                                                                    int64_t ld_c, float* scales) {
+  constexpr int kRows = LANES < kThreads ? kThreads / LANES : 1;
+  const int lane = threadIdx.x % LANES;
+  const int64_t m = (int64_t)blockIdx.x * kRows + threadIdx.x / LANES;
+  if (m >= M) return;  // whole rows of lanes: no barrier follows where a workgroup has several
   const char* row = static_cast<const char*>(x) + m * ld_x * (BF16 ? 2 : 4);
   int8_t* out = codes + m * ld_c;
-  const int64_t c0 = (int64_t)threadIdx.x * W;
-  constexpr int64_t kStep = (int64_t)kThreads * W;
+  const int64_t c0 = (int64_t)lane * W;
+  constexpr int64_t kStep = (int64_t)LANES * W;
   float v[H][W];
 #pragma unroll
   for (int h = 0; h < H; ++h) {
     if (c0 + h * kStep < K) {
-      load<BF16, W>(row, c0 + h * kStep, v[h]);
+      load<BF16, W, TAIL>(row, c0 + h * kStep, K, v[h]);
     } else {
 #pragma unroll
       for (int i = 0; i < W; ++i) v[h][i] = 0.0f;
@@ -93,78 +118,107 @@ __global__ __launch_bounds__(kThreads) void quant_kernel(const void* x, int64_t 
   for (int h = 0; h < H; ++h) see(v[h]);
   for (int64_t c = c0 + H * kStep; c < K; c += kStep) {
     float u[W];
-    load<BF16, W>(row, c, u);
+    load<BF16, W, TAIL>(row, c, K, u);
     see(u);
   }
+  top = __float_as_uint(fp8blk::row16_max_nonneg(__uint_as_float(top)));
+  if constexpr (LANES >= 64) {
+    top = max(top, (uint32_t)__shfl_xor((int)top, 16));
+    top = max(top, (uint32_t)__shfl_xor((int)top, 32));
+  }
+  if constexpr (LANES > 64) {
+    __shared__ uint32_t part[LANES / 64];
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = top;
+    __syncthreads();
 #pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d));
-  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = top;
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < kWaves; ++i) top = max(top, part[i]);
+    for (int i = 0; i < LANES / 64; ++i) top = max(top, part[i]);
+  }
   const float amax = __uint_as_float(top);
   const bool finite = top < 0x7f800000u;
   BlockDivisor b;
   b.d = top == 0 ? 1.0f : finite ? fmaxf(amax / 127.0f, 0x1.0p-126f) : amax / 127.0f;
   b.y = 1.0f / b.d;
   b.fast = amax >= 0x1.0p-62f;
-  if (threadIdx.x == 0) scales[m] = b.d;
+  if (lane == 0) scales[m] = b.d;
 #pragma unroll
   for (int h = 0; h < H; ++h)
-    if (c0 + h * kStep < K) quantise<W>(v[h], b, finite, out + c0 + h * kStep);
+    if (c0 + h * kStep < K) quantise<W, TAIL>(v[h], b, finite, out, c0 + h * kStep, K);
   for (int64_t c = c0 + H * kStep; c < K; c += kStep) {
     float u[W];
-    load<BF16, W>(row, c, u);
-    quantise<W>(u, b, finite, out + c);
+    load<BF16, W, TAIL>(row, c, K, u);
+    quantise<W, TAIL>(u, b, finite, out, c, K);
   }
 }
 
-// One thread per 16 bytes of the packed layout.
+// One wave per chunk of the packed layout.  A lane's 16 codes are one load where
+// rows start on 16 bytes.
+template <bool WIDE>
 __global__ __launch_bounds__(kThreads) void pack_kernel(const int8_t* __restrict__ w, int64_t N, int64_t K, int64_t ld,
                                                         int64_t stride, int64_t panels, int64_t chunks, int64_t G,
                                                         int8_t* __restrict__ out) {
   const int64_t per = panels * chunks;  // chunks of one matrix
-  for (int64_t c = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6); c < G * per;
-       c += (int64_t)gridDim.x * kWaves) {
+  const int lane = threadIdx.x & 63;
+  for (int64_t c = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6); c < G * per; c += (int64_t)gridDim.x * kWaves) {
     const int64_t g = c / per, in = c - g * per;
-    const int64_t kc = in / panels, p = in - kc * panels;
-    const int lane = threadIdx.x & 63;
+    // panels of 16 rows in turn for a run of 8 chunks (512 codes of a row), so
+    // that whole lines are read together
+    const int64_t run = in / (8 * panels), at = in - run * 8 * panels, wide = min((int64_t)8, chunks - 8 * run);
+    const int64_t p = at / wide, kc = 8 * run + at - p * wide;
     const int64_t n = 16 * p + (lane & 15), k0 = 64 * kc + 16 * (lane >> 4);
     const int8_t* row = w + g * stride + n * ld + k0;
-    uint32_t v[4] = {0, 0, 0, 0};
+    u32x4 v = {0, 0, 0, 0};
     if (n < N) {
+      if (WIDE && k0 + 16 <= K) {
+        v = *reinterpret_cast<const u32x4*>(row);
+      } else {
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (k0 + i < K) v[i / 4] |= (uint32_t)(uint8_t)row[i] << (8 * (i & 3));
+        for (int i = 0; i < 16; ++i)
+          if (k0 + i < K) v[i / 4] |= (uint32_t)(uint8_t)row[i] << (8 * (i & 3));
+      }
     }
-    *reinterpret_cast<u32x4*>(out + c * 1024 + 16 * lane) = u32x4{v[0], v[1], v[2], v[3]};
+    *reinterpret_cast<u32x4*>(out + (g * per + kc * panels + p) * 1024 + 16 * lane) = v;
   }
 }
 
 }  // namespace
 
 int launch_quant(const Mat& x, int64_t M, int64_t K, int8_t* codes, int64_t ld_c, float* scales, hipStream_t s) {
-  const bool wide = reinterpret_cast<uintptr_t>(x.p) % 16 == 0 && x.ld % (x.bf16 ? 8 : 4) == 0 && K % 8 == 0 &&
+  const bool wide = reinterpret_cast<uintptr_t>(x.p) % 4 == 0 && x.ld * (x.bf16 ? 2 : 4) % 4 == 0 &&
                     reinterpret_cast<uintptr_t>(codes) % 8 == 0 && ld_c % 8 == 0;
-  auto go = [&](auto b, auto w) {
-    constexpr int W = decltype(w)::value;
-    constexpr int H = W == 1 ? 8 : 4;
-    hipLaunchKernelGGL((quant_kernel<decltype(b)::value, W, H>), dim3((unsigned)M), dim3(kThreads), 0, s, x.p, K, x.ld,
-                       codes, ld_c, scales);
+  auto go = [&](auto b, auto w, auto lanes, auto h) {
+    constexpr int W = decltype(w)::value, LANES = decltype(lanes)::value, H = decltype(h)::value;
+    constexpr int kRows = LANES < kThreads ? kThreads / LANES : 1;
+    auto kernel = K % W == 0 ? &quant_kernel<decltype(b)::value, W, LANES, H, false>
+                             : &quant_kernel<decltype(b)::value, W, LANES, H, true>;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)((M + kRows - 1) / kRows)), dim3(kRows > 1 ? kThreads : LANES), 0, s, x.p,
+                       M, K, x.ld, codes, ld_c, scales);
     return check_launch();
   };
-  using W8 = std::integral_constant<int, 8>;
-  using W1 = std::integral_constant<int, 1>;
-  if (x.bf16) return wide ? go(std::true_type{}, W8{}) : go(std::true_type{}, W1{});
-  return wide ? go(std::false_type{}, W8{}) : go(std::false_type{}, W1{});
+  // Two pieces of a row to a thread, as few threads as that takes: 65536 rows of
+  // 128 take 7.3 us with 16 lanes each, 57 with 256; 128 rows of 20000 4.9 us
+  // with 1024, 11.6 with 256.
+  auto by_length = [&](auto b) {
+    using std::integral_constant;
+    using W8 = integral_constant<int, 8>;
+    using Two = integral_constant<int, 2>;
+    if (!wide) return go(b, integral_constant<int, 1>{}, integral_constant<int, 256>{}, integral_constant<int, 8>{});
+    if (K <= 16 * 16) return go(b, W8{}, integral_constant<int, 16>{}, Two{});
+    if (K <= 64 * 16) return go(b, W8{}, integral_constant<int, 64>{}, Two{});
+    if (K <= 256 * 16) return go(b, W8{}, integral_constant<int, 256>{}, Two{});
+    if (K <= 512 * 16) return go(b, W8{}, integral_constant<int, 512>{}, Two{});
+    return go(b, W8{}, integral_constant<int, 1024>{}, Two{});
+  };
+  return x.bf16 ? by_length(std::true_type{}) : by_length(std::false_type{});
 }
 
 int launch_pack(const int8_t* w, int64_t G, int64_t N, int64_t K, int64_t ld, int64_t stride, int8_t* out,
                 hipStream_t s) {
   const int64_t panels = (N + 15) / 16, chunks = (K + 127) / 128 * 2;
   const int64_t need = (G * panels * chunks + kWaves - 1) / kWaves;
-  hipLaunchKernelGGL(pack_kernel, dim3((unsigned)(need < 65536 ? need : 65536)), dim3(kThreads), 0, s, w, N, K, ld,
-                     stride, panels, chunks, G, out);
+  const bool wide = reinterpret_cast<uintptr_t>(w) % 16 == 0 && ld % 16 == 0 && stride % 16 == 0;
+  auto kernel = wide ? &pack_kernel<true> : &pack_kernel<false>;
+  hipLaunchKernelGGL(kernel, dim3((unsigned)(need < 65536 ? need : 65536)), dim3(kThreads), 0, s, w, N, K, ld, stride,
+                     panels, chunks, G, out);
   return check_launch();
 }
 
