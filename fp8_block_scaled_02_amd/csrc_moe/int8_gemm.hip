@@ -38,35 +38,53 @@ __device__ __forceinline__ v4i mfma(v4i w, v4i x, v4i c) {
 // time, four (8 bytes of bf16, 16 of fp32), or 16 bytes of either.
 enum class Stores { values, fours, lines };
 
-// Four columns n .. n+3 of row y (those below N), from their sums.
-template <bool BF16>
-__device__ __forceinline__ void store4(void* y, int64_t row, int64_t n, int64_t N, const v4i acc, float sa,
-                                       const float* __restrict__ sw, const float* __restrict__ bias, Stores store) {
-  float v[4];
+// The scales and biases of four columns n .. n+3 (those past the last are the
+// last one's).
+struct Four {
+  float scale[4], bias[4];
+};
+__device__ __forceinline__ Four four(const float* __restrict__ sw, const float* __restrict__ bias, int64_t n, int64_t N) {
+  Four f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int64_t c = min(n + i, N - 1);
-    v[i] = (float)acc[i] * (sa * sw[c]);
-    if (bias) v[i] += bias[c];
+    f.scale[i] = sw[c];
+    f.bias[i] = bias ? bias[c] : 0.0f;
   }
+  return f;
+}
+// One column's value from its sum.  (Without a bias nothing is added: -0 stays.)
+__device__ __forceinline__ float finish(int sum, float sa, float sw, float bias, bool biased) {
+  const float v = (float)sum * (sa * sw);
+  return biased ? v + bias : v;
+}
+
+// Four columns n .. n+3 of row y (those below N), from their sums.
+template <bool BF16>
+__device__ __forceinline__ void store4(const Product& p, int64_t row, int64_t n, const v4i acc, float sa, const Four& f,
+                                       Stores store) {
+  float v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = finish(acc[i], sa, f.scale[i], f.bias[i], p.bias != nullptr);
+  const bool whole = store != Stores::values && n + 4 <= p.N;
   if constexpr (BF16) {
-    uint16_t* p = static_cast<uint16_t*>(y) + row + n;
-    if (store != Stores::values && n + 4 <= N) {
-      *reinterpret_cast<u32x2*>(p) = u32x2{f32_to_bf16_bits(v[0]) | f32_to_bf16_bits(v[1]) << 16,
+    uint16_t* y = static_cast<uint16_t*>(p.y.p) + row + n;
+    if (whole) {
+      *reinterpret_cast<u32x2*>(y) = u32x2{f32_to_bf16_bits(v[0]) | f32_to_bf16_bits(v[1]) << 16,
                                            f32_to_bf16_bits(v[2]) | f32_to_bf16_bits(v[3]) << 16};
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (n + i < N) p[i] = (uint16_t)f32_to_bf16_bits(v[i]);
+        if (n + i < p.N) y[i] = (uint16_t)f32_to_bf16_bits(v[i]);
     }
   } else {
-    float* p = static_cast<float*>(y) + row + n;
-    if (store != Stores::values && n + 4 <= N) {
-      *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    float* y = static_cast<float*>(p.y.p) + row + n;
+    if (whole) {
+      *reinterpret_cast<float4*>(y) = make_float4(v[0], v[1], v[2], v[3]);
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (n + i < N) p[i] = v[i];
+        if (n + i < p.N) y[i] = v[i];
     }
   }
 }
@@ -106,6 +124,12 @@ __device__ __forceinline__ void stream_tile(const Product& p, const Rows& r, int
 #pragma unroll
   for (int j = 0; j < P; ++j) woff[j] = (uint32_t)(min(panel0 + j, panels - 1) * 1024) + 16 * lane;
   for (int i = threadIdx.x; i < MI * P * 256; i += kStreamThreads) sums[i] = 0;
+  // what the wave's first part of the output needs is asked for before the
+  // products (a small one's time is that of a few loads that wait for another)
+  auto scales_of = [&](int f) { return four(r.sw, p.bias, (panel0 + f % P) * 16 + 4 * g, p.N); };
+  auto row_scale = [&](int f) { return p.sa[r.token(16 * (f / P) + l16)]; };
+  Four scales = scales_of(min(wave, MI * P - 1));
+  float sa = row_scale(min(wave, MI * P - 1));
   v4i acc[MI][P];
 #pragma unroll
   for (int i = 0; i < MI; ++i)
@@ -162,7 +186,11 @@ __device__ __forceinline__ void stream_tile(const Product& p, const Rows& r, int
       v4i v;
 #pragma unroll
       for (int q = 0; q < 4; ++q) v[q] = sums[(f * 4 + q) * 64 + lane];
-      store4<BF16>(p.y.p, (r.m0 + m) * p.y.ld, n, p.N, v, p.sa[r.token(m)], r.sw, p.bias, store);
+      store4<BF16>(p, (r.m0 + m) * p.y.ld, n, v, sa, scales, store);
+    }
+    if (f + kStreamWaves < MI * P) {
+      scales = scales_of(f + kStreamWaves);
+      sa = row_scale(f + kStreamWaves);
     }
   }
 }
@@ -322,24 +350,15 @@ constexpr int kAhead = 2;  // LDS reads ahead of the products: 480 us with 2 to 
 // store instruction fills 64 bytes of a line or more.
 template <int MI, int NJ, bool BF16>
 __device__ __forceinline__ void store_tile(const Product& p, const Rows& r, int i0, int64_t first,
-                                           const v4i (&acc)[MI][NJ], Stores how) {
+                                           const v4i (&acc)[MI][NJ], const Four (&scales)[NJ], const float (&rows)[MI],
+                                           Stores how) {
   static_assert(NJ == 2 || NJ == 4, "transposed by twos or fours");
   const int lane = threadIdx.x & 63, l16 = lane & 15, g = lane >> 4;
   if (first * 16 >= p.N) return;
-  float scale[NJ][4], bias[NJ][4];
-#pragma unroll
-  for (int j = 0; j < NJ; ++j)
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int64_t n = min((first + j) * 16 + 4 * g + q, p.N - 1);
-      scale[j][q] = r.sw[n];
-      bias[j][q] = p.bias ? p.bias[n] : 0.0f;
-    }
   const bool whole = how == Stores::lines && (first + NJ) * 16 <= p.N;
 #pragma unroll
   for (int i = 0; i < MI; ++i) {
     const int m = i0 + 16 * i + l16;
-    const float sa = p.sa[r.token(m)];
     const int64_t row = (r.m0 + m) * p.y.ld;
     constexpr int D = BF16 ? 2 : 4;  // dwords of four columns
     uint32_t d[NJ][D];
@@ -347,10 +366,8 @@ __device__ __forceinline__ void store_tile(const Product& p, const Rows& r, int 
     for (int j = 0; j < NJ; ++j) {
       float v[4];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        v[q] = (float)acc[i][j][q] * (sa * scale[j][q]);
-        if (p.bias) v[q] += bias[j][q];
-      }
+      for (int q = 0; q < 4; ++q)
+        v[q] = finish(acc[i][j][q], rows[i], scales[j].scale[q], scales[j].bias[q], p.bias != nullptr);
       if constexpr (BF16) {
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
@@ -449,6 +466,18 @@ __device__ __forceinline__ void tile(const Product& p, const Rows& r, int64_t pa
     for (int q = 0; q < C::kA; ++q)
       load_lds(abuf, aoff[q], (uint32_t)(t * kStep), st + 1024 * (wave + C::kWaves * q));
   };
+  // the scales, before the products where there are registers for them (a small
+  // product's time is that of a few loads that wait for another)
+  constexpr bool kEarly = MI * NJ <= 8;
+  Four scales[NJ];
+  float row_scales[MI];
+  auto load_scales = [&] {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) scales[j] = four(r.sw, p.bias, (first + j) * 16 + 4 * g, p.N);
+#pragma unroll
+    for (int i = 0; i < MI; ++i) row_scales[i] = p.sa[r.token(16 * (MI * wm + i) + l16)];
+  };
+  if (kEarly) load_scales();
   v4i acc[MI][NJ];
 #pragma unroll
   for (int i = 0; i < MI; ++i)
@@ -522,7 +551,8 @@ __device__ __forceinline__ void tile(const Product& p, const Rows& r, int64_t pa
   tail(t + 4, st0, w0, st3);
   tail(t + 5, st1, w1, st0);
   wait_loads<0>();
-  store_tile<MI, NJ, BF16>(p, r, 16 * MI * wm, first, acc, store);
+  if (!kEarly) load_scales();
+  store_tile<MI, NJ, BF16>(p, r, 16 * MI * wm, first, acc, scales, row_scales, store);
 }
 
 // Output tile of workgroup `id`: workgroups go round the 8 XCDs in turn, so
