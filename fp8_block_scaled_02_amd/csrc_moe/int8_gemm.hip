@@ -311,13 +311,12 @@ __device__ __forceinline__ void load_lds(__amdgpu_buffer_rsrc_t r, uint32_t off,
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)lds, 16, off, step_off, 0, 0);
 }
 
-// WM x 4 waves, each with 16 MI rows of a and 16 NJ of the weights.
-// SETS sets of weight registers: a step's weights are asked for SETS steps ahead.
-template <int MI_, int WM_, int NJ_, int SETS_ = 2>
+// Four waves, each with all 16 MI rows of a and 16 NJ of the weights.
+template <int MI_, int NJ_>
 struct Cfg {
-  static constexpr int MI = MI_, WM = WM_, NJ = NJ_, SETS = SETS_;
-  static constexpr int kWaves = 4 * WM, kThreads = 64 * kWaves;
-  static constexpr int kRows = 16 * MI * WM, kCols = 64 * NJ;
+  static constexpr int MI = MI_, NJ = NJ_;
+  static constexpr int kWaves = 4, kThreads = 64 * kWaves;
+  static constexpr int kRows = 16 * MI, kCols = 64 * NJ;
   static constexpr int kA = kRows / 8 / kWaves;  // pieces of 8 rows of a that a wave brings in a step
   static_assert(kRows % (8 * kWaves) == 0, "pieces split evenly");
 };
@@ -343,13 +342,12 @@ struct Weights {
 
 constexpr int kAhead = 2;  // LDS reads ahead of the products: 480 us with 2 to 4 at 4096 x 7168 -> 18432, 512 with 1
 
-// A wave's sums to rows i0 .. i0 + 16 MI - 1 of y, columns from panel `first`
-// on.  Lane 16 g + l16 has four columns of row l16 of every panel, 8 bytes of
+// A wave's sums to 16 MI rows of y, columns from panel `first` on.  Lane 16 g + l16 has four columns of row l16 of every panel, 8 bytes of
 // bf16; where whole pieces are stored the four lanes of a row change places
 // first (v_permlane*_swap), so that each has 16 bytes or more in a row and a
 // store instruction fills 64 bytes of a line or more.
 template <int MI, int NJ, bool BF16>
-__device__ __forceinline__ void store_tile(const Product& p, const Rows& r, int i0, int64_t first,
+__device__ __forceinline__ void store_tile(const Product& p, const Rows& r, int64_t first,
                                            const v4i (&acc)[MI][NJ], const Four (&scales)[NJ], const float (&rows)[MI],
                                            Stores how) {
   static_assert(NJ == 2 || NJ == 4, "transposed by twos or fours");
@@ -358,7 +356,7 @@ __device__ __forceinline__ void store_tile(const Product& p, const Rows& r, int 
   const bool whole = how == Stores::lines && (first + NJ) * 16 <= p.N;
 #pragma unroll
   for (int i = 0; i < MI; ++i) {
-    const int m = i0 + 16 * i + l16;
+    const int m = 16 * i + l16;
     const int64_t row = (r.m0 + m) * p.y.ld;
     constexpr int D = BF16 ? 2 : 4;  // dwords of four columns
     uint32_t d[NJ][D];
@@ -432,13 +430,12 @@ __device__ __forceinline__ void store_tile(const Product& p, const Rows& r, int 
 template <class C, bool BF16, bool ONCE = false>
 __device__ __forceinline__ void tile(const Product& p, const Rows& r, int64_t panel0, Stores store, int8_t* st0,
                                      int8_t* st1, int8_t* st2, int8_t* st3) {
-  constexpr int MI = C::MI, NJ = C::NJ, SETS = C::SETS;
-  // (made anew for every tile: what follows from it is not kept from tile to
-  // tile in registers that the products need)
+  constexpr int MI = C::MI, NJ = C::NJ;
+  // (made anew in every branch of a kernel with several tiles: what follows
+  // from it is not kept in registers that the products need)
   int lane = threadIdx.x & 63;
   asm volatile("" : "+v"(lane));
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wn = wave & 3, wm = wave >> 2;
   const int l16 = lane & 15, g = lane >> 4;
   const int64_t panels = (p.N + 15) / 16;
   const int steps = (int)((p.K + kStep - 1) / kStep);
@@ -450,7 +447,7 @@ __device__ __forceinline__ void tile(const Product& p, const Rows& r, int64_t pa
     const int64_t t = r.index ? r.token(row) : min(row, r.rows - 1);
     aoff[q] = (uint32_t)(t * p.lda) + 16 * ((lane & 7) ^ ((row >> 1) & 7));
   }
-  const int64_t first = panel0 + wn * NJ;
+  const int64_t first = panel0 + wave * NJ;
   uint32_t woff[NJ];
 #pragma unroll
   for (int j = 0; j < NJ; ++j) woff[j] = (uint32_t)(min(first + j, panels - 1) * 1024) + 16 * lane;
@@ -475,7 +472,7 @@ __device__ __forceinline__ void tile(const Product& p, const Rows& r, int64_t pa
 #pragma unroll
     for (int j = 0; j < NJ; ++j) scales[j] = four(r.sw, p.bias, (first + j) * 16 + 4 * g, p.N);
 #pragma unroll
-    for (int i = 0; i < MI; ++i) row_scales[i] = p.sa[r.token(16 * (MI * wm + i) + l16)];
+    for (int i = 0; i < MI; ++i) row_scales[i] = p.sa[r.token(16 * i + l16)];
   };
   if (kEarly) load_scales();
   v4i acc[MI][NJ];
@@ -483,14 +480,14 @@ __device__ __forceinline__ void tile(const Product& p, const Rows& r, int64_t pa
   for (int i = 0; i < MI; ++i)
 #pragma unroll
     for (int j = 0; j < NJ; ++j) acc[i][j] = v4i{0, 0, 0, 0};
-  const int x_lo = lds_at(16 * MI * wm + l16, g);
-  // Step t multiplies stage t % 4 by the weights of set t % SETS: the first
+  const int x_lo = lds_at(l16, g);
+  // Step t multiplies stage t % 4 by the weights of set t % 2: the first
   // chunk's products, then the second's, each chunk's registers loaded again
-  // for step t + SETS as soon as its products are issued.
+  // for step t + 2 as soon as its products are issued.
   auto step = [&](int t, const int8_t* cur, Weights<NJ>& w, int8_t* refill, bool more_a, bool more_w, bool full) {
     // this wave's part of stage t is in LDS; what may still fly is younger:
     // the stages of t + 1 and t + 2, the weights from t on
-    if (full) wait_loads<2 * SETS * NJ + 2 * C::kA>(); else wait_loads<0>();
+    if (full) wait_loads<4 * NJ + 2 * C::kA>(); else wait_loads<0>();
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
@@ -504,7 +501,7 @@ __device__ __forceinline__ void tile(const Product& p, const Rows& r, int64_t pa
 #pragma unroll
         for (int j = 0; j < NJ; ++j) acc[i][j] = mfma(w.w[h][j], v, acc[i][j]);
       }
-      if (more_w) load_w(w.w[h], 2 * (t + SETS) + h);
+      if (more_w) load_w(w.w[h], 2 * (t + 2) + h);
     }
     // the order of the step's instructions: loads to LDS (0x20), LDS reads
     // (0x100), products (0x8), and the loads of weights behind each chunk
@@ -517,22 +514,18 @@ __device__ __forceinline__ void tile(const Product& p, const Rows& r, int64_t pa
       if (more_w && (i == MI - 1 || i == 2 * MI - 1)) __builtin_amdgcn_sched_group_barrier(0x020, NJ, 0);
     }
   };
-  Weights<NJ> sets[SETS];
-  Weights<NJ>&w0 = sets[0], &w1 = sets[SETS - 1];
+  Weights<NJ> w0, w1;
   // (the loads of steps that are not there read the last one's again: with a
   // branch the compiler would not know how many loads are in flight at the
   // head of the loop, and wait for all)
   const int last = steps - 1;
   issue(st0, 0);
   issue(st1, min(1, last));
-  if (SETS == 1) issue(st2, min(2, last));
   load_w(w0.w[0], 0);
   load_w(w0.w[1], 1);
-  if (SETS == 2) {
-    issue(st2, min(2, last));
-    load_w(w1.w[0], 2 * min(1, last));
-    load_w(w1.w[1], 2 * min(1, last) + 1);
-  }
+  issue(st2, min(2, last));
+  load_w(w1.w[0], 2 * min(1, last));
+  load_w(w1.w[1], 2 * min(1, last) + 1);
   int t = 0;
   for (; t + 7 <= steps; t += 4) {
     step(t, st0, w0, st3, true, true, true);
@@ -542,7 +535,7 @@ __device__ __forceinline__ void tile(const Product& p, const Rows& r, int64_t pa
   }
   // one to six more
   auto tail = [&](int u, const int8_t* cur, Weights<NJ>& w, int8_t* refill) {
-    if (u < steps) step(u, cur, w, refill, u + 3 < steps, u + SETS < steps, u + 2 < steps);
+    if (u < steps) step(u, cur, w, refill, u + 3 < steps, u + 2 < steps, u + 2 < steps);
   };
   tail(t, st0, w0, st3);
   tail(t + 1, st1, w1, st0);
@@ -552,7 +545,7 @@ __device__ __forceinline__ void tile(const Product& p, const Rows& r, int64_t pa
   tail(t + 5, st1, w1, st0);
   wait_loads<0>();
   if (!kEarly) load_scales();
-  store_tile<MI, NJ, BF16>(p, r, 16 * MI * wm, first, acc, scales, row_scales, store);
+  store_tile<MI, NJ, BF16>(p, r, first, acc, scales, row_scales, store);
 }
 
 // Output tile of workgroup `id`: workgroups go round the 8 XCDs in turn, so
@@ -659,7 +652,7 @@ template <int NJ, bool BF16>
 __global__ __launch_bounds__(256, 2) void grouped_tile_kernel(Product p, int64_t T, const int32_t* __restrict__ index,
                                                               const int32_t* __restrict__ offsets, int64_t R, int E,
                                                               int tiles_n, Stores store) {
-  using C = Cfg<8, 1, NJ>;
+  using C = Cfg<8, NJ>;
   __shared__ __attribute__((aligned(16))) int8_t st0[C::kRows * kStep];
   __shared__ __attribute__((aligned(16))) int8_t st1[C::kRows * kStep];
   __shared__ __attribute__((aligned(16))) int8_t st2[C::kRows * kStep];
@@ -685,9 +678,9 @@ __global__ __launch_bounds__(256, 2) void grouped_tile_kernel(Product p, int64_t
   const Rows r = item_rows(p, it, T, index);
   const int64_t panel0 = (int64_t)tn * NJ * 4;
   if (kind)
-    tile<Cfg<2, 1, NJ>, BF16, true>(p, r, panel0, store, st0, st1, st2, st3);
+    tile<Cfg<2, NJ>, BF16, true>(p, r, panel0, store, st0, st1, st2, st3);
   else if (it.rows <= 64)
-    tile<Cfg<4, 1, NJ>, BF16>(p, r, panel0, store, st0, st1, st2, st3);
+    tile<Cfg<4, NJ>, BF16>(p, r, panel0, store, st0, st1, st2, st3);
   else
     tile<C, BF16>(p, r, panel0, store, st0, st1, st2, st3);
 }
@@ -740,8 +733,7 @@ int launch_stream(const Product& p, int64_t M, hipStream_t s) {
   };
   auto with_rows = [&](auto pp) {
     if (M <= 16) return with_type(std::integral_constant<int, 1>{}, pp);
-    if (M <= 32) return with_type(std::integral_constant<int, 2>{}, pp);
-    return with_type(std::integral_constant<int, 4>{}, pp);
+    return with_type(std::integral_constant<int, 2>{}, pp);
   };
   switch (P) {
     case 1: return with_rows(std::integral_constant<int, 1>{});
@@ -767,15 +759,15 @@ int launch_stream(const Product& p, int64_t M, hipStream_t s) {
 int launch_gemm(const Product& p, int64_t M, hipStream_t s) {
   if (M <= 32) return launch_stream(p, M, s);
   auto tiles = [&](int64_t rows, int64_t cols) { return (M + rows - 1) / rows * ((p.N + cols - 1) / cols); };
-  if (tiles(128, 256) >= 256) return launch_tiles<Cfg<8, 1, 4>, 2>(p, M, s);
-  if (M > 64 && M <= 128 && tiles(128, 128) >= 128) return launch_tiles<Cfg<8, 1, 2>, 2>(p, M, s);
-  if (tiles(64, 128) >= 192) return launch_tiles<Cfg<4, 1, 2>, 3>(p, M, s);
-  return launch_tiles<Cfg<2, 1, 2>, 4>(p, M, s);
+  if (tiles(128, 256) >= 256) return launch_tiles<Cfg<8, 4>, 2>(p, M, s);
+  if (M > 64 && M <= 128 && tiles(128, 128) >= 128) return launch_tiles<Cfg<8, 2>, 2>(p, M, s);
+  if (tiles(64, 128) >= 192) return launch_tiles<Cfg<4, 2>, 3>(p, M, s);
+  return launch_tiles<Cfg<2, 2>, 4>(p, M, s);
 }
 
 int launch_grouped(const Product& p, int64_t T, const int32_t* row_index, const int32_t* offsets, int64_t R, int E,
                    hipStream_t s) {
-  constexpr int NJ = 4, kRows = Cfg<8, 1, NJ>::kRows, kCols = Cfg<8, 1, NJ>::kCols;
+  constexpr int NJ = 4, kRows = Cfg<8, NJ>::kRows, kCols = Cfg<8, NJ>::kCols;
   const Stores store = stores_of(p.y);
   // no more pieces than full ones and one begun per expert, nor than rows
   auto pieces = [&](int64_t rows) { return std::min(R, R / rows + E); };
