@@ -9,7 +9,7 @@
 // expert): that is its slot.  Where that does not hold (k > 16, more than 64
 // candidates, E > 256), k times over the largest key is found in the lane, then
 // over the lanes, and leaves.  Instructions bound it: for 16384 tokens, 8 of
-// 256 experts, the k-fold search took 14 us, this SELECTED.
+// 256 experts, the k-fold search took 14.4 us, this 9.7.
 // The first one chosen is the maximum that the softmax subtracts, so the
 // weights follow from the k chosen (or all E) logits without another pass.
 //
@@ -552,8 +552,7 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const float* __rest
     }
   }
   // the chosen experts' terms through LDS (an expert that is named more than
-  // once gets their sum, in the order of the slots: lanes of one instruction
-  // add in their order)
+  // once gets their sum; one wave adds them, whatever else runs)
 #pragma unroll
   for (int i = 0; i < V; ++i) row[l + i * G] = p[i];
   wave_sync();

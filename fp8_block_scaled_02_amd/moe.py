@@ -200,7 +200,7 @@ def int8_linear(x, w_packed, w_scales, bias=None, out_dtype=torch.bfloat16):
 
 def int8_moe_forward(x, logits, k: int, w_packed, w_scales, renormalize: bool = True, out_dtype=torch.bfloat16):
     """One expert projection: moe_route of the logits, int8_quant of the
-    tokens, int8_grouped_gemm (bf16 rows), moe_combine.  Returns (out [T, N],
-    the Routing)."""
+    tokens, int8_grouped_gemm (rows in out_dtype), moe_combine.  Returns
+    (out [T, N], the Routing)."""
     out = _call("forward", x, logits, k, w_packed, w_scales, renormalize, _fp32(out_dtype))
     return out[0], Routing(*out[1:])

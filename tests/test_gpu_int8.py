@@ -72,6 +72,16 @@ def test_quant(F, M, K, dtype):
         assert (codes[:, :at] == 5).all() and (codes[:, at + K:] == 5).all()
 
 
+@pytest.mark.parametrize("dtype", [bf16, f32])
+@pytest.mark.parametrize("M,K", [(2100, 8000), (17000, 1003), (140, 130001)])
+def test_quant_large(F, M, K, dtype):
+    x = torch.randn(M, K, generator=_gen(K), device=DEV).to(dtype)
+    want = O.quantise(x.float().cpu().numpy())
+    for t in (x, torch.nn.functional.pad(x, (1, 2))[:, 1:K + 1]):
+        c, s = F.int8_quant(t)
+        assert np.array_equal(c.cpu().numpy(), want[0]) and np.array_equal(s.cpu().numpy(), want[1])
+
+
 def test_quant_at_halves(F):
     """Quotients at and next to a half, for many scales: the whole number
     nearest to the fp32 quotient."""
@@ -180,6 +190,37 @@ def test_gemm(F, M, N, K, out, bias):
     _check_gemm(F, M, N, K, out, bias, M + N + K)
 
 
+@pytest.mark.parametrize("out,bias", [(bf16, False), (f32, True)])
+@pytest.mark.parametrize("panels", range(1, 9))
+def test_gemm_streamed(F, panels, out, bias):
+    """Few rows of outputs so wide that a workgroup has 1 to 8 panels."""
+    N = 4096 * panels - 5 * panels
+    for M, K in ((1, 64), (16, 200), (17, 1100), (32, 2600)):
+        _check_gemm(F, M, N, K, out, bias, panels)
+
+
+@pytest.mark.parametrize("out,bias", [(bf16, False), (f32, True)])
+@pytest.mark.parametrize("M,N", [(2050, 4101), (4200, 2048), (100, 16400), (65, 20001), (300, 5000), (900, 1700), (200, 6001)])
+def test_gemm_tiles(F, M, N, out, bias):
+    """The larger tiles, with one step of K, each number of steps up to the
+    ring's length, and some past it."""
+    for K in (100, 256, 300, 512, 640, 700, 800, 1000, 1500):
+        _check_gemm(F, M, N, K, out, bias, K)
+
+
+@pytest.mark.parametrize("out", [bf16, f32])
+@pytest.mark.parametrize("M,N", [(2050, 4098), (100, 16402), (300, 5002)])
+def test_gemm_tiles_into_strided_rows(F, M, N, out):
+    K, g = 400, _gen(M)
+    a, wp = _laid_out(_rand_codes((M, K), g)), F.int8_weight_pack(_rand_codes((N, K), g))
+    sa, sw = _scales(M, g), _scales(N, g)
+    want = F.int8_gemm(a, sa, wp, sw, None, out)
+    for ld, at in ((N + 1, 1), (N + 6, 0), (N + 30, 8)):
+        y = torch.full((M, ld), 4.0, dtype=out, device=DEV)
+        F.int8_gemm(a, sa, wp, sw, None, out, y[:, at:at + N])
+        assert torch.equal(y[:, at:at + N], want) and (y[:, :at] == 4).all() and (y[:, at + N:] == 4).all()
+
+
 @pytest.mark.parametrize("M", [1, 40, 300])
 def test_gemm_largest_sums(F, M):
     """Codes of -128 and 127 everywhere at the largest K: sums at the ends of 32 bits."""
@@ -278,6 +319,45 @@ def test_grouped(F, counts, N, K, out):
     _check_grouped(F, 0, counts, N, K, out, 1, spare=3, direct=True)
 
 
+@pytest.mark.parametrize("out", [bf16, f32])
+@pytest.mark.parametrize("N,K", [(1800, 100), (1793, 700), (1808, 1100), (2048, 512)])
+@pytest.mark.parametrize("counts", [
+    [1, 31, 32, 33, 64, 65, 127, 128, 129, 160, 161, 200, 300] + [0] * 27, [0] * 19 + [700] + [0] * 20, [0] * 40, [3] * 40,
+    [128] * 10 + [0, 1] * 15, [40] * 40, [1000, 0, 17] + [70] * 37])
+def test_grouped_tiles(F, counts, N, K, out):
+    """Experts and columns enough for tiles: pieces of every kind."""
+    _check_grouped(F, 37, counts, N, K, out, sum(counts), spare=40)
+    _check_grouped(F, 0, counts, N, K, out, 1, spare=45, direct=True)
+
+
+def test_grouped_of_many_experts(F):
+    rng = np.random.default_rng(3)
+    counts = [int(c) for c in np.minimum(rng.zipf(1.5, 1024), 400) * (rng.random(1024) < 0.6)]
+    _check_grouped(F, 500, counts, 70, 128, bf16, 3, spare=9)
+    _check_grouped(F, 500, [c // 4 for c in counts[:700]], 300, 130, f32, 4, spare=9)
+
+
+@pytest.mark.parametrize("out", [bf16, f32])
+@pytest.mark.parametrize("E,N", [(6, 203), (40, 1803)])
+def test_grouped_strides_and_given_output(F, E, N, out):
+    g, K, T, R = _gen(N), 256, 60, 333
+    a, w = _rand_codes((T, K), g), _rand_codes((E, N, K), g)
+    sa, sw = _scales(T, g), _scales(E * N, g).view(E, N)
+    index = torch.randint(0, T, (R,), generator=g, device=DEV).int()
+    offs = torch.sort(torch.randint(0, R + 1, (E + 1,), generator=g, device=DEV)).values.int()
+    offs[0] = 0
+    end = int(offs[-1])
+    wp = F.int8_weight_pack(w)
+    want = F.int8_grouped_gemm(a, sa, index, offs, wp, sw, out)
+    wide = _rand_codes((T, 3 * K), g)
+    wide[:, K:2 * K] = a
+    for ld, at in ((N, 0), (N + 1, 1), (N + 5, 0), (N + 53, 16)):
+        y = torch.full((R, ld), 4.0, dtype=out, device=DEV)
+        F.int8_grouped_gemm(wide[:, K:2 * K], sa, index, offs, wp, sw, out, y[:, at:at + N])
+        assert torch.equal(y[:end, at:at + N], want[:end]) and (y[end:] == 4).all()
+        assert (y[:, :at] == 4).all() and (y[:, at + N:] == 4).all()
+
+
 @pytest.mark.parametrize("seed", range(4))
 def test_grouped_skewed(F, seed):
     rng = np.random.default_rng(seed)
@@ -285,19 +365,21 @@ def test_grouped_skewed(F, seed):
     _check_grouped(F, 200, counts, int(rng.integers(1, 400)), int(rng.integers(1, 900)), bf16, seed, spare=11)
 
 
-def test_grouped_contract_broken(F):
+@pytest.mark.parametrize("E,N", [(5, 70), (40, 1800)])
+def test_grouped_contract_broken(F, E, N):
     """Offsets and tokens outside their ranges: unspecified rows, no others touched."""
     g = _gen(7)
-    T, E, N, K, R = 20, 5, 70, 128, 60
+    T, K, R = 20, 128, 60
     a, wp = _laid_out(_rand_codes((T, K), g)), F.int8_weight_pack(_rand_codes((E, N, K), g))
     sa, sw = _scales(T, g), _scales(E * N, g).view(E, N)
     index = torch.randint(-5, T + 5, (R,), generator=g, device=DEV).int()
     for offs in ([0, 10, 5, 30, 20, 60], [-4, 3, 9, 400, 2 ** 31 - 1, 70], [9, 8, 7, 6, 5, 4], [-2 ** 31] * 6):
         room = torch.full((R + 40, N), 5.0, device=DEV)
+        offs = offs + offs[-1:] * (E - 5)
         F.int8_grouped_gemm(a, sa, index, torch.tensor(offs, device=DEV).int(), wp, sw, f32, room[20:20 + R])
         torch.cuda.synchronize()
         assert (room[:20] == 5).all() and (room[20 + R:] == 5).all()
-    assert F.int8_grouped_gemm(a, sa, index[:0], torch.zeros(6, device=DEV).int(), wp, sw).shape == (0, N)
+    assert F.int8_grouped_gemm(a, sa, index[:0], torch.zeros(E + 1, device=DEV).int(), wp, sw).shape == (0, N)
 
 
 # ---- together ----------------------------------------------------------------
@@ -305,7 +387,8 @@ def test_grouped_contract_broken(F):
 
 @pytest.mark.parametrize("T,E,k,K,N,renorm", [(1, 8, 2, 256, 200, True), (5, 256, 8, 512, 96, True), (70, 12, 3, 300, 129, False),
                                               (600, 16, 4, 256, 256, True)])
-def test_expert_layer(F, T, E, k, K, N, renorm):
+@pytest.mark.parametrize("odt", [bf16, f32])
+def test_expert_layer(F, T, E, k, K, N, renorm, odt):
     """The layer's call is its parts' calls, and those are the definition."""
     g = _gen(T)
     x = W.activations(T, K, 2, 20.0, g)
@@ -315,12 +398,12 @@ def test_expert_layer(F, T, E, k, K, N, renorm):
     c, sw = F.int8_quant(w.view(E * N, K))
     c, sw = c.reshape(E, N, K), sw.view(E, N)
     wp = F.int8_weight_pack(c)
-    out, r = F.int8_moe_forward(x, l, k, wp, sw, renorm, f32)
+    out, r = F.int8_moe_forward(x, l, k, wp, sw, renorm, odt)
     r2 = F.moe_route(l, k, renorm)
     assert all(torch.equal(p, q) for p, q in zip(r, r2))
     a, sa = F.int8_quant(x)
-    y = F.int8_grouped_gemm(a, sa, r.row_index, r.expert_offsets, wp, sw)
-    assert torch.equal(F.moe_combine(y, r.token_rows, r.gates, f32), out)
+    y = F.int8_grouped_gemm(a, sa, r.row_index, r.expert_offsets, wp, sw, odt)
+    assert out.dtype == odt and torch.equal(F.moe_combine(y, r.token_rows, r.gates), out)
     oc, os = O.quantise(x.float().cpu().numpy())
     experts = O.choose(_np(l), k)
     gates, dist = O.gates(_np(l), experts, renorm)
@@ -330,8 +413,9 @@ def test_expert_layer(F, T, E, k, K, N, renorm):
         share = (gates * (experts == e)).sum(1)[:, None]
         ref += share * v
         mag += np.abs(share * v)
-    # rows rounded to bf16, products off by 4 u, weights by u (d + 2 n + 8), k sums
-    tol = mag * (H + U * (4 + dist.max() + 2 * (k if renorm else E) + 8 + k)) * (1 + H) + U * np.abs(ref)
+    # rows rounded to the output's type, products off by 4 u, weights by u (d + 2 n + 8), k sums
+    h = H if odt == bf16 else U
+    tol = mag * (h + U * (4 + dist.max() + 2 * (k if renorm else E) + 8 + k)) * (1 + h) + h * np.abs(ref)
     assert (np.abs(_np(out) - ref) <= tol).all()
     assert F.int8_moe_forward(x[:0], l[:0], k, wp, sw)[0].shape == (0, N)
 

@@ -146,6 +146,21 @@ def test_sort(F, T, E, k):
     _check_plan(*F.moe_sort(e, E), _ints(e), E)
 
 
+@pytest.mark.parametrize("T,E,k", [(150000, 300, 4), (40000, 1024, 64), (300001, 5, 1)])
+def test_sort_of_many_slots(F, T, E, k):
+    """More slots than a workgroup holds at a time; the definition by a stable sort."""
+    e = torch.randint(-1, E, (T, k), generator=_gen(T), device=DEV).int()
+    offsets, row_index, token_rows = map(_ints, F.moe_sort(e, E))
+    flat = _ints(e).ravel()
+    kept = np.nonzero(flat >= 0)[0]
+    order = kept[np.argsort(flat[kept], kind="stable")]
+    assert np.array_equal(offsets, np.concatenate(([0], np.cumsum(np.bincount(flat[kept], minlength=E)))))
+    assert np.array_equal(row_index[:len(order)], order // k) and (row_index[len(order):] == -1).all()
+    rows = np.full(T * k, -1)
+    rows[order] = np.arange(len(order))
+    assert np.array_equal(token_rows.ravel(), rows)
+
+
 def test_sort_extremes(F):
     e = torch.tensor([[2 ** 31 - 1, -2 ** 31, 0]] * 40, device=DEV).int()
     _check_plan(*F.moe_sort(e, 3), _ints(e), 3)
@@ -268,6 +283,45 @@ def test_combine_and_gradient(F, T, k, R, N, ydt, odt):
         tol = (H + U if ydt == bf16 else U) * np.abs(rdy)
         assert (np.abs(_np(dy) - rdy) <= tol).all()
         assert (np.abs(_np(dg) - rdg) <= (N / 256 + 18) * U * mag).all()
+
+
+@pytest.mark.parametrize("T,k,N,dtype", [(4100, 8, 4104, bf16), (4100, 8, 2052, f32), (30000, 3, 1501, bf16), (12000, 3, 2001, f32)])
+def test_more_rows_than_a_cache(F, T, k, N, dtype):
+    g = _gen(N)
+    R = T * k
+    tr = torch.randperm(R, generator=g, device=DEV).view(T, k).int()
+    tr[::5, k // 2] = -1
+    x, dout = (torch.randn(T, N, generator=g, device=DEV).to(dtype) for _ in range(2))
+    gates = torch.randn(T, k, generator=g, device=DEV)
+    held = torch.full((R, N), 3.0, dtype=dtype, device=DEV)
+    F.moe_gather(x, tr, out=held)
+    token = torch.full((R,), -1, device=DEV)
+    slot = token.clone()
+    t_of = torch.arange(T, device=DEV)[:, None].expand(T, k)
+    live = tr >= 0
+    token[tr[live].long()] = t_of[live]
+    slot[tr[live].long()] = torch.arange(k, device=DEV).expand(T, k)[live]
+    rest = token < 0
+    assert torch.equal(held[~rest], x[token[~rest]]) and (held[rest] == 3).all()
+    y = torch.randn(R, N, generator=g, device=DEV).to(dtype)
+    out, total = F.moe_combine(y, tr, gates), F.moe_gather_backward(y, tr)
+    held.fill_(3.0)
+    dy, dg = F.moe_combine_backward(dout, y, tr, gates, dy=held)
+    assert (dy[rest] == 3).all()
+    h = H if dtype == bf16 else U
+    for lo in range(0, T, 1000):
+        s = tr[lo:lo + 1000].long()
+        w = (s >= 0).double()[..., None]
+        rows, gt, d = y[s.clamp(min=0)].double() * w, gates[lo:lo + 1000].double()[..., None], dout[lo:lo + 1000].double()
+        for got, terms in ((out, rows * gt), (total, rows)):
+            ref, mag = terms.sum(1), terms.abs().sum(1)
+            assert ((got[lo:lo + 1000].double() - ref).abs() <= k * U * mag + h * ref.abs()).all()
+        terms = rows * d[:, None]
+        assert ((dg[lo:lo + 1000].double() - terms.sum(2)).abs() <= (N / 256 + 18) * U * terms.abs().sum(2)).all()
+        want = gt * d[:, None] * w
+        tol = (H + U if dtype == bf16 else U) * want.abs()
+        got = torch.where(w > 0, dy[s.clamp(min=0)].double(), 0.0)
+        assert ((got - want).abs() <= tol).all()
 
 
 def test_rows_outside_and_none(F):
