@@ -694,8 +694,7 @@ Stores stores_of(const Mat& y) {
 template <class C, int OCC>
 int launch_tiles(const Product& p, int64_t M, hipStream_t s) {
   const int64_t tiles_m = (M + C::kRows - 1) / C::kRows, tiles_n = (p.N + C::kCols - 1) / C::kCols;
-  if (tiles_m * tiles_n > (1 << 22)) return FP8B_EINVAL;
-  auto go = [&](auto b) {
+  auto go = [&](auto b) {  // (M N <= 2^36: at most 2^22 tiles)
     hipLaunchKernelGGL((tile_kernel<C, decltype(b)::value, OCC>), dim3((unsigned)(tiles_m * tiles_n)), dim3(C::kThreads),
                        0, s, p, M, (int)tiles_m, (int)tiles_n, stores_of(p.y));
     return check_launch();

@@ -213,7 +213,8 @@ int launch_quant(const Mat& x, int64_t M, int64_t K, int8_t* codes, int64_t ld_c
     if (!wide) return go(b, integral_constant<int, 1>{}, integral_constant<int, 256>{}, integral_constant<int, 8>{});
     if (K <= 16 * 16) return go(b, W8{}, integral_constant<int, 16>{}, Two{});
     if (K <= 64 * 16) return go(b, W8{}, integral_constant<int, 64>{}, Two{});
-    if (K <= 256 * 16) return go(b, W8{}, integral_constant<int, 256>{}, Two{});
+    // (a launch has fewer than 2^32 threads)
+    if (K <= 256 * 16 || M >= 1 << 22) return go(b, W8{}, integral_constant<int, 256>{}, Two{});
     if (K <= 512 * 16) return go(b, W8{}, integral_constant<int, 512>{}, Two{});
     return go(b, W8{}, integral_constant<int, 1024>{}, Two{});
   };

@@ -209,7 +209,7 @@ FP8B_EXPORT int int8_grouped_gemm(const int8_t* a, int64_t ld_a, const float* a_
     return FP8B_EINVAL;
   if (up(N, 16) * up(K, 128) >= kMaxCodes / E || R * N > kMaxOut || E * N > kMaxExpertRows) return FP8B_EINVAL;
   // the rows of a are reached by 32-bit offsets
-  if (T * ld_a >= (int64_t)1 << 32) return FP8B_EINVAL;
+  if (ld_a < 0 || ld_a >= (1 << 24) || T * ld_a >= (int64_t)1 << 32) return FP8B_EINVAL;
   if (R == 0) return FP8B_OK;
   const fp8moe::Product p{a, ld_a, a_scales, w_packed, w_scales, nullptr, N, K, mat(y, out_dtype, ld_y)};
   FP8B_TRY(product_check(p));

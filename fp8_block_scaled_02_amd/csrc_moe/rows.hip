@@ -263,10 +263,11 @@ bool wide(const Mat& m) {
   return reinterpret_cast<uintptr_t>(m.p) % 4 == 0 && m.ld * (m.bf16 ? 2 : 4) % 4 == 0;
 }
 
-// Threads of a workgroup: each has two pieces of a row where that fills them.
-unsigned threads_of(int64_t N, int C) {
-  const int64_t pieces = (N / C + 1) / 2;
-  return (unsigned)std::min<int64_t>(kMaxThreads, std::max<int64_t>(64, (pieces + 63) / 64 * 64));
+// Threads of a token's workgroup: each has two pieces of a row where that fills
+// them.  A launch has fewer than 2^32.
+unsigned threads_of(int64_t T, int64_t N, int C) {
+  const int64_t pieces = (N / C + 1) / 2, most = T < (1 << 22) ? kMaxThreads : kMaxThreads / 4;
+  return (unsigned)std::min(most, std::max<int64_t>(64, (pieces + 63) / 64 * 64));
 }
 
 // f(y is bf16, out is bf16, columns of a piece, rows past the cache)
@@ -295,7 +296,7 @@ int64_t row_bytes(const Mat& y, int64_t rows, int64_t N) { return rows * N * (y.
 int launch_gather(const Mat& x, int64_t T, int64_t N, const int32_t* token_rows, int k, int64_t R, const Mat& rows,
                   hipStream_t s) {
   return by_type(x.bf16, x.bf16, wide(x) && wide(rows), row_bytes(x, T * k, N), [&](auto b, auto, auto c, auto nt) {
-    hipLaunchKernelGGL((gather_kernel<b.value, c.value, nt.value>), dim3((unsigned)T), dim3(threads_of(N, c.value)), 0, s,
+    hipLaunchKernelGGL((gather_kernel<b.value, c.value, nt.value>), dim3((unsigned)T), dim3(threads_of(T, N, c.value)), 0, s,
                        x.p, x.ld, N, token_rows, k, R, rows.p, rows.ld);
     return check_launch();
   });
@@ -306,7 +307,7 @@ int launch_combine(const Mat& y, int64_t R, int64_t N, const int32_t* token_rows
   return by_type(y.bf16, out.bf16, wide(y) && wide(out), row_bytes(y, T * k, N), [&](auto yb, auto ob, auto c, auto nt) {
     return by_slots(k, [&](auto S) {
       hipLaunchKernelGGL((combine_kernel<yb.value, ob.value, c.value, nt.value, S.value>), dim3((unsigned)T),
-                         dim3(threads_of(N, c.value)), 0, s, y.p, y.ld, R, N, token_rows, gates, k, out.p, out.ld);
+                         dim3(threads_of(T, N, c.value)), 0, s, y.p, y.ld, R, N, token_rows, gates, k, out.p, out.ld);
       return check_launch();
     });
   });
@@ -318,7 +319,7 @@ int launch_combine_backward(const Mat& dout, const Mat& y, int64_t R, int64_t N,
                  [&](auto yb, auto ob, auto c, auto nt) {
                    return by_slots(k, [&](auto S) {
                      hipLaunchKernelGGL((combine_backward_kernel<yb.value, ob.value, c.value, nt.value, S.value>),
-                                        dim3((unsigned)T), dim3(threads_of(N, c.value)), 0, s, dout.p, dout.ld, y.p, y.ld,
+                                        dim3((unsigned)T), dim3(threads_of(T, N, c.value)), 0, s, dout.p, dout.ld, y.p, y.ld,
                                         R, N, token_rows, gates, k, dy.p, dy.ld, dgates);
                      return check_launch();
                    });

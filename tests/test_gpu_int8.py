@@ -27,6 +27,14 @@ def F():
     return F
 
 
+@pytest.fixture
+def big():
+    """Memory that others do not hold, given back afterwards."""
+    torch.cuda.empty_cache()
+    yield
+    torch.cuda.empty_cache()
+
+
 def _np(t):
     return t.detach().double().cpu().numpy()
 
@@ -80,6 +88,23 @@ def test_quant_large(F, M, K, dtype):
     for t in (x, torch.nn.functional.pad(x, (1, 2))[:, 1:K + 1]):
         c, s = F.int8_quant(t)
         assert np.array_equal(c.cpu().numpy(), want[0]) and np.array_equal(s.cpu().numpy(), want[1])
+
+
+def test_quant_past_32_bits(F, big):
+    """Values past 2^31, in rows that would take 2^32 threads together."""
+    M, K = (1 << 23) + 5, 4104
+    x = torch.empty(M, K, dtype=bf16, device=DEV)
+    x.copy_(torch.randn(1, K, generator=_gen(1), device=DEV))
+    power = torch.tensor([2.0 ** (i - 5) for i in range(11)], device=DEV)[torch.arange(M, device=DEV) % 11]
+    x *= power.to(bf16)[:, None]
+    x[M - 2:] = torch.randn(2, K, generator=_gen(2), device=DEV).to(bf16)
+    c, s = F.int8_quant(x)
+    one, scale = F.int8_quant(x[5:6])                                   # times 1
+    assert torch.equal(s[:M - 2], power[:M - 2] * scale)
+    for lo in (0, 1_234_567, 1 << 22, M - 1002):
+        assert (c[lo:lo + 1000] == one).all()
+    want = O.quantise(x[M - 2:].float().cpu().numpy())
+    assert np.array_equal(c[M - 2:].cpu().numpy(), want[0]) and np.array_equal(s[M - 2:].cpu().numpy(), want[1])
 
 
 def test_quant_at_halves(F):
@@ -219,6 +244,41 @@ def test_gemm_tiles_into_strided_rows(F, M, N, out):
         y = torch.full((M, ld), 4.0, dtype=out, device=DEV)
         F.int8_gemm(a, sa, wp, sw, None, out, y[:, at:at + N])
         assert torch.equal(y[:, at:at + N], want) and (y[:, :at] == 4).all() and (y[:, at + N:] == 4).all()
+
+
+@pytest.mark.parametrize("M,N", [(70000, 33000), (17, 20_000_000)])
+def test_gemm_past_32_bits(F, big, M, N):
+    """Results, or weights, past 2^31 bytes: parts are those of the part alone."""
+    K, g = 128, _gen(M)
+    a, wp = _rand_codes((M, K), g), F.int8_weight_pack(_rand_codes((N, K), g))
+    sa, sw = _scales(M, g), _scales(N, g)
+    y = F.int8_gemm(a, sa, wp, sw)
+    w = wp.view(2, -1, 1024)
+    for lo in (0, N // 2 // 16 * 16, N // 16 * 16 - 512):
+        part = w[:, lo // 16:lo // 16 + 32].contiguous().view(512, K)
+        for m in (0, M // 2, M - 17):
+            assert torch.equal(y[m:m + 17, lo:lo + 512], F.int8_gemm(a[m:m + 17], sa[m:m + 17], part, sw[lo:lo + 512]))
+
+
+def test_grouped_past_32_bits(F, big):
+    """Weights of 5 GB, rows of 4 GB: every expert has the same matrix, and
+    rows of the same token are equal."""
+    E, N, K, T, R = 160, 2048, 16384, 500, 1 << 20
+    g = _gen(9)
+    w = _rand_codes((N, K), g)
+    a = _rand_codes((T, K), g)
+    sa, sw = _scales(T, g), _scales(N, g)
+    wp = F.int8_weight_pack(w.expand(E, N, K))
+    swe = sw.expand(E, N).contiguous()
+    index = torch.randint(0, T, (R,), generator=g, device=DEV).int()
+    offs = torch.sort(torch.randint(0, R, (E + 1,), generator=g, device=DEV)).values.int()
+    offs[0], offs[-1] = 0, R
+    want = F.int8_gemm(a, sa, wp[0], sw)
+    y = F.int8_grouped_gemm(a, sa, index, offs, wp, swe)
+    for lo in range(0, R, 1 << 18):
+        assert torch.equal(y[lo:lo + (1 << 18)], want[index[lo:lo + (1 << 18)].long()])
+    few = torch.arange(E + 1, device=DEV).int()                         # a row of each expert
+    assert torch.equal(F.int8_grouped_gemm(a, sa, index[:E], few, wp, swe), want[index[:E].long()])
 
 
 @pytest.mark.parametrize("M", [1, 40, 300])
@@ -418,6 +478,32 @@ def test_expert_layer(F, T, E, k, K, N, renorm, odt):
     tol = mag * (h + U * (4 + dist.max() + 2 * (k if renorm else E) + 8 + k)) * (1 + h) + h * np.abs(ref)
     assert (np.abs(_np(out) - ref) <= tol).all()
     assert F.int8_moe_forward(x[:0], l[:0], k, wp, sw)[0].shape == (0, N)
+
+
+def test_the_plan_drives_the_fp8_layer(F):
+    """The router's plan in the block-scaled layer, whose combine is this one's."""
+    T, E, k, N, K = 150, 20, 4, 256, 512
+    g = _gen(21)
+    x = torch.randn(T, K, generator=g, device=DEV).to(bf16)
+    l = torch.randn(T, E, generator=g, device=DEV)
+    l[::10] = -INF
+    r = F.moe_route(l, k)
+    w = (torch.randn(E * N, K, generator=g, device=DEV) * 0.02).to(bf16)
+    wq, ws = F.fp8_weight_quant(w)
+    wq, ws = wq.view(E, N, K), ws.view(E, N // 128, K // 128)
+    a, sa = F.fp8_act_quant(x)
+    # the layer's own combine wants a row for every slot: those of tokens without experts weigh nothing
+    y = F.fp8_grouped_gemm(a, sa, r.row_index.clamp(min=0), r.expert_offsets, wq, ws, bf16, torch.zeros(T * k, N, dtype=bf16, device=DEV))
+    out = F.moe_combine(y, r.token_rows, r.gates)
+    assert torch.equal(out, F.fp8_moe_combine(y, r.token_rows.clamp(min=0), r.gates)) and not out[::10].any()
+    live = [t for t in range(T) if t % 10]
+    for t in live[::17]:
+        for j in range(k):
+            e, row = int(r.experts[t, j]), y[r.token_rows[t, j]].float()
+            ref = F.fp8_block_gemm(a[t:t + 1], sa[t:t + 1], wq[e], ws[e], f32)[0]
+            # either's sums of K products (codes add an eighth to a factor at most), and the row's rounding
+            mag = x[t].float().abs() @ w.view(E, N, K)[e].float().abs().T * 1.27
+            assert ((row - ref).abs() <= 2 * K * U * mag + H * ref.abs()).all()
 
 
 def test_a_training_step_of_the_routing(F):

@@ -37,6 +37,14 @@ def F():
     return F
 
 
+@pytest.fixture
+def big():
+    """Memory that others do not hold, given back afterwards."""
+    torch.cuda.empty_cache()
+    yield
+    torch.cuda.empty_cache()
+
+
 def _np(t):
     return t.detach().double().cpu().numpy()
 
@@ -286,7 +294,7 @@ def test_combine_and_gradient(F, T, k, R, N, ydt, odt):
 
 
 @pytest.mark.parametrize("T,k,N,dtype", [(4100, 8, 4104, bf16), (4100, 8, 2052, f32), (30000, 3, 1501, bf16), (12000, 3, 2001, f32)])
-def test_more_rows_than_a_cache(F, T, k, N, dtype):
+def test_more_rows_than_a_cache(F, big, T, k, N, dtype):
     g = _gen(N)
     R = T * k
     tr = torch.randperm(R, generator=g, device=DEV).view(T, k).int()
@@ -369,7 +377,54 @@ def test_gradient_against_differences(F):
         assert abs(want - slope) <= 2.0 ** -18 * (np.abs(_np(grad)) * np.abs(v)).sum() + 1e-6 * np.abs(_np(dout)).sum()
 
 
-def test_many_rows_past_32_bits(F):
+def test_routing_of_many_tokens_past_32_bits(F, big):
+    """Logits past 2^31 values: the choice and the weights of a part are those of the part alone."""
+    T, E, k = 9_000_000, 256, 8
+    l = torch.empty(T, E, device=DEV)
+    l.copy_(torch.rand(1, E, generator=_gen(1), device=DEV))
+    for lo in range(0, T, 1_000_000):
+        l[lo:lo + 1_000_000] += torch.rand(1_000_000, E, generator=_gen(lo), device=DEV)
+    r = F.moe_route(l, k)
+    assert int(r.expert_offsets[-1]) == T * k
+    named = torch.zeros(T * k, dtype=torch.bool, device=DEV)
+    named[r.token_rows.view(-1).long()] = True
+    assert named.all()
+    assert (r.row_index[r.token_rows.long()] == torch.arange(T, device=DEV)[:, None]).all()
+    of_row = torch.empty(T * k, dtype=i32, device=DEV)
+    of_row[r.token_rows.view(-1).long()] = r.experts.view(-1)
+    assert (of_row[1:] >= of_row[:-1]).all()
+    counts = torch.bincount(r.experts.view(-1), minlength=E)
+    assert torch.equal(r.expert_offsets[1:].long(), counts.cumsum(0))
+    d = torch.rand(T, k, generator=_gen(2), device=DEV)
+    dl = F.moe_route_backward(d, l, r.gates, r.experts, False)
+    for lo in (0, 4_400_000, 8_388_600, T - 1000):
+        part = slice(lo, lo + 1000)
+        q = F.moe_route(l[part], k)
+        assert torch.equal(q.experts, r.experts[part]) and torch.equal(q.gates, r.gates[part])
+        assert torch.equal(F.moe_route_backward(d[part], l[part], q.gates, q.experts, False), dl[part])
+
+
+def test_more_threads_than_a_launch(F, big):
+    """2^23 tokens of rows that would take 576 threads each."""
+    T, N, R = (1 << 23) + 3, 1025, 1000
+    x = torch.zeros(T, N, dtype=bf16, device=DEV)
+    tr = torch.full((T, 1), -1, dtype=i32, device=DEV)
+    at = torch.tensor([0, 77, 1 << 21, T - 4, T - 1], device=DEV)
+    tr[at, 0] = torch.tensor([5, 999, 0, 3, 4], device=DEV).int()
+    x[at] = torch.randn(5, N, generator=_gen(3), device=DEV).to(bf16)
+    held = torch.full((R, N), 3.0, dtype=bf16, device=DEV)
+    F.moe_gather(x, tr, out=held)
+    rows = tr[at, 0].long()
+    assert torch.equal(held[rows], x[at]) and int((held == 3).all(1).sum()) == R - 5
+    gates = torch.full((T, 1), 2.0, device=DEV)
+    dy, dg = F.moe_combine_backward(x, held, tr, gates, dy=torch.full_like(held, 3.0))
+    assert torch.equal(dy[rows], 2 * x[at]) and int((dy == 3).all(1).sum()) == R - 5
+    assert int((dg != 0).sum()) == 5 and (dg[at, 0] > 0).all()
+    F.moe_combine(held, tr, gates, out=x)
+    assert torch.equal(x[at], 2 * held[rows]) and not x[:77].any(1)[1:].any() and not x[T - 3:T - 1].any()
+
+
+def test_many_rows_past_32_bits(F, big):
     """Rows whose values lie past 2^31 elements."""
     N, R = 8192, 300000
     tr = torch.tensor([[R - 1, 7], [0, R - 2]], device=DEV).int()

@@ -133,3 +133,16 @@ def test_products(L):
         ({7: 1025}, EINVAL), ({10: 0}, EINVAL), ({11: 0}, EINVAL), ({4: None}, EINVAL), ({1: 112}, EINVAL), ({1: 136}, EALIGN),
         ({13: 63}, EINVAL), ({4: ODD}, EALIGN), ({5: ODD}, EALIGN), ({12: ODD}, EALIGN), ({6: 0, 0: None, 12: None}, OK),
         ({10: 1 << 25, 11: 131071, 7: 1024, 13: 1 << 25, 1: 131072}, EINVAL)] + [({i: None}, EINVAL) for i in (0, 2, 5, 8, 9, 12)])
+
+
+def test_largest_products(L):
+    """Sizes whose launches or offsets would not fit are refused, whatever the rest is."""
+    good = [GOOD, 128, GOOD, GOOD, GOOD, None, 4, 64, 100, GOOD, 64, BF16, None]
+    _refuses(L.int8_gemm, good, [({6: 1 << 23, 7: 8193, 10: 8193}, EINVAL), ({6: 4096, 7: 1 << 25, 10: 1 << 25}, EINVAL)])
+    good = [GOOD, 128, GOOD, 4, GOOD, GOOD, 8, 3, GOOD, GOOD, 64, 100, GOOD, 64, F32, None]
+    _refuses(L.int8_grouped_gemm, good, [
+        ({6: 1 << 23, 10: 8193, 13: 8193}, EINVAL),                       # R N
+        ({7: 1024, 10: (1 << 20) + 1, 13: 1 << 21}, EINVAL),              # E N
+        ({3: 1 << 23, 1: 512}, EINVAL),                                   # T ld
+        ({1: 1 << 24}, EINVAL), ({1: 1 << 61, 3: 8}, EINVAL), ({1: -128}, EINVAL)])
+    assert L.moe_sort_workspace(1 << 23, 8, 32) == EINVAL and L.moe_sort_workspace(1 << 23, 8, 31) > 0
