@@ -10,9 +10,21 @@
 // packed chunk of 1 KB, 16 bytes a lane; the activations' fragment is 16 bytes
 // of 16 rows.
 //
-// Streaming kernel.  A workgroup has P panels of 16 weight rows and up to
-// 16 MI tokens; its eight waves take every eighth chunk of K and add their
-// sums in LDS.
+// Streaming kernel, for few rows, which are bound by the weights' bytes: a
+// workgroup has P panels of 16 weight rows and up to 16 MI tokens; its eight
+// waves take every eighth chunk of K, both operands straight to registers, and
+// add their sums in LDS.  32 x 8192 -> 28672 takes 38.8 us, 6.1 TB/s of weights.
+//
+// Tiles, for more rows: four waves have all rows of the tile and a quarter of
+// its columns each.  The activations, which all four need, go through LDS, in
+// four stages of 128 codes asked for three steps ahead; the weights, which no
+// other wave of the workgroup needs, go to registers, two steps ahead, and the
+// loads of a chunk are issued behind its last product.  4096 x 7168 -> 18432
+// takes 413 us, 2620 TOPS: the matrix units are busy 74% of the time at the
+// 1.6 GHz that the power limit leaves; without any load it would take 307 us,
+// without stores 375.
+//
+// Grouped products take pieces of one expert's rows in either way.
 #include <algorithm>
 #include <type_traits>
 
@@ -748,19 +760,28 @@ int launch_stream(const Product& p, int64_t M, hipStream_t s) {
 
 }  // namespace
 
-// Which shape of tiles: the largest one that gives every compute unit work.
-// Measured (us; 128 x 256, 128 x 128, 64 x 128 and 32 x 128 rows x columns):
-//   4096 x 7168 -> 18432   413 505 658 947     1024 x 7168 -> 18432  138 147 179 279
-//   2048 x 4096 -> 4096     37  36  40  57     512 x 4096 -> 4096     44  27  17  18
-//   128 x 8192 -> 28672     81  57  66  92     128 x 4096 -> 4096     43  26  16  12
-// Up to 32 rows the weights are streamed: 38.8 us for 32 x 8192 -> 28672,
-// 41.2 by tiles of 32 rows.
+// Which shape of tiles: the one whose rounds (256 compute units take that many
+// tiles at a time) take the least time, by what one round of 7168 columns takes
+// in microseconds with many rounds or with one.  Measured (us; 128 x 256,
+// 128 x 128, 64 x 128 and 32 x 128 rows x columns, * for the one chosen):
+//   4096 x 7168 -> 18432  413* 505  658  947     1024 x 7168 -> 18432  138* 147  179  279
+//    512 x 7168 -> 18432   95   89* 102  141      256 x 7168 -> 18432   54*  65   68   87
+//    160 x 7168 -> 18432   48   58   47*  57      128 x 7168 -> 18432   54   39*  50   58
+//     64 x 7168 -> 18432   49   33   30*  43      256 x 18432 -> 7168  117   82   61*  88
+//   2048 x 4096 -> 4096    37*  36   40   57     1024 x 4096 -> 4096    29   21*  23   29
+//    512 x 4096 -> 4096    44   27   17*  18      256 x 4096 -> 4096    27   18   12   10*
+//     64 x 4096 -> 131072 100  106  103* 113      128 x 4096 -> 131072 109* 119  130  171
+// Up to 32 rows the weights are streamed: 38.8 us for 32 x 8192 -> 28672, 41.2
+// by tiles of 32 rows.
 int launch_gemm(const Product& p, int64_t M, hipStream_t s) {
   if (M <= 32) return launch_stream(p, M, s);
-  auto tiles = [&](int64_t rows, int64_t cols) { return (M + rows - 1) / rows * ((p.N + cols - 1) / cols); };
-  if (tiles(128, 256) >= 256) return launch_tiles<Cfg<8, 4>, 2>(p, M, s);
-  if (M > 64 && M <= 128 && tiles(128, 128) >= 128) return launch_tiles<Cfg<8, 2>, 2>(p, M, s);
-  if (tiles(64, 128) >= 192) return launch_tiles<Cfg<4, 2>, 3>(p, M, s);
+  auto time = [&](int64_t rows, int64_t cols, int64_t round) {
+    return ((M + rows - 1) / rows * ((p.N + cols - 1) / cols) + 255) / 256 * round;
+  };
+  const int64_t t84 = time(128, 256, 43), t82 = time(128, 128, 27), t42 = time(64, 128, 18), t22 = time(32, 128, 14);
+  if (t84 <= std::min({t82, t42, t22})) return launch_tiles<Cfg<8, 4>, 2>(p, M, s);
+  if (t82 <= std::min(t42, t22)) return launch_tiles<Cfg<8, 2>, 2>(p, M, s);
+  if (t42 <= t22) return launch_tiles<Cfg<4, 2>, 3>(p, M, s);
   return launch_tiles<Cfg<2, 2>, 4>(p, M, s);
 }
 

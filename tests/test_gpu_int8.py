@@ -225,7 +225,8 @@ def test_gemm_streamed(F, panels, out, bias):
 
 
 @pytest.mark.parametrize("out,bias", [(bf16, False), (f32, True)])
-@pytest.mark.parametrize("M,N", [(2050, 4101), (4200, 2048), (100, 16400), (65, 20001), (300, 5000), (900, 1700), (200, 6001)])
+@pytest.mark.parametrize("M,N", [(250, 16600), (2050, 4101), (4200, 2048), (100, 16400), (65, 20001), (300, 5000),
+                                 (900, 1700), (200, 6001)])
 def test_gemm_tiles(F, M, N, out, bias):
     """The larger tiles, with one step of K, each number of steps up to the
     ring's length, and some past it."""
@@ -234,7 +235,7 @@ def test_gemm_tiles(F, M, N, out, bias):
 
 
 @pytest.mark.parametrize("out", [bf16, f32])
-@pytest.mark.parametrize("M,N", [(2050, 4098), (100, 16402), (300, 5002)])
+@pytest.mark.parametrize("M,N", [(250, 16602), (2050, 4098), (300, 5002)])
 def test_gemm_tiles_into_strided_rows(F, M, N, out):
     K, g = 400, _gen(M)
     a, wp = _laid_out(_rand_codes((M, K), g)), F.int8_weight_pack(_rand_codes((N, K), g))
