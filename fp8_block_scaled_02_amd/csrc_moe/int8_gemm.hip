@@ -10,7 +10,7 @@
 // packed chunk of 1 KB, 16 bytes a lane; the activations' fragment is 16 bytes
 // of 16 rows.
 //
-// Streaming kernel, for few rows, which are bound by the weights' bytes: a
+// Streaming kernel, for up to 32 rows, which are bound by the weights' bytes: a
 // workgroup has P panels of 16 weight rows and up to 16 MI tokens; its eight
 // waves take every eighth chunk of K, both operands straight to registers, and
 // add their sums in LDS.  32 x 8192 -> 28672 takes 38.8 us, 6.1 TB/s of weights.
@@ -323,11 +323,13 @@ __device__ __forceinline__ void load_lds(__amdgpu_buffer_rsrc_t r, uint32_t off,
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)lds, 16, off, step_off, 0, 0);
 }
 
-// Four waves, each with all 16 MI rows of a and 16 NJ of the weights.
-template <int MI_, int NJ_>
+// G groups of four waves, each with all 16 MI rows of a and 16 NJ of the weights;
+// a group takes every G-th step of K.
+template <int MI_, int NJ_, int G_ = 1>
 struct Cfg {
-  static constexpr int MI = MI_, NJ = NJ_;
-  static constexpr int kWaves = 4, kThreads = 64 * kWaves;
+  static constexpr int MI = MI_, NJ = NJ_, G = G_;
+  static constexpr int kWaves = 4, kThreads = 64 * kWaves * G;
+  static constexpr int kStage = 16 * MI * kStep * G;  // bytes of LDS
   static constexpr int kRows = 16 * MI, kCols = 64 * NJ;
   static constexpr int kA = kRows / 8 / kWaves;  // pieces of 8 rows of a that a wave brings in a step
   static_assert(kRows % (8 * kWaves) == 0, "pieces split evenly");
@@ -362,10 +364,10 @@ template <int MI, int NJ, bool BF16>
 __device__ __forceinline__ void store_tile(const Product& p, const Rows& r, int64_t first,
                                            const v4i (&acc)[MI][NJ], const Four (&scales)[NJ], const float (&rows)[MI],
                                            Stores how) {
-  static_assert(NJ == 2 || NJ == 4, "transposed by twos or fours");
+  static_assert(NJ == 1 || NJ == 2 || NJ == 4, "transposed by twos or fours, or not");
   const int lane = threadIdx.x & 63, l16 = lane & 15, g = lane >> 4;
   if (first * 16 >= p.N) return;
-  const bool whole = how == Stores::lines && (first + NJ) * 16 <= p.N;
+  const bool whole = NJ > 1 && how == Stores::lines && (first + NJ) * 16 <= p.N;
 #pragma unroll
   for (int i = 0; i < MI; ++i) {
     const int m = 16 * i + l16;
@@ -398,7 +400,7 @@ __device__ __forceinline__ void store_tile(const Product& p, const Rows& r, int6
           swap32(d[1][q], d[3][q]);
           swap16(d[0][q], d[1][q]);
           swap16(d[2][q], d[3][q]);
-        } else {
+        } else if constexpr (NJ == 2) {
           swap16(d[0][q], d[1][q]);
         }
       }
@@ -437,20 +439,23 @@ __device__ __forceinline__ void store_tile(const Product& p, const Rows& r, int6
   }
 }
 
-// st0 .. st3: the stages, C::kRows * kStep bytes of LDS each, arrays of their
-// own (so that the compiler can tell which of them a load to LDS writes).
+// st0 .. st3: the stages, C::kStage bytes of LDS each, arrays of their own (so that the compiler can tell which of them a load to LDS writes).
 template <class C, bool BF16, bool ONCE = false>
 __device__ __forceinline__ void tile(const Product& p, const Rows& r, int64_t panel0, Stores store, int8_t* st0,
                                      int8_t* st1, int8_t* st2, int8_t* st3) {
-  constexpr int MI = C::MI, NJ = C::NJ;
+  constexpr int MI = C::MI, NJ = C::NJ, G = C::G;
   // (made anew in every branch of a kernel with several tiles: what follows
   // from it is not kept in registers that the products need)
   int lane = threadIdx.x & 63;
   asm volatile("" : "+v"(lane));
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int id = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wave = id & 3, group = G > 1 ? id >> 2 : 0;
   const int l16 = lane & 15, g = lane >> 4;
   const int64_t panels = (p.N + 15) / 16;
-  const int steps = (int)((p.K + kStep - 1) / kStep);
+  // Step t of the group is step G t + group of K; in the last one some groups
+  // may have nothing left: they read what is there and multiply nothing.
+  const int all = (int)((p.K + kStep - 1) / kStep), steps = (all + G - 1) / G;
+  auto of = [&](int t) { return G > 1 ? min(G * t + group, all - 1) : t; };
   const int8_t* abase = p.a + (r.index ? 0 : r.m0 * p.lda);
   uint32_t aoff[C::kA];
 #pragma unroll
@@ -470,10 +475,15 @@ __device__ __forceinline__ void tile(const Product& p, const Rows& r, int64_t pa
     for (int j = 0; j < NJ; ++j) w[j] = load16<ONCE>(b, woff[j]);
   };
   const __amdgpu_buffer_rsrc_t abuf = buffer_at(abase);
+  const int own = group * C::kRows * kStep;
+  st0 += own;
+  st1 += own;
+  st2 += own;
+  st3 += own;
   auto issue = [&](int8_t* st, int t) {
 #pragma unroll
     for (int q = 0; q < C::kA; ++q)
-      load_lds(abuf, aoff[q], (uint32_t)(t * kStep), st + 1024 * (wave + C::kWaves * q));
+      load_lds(abuf, aoff[q], (uint32_t)(of(t) * kStep), st + 1024 * (wave + C::kWaves * q));
   };
   // the scales, before the products where there are registers for them (a small
   // product's time is that of a few loads that wait for another)
@@ -496,7 +506,7 @@ __device__ __forceinline__ void tile(const Product& p, const Rows& r, int64_t pa
   // Step t multiplies stage t % 4 by the weights of set t % 2: the first
   // chunk's products, then the second's, each chunk's registers loaded again
   // for step t + 2 as soon as its products are issued.
-  auto step = [&](int t, const int8_t* cur, Weights<NJ>& w, int8_t* refill, bool more_a, bool more_w, bool full) {
+  auto step = [&](int t, const int8_t* cur, Weights<NJ>& w, int8_t* refill, bool more_a, bool more_w, bool full, bool live = true) {
     // this wave's part of stage t is in LDS; what may still fly is younger:
     // the stages of t + 1 and t + 2, the weights from t on
     if (full) wait_loads<4 * NJ + 2 * C::kA>(); else wait_loads<0>();
@@ -511,9 +521,10 @@ __device__ __forceinline__ void tile(const Product& p, const Rows& r, int64_t pa
       for (int i = 0; i < MI; ++i) {
         const v4i v = *reinterpret_cast<const v4i*>(x + 2048 * i);
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) acc[i][j] = mfma(w.w[h][j], v, acc[i][j]);
+        for (int j = 0; j < NJ; ++j)
+          if (live) acc[i][j] = mfma(w.w[h][j], v, acc[i][j]);
       }
-      if (more_w) load_w(w.w[h], 2 * (t + 2) + h);
+      if (more_w) load_w(w.w[h], 2 * of(t + 2) + h);
     }
     // the order of the step's instructions: loads to LDS (0x20), LDS reads
     // (0x100), products (0x8), and the loads of weights behind each chunk
@@ -533,11 +544,11 @@ __device__ __forceinline__ void tile(const Product& p, const Rows& r, int64_t pa
   const int last = steps - 1;
   issue(st0, 0);
   issue(st1, min(1, last));
-  load_w(w0.w[0], 0);
-  load_w(w0.w[1], 1);
+  load_w(w0.w[0], 2 * of(0));
+  load_w(w0.w[1], 2 * of(0) + 1);
   issue(st2, min(2, last));
-  load_w(w1.w[0], 2 * min(1, last));
-  load_w(w1.w[1], 2 * min(1, last) + 1);
+  load_w(w1.w[0], 2 * of(min(1, last)));
+  load_w(w1.w[1], 2 * of(min(1, last)) + 1);
   int t = 0;
   for (; t + 7 <= steps; t += 4) {
     step(t, st0, w0, st3, true, true, true);
@@ -547,7 +558,8 @@ __device__ __forceinline__ void tile(const Product& p, const Rows& r, int64_t pa
   }
   // one to six more
   auto tail = [&](int u, const int8_t* cur, Weights<NJ>& w, int8_t* refill) {
-    if (u < steps) step(u, cur, w, refill, u + 3 < steps, u + 2 < steps, u + 2 < steps);
+    if (u < steps)
+      step(u, cur, w, refill, u + 3 < steps, u + 2 < steps, u + 2 < steps, G == 1 || G * u + group < all);
   };
   tail(t, st0, w0, st3);
   tail(t + 1, st1, w1, st0);
@@ -556,6 +568,35 @@ __device__ __forceinline__ void tile(const Product& p, const Rows& r, int64_t pa
   tail(t + 4, st0, w0, st3);
   tail(t + 5, st1, w1, st0);
   wait_loads<0>();
+  if constexpr (G > 1) {
+    // the groups' sums join in LDS, 4 KB of a fragment of all four waves
+    constexpr int kIn = C::kStage / 4096;
+    static_assert(4 * kIn >= (G - 1) * MI * NJ, "the stages hold them");
+    st0 -= own;
+    st1 -= own;
+    st2 -= own;
+    st3 -= own;
+    auto at = [&](int f) {
+      int8_t* st = f / kIn == 0 ? st0 : f / kIn == 1 ? st1 : f / kIn == 2 ? st2 : st3;
+      return reinterpret_cast<v4i*>(st + f % kIn * 4096 + wave * 1024 + 16 * lane);
+    };
+    __syncthreads();
+#pragma unroll
+    for (int other = 1; other < G; ++other)
+      if (group == other)
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+          for (int j = 0; j < NJ; ++j) *at(((other - 1) * MI + i) * NJ + j) = acc[i][j];
+    __syncthreads();
+    if (group) return;
+#pragma unroll
+    for (int other = 1; other < G; ++other)
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) acc[i][j] += *at(((other - 1) * MI + i) * NJ + j);
+  }
   if (!kEarly) load_scales();
   store_tile<MI, NJ, BF16>(p, r, first, acc, scales, row_scales, store);
 }
@@ -580,10 +621,10 @@ __global__ __launch_bounds__(C::kThreads, OCC) void tile_kernel(Product p, int64
   tile_of(blockIdx.x, tiles_m, tiles_n, tm, tn);
   const int64_t m0 = (int64_t)tm * C::kRows;
   const Rows r{nullptr, M, m0, (int)min((int64_t)C::kRows, M - m0), p.w, p.sw};
-  __shared__ __attribute__((aligned(16))) int8_t st0[C::kRows * kStep];
-  __shared__ __attribute__((aligned(16))) int8_t st1[C::kRows * kStep];
-  __shared__ __attribute__((aligned(16))) int8_t st2[C::kRows * kStep];
-  __shared__ __attribute__((aligned(16))) int8_t st3[C::kRows * kStep];
+  __shared__ __attribute__((aligned(16))) int8_t st0[C::kStage];
+  __shared__ __attribute__((aligned(16))) int8_t st1[C::kStage];
+  __shared__ __attribute__((aligned(16))) int8_t st2[C::kStage];
+  __shared__ __attribute__((aligned(16))) int8_t st3[C::kStage];
   tile<C, BF16>(p, r, (int64_t)tn * C::NJ * 4, store, st0, st1, st2, st3);
 }
 
@@ -763,26 +804,35 @@ int launch_stream(const Product& p, int64_t M, hipStream_t s) {
 // Which shape of tiles: the one whose rounds (256 compute units take that many
 // tiles at a time) take the least time, by what one round of 7168 columns takes
 // in microseconds with many rounds or with one.  Measured (us; 128 x 256,
-// 128 x 128, 64 x 128 and 32 x 128 rows x columns, * for the one chosen):
-//   4096 x 7168 -> 18432  413* 505  658  947     1024 x 7168 -> 18432  138* 147  179  279
-//    512 x 7168 -> 18432   95   89* 102  141      256 x 7168 -> 18432   54*  65   68   87
-//    160 x 7168 -> 18432   48   58   47*  57      128 x 7168 -> 18432   54   39*  50   58
-//     64 x 7168 -> 18432   49   33   30*  43      256 x 18432 -> 7168  117   82   61*  88
-//   2048 x 4096 -> 4096    37*  36   40   57     1024 x 4096 -> 4096    29   21*  23   29
-//    512 x 4096 -> 4096    44   27   17*  18      256 x 4096 -> 4096    27   18   12   10*
-//     64 x 4096 -> 131072 100  106  103* 113      128 x 4096 -> 131072 109* 119  130  171
-// Up to 32 rows the weights are streamed: 38.8 us for 32 x 8192 -> 28672, 41.2
-// by tiles of 32 rows.
+// 128 x 128, 64 x 128, 32 x 128 and 32 x 64 rows x columns, * for the one chosen):
+//   4096 x 7168 -> 18432  413* 505  658  947       1024 x 7168 -> 18432  138* 147  179  279
+//    512 x 7168 -> 18432   95   89* 102  141        256 x 7168 -> 18432   54*  65   68   87
+//    160 x 7168 -> 18432   48   60   47*  57        128 x 7168 -> 18432   54   39*  50   58
+//     64 x 7168 -> 18432   49   33   30*  43   41   256 x 18432 -> 7168  117   82   61*  88
+//   2048 x 4096 -> 4096    37*  36   40   55       1024 x 4096 -> 4096    29   21*  22   29
+//    512 x 4096 -> 4096    44   19   13*  17        256 x 4096 -> 4096    27   18   11   10*  11
+//    128 x 4096 -> 4096    43   18   11    9    8*   64 x 7168 -> 2048         26   16   13   10*
+//     64 x 4096 -> 131072 100  106  103* 113        128 x 4096 -> 131072 109* 119  130  171
+// A compute unit with one small tile is bound by its loads; from 2048 columns on
+// two groups of waves that take the steps in turn are faster (64 x 7168 -> 2048
+// 9.6 against 11.2, 128 x 1480 -> 2048 5.0 against 4.5).  That did nothing for
+// the larger tiles.
+// Up to 16 rows the weights are streamed (16 x 4096 -> 4096 6.3 us, 7.1 by tiles
+// of 32 x 64), up to 32 where such tiles would be more than the compute units (32 x
+// 7168 -> 18432 25 against 30; 32 x 4096 -> 4096 8.2 against 7.5).
 int launch_gemm(const Product& p, int64_t M, hipStream_t s) {
-  if (M <= 32) return launch_stream(p, M, s);
-  auto time = [&](int64_t rows, int64_t cols, int64_t round) {
-    return ((M + rows - 1) / rows * ((p.N + cols - 1) / cols) + 255) / 256 * round;
+  auto rounds = [&](int64_t rows, int64_t cols) {
+    return ((M + rows - 1) / rows * ((p.N + cols - 1) / cols) + 255) / 256;
   };
-  const int64_t t84 = time(128, 256, 43), t82 = time(128, 128, 27), t42 = time(64, 128, 18), t22 = time(32, 128, 14);
-  if (t84 <= std::min({t82, t42, t22})) return launch_tiles<Cfg<8, 4>, 2>(p, M, s);
-  if (t82 <= std::min(t42, t22)) return launch_tiles<Cfg<8, 2>, 2>(p, M, s);
-  if (t42 <= t22) return launch_tiles<Cfg<4, 2>, 3>(p, M, s);
-  return launch_tiles<Cfg<2, 2>, 4>(p, M, s);
+  const int64_t r21 = rounds(32, 64);
+  if (M <= (r21 > 1 ? 32 : 16)) return launch_stream(p, M, s);
+  const int64_t t84 = rounds(128, 256) * 43, t82 = rounds(128, 128) * 27, t42 = rounds(64, 128) * 18,
+                t22 = rounds(32, 128) * 14, t21 = r21 * 10;
+  if (t84 <= std::min({t82, t42, t22, t21})) return launch_tiles<Cfg<8, 4>, 2>(p, M, s);
+  if (t82 <= std::min({t42, t22, t21})) return launch_tiles<Cfg<8, 2>, 2>(p, M, s);
+  if (t42 <= std::min(t22, t21)) return launch_tiles<Cfg<4, 2>, 3>(p, M, s);
+  if (t22 <= t21) return launch_tiles<Cfg<2, 2>, 4>(p, M, s);
+  return p.K < 2048 ? launch_tiles<Cfg<2, 1>, 4>(p, M, s) : launch_tiles<Cfg<2, 1, 2>, 4>(p, M, s);
 }
 
 int launch_grouped(const Product& p, int64_t T, const int32_t* row_index, const int32_t* offsets, int64_t R, int E,

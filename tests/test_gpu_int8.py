@@ -234,6 +234,15 @@ def test_gemm_tiles(F, M, N, out, bias):
         _check_gemm(F, M, N, K, out, bias, K)
 
 
+@pytest.mark.parametrize("out,bias", [(bf16, True), (f32, False)])
+@pytest.mark.parametrize("M,N", [(17, 64), (33, 130), (101, 1001), (250, 2000), (31, 16384)])
+def test_gemm_small_tiles(F, M, N, out, bias):
+    """Tiles of 32 x 64, by one group of waves and by two that take the steps
+    in turn, with even and odd numbers of steps."""
+    for K in (77, 1000, 2047, 2048, 2100, 2200, 2304, 2500, 4000, 8200):
+        _check_gemm(F, M, N, K, out, bias, K)
+
+
 @pytest.mark.parametrize("out", [bf16, f32])
 @pytest.mark.parametrize("M,N", [(250, 16602), (2050, 4098), (300, 5002)])
 def test_gemm_tiles_into_strided_rows(F, M, N, out):
