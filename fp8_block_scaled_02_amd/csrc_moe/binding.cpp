@@ -11,6 +11,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/core/TensorImpl.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -178,6 +179,39 @@ PyObject* tuple(std::initializer_list<Tensor> ts) {
 Tensor empty(at::IntArrayRef s, at::ScalarType type, const Tensor& like) {
   return at::empty(s, like.options().dtype(type));
 }
+int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
+
+// A call's outputs.  Small ones share one allocation, each from a 128-byte line
+// on: a tensor from the allocator costs the host 1 us, one of these a tenth (a
+// decode step's router, five tensors: 8.5 -> 5.9 us of the host).  Larger ones
+// have their own, since any part keeps the whole alive.
+struct Block {
+  static constexpr int64_t kShared = (int64_t)1 << 20;
+  const Tensor& like;
+  Tensor all;
+  int64_t at = 0;
+  Block(int64_t bytes, const Tensor& like_) : like(like_) {
+    if (bytes > 0 && bytes <= kShared) all = empty({bytes}, at::kByte, like);
+  }
+  static int64_t room(int64_t bytes) { return up(bytes, 128); }
+  // A vector, or rows `ld` elements apart (0: no gaps).
+  Tensor take(at::ScalarType type, at::IntArrayRef sizes, int64_t ld = 0) {
+    const bool gaps = ld && ld != sizes[1];
+    if (!all.defined()) return gaps ? empty({sizes[0], ld}, type, like).narrow(1, 0, sizes[1]) : empty(sizes, type, like);
+    const int64_t item = type == at::kChar ? 1 : 4, n = sizes.size() == 1 ? sizes[0] : sizes[0] * (ld ? ld : sizes[1]);
+    Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(),
+                                                        c10::scalarTypeToTypeMeta(type));
+    c10::TensorImpl* impl = t.unsafeGetTensorImpl();
+    impl->set_storage_offset(at / item);
+    if (gaps)
+      impl->set_sizes_and_strides(sizes, {ld, 1});
+    else
+      impl->set_sizes_contiguous(sizes);
+    at += room(n * item);
+    return t;
+  }
+};
+
 template <typename T>
 T* ptr(const Tensor& t) {
   return static_cast<T*>(t.data_ptr());
@@ -201,11 +235,12 @@ struct Router {
   }
   int run(const Tensor& logits, bool renormalize, void* stream, Plan& p) const {
     const int64_t T = l.rows;
-    p.gates = empty({T, k}, at::kFloat, logits);
-    p.experts = empty({T, k}, at::kInt, logits);
-    p.offsets = empty({l.cols + 1}, at::kInt, logits);
-    p.row_index = empty({T * k}, at::kInt, logits);
-    p.token_rows = empty({T, k}, at::kInt, logits);
+    Block b(4 * Block::room(4 * T * k) + Block::room(4 * (l.cols + 1)), logits);
+    p.gates = b.take(at::kFloat, {T, k});
+    p.experts = b.take(at::kInt, {T, k});
+    p.offsets = b.take(at::kInt, {l.cols + 1});
+    p.row_index = b.take(at::kInt, {T * k});
+    p.token_rows = b.take(at::kInt, {T, k});
     const Tensor ws = ws_bytes ? empty({ws_bytes}, at::kByte, logits) : Tensor();
     void* wsp = ws_bytes ? ws.data_ptr() : nullptr;
     return launch([&] {
@@ -248,8 +283,9 @@ PyObject* sort(PyObject* const* a) {
   if (bytes < 0) refuse("too many tokens: T < 2^24 and T * k < 2^28");
   on(experts.get_device(), {});
   void* stream = address(a[0]);
-  const Tensor offsets = empty({E + 1}, at::kInt, experts), row_index = empty({s.T * s.k}, at::kInt, experts);
-  const Tensor token_rows = empty({s.T, s.k}, at::kInt, experts);
+  Block b(Block::room(4 * (E + 1)) + 2 * Block::room(4 * s.T * s.k), experts);
+  const Tensor offsets = b.take(at::kInt, {E + 1}), row_index = b.take(at::kInt, {s.T * s.k});
+  const Tensor token_rows = b.take(at::kInt, {s.T, s.k});
   const Tensor ws = bytes ? empty({bytes}, at::kByte, experts) : Tensor();
   void* wsp = bytes ? ws.data_ptr() : nullptr;
   const int rc = launch([&] {
@@ -368,15 +404,6 @@ PyObject* combine_backward(PyObject* const* a) {
 
 // ---- 8-bit integers ---------------------------------------------------------
 
-int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
-
-// Codes [M, K] whose rows are whole 128-byte lines, the bytes from K on unwritten.
-Tensor empty_codes(int64_t M, int64_t K, const Tensor& like) {
-  const int64_t ld = up(K, 128);
-  Tensor t = empty({M, ld}, at::kChar, like);
-  return ld == K ? t : t.narrow(1, 0, K);
-}
-
 Mat quant_input(const Tensor& x) {
   const Mat m = real(x, "x");
   if (m.cols < 1) refuse("x must have a column");
@@ -399,8 +426,11 @@ PyObject* quant(PyObject* const* a) {
   }
   on(x.get_device(), {gc, gs});
   void* stream = address(a[0]);
-  const Tensor codes = gc ? *gc : empty_codes(m.rows, m.cols, x);
-  const Tensor scales = gs ? *gs : empty({m.rows}, at::kFloat, x);
+  // new codes have their rows whole 128-byte lines apart, the bytes behind them unwritten
+  const int64_t ld = up(m.cols, 128);
+  Block b((gc ? 0 : m.rows * ld) + (gs ? 0 : Block::room(4 * m.rows)), x);
+  const Tensor codes = gc ? *gc : b.take(at::kChar, {m.rows, m.cols}, ld);
+  const Tensor scales = gs ? *gs : b.take(at::kFloat, {m.rows});
   const Mat o = mat(codes, "codes");
   const int rc = launch([&] {
     return int8_quant(m.p, m.type, m.rows, m.cols, m.ld, static_cast<int8_t*>(o.p), o.ld, ptr<float>(scales), stream);
@@ -532,19 +562,19 @@ PyObject* grouped(PyObject* const* a) {
   return rc ? status(rc) : THPVariable_Wrap(y);
 }
 
-// x's codes and scales.
+// Room for x's codes and scales, one behind the other.
 struct Quantised {
-  Tensor c, s;
   int64_t ld;
+  Tensor both;
+  int8_t* c;
+  float* s;
+  Quantised(const Tensor& x, const Mat& m)
+      : ld(up(m.cols, 128)), both(empty({m.rows * (ld + (int64_t)sizeof(float))}, at::kChar, x)), c(ptr<int8_t>(both)),
+        s(reinterpret_cast<float*>(c + m.rows * ld)) {}
+  int make(const Mat& m, void* stream) const {
+    return int8_quant(m.p, m.type, m.rows, m.cols, m.ld, c, ld, s, stream);
+  }
 };
-int quantise(const Tensor& x, const Mat& m, void* stream, Quantised& q) {
-  q.c = empty({m.rows, up(m.cols, 128)}, at::kChar, x);
-  q.s = empty({m.rows}, at::kFloat, x);
-  q.ld = up(m.cols, 128);
-  return launch([&] {
-    return int8_quant(m.p, m.type, m.rows, m.cols, m.ld, ptr<int8_t>(q.c), q.ld, ptr<float>(q.s), stream);
-  });
-}
 
 // (stream, x, w_packed, w_scales, bias, fp32) -> y
 PyObject* linear(PyObject* const* a) {
@@ -556,13 +586,13 @@ PyObject* linear(PyObject* const* a) {
   const at::ScalarType type = out_type(a[5]);
   on(x.get_device(), {&w.w, &w.sw, bias});
   void* stream = address(a[0]);
-  Quantised q;
-  if (const int rc = quantise(x, m, stream, q)) return status(rc);
+  const Quantised q(x, m);
   const Tensor y = empty({m.rows, w.N}, type, x);
   void* yp = y.data_ptr();
   const int rc = launch([&] {
-    return int8_gemm(ptr<int8_t>(q.c), q.ld, ptr<float>(q.s), ptr<int8_t>(w.w), ptr<float>(w.sw), bp, m.rows, w.N,
-                     m.cols, yp, w.N, type_of(type), stream);
+    if (const int rc1 = q.make(m, stream)) return rc1;
+    return int8_gemm(q.c, q.ld, q.s, ptr<int8_t>(w.w), ptr<float>(w.sw), bp, m.rows, w.N, m.cols, yp, w.N, type_of(type),
+                     stream);
   });
   return rc ? status(rc) : THPVariable_Wrap(y);
 }
@@ -586,18 +616,18 @@ PyObject* forward(PyObject* const* a) {
   if (const int rc = r.run(logits, renormalize, stream, p)) return status(rc);
   const Tensor out = empty({T, w.N}, type, x);
   if (T > 0) {
-    Quantised q;
-    if (const int rc = quantise(x, m, stream, q)) return status(rc);
+    const Quantised q(x, m);
     // an expert's rows in the output's type: for bf16 each is rounded once more,
     // and half as many bytes go out and come back (at 4096 tokens, 8 slots of
     // 7168, 470 MB against 940); the sum over the slots is in fp32 either way
     const Tensor y = empty({R, w.N}, type, x);
     void *yp = y.data_ptr(), *op = out.data_ptr();
     const int rc = launch([&] {
-      const int rc1 = int8_grouped_gemm(ptr<int8_t>(q.c), q.ld, ptr<float>(q.s), T, ptr<int32_t>(p.row_index),
-                                        ptr<int32_t>(p.offsets), R, E, ptr<int8_t>(w.w), ptr<float>(w.sw), w.N, m.cols,
-                                        yp, w.N, type_of(type), stream);
-      if (rc1) return rc1;
+      if (const int rc1 = q.make(m, stream)) return rc1;
+      if (const int rc1 = int8_grouped_gemm(q.c, q.ld, q.s, T, ptr<int32_t>(p.row_index), ptr<int32_t>(p.offsets), R, E,
+                                            ptr<int8_t>(w.w), ptr<float>(w.sw), w.N, m.cols, yp, w.N, type_of(type),
+                                            stream))
+        return rc1;
       return moe_combine(yp, type_of(type), w.N, R, w.N, ptr<int32_t>(p.token_rows), ptr<float>(p.gates), T, k, op,
                          type_of(type), w.N, stream);
     });

@@ -8,7 +8,8 @@ tensors' device.  The calls go through a small native module
 There is no fallback: if libfp8moe.so or the module is missing the functions
 raise on first use.  Nothing here records a gradient: the backward passes are
 calls of their own.  Outputs given by the caller share no memory with each
-other or with inputs; 2-D tensors may have any row stride unless stated.
+other or with inputs; 2-D tensors may have any row stride unless stated.  New
+outputs of one call may be parts of one small allocation (up to 1 MB).
 """
 import ctypes
 import os

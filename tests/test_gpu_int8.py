@@ -107,6 +107,19 @@ def test_quant_past_32_bits(F, big):
     assert np.array_equal(c[M - 2:].cpu().numpy(), want[0]) and np.array_equal(s[M - 2:].cpu().numpy(), want[1])
 
 
+def test_outputs_hold_no_others_memory(F, big):
+    """Scales and weights kept after what came with them is dropped hold their own bytes only, but for small calls."""
+    x = torch.zeros(512, 1 << 16, dtype=bf16, device=DEV)
+    c, s = F.int8_quant(x)
+    assert s.untyped_storage().nbytes() == 2048 and c.untyped_storage().nbytes() == 512 << 16
+    r = F.moe_route(torch.zeros(1 << 17, 8, device=DEV), 2)
+    assert r.gates.untyped_storage().nbytes() == 1 << 20
+    parts = [t for t in (*F.moe_route(torch.zeros(5, 9, device=DEV), 3), *F.int8_quant(x[:3, :200]))]
+    for i, a in enumerate(parts):
+        for b in parts[:i]:
+            assert a.data_ptr() >= b.data_ptr() + b.numel() * b.element_size() or b.data_ptr() >= a.data_ptr() + a.numel() * a.element_size()
+
+
 def test_quant_at_halves(F):
     """Quotients at and next to a half, for many scales: the whole number
     nearest to the fp32 quotient."""
