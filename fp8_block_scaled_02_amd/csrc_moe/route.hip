@@ -3,13 +3,14 @@
 //
 // Choosing.  G lanes hold one token's E logits, V to a lane (lane l those of
 // experts l, l + G, ...), as unsigned keys that order like the numbers.  The
-// k-th largest of 16 lanes' largest keys is a lower bound of the token's k-th
-// largest key; what reaches it, rarely much more than k, goes to LDS, where
-// every candidate counts those before it (larger, or equal and of a lower
-// expert): that is its slot.  Where that does not hold (k > 16, more than 64
-// candidates, E > 256), k times over the largest key is found in the lane, then
-// over the lanes, and leaves.  Instructions bound it: for 16384 tokens, 8 of
-// 256 experts, the k-fold search took 14.4 us, this 9.4.
+// k-th largest of 16 lanes' largest keys (of 16 sets of four lanes' in a whole
+// wave) is a lower bound of the token's k-th largest key; what reaches it,
+// rarely much more than k, goes to LDS, where every candidate counts those
+// before it (larger, or equal and of a lower expert): that is its slot.  Where
+// that does not hold (k > 16, more than 64 candidates), k times over the largest
+// key is found in the lane, then over the lanes, and leaves.  Instructions bound
+// it: for 16384 tokens, 8 of 256 experts, the k-fold search took 14.4 us, this
+// 9.4; with the plan 8 of 512 took 48, now 24, and 32 tokens of 1024 20, now 9.7.
 // The first one chosen is the maximum that the softmax subtracts, so the
 // weights follow from the k chosen (or all E) logits without another pass.
 //
@@ -136,7 +137,7 @@ __device__ __forceinline__ void wave_sync() {
 }
 
 constexpr int kCandidates = 64;
-// Of the 16 lanes of a token; an entry is a key and the expert's complement.
+// Of the G lanes of a token; an entry is a key and the expert's complement.
 struct Candidates {
   uint64_t all[kCandidates], chosen[16];
 };
@@ -206,15 +207,20 @@ __device__ __forceinline__ int shifted(int v) {  // from the lane CTRL - 0x110 b
   return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xF, 0xF, true);
 }
 
-// The choices by candidates, of 16 lanes; false (in every lane of the wave,
-// nothing chosen) where a token of the wave has too many.
-template <int V>
-__device__ __forceinline__ bool select(const uint32_t (&key)[V], int k, Candidates& lds, Choice<4>& c, uint32_t& top) {
-  const int l = threadIdx.x & 15;
+// The choices by candidates, k <= 16; false (in every lane of the wave, nothing
+// chosen) where a token of the wave has too many.
+template <int G, int V>
+__device__ __forceinline__ bool select(const uint32_t (&key)[V], int k, Candidates& lds, Choice<64 / G>& c,
+                                       uint32_t& top) {
+  const int l = threadIdx.x % G;
   uint32_t best = key[0];
 #pragma unroll
   for (int i = 1; i < V; ++i) best = max(best, key[i]);
-  // how many lanes have a larger one
+  if constexpr (G == 64) {  // of the four lanes l, l + 16, ...: every row of 16 has the same
+    best = max(best, (uint32_t)__shfl_xor((int)best, 16));
+    best = max(best, (uint32_t)__shfl_xor((int)best, 32));
+  }
+  // how many of the row have a larger one
   int above = 0;
   auto turn = [&](auto n) { above += dpp<0x120 + decltype(n)::value>(best) > best; };
   using std::integral_constant;
@@ -237,19 +243,24 @@ __device__ __forceinline__ bool select(const uint32_t (&key)[V], int k, Candidat
   int mine = 0;
 #pragma unroll
   for (int i = 0; i < V; ++i) mine += key[i] >= bound;
-  int end = mine;  // inclusive sum over the lanes
-  end += shifted<0x111>(end);
-  end += shifted<0x112>(end);
-  end += shifted<0x114>(end);
-  end += shifted<0x118>(end);
-  const int n = (int)max_of<16>((uint32_t)end);
+  int end = mine, n;  // inclusive sum over the lanes, and the last one's
+  if constexpr (G == 64) {
+    end = wave_scan(mine);
+    n = __builtin_amdgcn_readlane(end, 63);
+  } else {
+    end += shifted<0x111>(end);
+    end += shifted<0x112>(end);
+    end += shifted<0x114>(end);
+    end += shifted<0x118>(end);
+    n = (int)max_of<16>((uint32_t)end);
+  }
   if (__any(n > kCandidates)) return false;
   int at = end - mine;
 #pragma unroll
   for (int i = 0; i < V; ++i)
-    if (key[i] >= bound) lds.all[at++] = (uint64_t)key[i] << 32 | (uint32_t)~(l + i * 16);
+    if (key[i] >= bound) lds.all[at++] = (uint64_t)key[i] << 32 | (uint32_t)~(l + i * G);
   wave_sync();
-  for (int w = l; w < n; w += 16) {
+  for (int w = l; w < n; w += G) {
     const uint64_t own = lds.all[w];
     int before = 0;
     // (four at a time, whose reads are in flight together, 6.6 us for 32 tokens
@@ -279,7 +290,7 @@ __device__ __forceinline__ bool select(const uint32_t (&key)[V], int k, Candidat
 // left in `local` too where that is given.
 template <bool BF16, int G, int V>
 __device__ __forceinline__ void choose(const Route& r, int64_t t, int32_t* __restrict__ experts, int* count,
-                                       int* local, Candidates* lds) {
+                                       int* local, Candidates& lds) {
   const int l = threadIdx.x % G;
   float x[V];
   uint32_t key[V];
@@ -296,8 +307,7 @@ __device__ __forceinline__ void choose(const Route& r, int64_t t, int32_t* __res
   }
   uint32_t top = 0;
   bool done = false;
-  if constexpr (G == 16)
-    if (r.k <= 16) done = select<V>(key, r.k, *lds, c, top);
+  if (r.k <= 16) done = select<G, V>(key, r.k, lds, c, top);
   if (!done) top = search<G, V>(key, r.k, c);
   const float m = top > kNone ? of_key(top) : 0.0f;
   float sum = 0.0f, p[W];
@@ -493,10 +503,9 @@ __global__ __launch_bounds__(kThreads) void route_kernel(Route r, Sort s) {
   for (int e = threadIdx.x; e < r.E; e += kThreads) count[e] = 0;
   __syncthreads();
   const int64_t end = min(r.T, (int64_t)(blockIdx.x + 1) * s.per_block);
-  __shared__ Candidates candidates[G == 16 ? kGroups : 1];
-  Candidates* own = G == 16 ? &candidates[threadIdx.x / 16] : nullptr;
+  __shared__ Candidates candidates[kGroups];
   for (int64_t t = (int64_t)blockIdx.x * s.per_block + threadIdx.x / G; t < end; t += kGroups)
-    choose<BF16, G, V>(r, t, s.p.experts, count, ALONE ? slots : nullptr, own);
+    choose<BF16, G, V>(r, t, s.p.experts, count, ALONE ? slots : nullptr, candidates[threadIdx.x / G]);
   __syncthreads();
   if constexpr (ALONE) {
     __shared__ PlaceLds lds;
@@ -607,6 +616,7 @@ int by_width(bool bf16, int E, F f) {
     if (E <= 64) return f(b, integral_constant<int, 16>{}, integral_constant<int, 4>{});
     if (E <= 128) return f(b, integral_constant<int, 16>{}, integral_constant<int, 8>{});
     if (E <= 256) return f(b, integral_constant<int, 16>{}, integral_constant<int, 16>{});
+    if (E <= 512) return f(b, integral_constant<int, 64>{}, integral_constant<int, 8>{});
     return f(b, integral_constant<int, 64>{}, integral_constant<int, 16>{});
   };
   return bf16 ? with(std::true_type{}) : with(std::false_type{});

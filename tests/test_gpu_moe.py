@@ -91,7 +91,7 @@ def _check_route(r, logits, k, renorm):
 @pytest.mark.parametrize("dtype", [bf16, f32])
 @pytest.mark.parametrize("T,E,k", [
     (1, 1, 1), (1, 256, 8), (7, 3, 3), (31, 16, 2), (33, 17, 5), (64, 60, 4), (65, 64, 64), (100, 65, 6), (129, 128, 8),
-    (200, 160, 6), (96, 256, 8), (40, 257, 8), (50, 512, 10), (65, 1000, 33), (33, 1024, 64), (1000, 8, 2)])
+    (200, 160, 6), (96, 256, 8), (40, 257, 8), (50, 512, 10), (100, 384, 16), (70, 1024, 16), (9, 200, 8), (16, 100, 16), (65, 1000, 33), (33, 1024, 64), (1000, 8, 2)])
 def test_route(F, T, E, k, dtype, renorm):
     l = torch.randn(T, E, generator=_gen(T + E), device=DEV).to(dtype)
     _check_route(F.moe_route(l, k, renorm), l, k, renorm)
