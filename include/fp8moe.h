@@ -73,7 +73,8 @@ int64_t moe_sort_workspace(int64_t T, int64_t E, int64_t k);
  *
  *   logits     fp32 or bf16 [T][ld].
  *   gates      float [T][k];  the plan as above;  workspace 16-byte aligned.
- *   T = 0 writes expert_offsets (zeros) alone.
+ *   T = 0 writes expert_offsets (zeros) alone.  A token's gates have the same
+ *   bits in a batch of any size.
  */
 int moe_route(const void *logits, int dtype, int64_t ld, int64_t T, int64_t E,
               int64_t k, int renormalize, float *gates, int32_t *experts,

@@ -91,10 +91,25 @@ def _check_route(r, logits, k, renorm):
 @pytest.mark.parametrize("dtype", [bf16, f32])
 @pytest.mark.parametrize("T,E,k", [
     (1, 1, 1), (1, 256, 8), (7, 3, 3), (31, 16, 2), (33, 17, 5), (64, 60, 4), (65, 64, 64), (100, 65, 6), (129, 128, 8),
-    (200, 160, 6), (96, 256, 8), (40, 257, 8), (50, 512, 10), (100, 384, 16), (70, 1024, 16), (9, 200, 8), (16, 100, 16), (65, 1000, 33), (33, 1024, 64), (1000, 8, 2)])
+    (200, 160, 6), (96, 256, 8), (40, 257, 8), (50, 512, 10), (100, 384, 16), (70, 1024, 16), (9, 200, 8), (16, 100, 16), (3, 250, 20), (17, 100, 16), (65, 1000, 33), (33, 1024, 64), (1000, 8, 2)])
 def test_route(F, T, E, k, dtype, renorm):
     l = torch.randn(T, E, generator=_gen(T + E), device=DEV).to(dtype)
     _check_route(F.moe_route(l, k, renorm), l, k, renorm)
+
+
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("E", [20, 100, 256, 500, 900])
+def test_route_does_not_depend_on_the_batch(F, E, renorm):
+    """A token's weights and gradient have the same bits, alone or among others."""
+    l = torch.randn(3000, E, generator=_gen(E), device=DEV)
+    d = torch.randn(3000, 6, generator=_gen(1), device=DEV)
+    r = F.moe_route(l, 6, renorm)
+    dl = F.moe_route_backward(d, l, r.gates, r.experts, renorm)
+    for lo, n in ((0, 1), (5, 16), (100, 17), (7, 64), (1000, 65)):
+        s = slice(lo, lo + n)
+        q = F.moe_route(l[s], 6, renorm)
+        assert torch.equal(q.gates, r.gates[s]) and torch.equal(q.experts, r.experts[s])
+        assert torch.equal(F.moe_route_backward(d[s], l[s], q.gates, q.experts, renorm), dl[s])
 
 
 @pytest.mark.parametrize("T,E,k", [(8200, 32, 3), (16500, 8, 2)])
@@ -181,7 +196,7 @@ def test_sort_extremes(F):
 @pytest.mark.parametrize("renorm", [True, False])
 @pytest.mark.parametrize("dtype", [bf16, f32])
 @pytest.mark.parametrize("T,E,k", [(1, 1, 1), (3, 5, 5), (40, 16, 2), (33, 60, 4), (50, 128, 8), (65, 256, 8),
-                                   (20, 300, 12), (17, 1024, 64)])
+                                   (20, 300, 12), (17, 1024, 64), (9000, 100, 4), (8500, 256, 8)])
 def test_route_backward(F, T, E, k, dtype, renorm):
     g = _gen(T * E)
     l = (3 * torch.randn(T, E, generator=g, device=DEV)).to(dtype)
