@@ -638,9 +638,10 @@ int launch_route(const Mat& logits, int64_t T, int E, int k, bool renormalize, f
   const Route r{logits.p, logits.ld, T, E, k, renormalize, gates};
   // As many tokens as a workgroup has waves: a wave each (8 tokens of 256 4.9 us
   // against 6.2 with 16 lanes each, 16 5.5 against 6.3; 32 are even, 64 11.5
-  // against 7.7).  Not where the sum is over all E, whose order is the lanes': a
-  // token's weights would depend on how many others there are.
-  const int rc = by_width<true>(logits.bf16, E, renormalize && T <= kThreads / 64, [&](auto b, auto G, auto V) {
+  // against 7.7).  Not where the sum is over all E, or over more chosen ones
+  // than 16 lanes have, whose order is the lanes': a token's weights would depend
+  // on how many others there are.
+  const int rc = by_width<true>(logits.bf16, E, renormalize && k <= 16 && T <= kThreads / 64, [&](auto b, auto G, auto V) {
     if (blocks == 1)
       hipLaunchKernelGGL((route_kernel<b.value, G.value, V.value, true>), dim3(1), dim3(kThreads), 0, s, r, sort);
     else

@@ -99,15 +99,16 @@ def test_route(F, T, E, k, dtype, renorm):
 
 @pytest.mark.parametrize("renorm", [True, False])
 @pytest.mark.parametrize("E", [20, 100, 256, 500, 900])
-def test_route_does_not_depend_on_the_batch(F, E, renorm):
+@pytest.mark.parametrize("k", [6, 16, 20])
+def test_route_does_not_depend_on_the_batch(F, E, k, renorm):
     """A token's weights and gradient have the same bits, alone or among others."""
     l = torch.randn(3000, E, generator=_gen(E), device=DEV)
-    d = torch.randn(3000, 6, generator=_gen(1), device=DEV)
-    r = F.moe_route(l, 6, renorm)
+    d = torch.randn(3000, k, generator=_gen(1), device=DEV)
+    r = F.moe_route(l, k, renorm)
     dl = F.moe_route_backward(d, l, r.gates, r.experts, renorm)
     for lo, n in ((0, 1), (5, 16), (100, 17), (7, 64), (1000, 65)):
         s = slice(lo, lo + n)
-        q = F.moe_route(l[s], 6, renorm)
+        q = F.moe_route(l[s], k, renorm)
         assert torch.equal(q.gates, r.gates[s]) and torch.equal(q.experts, r.experts[s])
         assert torch.equal(F.moe_route_backward(d[s], l[s], q.gates, q.experts, renorm), dl[s])
 
