@@ -356,10 +356,11 @@ struct Weights {
 
 constexpr int kAhead = 2;  // LDS reads ahead of the products: 480 us with 2 to 4 at 4096 x 7168 -> 18432, 512 with 1
 
-// A wave's sums to 16 MI rows of y, columns from panel `first` on.  Lane 16 g + l16 has four columns of row l16 of every panel, 8 bytes of
-// bf16; where whole pieces are stored the four lanes of a row change places
-// first (v_permlane*_swap), so that each has 16 bytes or more in a row and a
-// store instruction fills 64 bytes of a line or more.
+// A wave's sums to 16 MI rows of y, columns from panel `first` on.  Lane
+// 16 g + l16 has four columns of row l16 of every panel, 8 bytes of bf16; where
+// whole pieces are stored the four lanes of a row change places first
+// (v_permlane*_swap), so that each has 16 bytes or more in a row and a store
+// instruction fills 64 bytes of a line or more.
 template <int MI, int NJ, bool BF16>
 __device__ __forceinline__ void store_tile(const Product& p, const Rows& r, int64_t first,
                                            const v4i (&acc)[MI][NJ], const Four (&scales)[NJ], const float (&rows)[MI],
@@ -439,7 +440,8 @@ __device__ __forceinline__ void store_tile(const Product& p, const Rows& r, int6
   }
 }
 
-// st0 .. st3: the stages, C::kStage bytes of LDS each, arrays of their own (so that the compiler can tell which of them a load to LDS writes).
+// st0 .. st3: the stages, C::kStage bytes of LDS each, arrays of their own (so
+// that the compiler can tell which of them a load to LDS writes).
 template <class C, bool BF16, bool ONCE = false>
 __device__ __forceinline__ void tile(const Product& p, const Rows& r, int64_t panel0, Stores store, int8_t* st0,
                                      int8_t* st1, int8_t* st2, int8_t* st3) {
@@ -506,7 +508,8 @@ __device__ __forceinline__ void tile(const Product& p, const Rows& r, int64_t pa
   // Step t multiplies stage t % 4 by the weights of set t % 2: the first
   // chunk's products, then the second's, each chunk's registers loaded again
   // for step t + 2 as soon as its products are issued.
-  auto step = [&](int t, const int8_t* cur, Weights<NJ>& w, int8_t* refill, bool more_a, bool more_w, bool full, bool live = true) {
+  auto step = [&](int t, const int8_t* cur, Weights<NJ>& w, int8_t* refill, bool more_a, bool more_w, bool full,
+                  bool live = true) {
     // this wave's part of stage t is in LDS; what may still fly is younger:
     // the stages of t + 1 and t + 2, the weights from t on
     if (full) wait_loads<4 * NJ + 2 * C::kA>(); else wait_loads<0>();
