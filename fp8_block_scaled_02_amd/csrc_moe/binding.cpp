@@ -597,7 +597,7 @@ PyObject* linear(PyObject* const* a) {
   return rc ? status(rc) : THPVariable_Wrap(y);
 }
 
-// (stream, x, logits, k, w_packed, w_scales, renormalize, fp32)
+// (stream, x, logits, k, w_packed, w_scales, renormalize, fp32 rows, fp32 output)
 //   -> (out, gates, experts, expert_offsets, row_index, token_rows)
 PyObject* forward(PyObject* const* a) {
   const Tensor &x = tensor(a[1], "x"), &logits = tensor(a[2], "logits");
@@ -607,7 +607,7 @@ PyObject* forward(PyObject* const* a) {
   if (r.l.rows != m.rows) refuse("logits must have " + std::to_string(m.rows) + " rows");
   if (r.l.cols != w.w.size(0)) refuse("logits must be of " + std::to_string(w.w.size(0)) + " experts");
   const bool renormalize = truth(a[6]);
-  const at::ScalarType type = out_type(a[7]);
+  const at::ScalarType rows = out_type(a[7]), type = out_type(a[8]);
   const int64_t T = m.rows, k = r.k, R = T * k, E = r.l.cols;
   if (R >= (1 << 24)) refuse("too many rows: T * k < 2^24");
   on(x.get_device(), {&logits, &w.w, &w.sw});
@@ -617,18 +617,19 @@ PyObject* forward(PyObject* const* a) {
   const Tensor out = empty({T, w.N}, type, x);
   if (T > 0) {
     const Quantised q(x, m);
-    // an expert's rows in the output's type: for bf16 each is rounded once more,
-    // and half as many bytes go out and come back (at 4096 tokens, 8 slots of
-    // 7168, 470 MB against 940); the sum over the slots is in fp32 either way
-    const Tensor y = empty({R, w.N}, type, x);
+    // rows of bf16 are rounded once more than the output, for half as many bytes
+    // out and back (8 of 256 experts, 7168 -> 2048: 32 tokens 127 us with rows in
+    // fp32, 125 in bf16, 4096 tokens 897 and 824); the sum over the slots is in
+    // fp32 either way
+    const Tensor y = empty({R, w.N}, rows, x);
     void *yp = y.data_ptr(), *op = out.data_ptr();
     const int rc = launch([&] {
       if (const int rc1 = q.make(m, stream)) return rc1;
       if (const int rc1 = int8_grouped_gemm(q.c, q.ld, q.s, T, ptr<int32_t>(p.row_index), ptr<int32_t>(p.offsets), R, E,
-                                            ptr<int8_t>(w.w), ptr<float>(w.sw), w.N, m.cols, yp, w.N, type_of(type),
+                                            ptr<int8_t>(w.w), ptr<float>(w.sw), w.N, m.cols, yp, w.N, type_of(rows),
                                             stream))
         return rc1;
-      return moe_combine(yp, type_of(type), w.N, R, w.N, ptr<int32_t>(p.token_rows), ptr<float>(p.gates), T, k, op,
+      return moe_combine(yp, type_of(rows), w.N, R, w.N, ptr<int32_t>(p.token_rows), ptr<float>(p.gates), T, k, op,
                          type_of(type), w.N, stream);
     });
     if (rc) return status(rc);
@@ -668,7 +669,7 @@ PyMethodDef methods[] = {method<route, 4>("route"),
                          method<gemm, 8>("gemm"),
                          method<grouped, 9>("grouped"),
                          method<linear, 6>("linear"),
-                         method<forward, 8>("forward"),
+                         method<forward, 9>("forward"),
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_moe_binding", "Host side of moe.py's calls.", -1, methods,

@@ -99,10 +99,10 @@ def _call(fn, first, *args):
     return out
 
 
-def _fp32(out_dtype):
-    if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
-        raise ValueError("out_dtype must be bfloat16 or float32")
-    return out_dtype is torch.float32
+def _fp32(dtype, name="out_dtype"):
+    if dtype is not torch.bfloat16 and dtype is not torch.float32:
+        raise ValueError(f"{name} must be bfloat16 or float32")
+    return dtype is torch.float32
 
 
 class Routing(NamedTuple):
@@ -199,9 +199,15 @@ def int8_linear(x, w_packed, w_scales, bias=None, out_dtype=torch.bfloat16):
     return _call("linear", x, w_packed, w_scales, bias, _fp32(out_dtype))
 
 
-def int8_moe_forward(x, logits, k: int, w_packed, w_scales, renormalize: bool = True, out_dtype=torch.bfloat16):
+def int8_moe_forward(x, logits, k: int, w_packed, w_scales, renormalize: bool = True, out_dtype=None, rows_dtype=None):
     """One expert projection: moe_route of the logits, int8_quant of the
-    tokens, int8_grouped_gemm (rows in out_dtype), moe_combine.  Returns
-    (out [T, N], the Routing)."""
-    out = _call("forward", x, logits, k, w_packed, w_scales, renormalize, _fp32(out_dtype))
+    tokens, int8_grouped_gemm, moe_combine.  Returns (out [T, N], the Routing).
+    With neither type given the experts' rows are held in fp32, and only the
+    output is rounded, once, to bf16.  out_dtype is the type of both, so that
+    bf16 rows are rounded before their sum and take half the bytes; rows_dtype
+    gives the rows' own."""
+    if rows_dtype is None:
+        rows_dtype = torch.float32 if out_dtype is None else out_dtype
+    out = _call("forward", x, logits, k, w_packed, w_scales, renormalize, _fp32(rows_dtype, "rows_dtype"),
+                out_dtype is not None and _fp32(out_dtype))
     return out[0], Routing(*out[1:])

@@ -1,0 +1,75 @@
+"""Expert routing and the integer layers at the edges of their ranges, on the
+GPU against the 64-bit oracle.
+
+Tolerances as where the operators are tested in general: u = 2^-24, a rounding
+of fp32; h = 2^-8, one of bf16.
+"""
+import numpy as np
+import pytest
+import torch
+
+import workloads as W
+from oracle import moe as O
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+U, H = 2.0 ** -24, 2.0 ** -8
+bf16, f32, i8 = torch.bfloat16, torch.float32, torch.int8
+INF, NAN = float("inf"), float("nan")
+
+
+@pytest.fixture(scope="module")
+def F():
+    import fp8_block_scaled_02_amd as F
+    assert torch.cuda.is_available()
+    return F
+
+
+def _np(t):
+    return t.detach().double().cpu().numpy()
+
+
+def _gen(seed):
+    return torch.Generator(device=DEV).manual_seed(seed)
+
+
+# ---- the expert layer's rows --------------------------------------------------
+
+
+@pytest.mark.parametrize("T,E,k,K,N,renorm", [(1, 8, 2, 256, 200, True), (7, 256, 8, 512, 1800, True), (70, 12, 3, 300, 129, False),
+                                              (600, 16, 8, 256, 256, True)])
+def test_layer_rounds_once(F, T, E, k, K, N, renorm):
+    """By default the experts' rows keep 32 bits: nothing but the output is
+    rounded to bf16.
+
+    A row is off by 3 u (its sum's conversion and two products), a weight by
+    u (d + 2 n + 8), the k fused multiply-adds by k u, all of the sum of
+    magnitudes; their products are below 2^-10 of that.  Then h |out|."""
+    g = _gen(T + N)
+    x = W.activations(T, K, 2, 20.0, g)
+    l = torch.randn(T, E, generator=g, device=DEV)
+    l[3::7] = -INF
+    w = torch.randn(E * N, K, generator=g, device=DEV) * 0.02
+    c, sw = F.int8_quant(w)
+    c, sw = c.reshape(E, N, K), sw.view(E, N)
+    out, r = F.int8_moe_forward(x, l, k, F.int8_weight_pack(c), sw, renorm)
+    assert out.dtype == bf16
+    oc, os = O.quantise(x.float().cpu().numpy())
+    experts = O.choose(_np(l), k)
+    gates, dist = O.gates(_np(l), experts, renorm)
+    ref, mag = np.zeros((T, N)), np.zeros((T, N))
+    for e in range(E):
+        v = O.product(oc, c[e].cpu().numpy()) * os[:, None].astype(np.float64) * _np(sw)[e]
+        share = (gates * (experts == e)).sum(1)[:, None]
+        ref += share * v
+        mag += np.abs(share * v)
+    err = mag * U * (3 + dist.max() + 2 * (k if renorm else E) + 8 + k) * (1 + 2.0 ** -10)
+    assert (np.abs(_np(out) - ref) <= err + H * (np.abs(ref) + err)).all()
+    # rows of a type that the caller chooses: the parts' calls with it
+    a, sa = F.int8_quant(x)
+    for rows, odt in ((f32, bf16), (bf16, bf16), (bf16, f32), (f32, f32)):
+        y = F.int8_grouped_gemm(a, sa, r.row_index, r.expert_offsets, F.int8_weight_pack(c), sw, rows)
+        got, _ = F.int8_moe_forward(x, l, k, F.int8_weight_pack(c), sw, renorm, odt, rows)
+        assert got.dtype == odt and torch.equal(got, F.moe_combine(y, r.token_rows, r.gates, odt))
+        if (rows, odt) == (f32, bf16):
+            assert torch.equal(got, out)
