@@ -557,10 +557,15 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const float* __rest
     p[i] = 0.0f;
   }
   float dot = 0.0f;
+  uint32_t some = 0;
   for (int j = l; j < k; j += G)
-    if ((unsigned)experts[t * k + j] < (unsigned)E) dot += gates[t * k + j] * dgates[t * k + j];
+    if ((unsigned)experts[t * k + j] < (unsigned)E) {
+      dot += gates[t * k + j] * dgates[t * k + j];
+      some = 1;
+    }
   dot = sum_of<G>(dot);
-  if (!renormalize) {
+  // (without an expert the gradient is 0, also where a logit is no number)
+  if (!renormalize && max_of<G>(some)) {
     // the maximum is that of the numbers; a NaN or +inf makes the sum NaN as in the forward pass
     uint32_t top = 0;
 #pragma unroll

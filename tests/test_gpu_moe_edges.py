@@ -73,3 +73,27 @@ def test_layer_rounds_once(F, T, E, k, K, N, renorm):
         assert got.dtype == odt and torch.equal(got, F.moe_combine(y, r.token_rows, r.gates, odt))
         if (rows, odt) == (f32, bf16):
             assert torch.equal(got, out)
+
+
+# ---- the router's gradient ------------------------------------------------------
+
+
+@pytest.mark.parametrize("E", [9, 60, 200, 700])
+@pytest.mark.parametrize("dtype", [bf16, f32])
+def test_gradient_of_tokens_without_experts(F, E, dtype):
+    """Zeros, whatever their logits and the gates' gradient are."""
+    T, k = 40, 4
+    l = torch.randn(T, E, generator=_gen(E), device=DEV).to(dtype)
+    l[::5, E // 2] = NAN
+    l[1::5, 0] = INF
+    l[2::5] = -INF
+    for renorm in (True, False):
+        r = F.moe_route(l, k, renorm)
+        experts, gates = r.experts.clone(), r.gates.clone()
+        experts[:30], gates[:30] = -1, 0.0
+        experts[25:30] = E + 5                                                       # ids outside: none either
+        d = torch.randn(T, k, generator=_gen(1), device=DEV)
+        d[10:20] = NAN
+        got = F.moe_route_backward(d, l, gates, experts, renorm)
+        assert (got[:30] == 0).all()
+        assert torch.equal(got[30:].nan_to_num(7.0), F.moe_route_backward(d, l, r.gates, r.experts, renorm)[30:].nan_to_num(7.0))
