@@ -209,8 +209,9 @@ def fp8_weight_dequant(q: torch.Tensor, scales: torch.Tensor, w=None):
 
 def fp8_moe_combine(y: torch.Tensor, token_rows: torch.Tensor, gates: torch.Tensor, out_dtype=torch.bfloat16,
                     out=None):
-    """out[t] = sum_j gates[t, j] * y[token_rows[t, j]] (fp32 accumulation):
-    y bf16 [R, N] routed rows, token_rows int32 [T, k], gates fp32 [T, k]."""
+    """out[t] = sum_j gates[t, j] * y[token_rows[t, j]] over the slots that have
+    a row (fp32 accumulation): y bf16 [R, N] routed rows, token_rows int32
+    [T, k] (-1 for an empty slot), gates fp32 [T, k]."""
     _need(y.dtype == torch.bfloat16 and y.dim() == 2 and y.is_contiguous(), "y must be contiguous 2-D bf16")
     _need(token_rows.dtype == torch.int32 and token_rows.is_contiguous(), "token_rows must be contiguous int32")
     _need(gates.dtype == torch.float32 and gates.is_contiguous(), "gates must be contiguous float32")

@@ -5,8 +5,8 @@
 // After the grouped GEMM has produced one output row per routed (token,
 // slot) pair, each token's output is the gate-weighted sum of its rows:
 //   out[t][n] = sum_j gates[t][j] * y[token_rows[t][j]][n],
-// accumulated in fp32 in slot order (one FMA per slot), then written as
-// fp32 or bf16 (nearest even).  HBM-bound: every routed row is read once
+// over the slots that have a row, accumulated in fp32 in slot order (one FMA
+// per slot), then written as fp32 or bf16 (nearest even).  HBM-bound: every routed row is read once
 // (2 bytes per element) and every token row written once; each thread
 // covers 8 consecutive columns (one 16-byte load per slot).
 #include "common.hpp"
@@ -28,16 +28,28 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(
   for (int j0 = 0; j0 < topk; j0 += 8) {
     uint4 v[8];
     float g[8];
+    int empty = 0;  // slots without a row, a bit each
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       v[j] = make_uint4(0, 0, 0, 0);
       g[j] = 0.0f;
       if (j0 + j < topk) {
-        // rows outside [0, R) are a contract violation: clamp so nothing faults
-        const int64_t r = min(max((int64_t)token_rows[t * topk + j0 + j], (int64_t)0), R - 1);
+        // (row 0 is read in place of one outside [0, R), so that there is no
+        // branch between the loads)
+        const int64_t r = token_rows[t * topk + j0 + j];
+        const bool has = r >= 0 && r < R;
+        empty |= has ? 0 : 1 << j;
         g[j] = gates[t * topk + j0 + j];
-        v[j] = *reinterpret_cast<const uint4*>(y + r * N + n);
+        v[j] = *reinterpret_cast<const uint4*>(y + (has ? r : 0) * N + n);
       }
+    }
+    if (__any(empty)) {  // an empty slot counts as zeros, whatever its gate and row 0 hold
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (empty >> j & 1) {
+          v[j] = make_uint4(0, 0, 0, 0);
+          g[j] = 0.0f;
+        }
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {

@@ -277,8 +277,9 @@ int fp8_grouped_gemm_packed(const uint8_t *a, const float *a_scales,
  *   y           bf16 [R][N] (the grouped GEMM's rows in routed order),
  *               contiguous, 16-byte aligned; R >= 1.
  *   N           > 0, N % 8 == 0.
- *   token_rows  int32 [T][topk]: routed row of (token, slot); rows outside
- *               [0, R) give unspecified outputs but never fault.
+ *   token_rows  int32 [T][topk]: routed row of (token, slot); a slot whose
+ *               row is outside [0, R), as -1, is empty: neither its gate nor
+ *               a row counts.
  *   gates       float [T][topk] gate weights (the model's gating function
  *               is the caller's).
  *   T >= 0 (0 is a no-op); 1 <= topk <= 64.

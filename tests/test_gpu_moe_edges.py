@@ -97,3 +97,23 @@ def test_gradient_of_tokens_without_experts(F, E, dtype):
         got = F.moe_route_backward(d, l, gates, experts, renorm)
         assert (got[:30] == 0).all()
         assert torch.equal(got[30:].nan_to_num(7.0), F.moe_route_backward(d, l, r.gates, r.experts, renorm)[30:].nan_to_num(7.0))
+
+
+# ---- the plan in the block-scaled layer ---------------------------------------
+
+
+@pytest.mark.parametrize("out", [bf16, f32])
+@pytest.mark.parametrize("T,k,R,N", [(1, 1, 3, 8), (37, 8, 100, 136), (20, 17, 400, 520), (300, 4, 1300, 1024)])
+def test_block_scaled_combine_of_empty_slots(F, T, k, R, N, out):
+    g = _gen(N)
+    tr = torch.randperm(max(R, T * k), generator=g, device=DEV)[:T * k].view(T, k).int()
+    tr[torch.rand(T, k, generator=g, device=DEV) < 0.3] = -1
+    tr[::3] = -1
+    tr[2::9, 0] = 2 ** 31 - 1
+    y = torch.randn(R, N, generator=g, device=DEV).to(bf16)
+    y[0] = NAN                                                                       # which no slot names
+    tr[tr == 0] = -1
+    gates = torch.randn(T, k, generator=g, device=DEV)
+    gates[tr < 0] = NAN
+    got = F.fp8_moe_combine(y, tr, gates, out)
+    assert torch.equal(got, F.moe_combine(y, tr, gates, out)) and not got[::3].any()
