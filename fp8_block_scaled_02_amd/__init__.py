@@ -236,7 +236,10 @@ def moe_forward(x: torch.Tensor, row_index, expert_offsets, token_rows, gates, w
     of the tokens (once per token, per 128 channels, fp32 scales), the
     grouped GEMM over the routed rows (gather inside), then the gate-weighted
     combine back to tokens.  packed: w_q is fp8_weight_pack of the expert
-    weights.  Returns (out [T, N], y routed rows [R, N])."""
+    weights.  The plan is that of moe_route, moe_sort or the caller; rows from
+    expert_offsets[E] on belong to no expert and slots of token_rows -1 have no
+    row.  Returns (out [T, N], y routed rows [R, N], undefined from
+    expert_offsets[E] on)."""
     a, sa = fp8_act_quant(x, 128, "fp32")
     gemm = fp8_grouped_gemm_packed if packed else fp8_grouped_gemm
     y = gemm(a, sa, row_index, expert_offsets, w_q, w_scales, torch.bfloat16)
@@ -474,7 +477,8 @@ def mxfp8_gemm(a, a_e8m0, b, b_e8m0, y=None):
 def fp8_grouped_gemm(a, a_scales, row_index, expert_offsets, w, w_scales, out_dtype=torch.bfloat16, y=None):
     """Grouped MoE GEMM: a [T, K] token codes, a_scales [T, K/128],
     row_index int32 [R], expert_offsets int32 [E+1] (device), w [E, N, K],
-    w_scales [E, N/128, K/128] -> y [R, N] in routed order."""
+    w_scales [E, N/128, K/128] -> y [R, N] in routed order.  Rows from
+    expert_offsets[E] on are left as they were."""
     T, R, E, N, K, od = _grouped_operands(a, a_scales, row_index, expert_offsets, w, w_scales, out_dtype)
     if y is None:
         y = torch.empty(R, N, dtype=out_dtype, device=a.device)

@@ -235,8 +235,11 @@ int mxfp8_gemm(const uint8_t *a, int64_t ld_a, const uint8_t *a_e8m0,
  *   a_scales        float [T][K/128].
  *   row_index       int32 [R] (device) token of each routed row.
  *   expert_offsets  int32 [E+1] (device), non-decreasing, [0] = 0,
- *                   [E] = R.  Entries outside that contract, or token ids
- *                   outside [0, T), give unspecified rows but never fault.
+ *                   [E] <= R.  Rows from [E] on are left as they were and
+ *                   their row_index is not looked at (the plan of moe_route,
+ *                   fp8moe.h, has -1 there).  Entries outside that contract,
+ *                   or other token ids outside [0, T), give unspecified rows
+ *                   but never fault.
  *   T >= 1, R >= 0 (0 is a no-op), 1 <= E <= 1024; T * K < 2^32 (the
  *   token matrix is gathered with 32-bit offsets).
  *   w               codes [E][N][K] (contiguous, 16-byte aligned).

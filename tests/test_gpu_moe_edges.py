@@ -117,3 +117,36 @@ def test_block_scaled_combine_of_empty_slots(F, T, k, R, N, out):
     gates[tr < 0] = NAN
     got = F.fp8_moe_combine(y, tr, gates, out)
     assert torch.equal(got, F.moe_combine(y, tr, gates, out)) and not got[::3].any()
+
+
+@pytest.mark.parametrize("packed", [True, False])
+@pytest.mark.parametrize("T,every", [(3, 2), (150, 3), (700, 5), (40, 1)])
+def test_plan_drives_the_block_scaled_layer(F, T, every, packed):
+    """The router's plan as it is, with every n-th token padding (with 1: all of
+    them, and no row is written), in the grouped product and the whole layer."""
+    E, k, N, K = 20, 4, 256, 512
+    g = _gen(T)
+    x = torch.randn(T, K, generator=g, device=DEV).to(bf16)
+    l = torch.randn(T, E, generator=g, device=DEV)
+    l[::every] = -INF
+    r = F.moe_route(l, k)
+    live = int(r.expert_offsets[-1])
+    assert live == k * (T - len(range(0, T, every)))
+    wq, ws = F.fp8_weight_quant((torch.randn(E * N, K, generator=g, device=DEV) * 0.02).to(bf16))
+    wq, ws = wq.view(E, N, K), ws.view(E, N // 128, K // 128)
+    w = F.fp8_weight_pack(wq) if packed else wq
+    gemm = F.fp8_grouped_gemm_packed if packed else F.fp8_grouped_gemm
+    a, sa = F.fp8_act_quant(x)
+    y = gemm(a, sa, r.row_index, r.expert_offsets, w, ws, bf16, torch.full((T * k, N), NAN, dtype=bf16, device=DEV))
+    assert torch.isfinite(y[:live]).all() and y[live:].isnan().all()
+    part = r.row_index[:live].contiguous()                                           # the live rows alone
+    if live:
+        assert torch.equal(y[:live], gemm(a, sa, part, r.expert_offsets, w, ws, bf16))
+    want = F.moe_combine(y, r.token_rows, r.gates)
+    assert torch.isfinite(want).all() and not want[::every].any()
+    assert torch.equal(F.fp8_moe_combine(y, r.token_rows, r.gates), want)
+    del y
+    # memory that the layer's rows may come to lie in holds NaN
+    torch.full((T * k, N), NAN, dtype=bf16, device=DEV)
+    out, y = F.moe_forward(x, r.row_index, r.expert_offsets, r.token_rows, r.gates, w, ws, packed=packed)
+    assert torch.equal(out, want)
