@@ -186,11 +186,10 @@ int int8_weight_pack(const int8_t *w, int64_t G, int64_t N, int64_t K,
                      void *stream);
 
 /*
- * int8_gemm -- y[m][n] = fp32(sum_k a[m][k] * w[n][k]) * (a_scales[m] *
- * w_scales[n]) + bias[n], the sum in 32-bit integers (exact: K <= 131071
- * products of at most 2^14), the rest in fp32, rounded once to y's type.
- * As in fp8_block_gemm the product of the two scales has to be a normal fp32
- * number for y to be as exact as that.
+ * int8_gemm -- y[m][n] = fp32(sum_k a[m][k] * w[n][k]) * a_scales[m] *
+ * w_scales[n] + bias[n], the sum in 32-bit integers (exact: K <= 131071
+ * products of at most 2^14), the rest in fp32, rounded once to y's type.  The
+ * product of the two scales alone may leave fp32's range.
  *
  *   a         int8 [M][ld_a], 16-byte aligned, ld_a % 16 == 0, ld_a >= Kp (K
  *             rounded up to 128): the bytes from K to Kp of every row are
@@ -211,7 +210,7 @@ int int8_gemm(const int8_t *a, int64_t ld_a, const float *a_scales,
  * expert e (expert_offsets[e] <= r < expert_offsets[e+1]) is row
  * t = row_index[r] of a, or row r itself where row_index is NULL (a in
  * expert order, T = R):
- *   y[r][n] = fp32(sum_k a[t][k] * w[e][n][k]) * (a_scales[t] * w_scales[e][n])
+ *   y[r][n] = fp32(sum_k a[t][k] * w[e][n][k]) * a_scales[t] * w_scales[e][n]
  *   Rows from expert_offsets[E] on are left as they were.
  *
  *   expert_offsets  int32 [E+1], non-decreasing within 0 .. R; others, or

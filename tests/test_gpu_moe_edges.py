@@ -150,3 +150,81 @@ def test_plan_drives_the_block_scaled_layer(F, T, every, packed):
     torch.full((T * k, N), NAN, dtype=bf16, device=DEV)
     out, y = F.moe_forward(x, r.row_index, r.expert_offsets, r.token_rows, r.gates, w, ws, packed=packed)
     assert torch.equal(out, want)
+
+
+# ---- scales whose product leaves fp32's range -----------------------------------
+
+
+def _codes(shape, g):
+    return torch.randint(-128, 128, shape, generator=g, device=DEV, dtype=torch.int32).to(i8)
+
+
+def _near(n, s, g):
+    return s * (1 + torch.rand(n, generator=g, device=DEV))
+
+
+def _scaled(y, v, out):
+    """Conversion, the scales' product and the one with the sum: 3 u; where the
+    result is subnormal half a step of those, 2^-150, or 2^-134 of bf16's."""
+    tol = 3 * U * np.abs(v) * (1 + 2.0 ** -10) + 2.0 ** -149
+    if out == bf16:
+        tol += H * (np.abs(v) + tol) + 2.0 ** -134
+    return (np.abs(_np(y) - v) <= tol).all()
+
+
+SCALES = [(2.0 ** -75, 2.0 ** -58), (2.0 ** -58, 2.0 ** -75), (2.0 ** -100, 2.0 ** -48), (2.0 ** 100, 2.0 ** -100),
+          (2.0 ** -100, 2.0 ** 100), (2.0 ** -135, 2.0 ** 120), (2.0 ** 120, 2.0 ** -135), (-2.0 ** -90, 2.0 ** -50)]
+
+
+@pytest.mark.parametrize("out", [f32, bf16])
+@pytest.mark.parametrize("M,N,K", [(3, 70, 5000), (24, 130, 4096), (100, 300, 6000), (300, 16700, 640), (2050, 4100, 384)])
+@pytest.mark.parametrize("sa,sw", SCALES)
+def test_products_of_small_and_large_scales(F, M, N, K, sa, sw, out):
+    """Values within the range, scales' products below it, and scales of either
+    end: every kind of kernel."""
+    g = _gen(M + N)
+    a, w = _codes((M, K), g), _codes((N, K), g)
+    a[0] = 0
+    room = torch.zeros(M, -(-K // 128) * 128, dtype=i8, device=DEV)
+    room[:, :K] = a
+    sa, sw = _near(M, sa, g), _near(N, sw, g)
+    v = O.product(a.cpu().numpy(), w.cpu().numpy()) * _np(sa)[:, None] * _np(sw)
+    wp = F.int8_weight_pack(w)
+    y = F.int8_gemm(room[:, :K], sa, wp, sw, None, out)
+    assert _scaled(y, v, out) and not y[0].any()
+    # a bias of the values' size: one rounding of the sum of both, 2^-148 below the normal range
+    bias = torch.randn(N, generator=g, device=DEV) * float(np.abs(v).max())
+    ref = v + _np(bias)
+    tol = 2 * U * np.abs(v) * (1 + 2.0 ** -10) + U * np.abs(ref) + 2.0 ** -148
+    if out == bf16:
+        tol += H * (np.abs(ref) + tol) + 2.0 ** -134
+    assert (np.abs(_np(F.int8_gemm(room[:, :K], sa, wp, sw, bias, out)) - ref) <= tol * (1 + 2.0 ** -10)).all()
+
+
+@pytest.mark.parametrize("out", [f32, bf16])
+@pytest.mark.parametrize("counts,N", [([5, 0, 40, 3], 130), ([1, 31, 33, 64, 65, 128, 200] + [2] * 33, 1800)])
+@pytest.mark.parametrize("sa,sw", SCALES)
+def test_grouped_products_of_small_and_large_scales(F, counts, N, sa, sw, out):
+    E, R, K = len(counts), sum(counts), 1024
+    g = _gen(N)
+    a, w = _codes((R, K), g), _codes((E, N, K), g)
+    sa, sw = _near(R, sa, g), _near(E * N, sw, g).view(E, N)
+    offs = torch.tensor([0] + list(np.cumsum(counts)), device=DEV).int()
+    y = F.int8_grouped_gemm(a, sa, None, offs, F.int8_weight_pack(w), sw, out)
+    for e in range(E):
+        s = slice(int(offs[e]), int(offs[e + 1]))
+        v = O.product(a[s].cpu().numpy(), w[e].cpu().numpy()) * _np(sa)[s, None] * _np(sw)[e]
+        assert _scaled(y[s], v, out), e
+
+
+def test_scales_whose_product_overflows(F):
+    """A sum of zero stays zero, others are infinite; an infinite or NaN scale gives NaN."""
+    g = _gen(1)
+    a, w = _codes((40, 256), g), _codes((50, 256), g)
+    a[:20] = 0
+    for s in (2.0 ** 70, -2.0 ** 100):
+        y = F.int8_gemm(a, torch.full((40,), s, device=DEV), F.int8_weight_pack(w), torch.full((50,), 2.0 ** 80, device=DEV))
+        assert not y[:20].any() and torch.isinf(y[20:][O.product(a.cpu().numpy()[20:], w.cpu().numpy()) != 0]).all()
+    for s in (INF, NAN):
+        y = F.int8_gemm(a, torch.full((40,), s, device=DEV), F.int8_weight_pack(w), torch.ones(50, device=DEV))
+        assert y[:20].isnan().all()
