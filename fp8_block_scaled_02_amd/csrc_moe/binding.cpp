@@ -11,6 +11,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/core/GradMode.h>
 #include <c10/core/TensorImpl.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -59,6 +60,14 @@ const Tensor& tensor(PyObject* o, const char* name) {
 }
 const Tensor* maybe(PyObject* o, const char* name) { return o == Py_None ? nullptr : &tensor(o, name); }
 
+// No call records a gradient, so none takes a tensor that is to have one: it
+// would be lost without a word.
+void plain(const Tensor& t, const char* name) {
+  if (t.requires_grad() && c10::GradMode::is_enabled())
+    refuse(std::string(name) + " requires a gradient, which is not recorded here: call this under torch.no_grad() or in "
+           "a torch.autograd.Function, and the backward calls for the gradient");
+}
+
 void shape(const Tensor& t, at::IntArrayRef s, const char* name) {
   if (t.sizes() != s) refuse(std::string(name) + " must have shape " + list(s) + ", not " + list(t.sizes()));
 }
@@ -71,6 +80,7 @@ template <typename T>
 T* flat(const Tensor& t, at::ScalarType type, std::initializer_list<int64_t> s, const char* name) {
   if (t.scalar_type() != type || !t.is_contiguous()) refuse(std::string(name) + " must be contiguous " + name_of(type));
   shape(t, s, name);
+  plain(t, name);
   return static_cast<T*>(t.data_ptr());
 }
 
@@ -93,11 +103,13 @@ Mat mat(const Tensor& t, const char* name) {
 Mat real(const Tensor& t, const char* name) {
   if (t.scalar_type() != at::kBFloat16 && t.scalar_type() != at::kFloat)
     refuse(std::string(name) + " must be bfloat16 or float32");
+  plain(t, name);
   return mat(t, name);
 }
 Mat real(const Tensor& t, at::ScalarType type, std::initializer_list<int64_t> s, const char* name) {
   if (t.scalar_type() != type) refuse(std::string(name) + " must be " + name_of(type));
   shape(t, s, name);
+  plain(t, name);
   return mat(t, name);
 }
 
@@ -478,6 +490,7 @@ struct Weights {
                      : "w_packed must be contiguous int8 [Np, Kp] from int8_weight_pack");
     if (sw.scalar_type() != at::kFloat || sw.dim() != 1 + d || !sw.is_contiguous())
       refuse(experts ? "w_scales must be contiguous float32 [E, N]" : "w_scales must be contiguous float32 [N]");
+    plain(sw, "w_scales");
     N = sw.size(d);
     if (experts && sw.size(0) != w.size(0)) refuse("w_scales must be of as many experts as w_packed");
     if (N < 1 || w.size(d) != up(N, 16)) refuse("w_packed must have the " + std::to_string(N) + " rows of w_scales, filled up to a multiple of 16");

@@ -7,7 +7,8 @@ tensors' device.  The calls go through a small native module
 (csrc_moe/binding.cpp), since those of a decode step are bound by the host.
 There is no fallback: if libfp8moe.so or the module is missing the functions
 raise on first use.  Nothing here records a gradient: the backward passes are
-calls of their own.  Outputs given by the caller share no memory with each
+calls of their own, and tensors that require a gradient are refused except
+under torch.no_grad() or in a torch.autograd.Function.  Outputs given by the caller share no memory with each
 other or with inputs; 2-D tensors may have any row stride unless stated.  New
 outputs of one call may be parts of one small allocation (up to 1 MB).
 """

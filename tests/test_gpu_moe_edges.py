@@ -29,6 +29,10 @@ def _np(t):
     return t.detach().double().cpu().numpy()
 
 
+def _ints(t):
+    return t.detach().cpu().numpy()
+
+
 def _gen(seed):
     return torch.Generator(device=DEV).manual_seed(seed)
 
@@ -97,6 +101,58 @@ def test_gradient_of_tokens_without_experts(F, E, dtype):
         got = F.moe_route_backward(d, l, gates, experts, renorm)
         assert (got[:30] == 0).all()
         assert torch.equal(got[30:].nan_to_num(7.0), F.moe_route_backward(d, l, r.gates, r.experts, renorm)[30:].nan_to_num(7.0))
+
+
+class Experts(torch.autograd.Function):
+    """Tokens to their experts and back, weighted: a user's training step."""
+
+    @staticmethod
+    def forward(ctx, x, logits, scale, k, renorm):
+        import fp8_block_scaled_02_amd as F
+        r = F.moe_route(logits, k, renorm)
+        rows = F.moe_gather(x, r.token_rows, out=x.new_zeros(x.shape[0] * k, x.shape[1]))
+        of = torch.searchsorted(r.expert_offsets[1:].contiguous(), torch.arange(rows.shape[0], device=DEV).int(), right=True)
+        f = torch.where(of < scale.numel(), scale[of.clamp(max=scale.numel() - 1)], 0.0)[:, None]   # an expert is a factor
+        y = rows * f
+        ctx.save_for_backward(logits, f, y, r.gates, r.experts, r.token_rows)
+        ctx.renorm = renorm
+        return F.moe_combine(y, r.token_rows, r.gates)
+
+    @staticmethod
+    def backward(ctx, dout):
+        import fp8_block_scaled_02_amd as F
+        logits, f, y, gates, experts, rows = ctx.saved_tensors
+        dy, dg = F.moe_combine_backward(dout.contiguous(), y, rows, gates, dy=torch.zeros_like(y))
+        return (F.moe_gather_backward(dy * f, rows), F.moe_route_backward(dg, logits, gates, experts, ctx.renorm), None,
+                None, None)
+
+
+@pytest.mark.parametrize("renorm", [True, False])
+def test_in_an_autograd_function(F, renorm):
+    """Leaves that require a gradient get the one that the backward calls give."""
+    T, E, k, N = 90, 10, 3, 40
+    g = _gen(3)
+    x, l, w = (torch.randn(s, generator=g, device=DEV) for s in ((T, N), (T, E), (T, N)))
+    l[::9] = -INF
+    scale = 1.0 + torch.arange(E, device=DEV)
+    x.requires_grad_()
+    l.requires_grad_()
+    out = Experts.apply(x, l, scale, k, renorm)
+    (out * w).sum().backward()
+    with torch.no_grad():
+        r = F.moe_route(l, k, renorm)
+        rows = F.moe_gather(x, r.token_rows, out=torch.zeros(T * k, N, device=DEV))
+        of = torch.searchsorted(r.expert_offsets[1:].contiguous(), torch.arange(T * k, device=DEV).int(), right=True)
+        y = rows * torch.where(of < E, scale[of.clamp(max=E - 1)], 0.0)[:, None]
+        assert torch.equal(out, F.moe_combine(y, r.token_rows, r.gates))
+        dg = (w[:, None] * y[r.token_rows.clamp(min=0).long()]).double().sum(2) * (r.experts >= 0)
+        ref, mag = O.route_backward(_np(dg), np.where(np.isinf(_np(l)), -np.inf, _np(l)), _np(r.gates), _np(r.experts).astype(np.int64), renorm)
+    # the weights' gradients are sums of N terms, the logits' of those: (N / 256 + 18) + (2 E + k + 16) and d <= 10 roundings
+    reach = np.abs(_np(w)[:, None] * _np(y)[np.maximum(_ints(r.token_rows), 0)]).sum((1, 2))[:, None]
+    assert (np.abs(_np(l.grad) - ref) <= U * (N + 18 + 10 + 2 * E + k + 16) * 2 * reach).all()
+    # a token's gradient: its weighted factors
+    want = (r.gates.double() * torch.where(r.experts >= 0, scale.double()[r.experts.clamp(min=0).long()], 0.0)).sum(1, keepdim=True) * w.double()
+    assert ((x.grad.double() - want).abs() <= (k + 3) * U * want.abs()).all()
 
 
 # ---- the plan in the block-scaled layer ---------------------------------------
