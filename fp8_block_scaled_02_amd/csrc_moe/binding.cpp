@@ -575,6 +575,21 @@ PyObject* grouped(PyObject* const* a) {
   return rc ? status(rc) : THPVariable_Wrap(y);
 }
 
+// The limits of int8_quant and int8_gemm, or of int8_grouped_gemm and what it
+// reads and writes, for calls that make more than one of them: all are refused
+// before the first is made.
+void rows_fit(int64_t M, int64_t R, const Weights& w) {
+  if (M >= (1 << 24) || R >= (1 << 24)) refuse("too many rows: fewer than 2^24 are taken");
+  if (w.N > (1 << 25)) refuse("w_scales must be of 2^25 columns or fewer");
+  if (R * w.N > ((int64_t)1 << 36)) refuse("too many results: rows times columns may be 2^36");
+}
+void experts_fit(int64_t T, int64_t K, int64_t R, int64_t E, const Weights& w) {
+  rows_fit(T, R, w);
+  if (T * up(K, 128) >= ((int64_t)1 << 32))
+    refuse("too many codes: tokens times columns, filled up to a multiple of 128, must be below 2^32");
+  if (E * w.N > ((int64_t)1 << 30)) refuse("too many weight rows: experts times columns may be 2^30");
+}
+
 // Room for x's codes and scales, one behind the other.
 struct Quantised {
   int64_t ld;
@@ -597,6 +612,7 @@ PyObject* linear(PyObject* const* a) {
   const Tensor* bias = maybe(a[4], "bias");
   const float* bp = bias ? flat<float>(*bias, at::kFloat, {w.N}, "bias") : nullptr;
   const at::ScalarType type = out_type(a[5]);
+  rows_fit(m.rows, m.rows, w);
   on(x.get_device(), {&w.w, &w.sw, bias});
   void* stream = address(a[0]);
   const Quantised q(x, m);
@@ -622,7 +638,7 @@ PyObject* forward(PyObject* const* a) {
   const bool renormalize = truth(a[6]);
   const at::ScalarType rows = out_type(a[7]), type = out_type(a[8]);
   const int64_t T = m.rows, k = r.k, R = T * k, E = r.l.cols;
-  if (R >= (1 << 24)) refuse("too many rows: T * k < 2^24");
+  experts_fit(T, m.cols, R, E, w);
   on(x.get_device(), {&logits, &w.w, &w.sw});
   void* stream = address(a[0]);
   Plan p;

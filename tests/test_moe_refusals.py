@@ -56,3 +56,38 @@ def test_inside_an_autograd_function():
             return F.moe_route(logits, 2).gates
 
     _raises("on a GPU", Route.apply, torch.zeros(4, 16, requires_grad=True))
+
+
+def _meta(shape, dtype=i8):
+    """Sizes alone, of arrays that no machine holds."""
+    return torch.empty(shape, dtype=dtype, device="meta")
+
+
+def test_limits_of_a_whole_layer():
+    """A size that any part of int8_linear or int8_moe_forward does not take is
+    refused before the first part runs."""
+    def layer(T, K, E, k, N):
+        F.int8_moe_forward(_meta((T, K), bf16), _meta((T, E), bf16), k, _meta((E, -(-N // 16) * 16, -(-K // 128) * 128)),
+                           _meta((E, N), f32))
+
+    _raises("fewer than 2.24", layer, 1 << 22, 16, 8, 4, 16)
+    _raises("on a GPU", layer, (1 << 22) - 1, 16, 8, 4, 16)
+    _raises("too many codes", layer, 1 << 16, 1 << 16, 8, 2, 16)
+    _raises("too many codes", layer, 1 << 23, 400, 8, 1, 16)
+    _raises("on a GPU", layer, (1 << 16) - 1, 1 << 16, 8, 2, 16)
+    _raises("too many results", layer, 1 << 23, 16, 8, 1, 8193)
+    _raises("on a GPU", layer, 1 << 23, 16, 8, 1, 8192)
+    _raises("too many weight rows", layer, 8, 16, 1024, 2, (1 << 20) + 1)
+    _raises("on a GPU", layer, 8, 16, 1024, 2, 1 << 20)
+    _raises("2.25 columns", layer, 8, 16, 1, 1, (1 << 25) + 1)
+    _raises("rows_dtype must be", F.int8_moe_forward, _meta((8, 16), bf16), _meta((8, 4)), 2, _meta((4, 16, 128)),
+            _meta((4, 16), f32), True, None, torch.float16)
+
+    def linear(M, K, N):
+        F.int8_linear(_meta((M, K), bf16), _meta((-(-N // 16) * 16, -(-K // 128) * 128)), _meta((N,), f32))
+
+    _raises("fewer than 2.24", linear, 1 << 24, 16, 16)
+    _raises("too many results", linear, 1 << 23, 16, 8193)
+    _raises("2.25 columns", linear, 8, 16, (1 << 25) + 1)
+    _raises("on a GPU", linear, 1 << 23, 16, 8192)
+    _raises("on a GPU", linear, 2048, 16, 1 << 25)
