@@ -11,7 +11,8 @@ using fp8moe::Mat;
 
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 inline hipStream_t as_stream(void* s) { return static_cast<hipStream_t>(s); }
-constexpr int64_t kMaxLd = (int64_t)1 << 40;       // row numbers below 2^30 times this stay in 64 bits
+constexpr int64_t kMaxLd = (int64_t)1 << 40;
+constexpr int64_t kMaxBytes = (int64_t)1 << 62;    // of an array, first row to last: offsets stay in 64 bits
 constexpr int64_t kMaxTokens = (int64_t)1 << 24;
 constexpr int64_t kMaxRows = (int64_t)1 << 30;
 constexpr int64_t kMaxCols = (int64_t)1 << 29;    // of a row: 32-bit byte offsets, with room behind it
@@ -26,8 +27,11 @@ bool type_ok(int t) { return t == FP8B_OUT_F32 || t == FP8B_OUT_BF16; }
 int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 
 Mat mat(const void* p, int type, int64_t ld) { return {const_cast<void*>(p), ld, type == FP8B_OUT_BF16}; }
-int mat_check(const Mat& m, int64_t cols) {
-  if (!m.p || m.ld < cols || m.ld > kMaxLd) return FP8B_EINVAL;
+// Whether rows `ld` items apart (which is no more than kMaxLd, and cols no less
+// than 1) have offsets in range.
+bool rows_fit(int64_t rows, int64_t ld, int64_t item) { return rows <= 1 || ld <= kMaxBytes / item / rows; }
+int mat_check(const Mat& m, int64_t rows, int64_t cols) {
+  if (!m.p || m.ld < cols || m.ld > kMaxLd || !rows_fit(rows, m.ld, m.bf16 ? 2 : 4)) return FP8B_EINVAL;
   return aligned(m.p, m.bf16 ? 2 : 4) ? FP8B_OK : FP8B_EALIGN;
 }
 // 4-byte arrays that have to be there.
@@ -58,13 +62,13 @@ int row_sizes(int64_t T, int64_t N, int64_t k, int64_t R) {
   return FP8B_OK;
 }
 
-int product_check(const fp8moe::Product& p) {
+int product_check(const fp8moe::Product& p, int64_t rows) {
   if (!p.a || !p.sa || !p.w || !p.sw || !p.y.p) return FP8B_EINVAL;
   if (p.lda < up(p.K, 128) || p.lda >= (1 << 24)) return FP8B_EINVAL;
   if (!aligned(p.a, 16) || p.lda % 16 != 0 || !aligned(p.w, 16) || !aligned(p.sa, 4) || !aligned(p.sw, 4) ||
       !aligned(p.bias, 4))
     return FP8B_EALIGN;
-  return mat_check(p.y, p.N);
+  return mat_check(p.y, rows, p.N);
 }
 int product_sizes(int64_t N, int64_t K, int out_dtype) {
   if (!type_ok(out_dtype)) return FP8B_EUNSUPPORTED;
@@ -99,7 +103,7 @@ FP8B_EXPORT int moe_route(const void* logits, int dtype, int64_t ld, int64_t T, 
   const fp8moe::Plan p{experts, expert_offsets, row_index, token_rows};
   FP8B_TRY(plan_check(p, T, workspace));
   if (T > 0) {
-    FP8B_TRY(mat_check(mat(logits, dtype, ld), E));
+    FP8B_TRY(mat_check(mat(logits, dtype, ld), T, E));
     FP8B_TRY(words_check({gates}));
   }
   return fp8moe::launch_route(mat(logits, dtype, ld), T, (int)E, (int)k, renormalize != 0, gates, p,
@@ -120,9 +124,9 @@ FP8B_EXPORT int moe_route_backward(const float* dgates, const void* logits, int 
   if (!type_ok(dtype)) return FP8B_EUNSUPPORTED;
   FP8B_TRY(sort_sizes(T, E, k));
   if (T == 0) return FP8B_OK;
-  if (!renormalize) FP8B_TRY(mat_check(mat(logits, dtype, ld), E));
+  if (!renormalize) FP8B_TRY(mat_check(mat(logits, dtype, ld), T, E));
   FP8B_TRY(words_check({dgates, gates, experts}));
-  FP8B_TRY(mat_check(mat(dlogits, dtype, ld_d), E));
+  FP8B_TRY(mat_check(mat(dlogits, dtype, ld_d), T, E));
   return fp8moe::launch_route_backward(dgates, mat(logits, dtype, ld), gates, experts, T, (int)E, (int)k,
                                        renormalize != 0, mat(dlogits, dtype, ld_d), as_stream(stream));
 }
@@ -132,9 +136,9 @@ FP8B_EXPORT int moe_gather(const void* x, int dtype, int64_t ld_x, int64_t T, in
   if (!type_ok(dtype)) return FP8B_EUNSUPPORTED;
   FP8B_TRY(row_sizes(T, N, k, R));
   if (T == 0 || R == 0) return FP8B_OK;
-  FP8B_TRY(mat_check(mat(x, dtype, ld_x), N));
+  FP8B_TRY(mat_check(mat(x, dtype, ld_x), T, N));
   FP8B_TRY(words_check({token_rows}));
-  FP8B_TRY(mat_check(mat(rows, dtype, ld_r), N));
+  FP8B_TRY(mat_check(mat(rows, dtype, ld_r), R, N));
   return fp8moe::launch_gather(mat(x, dtype, ld_x), T, N, token_rows, (int)k, R, mat(rows, dtype, ld_r),
                                as_stream(stream));
 }
@@ -145,10 +149,10 @@ FP8B_EXPORT int moe_combine(const void* y, int y_dtype, int64_t ld_y, int64_t R,
   if (!type_ok(y_dtype) || !type_ok(out_dtype)) return FP8B_EUNSUPPORTED;
   FP8B_TRY(row_sizes(T, N, k, R));
   if (T == 0) return FP8B_OK;
-  if (R > 0) FP8B_TRY(mat_check(mat(y, y_dtype, ld_y), N));
+  if (R > 0) FP8B_TRY(mat_check(mat(y, y_dtype, ld_y), R, N));
   FP8B_TRY(words_check({token_rows}));
   if (!aligned(gates, 4)) return FP8B_EALIGN;
-  FP8B_TRY(mat_check(mat(out, out_dtype, ld_o), N));
+  FP8B_TRY(mat_check(mat(out, out_dtype, ld_o), T, N));
   return fp8moe::launch_combine(mat(y, y_dtype, ld_y), R, N, token_rows, gates, T, (int)k, mat(out, out_dtype, ld_o),
                                 as_stream(stream));
 }
@@ -159,10 +163,10 @@ FP8B_EXPORT int moe_combine_backward(const void* dout, int out_dtype, int64_t ld
   if (!type_ok(y_dtype) || !type_ok(out_dtype)) return FP8B_EUNSUPPORTED;
   FP8B_TRY(row_sizes(T, N, k, R));
   if (T == 0) return FP8B_OK;
-  FP8B_TRY(mat_check(mat(dout, out_dtype, ld_o), N));
+  FP8B_TRY(mat_check(mat(dout, out_dtype, ld_o), T, N));
   if (R > 0) {
-    FP8B_TRY(mat_check(mat(y, y_dtype, ld_y), N));
-    FP8B_TRY(mat_check(mat(dy, y_dtype, ld_dy), N));
+    FP8B_TRY(mat_check(mat(y, y_dtype, ld_y), R, N));
+    FP8B_TRY(mat_check(mat(dy, y_dtype, ld_dy), R, N));
   }
   FP8B_TRY(words_check({token_rows, gates, dgates}));
   return fp8moe::launch_combine_backward(mat(dout, out_dtype, ld_o), mat(y, y_dtype, ld_y), R, N, token_rows, gates, T,
@@ -174,8 +178,8 @@ FP8B_EXPORT int int8_quant(const void* x, int dtype, int64_t M, int64_t K, int64
   if (!type_ok(dtype)) return FP8B_EUNSUPPORTED;
   if (M < 0 || M >= kMaxTokens || K < 1 || K >= kMaxCols) return FP8B_EINVAL;
   if (M == 0) return FP8B_OK;
-  FP8B_TRY(mat_check(mat(x, dtype, ld_x), K));
-  if (!codes || ld_c < K || ld_c > kMaxLd) return FP8B_EINVAL;
+  FP8B_TRY(mat_check(mat(x, dtype, ld_x), M, K));
+  if (!codes || ld_c < K || ld_c > kMaxLd || !rows_fit(M, ld_c, 1)) return FP8B_EINVAL;
   FP8B_TRY(words_check({scales}));
   return fp8moe::launch_quant(mat(x, dtype, ld_x), M, K, codes, ld_c, scales, as_stream(stream));
 }
@@ -185,6 +189,7 @@ FP8B_EXPORT int int8_weight_pack(const int8_t* w, int64_t G, int64_t N, int64_t 
   if (G < 1 || N < 1 || N > kMaxN || K < 1 || K > kMaxK) return FP8B_EINVAL;
   if (G >= kMaxCodes || up(N, 16) * up(K, 128) >= kMaxCodes / G) return FP8B_EINVAL;
   if (!w || !w_packed || ld_w < K || ld_w > kMaxLd || stride_w < 0 || stride_w > kMaxLd) return FP8B_EINVAL;
+  if (!rows_fit(N, ld_w, 1) || !rows_fit(G, stride_w, 1)) return FP8B_EINVAL;
   if (!aligned(w_packed, 16)) return FP8B_EALIGN;
   return fp8moe::launch_pack(w, G, N, K, ld_w, stride_w, w_packed, as_stream(stream));
 }
@@ -196,7 +201,7 @@ FP8B_EXPORT int int8_gemm(const int8_t* a, int64_t ld_a, const float* a_scales, 
   if (M < 0 || M >= kMaxTokens || M * N > kMaxOut) return FP8B_EINVAL;
   if (M == 0) return FP8B_OK;
   const fp8moe::Product p{a, ld_a, a_scales, w_packed, w_scales, bias, N, K, mat(y, out_dtype, ld_y)};
-  FP8B_TRY(product_check(p));
+  FP8B_TRY(product_check(p, M));
   return fp8moe::launch_gemm(p, M, as_stream(stream));
 }
 
@@ -212,7 +217,7 @@ FP8B_EXPORT int int8_grouped_gemm(const int8_t* a, int64_t ld_a, const float* a_
   if (ld_a < 0 || ld_a >= (1 << 24) || T * ld_a >= (int64_t)1 << 32) return FP8B_EINVAL;
   if (R == 0) return FP8B_OK;
   const fp8moe::Product p{a, ld_a, a_scales, w_packed, w_scales, nullptr, N, K, mat(y, out_dtype, ld_y)};
-  FP8B_TRY(product_check(p));
+  FP8B_TRY(product_check(p, R));
   FP8B_TRY(words_check({expert_offsets}));
   if (!aligned(row_index, 4)) return FP8B_EALIGN;
   return fp8moe::launch_grouped(p, T, row_index, expert_offsets, R, (int)E, as_stream(stream));

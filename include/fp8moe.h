@@ -27,7 +27,8 @@
  *
  * Types of arrays that may be fp32 or bf16 are given by fp8b_out_dtype.
  * Leading dimensions ld_* are in elements, at least the row length, at most
- * 2^40; arrays need the alignment of their type only, unless stated.
+ * 2^40, and rows times ld_* times the element's size at most 2^62 bytes where
+ * there is more than one row; arrays need the alignment of their type only, unless stated.
  */
 #ifndef FP8MOE_H
 #define FP8MOE_H
@@ -178,7 +179,8 @@ int int8_quant(const void *x, int dtype, int64_t M, int64_t K, int64_t ld_x,
  *
  *   w         int8, matrix i, row n at w + i * stride_w + n * ld_w
  *             (0 <= stride_w <= 2^40).
- *   G >= 1; 1 <= N <= 2^25; 1 <= K <= 131071; G * Np * Kp < 2^46.
+ *   G >= 1; 1 <= N <= 2^25; 1 <= K <= 131071; G * Np * Kp < 2^46;
+ *   G * stride_w <= 2^62.
  *   w_packed  G * Np * Kp bytes, 16-byte aligned, not overlapping w.
  */
 int int8_weight_pack(const int8_t *w, int64_t G, int64_t N, int64_t K,

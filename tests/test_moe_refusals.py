@@ -91,3 +91,44 @@ def test_limits_of_a_whole_layer():
     _raises("2.25 columns", linear, 8, 16, (1 << 25) + 1)
     _raises("on a GPU", linear, 1 << 23, 16, 8192)
     _raises("on a GPU", linear, 2048, 16, 1 << 25)
+
+
+EINVAL, F32, BF16 = -1, 0, 1
+GOOD = 1 << 20                                                      # an address, never dereferenced here
+
+
+def _refuses(f, good, cases):
+    """Each case: (position: value, ..., status), the other arguments as in good."""
+    for over, want in cases:
+        a = list(good)
+        for i, v in over.items():
+            a[i] = v
+        assert f(*a) == want, (over, want)
+
+
+def test_leading_dimensions_whose_offsets_would_not_fit():
+    """Rows times their distance: offsets in bytes stay within 63 bits."""
+    L, far = F.moe_lib(), 1 << 40
+    T = (1 << 24) - 1                                       # times 2^40 elements: past 2^63 bytes
+    good = [GOOD, BF16, 64, 4, 64, 8, 1, GOOD, GOOD, GOOD, GOOD, GOOD, GOOD, None]
+    _refuses(L.moe_route, good, [({3: T, 2: far}, EINVAL)])
+    good = [GOOD, GOOD, F32, 64, GOOD, GOOD, 4, 64, 8, 0, GOOD, 64, None]
+    _refuses(L.moe_route_backward, good, [({6: T, 3: far}, EINVAL), ({6: T, 11: far}, EINVAL)])
+    good = [GOOD, F32, 64, 4, 64, GOOD, 8, 32, GOOD, 64, None]
+    _refuses(L.moe_gather, good, [({3: T, 2: far}, EINVAL), ({7: (1 << 30) - 1, 9: far}, EINVAL)])
+    good = [GOOD, F32, 64, 32, 64, GOOD, GOOD, 4, 8, GOOD, BF16, 64, None]
+    _refuses(L.moe_combine, good, [({3: (1 << 30) - 1, 2: far}, EINVAL), ({7: T, 11: far}, EINVAL)])
+    good = [GOOD, BF16, 64, GOOD, F32, 64, 32, 64, GOOD, GOOD, 4, 8, GOOD, 64, GOOD, None]
+    _refuses(L.moe_combine_backward, good, [({10: T, 2: far}, EINVAL), ({6: (1 << 30) - 1, 5: far}, EINVAL),
+                                            ({6: (1 << 30) - 1, 13: far}, EINVAL)])
+    good = [GOOD, F32, 4, 64, 64, GOOD, 64, GOOD, None]
+    _refuses(L.int8_quant, good, [({2: T, 4: far}, EINVAL), ({2: T, 6: far}, EINVAL)])
+    good = [GOOD, 2, 64, 64, 64, 4096, GOOD, None]
+    _refuses(L.int8_weight_pack, good, [({2: 1 << 25, 4: far}, EINVAL), ({1: 1 << 30, 5: far}, EINVAL)])
+    good = [GOOD, 128, GOOD, GOOD, GOOD, None, 4, 64, 100, GOOD, 64, BF16, None]
+    _refuses(L.int8_gemm, good, [({6: T, 10: far}, EINVAL)])
+    good = [GOOD, 128, GOOD, 4, GOOD, GOOD, 8, 3, GOOD, GOOD, 64, 100, GOOD, 64, F32, None]
+    _refuses(L.int8_grouped_gemm, good, [({6: T, 13: far}, EINVAL)])
+    # one row has no distance to another
+    good = [GOOD, F32, 0, 64, far, GOOD, 64, GOOD, None]
+    _refuses(L.int8_quant, good, [({}, 0)])
