@@ -284,3 +284,33 @@ def test_scales_whose_product_overflows(F):
     for s in (INF, NAN):
         y = F.int8_gemm(a, torch.full((40,), s, device=DEV), F.int8_weight_pack(w), torch.ones(50, device=DEV))
         assert y[:20].isnan().all()
+
+
+# ---- the weights' gradient ------------------------------------------------------
+
+
+def _roundings(T, N, ydt, odt, aligned):
+    """Of a sum of N products in the combine's gradient: a lane's fused
+    multiply-adds (its pieces of C columns, then single ones), six sums over the
+    lanes of a wave, and one a wave."""
+    C = (8 if bf16 in (ydt, odt) else 4) if aligned else 1
+    most = 1024 if T < 1 << 22 else 256
+    threads = min(most, max(64, -(-(-(-(N // C) // 2)) // 64) * 64))
+    return -(-(N // C) // threads) * C + -(-(N % C) // threads) + 6 + threads // 64
+
+
+@pytest.mark.parametrize("ydt,odt", [(bf16, bf16), (bf16, f32), (f32, f32), (f32, bf16)])
+@pytest.mark.parametrize("N", [8, 24, 520, 1001, 2056, 5000, 7168, 16384, 40000])
+def test_gradient_of_the_weights(F, N, ydt, odt):
+    T, k = 30, 3
+    g = _gen(N)
+    y, dout = torch.randn(T * k, N, generator=g, device=DEV).to(ydt), torch.randn(T, N, generator=g, device=DEV).to(odt)
+    tr = torch.randperm(T * k, generator=g, device=DEV).view(T, k).int()
+    gates = torch.rand(T, k, generator=g, device=DEV)
+    terms = _np(y)[_ints(tr)] * _np(dout)[:, None]
+    wide = torch.zeros(T * k, N + 3, dtype=ydt, device=DEV)
+    wide[:, 1:N + 1] = y
+    for v, aligned in ((y, N % 2 == 0 or (ydt, odt) == (f32, f32)), (wide[:, 1:N + 1], ydt == f32 and (odt == f32 or N % 2 == 0))):
+        _, dg = F.moe_combine_backward(dout, v, tr, gates)
+        n = _roundings(T, N, ydt, odt, aligned)
+        assert (np.abs(_np(dg) - terms.sum(2)) <= n * U * (1 + 2.0 ** -10) * np.abs(terms).sum(2)).all()
