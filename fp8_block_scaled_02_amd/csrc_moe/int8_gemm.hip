@@ -10,7 +10,8 @@
 // packed chunk of 1 KB, 16 bytes a lane; the activations' fragment is 16 bytes
 // of 16 rows.
 //
-// Streaming kernel, for up to 32 rows, which are bound by the weights' bytes: a
+// Streaming kernel, for up to 32 rows, which are bound by the weights' bytes
+// (16 at a time in grouped products of few tiles, however many there are): a
 // workgroup has P panels of 16 weight rows and up to 16 MI tokens; its eight
 // waves take every eighth chunk of K, both operands straight to registers, and
 // add their sums in LDS.  32 x 8192 -> 28672 takes 38.8 us, 6.1 TB/s of weights.
@@ -875,8 +876,12 @@ int launch_grouped(const Product& p, int64_t T, const int32_t* row_index, const 
     constexpr bool BF16 = decltype(b)::value;
     const int64_t tiles_n = (p.N + kCols - 1) / kCols, tiles = pieces(kRows) * tiles_n;
     // Tiles of 256 columns that would leave compute units without work: panels
-    // by two instead (8 experts' 7168 -> 2048 31 us against 43; from 32 experts
-    // on tiles are faster, 47 against 51).
+    // by two instead, 16 rows at a time (8 tokens, 2 of 8 experts, 7168 -> 2048
+    // 18.8 us against 38; from 32 experts on tiles are faster, 47 against 51).
+    // Each expert's weights are read again for every 16 of its rows, which the
+    // rule does not look at, so it holds for up to about 32 rows an expert (2 of
+    // 8 experts, 4096 -> 1792: 64 tokens 18 against 26, 128 25 against 26) and
+    // loses beyond (256 tokens 40 against 29, 1024 136 against 36).
     if (tiles < 256) {
       constexpr int MI = 1, P = 2;
       const int64_t columns = (p.N + 16 * P - 1) / (16 * P);
