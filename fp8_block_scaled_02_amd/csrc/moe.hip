@@ -6,9 +6,9 @@
 // slot) pair, each token's output is the gate-weighted sum of its rows:
 //   out[t][n] = sum_j gates[t][j] * y[token_rows[t][j]][n],
 // over the slots that have a row, accumulated in fp32 in slot order (one FMA
-// per slot), then written as fp32 or bf16 (nearest even).  HBM-bound: every routed row is read once
-// (2 bytes per element) and every token row written once; each thread
-// covers 8 consecutive columns (one 16-byte load per slot).
+// per slot), then written as fp32 or bf16 (nearest even).  HBM-bound: every
+// routed row is read once (2 bytes per element) and every token row written
+// once; each thread covers 8 consecutive columns (one 16-byte load per slot).
 #include "common.hpp"
 #include "launch.hpp"
 

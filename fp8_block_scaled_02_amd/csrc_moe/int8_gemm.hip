@@ -51,7 +51,7 @@ __device__ __forceinline__ v4i mfma(v4i w, v4i x, v4i c) {
 // time, four (8 bytes of bf16, 16 of fp32), or 16 bytes of either.
 enum class Stores { values, fours, lines };
 
-// A scale as m * 2^e, 1 <= |m| < 2 (or m is 0, infinite or NaN).  The product of
+// A scale as m * 2^e, 1/2 <= |m| < 1 (or m is 0, infinite or NaN).  The product of
 // two scales may leave fp32's range where the value that they scale does not;
 // that of their m cannot, and the powers of two are exact.
 // (With the scales as they are 4096 x 7168 -> 18432 took 397 us against 398, 4096
@@ -61,7 +61,7 @@ struct Scale {
   int e;
 };
 __device__ __forceinline__ Scale split(float s) {
-  return {2.0f * __builtin_amdgcn_frexp_mantf(s), __builtin_amdgcn_frexp_expf(s) - 1};
+  return {__builtin_amdgcn_frexp_mantf(s), __builtin_amdgcn_frexp_expf(s)};
 }
 
 // The scales and biases of four columns n .. n+3 (those past the last are the
@@ -82,12 +82,10 @@ __device__ __forceinline__ Four four(const float* __restrict__ sw, const float* 
 }
 // One column's value from its sum.  (Without a bias nothing is added: -0 stays.)
 __device__ __forceinline__ float finish(int sum, Scale sa, Scale sw, float bias, bool biased) {
-  const float m = sa.m * sw.m;
-  const int e = sa.e + sw.e;
-  // with a bias the sum takes the powers of two, so that one rounding does the
-  // rest; where that leaves the normal range it costs less than 2^-148
-  return biased ? __builtin_fmaf(__builtin_amdgcn_ldexpf((float)sum, e), m, bias)
-                : __builtin_amdgcn_ldexpf((float)sum * m, e);
+  // (the powers of two last: taken by the sum, which would save a rounding with a
+  // bias, they would make NaN of a scale of zero beside a large one)
+  const float v = __builtin_amdgcn_ldexpf((float)sum * (sa.m * sw.m), sa.e + sw.e);
+  return biased ? v + bias : v;
 }
 
 // Four columns n .. n+3 of row y (those below N), from their sums.

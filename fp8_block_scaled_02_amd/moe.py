@@ -8,10 +8,11 @@ tensors' device.  The calls go through a small native module
 There is no fallback: if libfp8moe.so or the module is missing the functions
 raise on first use.  Nothing here records a gradient: the backward passes are
 calls of their own, and tensors that require a gradient are refused except
-under torch.no_grad() or in a torch.autograd.Function.  Outputs given by the caller share no memory with each
-other or with inputs; 2-D tensors may have any row stride unless stated.  New
-outputs of one call may be parts of one small allocation (up to 1 MB): copy one
-before it is resized in place.  No row is named twice in token_rows.
+under torch.no_grad() or in a torch.autograd.Function.  Outputs given by the
+caller share no memory with each other or with inputs; 2-D tensors may have any
+row stride unless stated.  New outputs of one call may be parts of one small
+allocation (up to 1 MB): copy one before it is resized in place.  No row is
+named twice in token_rows.
 """
 import ctypes
 import os

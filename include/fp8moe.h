@@ -28,7 +28,8 @@
  * Types of arrays that may be fp32 or bf16 are given by fp8b_out_dtype.
  * Leading dimensions ld_* are in elements, at least the row length, at most
  * 2^40, and rows times ld_* times the element's size at most 2^62 bytes where
- * there is more than one row; arrays need the alignment of their type only, unless stated.
+ * there is more than one row; arrays need the alignment of their type only,
+ * unless stated.
  */
 #ifndef FP8MOE_H
 #define FP8MOE_H
@@ -191,7 +192,8 @@ int int8_weight_pack(const int8_t *w, int64_t G, int64_t N, int64_t K,
  * int8_gemm -- y[m][n] = fp32(sum_k a[m][k] * w[n][k]) * a_scales[m] *
  * w_scales[n] + bias[n], the sum in 32-bit integers (exact: K <= 131071
  * products of at most 2^14), the rest in fp32, rounded once to y's type.  The
- * product of the two scales alone may leave fp32's range.
+ * product of the two scales alone may leave fp32's range; a scale of 0 gives 0
+ * beside any number.
  *
  *   a         int8 [M][ld_a], 16-byte aligned, ld_a % 16 == 0, ld_a >= Kp (K
  *             rounded up to 128): the bytes from K to Kp of every row are

@@ -248,10 +248,10 @@ def test_products_of_small_and_large_scales(F, M, N, K, sa, sw, out):
     wp = F.int8_weight_pack(w)
     y = F.int8_gemm(room[:, :K], sa, wp, sw, None, out)
     assert _scaled(y, v, out) and not y[0].any()
-    # a bias of the values' size: one rounding of the sum of both, 2^-148 below the normal range
+    # a bias of the values' size: one rounding more, of the sum of both
     bias = torch.randn(N, generator=g, device=DEV) * float(np.abs(v).max())
     ref = v + _np(bias)
-    tol = 2 * U * np.abs(v) * (1 + 2.0 ** -10) + U * np.abs(ref) + 2.0 ** -148
+    tol = 3 * U * np.abs(v) * (1 + 2.0 ** -10) + U * np.abs(ref) + 2.0 ** -149
     if out == bf16:
         tol += H * (np.abs(ref) + tol) + 2.0 ** -134
     assert (np.abs(_np(F.int8_gemm(room[:, :K], sa, wp, sw, bias, out)) - ref) <= tol * (1 + 2.0 ** -10)).all()
@@ -284,6 +284,32 @@ def test_scales_whose_product_overflows(F):
     for s in (INF, NAN):
         y = F.int8_gemm(a, torch.full((40,), s, device=DEV), F.int8_weight_pack(w), torch.ones(50, device=DEV))
         assert y[:20].isnan().all()
+
+
+@pytest.mark.parametrize("M", [5, 90, 300])
+def test_scales_of_zero_and_infinity(F, M):
+    """Beside the largest and smallest of the other side, with a bias and without."""
+    g = _gen(M)
+    N, K = 60, 640
+    a, w = _codes((M, K), g), _codes((N, K), g)
+    w[7] = 0
+    a[1:3], w[:2] = 1, -1                                                            # and sums of K with either sign
+    a[2] = 0
+    a[2, 0] = 1                                                                      # and of one
+    sums = torch.from_numpy(O.product(a.cpu().numpy(), w.cpu().numpy())).to(DEV)
+    bias = torch.randn(N, generator=g, device=DEV)
+    wp = F.int8_weight_pack(w)
+    for other in (2.0 ** 127, 2.0 ** 100, 1.0, 2.0 ** -126, 2.0 ** -149):
+        for b in (None, bias):
+            rest = torch.zeros_like(sums) if b is None else bias.double().expand(M, N)
+            zero, inf, most = (torch.full((n,), v, device=DEV) for n, v in ((M, 0.0), (M, INF), (N, other)))
+            y = F.int8_gemm(a, zero, wp, most, b, f32)
+            assert torch.equal(y.double(), rest)
+            y = F.int8_gemm(a, torch.full((M,), other, device=DEV), wp, torch.zeros(N, device=DEV), b, f32)
+            assert torch.equal(y.double(), rest)
+            want = torch.where(sums == 0, NAN, torch.sign(sums) * INF)
+            y = F.int8_gemm(a, inf, wp, most, b, f32).double()
+            assert torch.equal(y.isnan(), want.isnan()) and torch.equal(y[~want.isnan()], want[~want.isnan()])
 
 
 # ---- the weights' gradient ------------------------------------------------------
